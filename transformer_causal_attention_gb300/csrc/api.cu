@@ -12,8 +12,7 @@
 
 #include <cudaTypedefs.h>
 
-#include "attn.h"
-#include "kernels.h"
+#include "api.h"
 
 namespace attn {
 namespace {
@@ -25,14 +24,10 @@ std::atomic<unsigned long long> g_launches{0};
 std::atomic<unsigned long long> g_wait_limit_ns{2000000000ull};
 
 constexpr int kMaxDevices = 64;
-struct DeviceInfo {
-  bool ready;
-  int sms;
-  int l2_bytes;
-  unsigned int* status;
-};
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
+
+}  // namespace
 
 // Per-device facts, fetched once per device with that device current.
 int device_info(DeviceInfo* out) {
@@ -50,7 +45,7 @@ int device_info(DeviceInfo* out) {
   return ATTN_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -84,7 +79,7 @@ bool make_map4(CUtensorMap* map, const void* base, int D, int heads, int rows, i
 
 // 3-D tensor map over a bf16 tensor indexed (d, row, batch): boxes of 64 dims x
 // box_rows rows x 1 batch, 128-byte swizzle, zero fill outside.
-bool make_map3(CUtensorMap* map, const void* base, int D, int rows, int B, unsigned long long row_stride,
+static bool make_map3(CUtensorMap* map, const void* base, int D, int rows, int B, unsigned long long row_stride,
                unsigned long long batch_stride, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return false;
@@ -98,12 +93,12 @@ bool make_map3(CUtensorMap* map, const void* base, int D, int rows, int B, unsig
 }
 
 // MLA shape served by the tensor-core decode kernel (one 576-dim latent head, V = its first 512 dims).
-bool mla_shape(int B, int n_h, int n_kv, int D_qk, int D_v, bool bf16) {
+static bool mla_shape(int B, int n_h, int n_kv, int D_qk, int D_v, bool bf16) {
   return bf16 && n_h == 128 && n_kv == 1 && D_qk == 576 && D_v == 512 && B <= 1024;
 }
 
 // Dense BSHD tensor [B, S, heads, D], boxes of 128 positions.
-bool make_bshd_map(CUtensorMap* map, const void* base, int B, int S, int heads, int D) {
+static bool make_bshd_map(CUtensorMap* map, const void* base, int B, int S, int heads, int D) {
   const unsigned long long hs = static_cast<unsigned long long>(D) * 2;
   return make_map4(map, base, D, heads, S, B, hs, hs * heads, hs * heads * S, 128);
 }
@@ -136,19 +131,14 @@ RopeFreq make_rope(float base, int dims, bool half) {
   return f;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 int finish(cudaError_t e, int launches) {
   g_launches.fetch_add(static_cast<unsigned long long>(launches));
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-const float kLog2e = 1.4426950408889634f;
+namespace {
 
 // One warp waits on a barrier that nothing arrives on; the bounded wait gives
 // up after limit_ns and records STATUS_TIMEOUT.

@@ -90,7 +90,52 @@ struct KvAppendArgs {
   const int* start;   // device [B]: slot of the first new token of each sequence
   int B, C, n_kv, D_qk, D_v, max_len, rope_offset;
   int head_groups;    // set by the launcher: threads per (token, 8-dim chunk), each owning n_kv / head_groups heads
+  // a paged cache (launch_kv_append_paged): row c of the one sequence goes to slots[c], rotated at positions[c]
+  const int* slots;
+  const int* positions;  // nullable without RoPE
+  int n_slots;
 };
+
+// One step's page plan (attn_page_plan).
+struct PagePlanArgs {
+  const int* lens;
+  const int* n_new;
+  int* block_table;
+  const int* free_pages;
+  const int* n_free;
+  int* seqlens;
+  int* cu_new;
+  int* slots;
+  int* positions;
+  int* n_left;
+  int B, max_blocks, page_shift, n_pages, free_cap, max_tokens;
+};
+constexpr int kMaxPlanRequests = 16384;
+
+// Single-token decode over a paged cache, behind a shared prefix (prefix_len > 0) or alone.
+struct PagedDecodeArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  long long v_token_stride;  // elements
+  const int* prefix_pages;   // [prefix_len >> page_shift]
+  const int* block_table;    // [B, max_blocks]
+  const int* seqlens;
+  void* out;
+  float* lse;  // nullable
+  int B, n_h, n_kv, D_qk, D_v, n_pages, page_shift, max_blocks, prefix_len;
+  int rope_offset;
+  float scale_log2;
+  void* workspace;
+  unsigned int* status;
+  unsigned long long wait_limit_ns;
+};
+
+// Keys of request b; at most prefix_len (0 without a prefix) for an empty place of the batch.
+__device__ __forceinline__ int paged_len(const PagedDecodeArgs& a, int b) {
+  const long long cap = static_cast<long long>(a.max_blocks) << a.page_shift;
+  return static_cast<int>(min(static_cast<long long>(a.seqlens[b]), cap));
+}
 
 // Each launcher returns the launch error (cudaSuccess when enqueued) and adds
 // the number of kernels it enqueued to *launches.
@@ -106,6 +151,13 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, const RopeFreq& rope, const 
                               int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_rope(const RopeArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches);
 cudaError_t launch_kv_append(const KvAppendArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches);
+cudaError_t launch_kv_append_paged(const KvAppendArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
+                                   int* launches);
+cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st, int* launches);
+// CUDA-core decode over a paged cache (any supported shape) and the scratch it needs.
+size_t decode_paged_workspace(const PagedDecodeArgs& a);
+cudaError_t launch_decode_paged(const PagedDecodeArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
+                                int* launches);
 int decode_plan_splits(int B, int n_h, int n_kv, int D_qk, int D_v, int max_len, int* chunk);
 cudaError_t launch_decode(const DecodeArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
                           int* launches);

@@ -185,7 +185,10 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, RopeFreq rf) {
 // the GPU's loads in flight when each thread walks all heads one after another, so the
 // launcher then gives every head its own thread (head_groups = n_kv; each thread computes
 // its own sin/cos), and otherwise one thread per (token, chunk) for all heads.
-template <typename T>
+//
+// PAGED: the tokens form one row of C packed ones, token c at position positions[c], and go to
+// slots[c] of a cache of n_slots slots (pages laid end to end).
+template <typename T, bool PAGED>
 __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a, RopeFreq rf) {
   __shared__ float freq[2 * kMaxRopePairs];
   const SmemFreq f = stage_freq(rf, freq);
@@ -201,9 +204,17 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a, RopeFreq
     const long long bc = r / hg;
     const int c = static_cast<int>(bc % a.C);
     const int b = static_cast<int>(bc / a.C);
-    const int pos = a.start[b] + c;
-    if (pos < 0 || pos >= a.max_len) continue;  // slots outside the cache are never written
-    const long long slot = static_cast<long long>(b) * a.max_len + pos;
+    int pos;
+    long long slot;
+    if constexpr (PAGED) {
+      slot = a.slots[c];
+      if (slot < 0 || slot >= a.n_slots) continue;
+      pos = f.n_pairs ? a.positions[c] : 0;
+    } else {
+      pos = a.start[b] + c;
+      if (pos < 0 || pos >= a.max_len) continue;  // slots outside the cache are never written
+      slot = static_cast<long long>(b) * a.max_len + pos;
+    }
     if (ch < kch) {
       const int d0 = ch * 8;
       const int rel = d0 - a.rope_offset;
@@ -250,8 +261,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a, RopeFreq
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvAppendArgs& args, const RopeFreq& rope, bool bf16, cudaStream_t st,
-                             int* launches) {
+namespace {
+template <bool PAGED>
+cudaError_t launch_append(const KvAppendArgs& args, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches) {
   KvAppendArgs a = args;
   const int per_tok = a.D_qk / 8 + (a.v_new ? a.D_v / 8 : 0);
   const long long items = static_cast<long long>(a.B) * a.C * per_tok;
@@ -263,11 +275,21 @@ cudaError_t launch_kv_append(const KvAppendArgs& args, const RopeFreq& rope, boo
   if (blocks > 152LL * 16) blocks = 152LL * 16;
   if (blocks < 1) blocks = 1;
   if (bf16)
-    kv_append_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, rope);
+    kv_append_kernel<__nv_bfloat16, PAGED><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, rope);
   else
-    kv_append_kernel<float><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, rope);
+    kv_append_kernel<float, PAGED><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, rope);
   *launches += 1;
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches) {
+  return launch_append<false>(a, rope, bf16, st, launches);
+}
+
+cudaError_t launch_kv_append_paged(const KvAppendArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
+                                   int* launches) {
+  return launch_append<true>(a, rope, bf16, st, launches);
 }
 
 cudaError_t launch_rope(const RopeArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches) {
