@@ -50,7 +50,13 @@ int check_sizes(int B, int n_h, int n_kv, int D_qk, int D_v, int n_pages, int pa
   return ATTN_OK;
 }
 
-size_t workspace_of(const PagedDecodeArgs& a) { return decode_paged_workspace(a); }
+// Scratch of either path (which one a call takes also depends on its RoPE span).
+size_t workspace_of(const PagedDecodeArgs& a, bool bf16) {
+  const size_t n = decode_paged_workspace(a);
+  if (!decode_paged_tc_supported(a, bf16, 0, 0, false)) return n;
+  const size_t tc = decode_paged_tc_workspace(a);
+  return tc > n ? tc : n;
+}
 
 int decode_impl(const void* q, const void* k_pages, const void* v_pages, int v_token_stride, const int* prefix_pages,
                 int prefix_len, const int* block_table, const int* seqlens, void* out, float* lse, int B, int n_h,
@@ -75,7 +81,7 @@ int decode_impl(const void* q, const void* k_pages, const void* v_pages, int v_t
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(workspace) ||
       !aligned4(block_table) || !aligned4(seqlens) || !aligned4(prefix_pages) || !aligned4(lse))
     return ATTN_ERR_ALIGN;
-  if (workspace_bytes < workspace_of(a)) return ATTN_ERR_WORKSPACE;
+  if (workspace_bytes < workspace_of(a, bf16)) return ATTN_ERR_WORKSPACE;
 
   DeviceInfo dev;
   if (int rc = device_info(&dev)) return rc;
@@ -96,8 +102,18 @@ int decode_impl(const void* q, const void* k_pages, const void* v_pages, int v_t
   a.wait_limit_ns = wait_limit_ns();
   const RopeFreq rf = make_rope(rope_base, rope ? rope_dims : 0, half);
   int launches = 0;
-  const cudaError_t e = launch_decode_paged(a, rf, bf16, static_cast<cudaStream_t>(stream), &launches);
-  return finish(e, launches);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!decode_paged_tc_supported(a, bf16, rope_offset, rope_dims, rope))
+    return finish(launch_decode_paged(a, rf, bf16, st, &launches), launches);
+  // one box: 64 dims of one head, the rows of a page (half of them where a page is two tiles)
+  CUtensorMap maps[2];
+  const unsigned long long hs = static_cast<unsigned long long>(D_qk) * 2;
+  const unsigned long long ks = hs * n_kv, vs = static_cast<unsigned long long>(ldv) * 2;
+  const int box_rows = page_size < 128 ? page_size : 128;
+  if (!make_map4(&maps[0], k_pages, D_qk, n_kv, page_size, n_pages, hs, ks, ks * page_size, box_rows) ||
+      !make_map4(&maps[1], v_pages, D_v, n_kv, page_size, n_pages, hs, vs, vs * page_size, box_rows))
+    return finish(cudaErrorInvalidValue, launches);
+  return finish(launch_decode_paged_tc(a, rf, maps, dev.sms, st, &launches), launches);
 }
 
 }  // namespace
@@ -194,7 +210,7 @@ size_t attn_decode_paged_workspace_size(int B, int n_h, int n_kv, int D_qk, int 
   bool bf16 = false, half = false;
   if (check_sizes(B, n_h, n_kv, D_qk, D_v, 1, page_size, max_blocks, prefix_len, dtype, &a, &bf16, &half))
     return static_cast<size_t>(-1);
-  return workspace_of(a);
+  return workspace_of(a, bf16);
 }
 
 int attn_decode_paged(const void* q, const void* k_pages, const void* v_pages, int v_token_stride,
