@@ -18,24 +18,29 @@
 //
 // Work split.  All tiles of the call lie on one line - first the pair tiles, KV head by
 // KV head, then the single ones (prefix tiles of an odd last row tile, then request
-// after request, KV head fastest) - weighted kPairCost : kSingleCost, and the line is
-// cut into equal parts, one per CTA (one persistent CTA per SM).  A CTA's single tiles
-// are cut once more, into halves for its two workers.  Cuts fall anywhere, also inside
-// a request: each (worker, segment) piece writes one normalised partial and its
+// after request, KV head fastest).  A tile is a few points long (kPairCost, kSingleCost)
+// and each segment is led by kPieceCost points for what starting it costs; the line is
+// cut into equal parts, one per CTA (one persistent CTA per SM), and the single tiles of
+// a CTA's part once more, into halves for its two workers.  Cuts fall anywhere, also
+// inside a request: each (worker, segment) piece writes one normalised partial and its
 // log-sum-exp, and the combine kernel merges the pieces of a row.  So the SMs finish
 // together whatever the lengths are, without a counter in memory, and partials are few.
 // Where a piece's partial goes needs no table either: walking the line, each step to
 // the next piece raises the worker's index or the segment's, so their sum numbers the
-// pieces.  Only the requests' places on the line come from the lengths: every CTA sums
-// them at its start (384 threads), CTA 0 leaves the sums for the combine kernel.
+// pieces.
 //
-// A CTA (384 threads): warps 0 and 2 load K and V tiles by TMA, one box per page and
-// 64 dims (a page is part of a tile, the tile, or twice the tile), the lanes of the warp
-// issuing one box each and holding the next tile's page indices; warp 1 issues the MMAs;
-// warp 3 clears value rows behind a segment's last key, which may hold anything; warps
-// 4-7 and 8-11 are the two workers' softmax.  The workers run separate pieces (their
-// tiles alternate in the K and V rings), so that one's MMAs and loads fill the other's
-// softmax and piece ends; on pair tiles they hold the two row tiles.
+// A CTA (384 threads): warp 3 walks the CTA's part of the line (it sums the requests'
+// points at its start; CTA 0's leaves the sums for the combine kernel) and hands the
+// pieces to the other roles through two small queues in shared memory, a few pieces
+// ahead; it also clears value rows behind a segment's last key, which may hold anything.
+// Warps 0 and 2 load K and V tiles by TMA, one box per page and 64 dims (a page is part
+// of a tile, the tile, or twice the tile), the lanes of the warp issuing one box each;
+// warp 1 issues the MMAs; warps 4-7 and 8-11 are the two workers' softmax.  The workers
+// run separate pieces (their tiles alternate in the K and V rings), so that one's MMAs
+// and loads fill the other's softmax and piece ends; on pair tiles they hold the two
+// row tiles.  Every role's code at a piece's boundary is kept small, one copy of each
+// part: with the walk inlined into every role a one-tile piece took 7 us, most of it
+// instruction fetches.
 // TMEM: S/P of the workers in columns [0, 128) and [128, 256), O behind them.
 #include <math.h>
 
@@ -44,19 +49,42 @@
 #include "kernels.h"
 
 namespace attn {
+
+// The cut of a call that does not depend on the lengths, and the layout of its workspace.
+struct PagedTcPlan {
+  int ctas;
+  int n_pairs;       // pairs of 128-row tiles of a KV head's prefix rows
+  int odd;           // 1: one more row tile, of rows1 rows
+  int rows1;
+  int prefix_tiles;  // key tiles of the prefix
+  // float offsets into the workspace: partial outputs and log-sum-exps of pair pieces [256 rows],
+  // single prefix pieces [rows1] and own pieces [G]; then (int) B + 1 sums of points
+  long long o2, o1, o0, l2, l1, l0, sums, end;
+};
+
 namespace {
 
 constexpr int BM = 128;  // rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr int kPairCost = 2, kSingleCost = 1;
+// Points on the line: a pair tile, a single tile, the start of a segment.
+constexpr int kPairCost = 14, kSingleCost = 8, kPieceCost = 8;
 
 // Register split as in prefill_tc.cu: a softmax thread holds a row of 128 scores.
 constexpr int kLaunchRegs = 168;
 constexpr int kRegsCtl = 152, kRegsSoftmax = 176;
 constexpr int kRegsNeeded = 4 * 32 * kRegsCtl + 8 * 32 * kRegsSoftmax;
 static_assert(kRegsNeeded <= kThreads * kLaunchRegs, "register split exceeds the launch's pool");
+
+// A piece: tiles [t, t_end) of one segment for one worker (or, on pair tiles, both).
+enum : int { kNone = -1, kPair = 0, kPrefix = 1, kOwn = 2 };
+struct Piece {
+  int kind, g;
+  int b;         // own: the request; pair: the pair of row tiles
+  int t, t_end;
+  int keys;      // keys of the whole segment: tile t holds min(128, keys - 128 t) of them
+};
 
 template <int D>
 struct Cfg {
@@ -66,11 +94,19 @@ struct Cfg {
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
   static constexpr int kKStages = D == 128 ? 2 : 5;
   static constexpr int kVStages = D == 128 ? 3 : 6;
+  // Pieces that warp 3 has handed out and not passed itself, and the queues' length.  An entry is
+  // written again kQueue - kAhead pieces after warp 3 saw its piece's last V tile, and then at most
+  // kVStages + 1 of a worker's pieces are unfinished (a V stage is reloaded only after its P V, a
+  // piece's P only written after the epilogue of the piece before).
+  static constexpr int kAhead = 4;
+  static constexpr int kQueue = D == 128 ? 8 : 16;
+  static_assert(kQueue - kAhead >= kVStages + 1, "queue entries in use");
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + 2 * kTileBytes;
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
   static constexpr int kBarOff = kVOff + kVStages * kTileBytes;
-  static constexpr int kFreqOff = kBarOff + 512;     // RoPE frequencies, hi then lo words
+  static constexpr int kBarBytes = D == 128 ? 1024 : 2048;
+  static constexpr int kFreqOff = kBarOff + kBarBytes;  // RoPE frequencies, hi then lo words
   static constexpr int kSmemBytes = kFreqOff + D * 4 + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kOCol = 256;             // O of worker w at kOCol + w D
@@ -78,138 +114,139 @@ struct Cfg {
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(BM, D, true);
 };
 
+template <int D>
 struct Bars {
-  uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_fixed[6];
-  uint64_t q_ready[2], s_full[2], p_full[2], o_done[2], o_empty[2];
+  using C = Cfg<D>;
+  uint64_t k_full[C::kKStages], k_empty[C::kKStages];
+  uint64_t v_full[C::kVStages], v_empty[C::kVStages], v_fixed[C::kVStages];
+  uint64_t q_ready[2][2];  // per worker, alternating between its pieces: the next one's rows may be ready early
+  uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
+  uint64_t piece_full[2][C::kQueue];
   uint64_t fin;
-  long long line[2];       // scan results: tiles before a worker's first request, per KV head
-  long long warp_sum[kThreads / 32];
-  int start_b[2];          // the request in which a worker's single tiles begin
+  Piece piece[2][C::kQueue];
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars<64>) <= Cfg<64>::kBarBytes && sizeof(Bars<128>) <= Cfg<128>::kBarBytes, "barrier block");
 
-}  // namespace
+// ------------------------------------------------------------------------------------- the line
+// Points are 32-bit: decode_paged_tc_supported bounds the line.
+// The first tile of a segment (n tiles of `cost` points each, its first one at point p0) that starts
+// at or behind point x.
+__device__ __forceinline__ int tile_at(int x, int p0, int cost, int n) {
+  const int d = x - p0;
+  return d <= 0 ? 0 : min(n, static_cast<int>((static_cast<unsigned>(d) + cost - 1) / static_cast<unsigned>(cost)));
+}
+__device__ __forceinline__ int seg_points(int tiles, int cost) { return tiles > 0 ? tiles * cost + kPieceCost : 0; }
+__device__ __forceinline__ int own_tiles(const PagedDecodeArgs& a, int b) {
+  const int L = paged_len(a, b);
+  return L > a.prefix_len ? static_cast<int>((static_cast<unsigned>(L - a.prefix_len) + BN - 1) / BN) : 0;
+}
 
-// The cut of a call that does not depend on the lengths, and the layout of its workspace.
-struct PagedTcPlan {
-  int ctas;
-  int n_pairs;      // pairs of 128-row tiles of a KV head's prefix rows
-  int odd;          // 1: one more row tile, of rows1 rows
-  int rows1;
-  int prefix_tiles; // key tiles of the prefix
-  // float offsets into the workspace: partial outputs and log-sum-exps of pair pieces [256 rows],
-  // single prefix pieces [rows1] and own pieces [G]; then (long long) B + 1 tile counts
-  long long o2, o1, o0, l2, l1, l0, sums, end;
-};
-
-namespace {
-
-__host__ __device__ __forceinline__ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
-
-// The line of tiles and its cut, once the sum of the requests' own tiles (per KV head) is known.
+// The line and its cut, once the sum of the requests' own points (of one KV head) is known.
 struct Line {
-  long long pair_tiles, single_prefix, total;  // tiles; total in cost units
-  __device__ __forceinline__ Line(const PagedTcPlan& p, int n_kv, long long own) {
-    pair_tiles = static_cast<long long>(p.n_pairs) * n_kv * p.prefix_tiles;
-    single_prefix = static_cast<long long>(p.odd) * n_kv * p.prefix_tiles;
-    total = pair_tiles * kPairCost + (single_prefix + own * n_kv) * kSingleCost;
+  int pair_end, prefix_end, total;  // [0, pair_end) pairs, [.., prefix_end) single prefix tiles, own tiles
+  int part, extra, ctas;            // points per CTA, one more for the first `extra` CTAs
+  __device__ __forceinline__ Line(const PagedTcPlan& p, int n_kv, int own) {
+    pair_end = p.n_pairs * n_kv * seg_points(p.prefix_tiles, kPairCost);
+    prefix_end = pair_end + p.odd * n_kv * seg_points(p.prefix_tiles, kSingleCost);
+    total = prefix_end + own * n_kv;
+    ctas = p.ctas;
+    part = static_cast<int>(static_cast<unsigned>(total) / static_cast<unsigned>(ctas));
+    extra = total - part * ctas;
   }
-  // The line's tiles that start in [0, x): the first pair / single tile at or behind point x.
-  __device__ __forceinline__ long long pair_at(long long x) const {
-    return min(ceil_div(x, kPairCost), pair_tiles);
-  }
-  __device__ __forceinline__ long long single_at(long long x) const {
-    return max(0LL, ceil_div(x - pair_tiles * kPairCost, kSingleCost));
-  }
-  __device__ __forceinline__ long long cut(int c, int ctas) const { return total * c / ctas; }
+  __device__ __forceinline__ int cut(int c) const { return part * c + min(c, extra); }
   // The CTA whose part holds point x.
-  __device__ __forceinline__ int cta_of(long long x, int ctas) const {
-    return static_cast<int>(ceil_div((x + 1) * ctas, total) - 1);
+  __device__ __forceinline__ int cta_of(int x) const {
+    const int wide = extra * (part + 1);  // the end of the parts that are one point longer
+    const bool in_wide = x < wide;
+    const unsigned len = in_wide ? part + 1 : part;  // part > 0 behind `wide`
+    return (in_wide ? 0 : extra) + static_cast<int>(static_cast<unsigned>(in_wide ? x : x - wide) / len);
   }
-  // Worker w of CTA c takes single tiles [lo, hi).
-  __device__ __forceinline__ void singles(int c, int w, int ctas, long long* lo, long long* hi) const {
-    const long long a = single_at(cut(c, ctas)), b = single_at(cut(c + 1, ctas));
-    const long long mid = a + (b - a + 1) / 2;
+  // Worker w of CTA c takes the single tiles that start in [lo, hi).
+  __device__ __forceinline__ void single_part(int c, int w, int* lo, int* hi) const {
+    const int a = max(cut(c), pair_end), b = max(cut(c + 1), pair_end);
+    const int mid = a + (b - a + 1) / 2;
     *lo = w ? mid : a;
     *hi = w ? b : mid;
   }
+  __device__ __forceinline__ int worker_of(int x) const {  // x >= pair_end
+    const int c = cta_of(x);
+    int lo, hi;
+    single_part(c, 1, &lo, &hi);
+    return 2 * c + (x >= lo ? 1 : 0);
+  }
 };
 
-__device__ __forceinline__ int own_tiles(const PagedDecodeArgs& a, int b) {
-  const int L = paged_len(a, b);
-  return L > a.prefix_len ? (L - a.prefix_len + BN - 1) / BN : 0;
-}
-
-// A piece: tiles [t, t_end) of one segment for one worker (or, on pair tiles, both).
-enum : int { kPair = 0, kPrefix = 1, kOwn = 2 };
-struct Piece {
-  int kind, b, g, row0, n_rows;  // own: request b; prefix: rows row0.. of KV head g
-  int t, t_end, keys;            // keys of the whole segment: tile t holds min(128, keys - 128 t) of them
-  long long slot;
-};
-
-// A walk along one worker's part of the line.
+// A walk along one worker's part of the line: the next segment, its first point, its next tile, and
+// where the part ends.  Pair pieces come first (in both workers' walks), then single prefix pieces,
+// then own ones.
 struct Walk {
-  long long p, p_end;        // pair tiles of the CTA
-  long long j, j_end, base;  // single tiles of the worker; base: the first one of request b
-  int b, w;
+  int kind, g, b, t, s0, end;                                   // of the pairs, then of the rest
+  int rest_kind, rest_g, rest_b, rest_t, rest_s0, rest_end;  // where the single tiles begin
 };
 
-template <bool PAIRS>
-__device__ __forceinline__ bool next_piece(const PagedDecodeArgs& a, const PagedTcPlan& pl, Walk& w, Piece& u) {
-  if (PAIRS) {
-    if (w.p >= w.p_end) return false;
-    const int seg = static_cast<int>(w.p / pl.prefix_tiles);
-    u.kind = kPair;
-    u.t = static_cast<int>(w.p - static_cast<long long>(seg) * pl.prefix_tiles);
-    u.t_end = static_cast<int>(min(static_cast<long long>(pl.prefix_tiles), u.t + w.p_end - w.p));
-    u.g = seg / pl.n_pairs;
-    u.row0 = (seg % pl.n_pairs) * 2 * BM + w.w * BM;
-    u.n_rows = min(BM, a.B * (a.n_h / a.n_kv) - u.row0);
-    u.keys = a.prefix_len;
-    u.b = 0;
-    u.slot = static_cast<long long>(blockIdx.x) + seg;
-    w.p += u.t_end - u.t;
-    return true;
-  }
-  if (w.j >= w.j_end) return false;
-  const long long own0 = static_cast<long long>(pl.odd) * a.n_kv * pl.prefix_tiles;
-  const int worker = 2 * static_cast<int>(blockIdx.x) + w.w;
-  if (w.j < own0) {
-    u.kind = kPrefix;
-    u.g = static_cast<int>(w.j / pl.prefix_tiles);
-    u.t = static_cast<int>(w.j - static_cast<long long>(u.g) * pl.prefix_tiles);
-    u.t_end = static_cast<int>(min(static_cast<long long>(pl.prefix_tiles), u.t + w.j_end - w.j));
-    u.row0 = pl.n_pairs * 2 * BM;
-    u.n_rows = pl.rows1;
-    u.keys = a.prefix_len;
-    u.b = 0;
-    u.slot = static_cast<long long>(worker) + u.g;
-  } else {
-    int nt = own_tiles(a, w.b);
-    while (w.j - own0 - w.base >= static_cast<long long>(nt) * a.n_kv) {
-      w.base += static_cast<long long>(nt) * a.n_kv;
-      nt = own_tiles(a, ++w.b);
+// The next piece of a walk; kind kNone at its end.
+__device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const PagedTcPlan& pl, Walk& w) {
+  Piece u;
+  if (w.kind == kPair) {
+    const int t_end = tile_at(w.end, w.s0 + kPieceCost, kPairCost, pl.prefix_tiles);
+    if (w.g < a.n_kv && w.t < t_end) {
+      u = Piece{kPair, w.g, w.b, w.t, t_end, a.prefix_len};
+      w.t = t_end;
+      if (t_end == pl.prefix_tiles) {
+        w.t = 0;
+        w.s0 += seg_points(pl.prefix_tiles, kPairCost);
+        if (++w.b == pl.n_pairs) {
+          w.b = 0;
+          ++w.g;
+        }
+      }
+      return u;
     }
-    const long long r = w.j - own0 - w.base;
-    u.kind = kOwn;
-    u.b = w.b;
-    u.g = static_cast<int>(r / nt);
-    u.t = static_cast<int>(r - static_cast<long long>(u.g) * nt);
-    u.t_end = static_cast<int>(min(static_cast<long long>(nt), u.t + w.j_end - w.j));
-    u.row0 = 0;
-    u.n_rows = a.n_h / a.n_kv;
-    u.keys = paged_len(a, w.b) - a.prefix_len;
-    u.slot = static_cast<long long>(worker) + static_cast<long long>(w.b) * a.n_kv + u.g;
+    w.kind = w.rest_kind;
+    w.g = w.rest_g;
+    w.b = w.rest_b;
+    w.t = w.rest_t;
+    w.s0 = w.rest_s0;
+    w.end = w.rest_end;
   }
-  w.j += u.t_end - u.t;
-  return true;
+  u.kind = kNone;
+  for (;;) {
+    if (w.kind == kPrefix && w.g == a.n_kv) {  // on to the requests
+      w.kind = kOwn;
+      w.g = 0;
+    }
+    if (w.kind == kOwn && w.b >= a.B) return u;
+    const int keys = w.kind == kOwn ? paged_len(a, w.b) - a.prefix_len : a.prefix_len;
+    if (keys <= 0) {  // an empty place of the batch
+      ++w.b;
+      continue;
+    }
+    const int nt = static_cast<int>((static_cast<unsigned>(keys) + BN - 1) / BN);
+    const int t_end = tile_at(w.end, w.s0 + kPieceCost, kSingleCost, nt);
+    if (w.t >= t_end) {
+      if (w.t < nt) return u;  // the part ends here
+    } else {
+      u = Piece{w.kind, w.g, w.b, w.t, t_end, keys};
+      w.t = t_end;
+    }
+    if (w.t == nt) {
+      w.t = 0;
+      w.s0 += seg_points(nt, kSingleCost);
+      if (++w.g == a.n_kv && w.kind == kOwn) {
+        w.g = 0;
+        ++w.b;
+      }
+    }
+    if (u.kind != kNone) return u;
+  }
 }
 
+// Keys of tile t.
 __device__ __forceinline__ int tile_keys(const Piece& u, int t) { return min(BN, u.keys - t * BN); }
 
+// ------------------------------------------------------------------------------------- waits
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
   const bool ok = mbar_wait(bar, parity, w);
   return __all_sync(0xffffffffu, ok);
@@ -222,44 +259,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsig
   }
 }
 
-// Byte offset of the 16-byte chunk c (dims 8 c ..) of row r of a K-major, 128-byte-swizzled tile.
-__device__ __forceinline__ uint32_t chunk_off(int r, int c) {
-  return (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
-
-// One loading warp's view of a stream of tiles: the piece, its tile, and in lane l < pages per
-// tile the index of the tile's l-th page (loaded a tile ahead).
-template <bool PAIRS>
-struct Stream {
-  Walk w;
-  Piece u;
-  int t;
-  bool live;
-  int id;
-
-  __device__ __forceinline__ void fetch(const PagedDecodeArgs& a, int lane) {
-    if (!live) return;
-    const int* tbl = u.kind == kOwn ? a.block_table + static_cast<long long>(u.b) * a.max_blocks +
-                                          (a.prefix_len >> a.page_shift)
-                                    : a.prefix_pages;
-    const int key = t * BN + (lane << a.page_shift);
-    id = (lane == 0 || (lane << a.page_shift) < BN) && key < u.keys ? tbl[key >> a.page_shift] : -1;
-  }
-  __device__ __forceinline__ void start(const PagedDecodeArgs& a, const PagedTcPlan& pl, const Walk& walk, int lane) {
-    w = walk;
-    live = next_piece<PAIRS>(a, pl, w, u);
-    t = live ? u.t : 0;
-    fetch(a, lane);
-  }
-  __device__ __forceinline__ void advance(const PagedDecodeArgs& a, const PagedTcPlan& pl, int lane) {
-    if (++t == u.t_end) {
-      live = next_piece<PAIRS>(a, pl, w, u);
-      t = live ? u.t : 0;
-    }
-    fetch(a, lane);
-  }
-};
-
 struct Ring {
   uint32_t st = 0, ph = 0;
   __device__ __forceinline__ void next(uint32_t n) {
@@ -270,6 +269,97 @@ struct Ring {
   }
 };
 
+// A role's place in one worker's queue: the piece it is in and its tile there.
+template <int D>
+struct Cursor {
+  Piece u;
+  int t, w;
+  uint32_t n;  // pieces taken
+  __device__ __forceinline__ bool take(Bars<D>* bars, const WaitCtl& wc, bool whole_warp) {
+    constexpr uint32_t kQueue = Cfg<D>::kQueue;
+    uint64_t* bar = &bars->piece_full[w][n % kQueue];
+    const uint32_t par = (n / kQueue) & 1u;
+    const bool ok = whole_warp ? warp_wait(bar, par, wc) : mbar_wait(bar, par, wc);
+    if (ok) u = bars->piece[w][n % kQueue];
+    else u.kind = kNone;
+    t = u.t;
+    ++n;
+    return ok;
+  }
+  __device__ __forceinline__ bool live() const { return u.kind != kNone; }
+};
+
+// ------------------------------------------------------------------------------------- query rows
+// Byte offset of the 16-byte chunk c (dims 8 c ..) of row r of a K-major, 128-byte-swizzled tile.
+__device__ __forceinline__ uint32_t chunk_off(int r, int c) {
+  return (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Where a piece's query rows lie in its worker's Q tile: pieces of at most 64 rows alternate between
+// the tile's halves, so that the next piece's rows are written while this one's are read (an MMA reads
+// 128 rows from either; what lies behind a piece's rows reaches only lanes that nobody reads).
+constexpr int kHalfRows = 64;
+__device__ __forceinline__ uint32_t next_q_off(int prev_rows, uint32_t prev_off, int rows) {
+  return prev_rows <= kHalfRows && rows <= kHalfRows ? prev_off ^ (kHalfRows * 128u) : 0u;
+}
+// Rows that a piece's Q tile is counted with there (a pair's tiles as full ones).
+__device__ __forceinline__ int q_rows(const PagedDecodeArgs& a, const PagedTcPlan& pl, const Piece& u) {
+  return u.kind == kPair ? BM : u.kind == kPrefix ? pl.rows1 : a.n_h / a.n_kv;
+}
+
+// Query rows row0 .. row0 + n_rows - 1 of KV head g (row r: head r mod G of request r / G) into the
+// swizzled tile at dst, rotated at their requests' last positions.  Thread r of 128 copies and
+// rotates the chunk pairs (c, c + D / 16) of row i with i D / 16 + c = r mod 128.  One copy of this
+// code, out of line, with the frequencies in shared memory.
+template <int D>
+__device__ __noinline__ void load_q_rows(const PagedDecodeArgs* ap, uint8_t* dst, const float* f_hi, const float* f_lo,
+                                         int n_pairs, int half, int g, int row0, int n_rows, int r) {
+  constexpr int kCP = D / 16;
+  const int G = ap->n_h / ap->n_kv, n_h = ap->n_h;
+  const __nv_bfloat16* const q0 = static_cast<const __nv_bfloat16*>(ap->q) + static_cast<long long>(g) * G * D;
+  const int n_items = n_rows * kCP;
+#pragma unroll 4
+  for (int idx = r; idx < n_items; idx += 128) {
+    const int i = idx / kCP, c = idx % kCP;
+    const int b = (row0 + i) / G, h = row0 + i - b * G;
+    const uint4* q = reinterpret_cast<const uint4*>(q0 + (static_cast<long long>(b) * n_h + h) * D) + c;
+    const uint4 lo = __ldg(q), hi = __ldg(q + kCP);
+    *reinterpret_cast<uint4*>(dst + chunk_off(i, c)) = lo;
+    *reinterpret_cast<uint4*>(dst + chunk_off(i, c + kCP)) = hi;
+  }
+  if (n_pairs) {
+#pragma unroll 1
+    for (int idx = r; idx < n_items; idx += 128) {
+      const int i = idx / kCP, c = idx % kCP;
+      const int pos = max(paged_len(*ap, (row0 + i) / G), 1) - 1;
+      uint4* const p0 = reinterpret_cast<uint4*>(dst + chunk_off(i, c));
+      uint4* const p1 = reinterpret_cast<uint4*>(dst + chunk_off(i, c + kCP));
+      float x0[8], x1[8], sn[8], cs[8];
+      bf16x8_to_f32(*p0, x0);
+      bf16x8_to_f32(*p1, x1);
+      // split halves: pair c 8 + e is (x0[e], x1[e]); adjacent: the chunks hold four whole pairs each
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = half ? c * 8 + e : (e < 4 ? c * 4 + e : D / 4 + c * 4 + e - 4);
+        rope_sincos_fast(pos, f_hi[j], f_lo[j], &sn[e], &cs[e]);
+      }
+      if (half) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rotate_pair(x0[e], x1[e], sn[e], cs[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          rotate_pair(x0[2 * e], x0[2 * e + 1], sn[e], cs[e]);
+          rotate_pair(x1[2 * e], x1[2 * e + 1], sn[4 + e], cs[4 + e]);
+        }
+      }
+      *p0 = f32_to_bf16x8(x0);
+      *p1 = f32_to_bf16x8(x1);
+    }
+  }
+  fence_proxy_async_smem();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ RopeFreq f,
@@ -278,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
+  Bars<D>* bars = reinterpret_cast<Bars<D>*>(smem + C::kBarOff);
   float* const f_hi = reinterpret_cast<float*>(smem + C::kFreqOff);
   float* const f_lo = f_hi + D / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -297,13 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->v_fixed[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&bars->q_ready[w], 128);
+      mbar_init(&bars->q_ready[w][0], 128);
+      mbar_init(&bars->q_ready[w][1], 128);
       mbar_init(&bars->s_full[w], 1);
       mbar_init(&bars->p_full[w], 128);
       mbar_init(&bars->o_done[w], 1);
       mbar_init(&bars->o_empty[w], 128);
-      bars->line[w] = 0;
-      bars->start_b[w] = 0;
+      for (int i = 0; i < C::kQueue; ++i) mbar_init(&bars->piece_full[w][i], 1);
     }
     mbar_init(&bars->fin, 1);
     bars->abort_flag = 0;
@@ -313,66 +403,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
-
-  // ---- the requests' places on the line: thread i sums the own tiles of requests [i s, (i + 1) s)
-  const int strip = (a.B + kThreads - 1) / kThreads;
-  const int b_lo = min(a.B, static_cast<int>(threadIdx.x) * strip), b_hi = min(a.B, b_lo + strip);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += own_tiles(a, b);
-  long long before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += x;
-  }
-  if (lane == 31) bars->warp_sum[warp] = before;
-  before -= mine;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  long long own = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += bars->warp_sum[i];
-    own += bars->warp_sum[i];
-  }
-  const Line line(pl, a.n_kv, own);
-  Walk walk[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    walk[w].w = w;
-    walk[w].p = line.pair_at(line.cut(blockIdx.x, pl.ctas));
-    walk[w].p_end = line.pair_at(line.cut(blockIdx.x + 1, pl.ctas));
-    line.singles(blockIdx.x, w, pl.ctas, &walk[w].j, &walk[w].j_end);
-    // the thread whose requests hold the worker's first own tile finds it
-    const long long first = max(walk[w].j - line.single_prefix, 0LL);
-    if (walk[w].j < walk[w].j_end && first >= before * a.n_kv && first < (before + mine) * a.n_kv) {
-      long long at = before;
-      int b = b_lo;
-      for (int nt = own_tiles(a, b); first >= (at + nt) * a.n_kv; nt = own_tiles(a, ++b)) at += nt;
-      bars->line[w] = at * a.n_kv;
-      bars->start_b[w] = b;
-    }
-  }
-  if (blockIdx.x == 0) {
-    long long* const sums = reinterpret_cast<long long*>(static_cast<float*>(a.workspace) + pl.sums);
-    long long at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      sums[b] = at;
-      at += own_tiles(a, b);
-    }
-    if (threadIdx.x == 0) sums[a.B] = own;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    walk[w].base = bars->line[w];
-    walk[w].b = bars->start_b[w];
-  }
   const uint32_t tmem = bars->tmem_base;
   const WaitCtl wc{&bars->abort_flag, a.status, a.wait_limit_ns};
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsCtl>();
+    Cursor<D> cur, oth;  // the worker whose turn it is, and the other one
+    cur.w = 0;
+    oth.w = 1;
+    cur.n = oth.n = 0;
     if (warp == 0 || warp == 2) {
       // ------------------------------------------------------------ TMA producers
       const bool is_v = warp == 2;
@@ -384,51 +426,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tma_prefetch_desc(map);
       const int box_shift = min(a.page_shift, 7);  // rows per box: a page, or half of a 256-token page
       const int boxes = BN >> box_shift;            // per column block of a tile
+      const int box = lane & (boxes - 1), blk = lane / boxes;  // lane l loads block l / boxes of page l mod boxes
       Ring r;
       uint32_t issued = 0, last_ph = 0;
-      // one tile: lane l loads column block l / boxes of page l mod boxes
-      auto load = [&](const Piece& u, int t, int id) -> bool {
-        if (!warp_wait(&empty[r.st], r.ph ^ 1, wc)) return false;
-        const int n = tile_keys(u, t);
-        const int n_boxes = (n + (1 << box_shift) - 1) >> box_shift;  // pages without keys are not loaded
-        if (lane == 0) mbar_arrive_expect_tx(&full[r.st], static_cast<uint32_t>(n_boxes * C::kBlocks) << (box_shift + 7));
-        __syncwarp();
-        const int box = lane & (boxes - 1), blk = lane / boxes;
-        const int page = __shfl_sync(0xffffffffu, id, box);
-        if (blk < C::kBlocks && box < n_boxes)
-          tma_load_4d(ring + r.st * C::kTileBytes + blk * C::kBlockBytes + (box << (box_shift + 7)), map, &full[r.st],
-                      blk * 64, u.g, (t * BN) & ((1 << a.page_shift) - 1), page);
-        issued |= 1u << r.st;
-        last_ph = (last_ph & ~(1u << r.st)) | (r.ph << r.st);
-        r.next(n_stages);
-        return true;
+      int id_cur = -1, id_oth = -1;  // the lane's page of each worker's next tile
+      auto fetch = [&](const Cursor<D>& s) -> int {
+        const int* tbl = s.u.kind == kOwn ? a.block_table + static_cast<long long>(s.u.b) * a.max_blocks +
+                                                (a.prefix_len >> a.page_shift)
+                                          : a.prefix_pages;
+        const int key = s.t * BN + (box << box_shift);
+        return s.live() && blk < C::kBlocks && key < s.u.keys ? tbl[key >> a.page_shift] : -1;
       };
-      bool ok = true;
-      {
-        Stream<true> s;
-        s.start(a, pl, walk[0], lane);
-        while (ok && s.live) {
-          const Piece u = s.u;
-          const int t = s.t, id = s.id;
-          s.advance(a, pl, lane);
-          ok = load(u, t, id);
+      bool ok = cur.take(bars, wc, true) && oth.take(bars, wc, true);
+      id_cur = fetch(cur);
+      id_oth = fetch(oth);
+      while (ok && (cur.live() || oth.live())) {
+        if (cur.live()) {
+          if (!warp_wait(&empty[r.st], r.ph ^ 1, wc)) break;
+          const int n_boxes = (tile_keys(cur.u, cur.t) + (1 << box_shift) - 1) >> box_shift;  // others hold no key
+          if (lane == 0)
+            mbar_arrive_expect_tx(&full[r.st], static_cast<uint32_t>(n_boxes * C::kBlocks) << (box_shift + 7));
+          __syncwarp();
+          if (blk < C::kBlocks && box < n_boxes)
+            tma_load_4d(ring + r.st * C::kTileBytes + blk * C::kBlockBytes + (box << (box_shift + 7)), map,
+                        &full[r.st], blk * 64, cur.u.g, (cur.t * BN) & ((1 << a.page_shift) - 1), id_cur);
+          issued |= 1u << r.st;
+          last_ph = (last_ph & ~(1u << r.st)) | (r.ph << r.st);
+          r.next(n_stages);
+          const bool pair = cur.u.kind == kPair;
+          if (++cur.t == cur.u.t_end) {
+            ok = cur.take(bars, wc, true);
+            if (ok && pair) {  // a pair piece stands in both queues
+              ok = oth.take(bars, wc, true);
+              id_oth = fetch(oth);
+            }
+          }
+          id_cur = fetch(cur);
+          if (pair) continue;  // the first single tile is worker 0's
         }
-      }
-      Stream<false> s0, s1;
-      s0.start(a, pl, walk[0], lane);
-      s1.start(a, pl, walk[1], lane);
-      while (ok && (s0.live || s1.live)) {
-        if (s0.live) {
-          const Piece u = s0.u;
-          const int t = s0.t, id = s0.id;
-          s0.advance(a, pl, lane);
-          ok = load(u, t, id);
-        }
-        if (ok && s1.live) {
-          const Piece u = s1.u;
-          const int t = s1.t, id = s1.id;
-          s1.advance(a, pl, lane);
-          ok = load(u, t, id);
+        if (oth.live()) {
+          const Cursor<D> x = cur;
+          cur = oth;
+          oth = x;
+          const int y = id_cur;
+          id_cur = id_oth;
+          id_oth = y;
         }
       }
       if (bars->abort_flag) {  // let every copy in flight land before shared memory goes away
@@ -443,9 +485,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t k_desc0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
         const uint64_t v_desc0 = sdesc_sw128(smem_u32(smem + C::kVOff), C::kBlockBytes, 1024);
         Ring kr, vr;
-        uint32_t pph = 0, qph = 0, oph = 0, fix_ph = 0;  // parities, one bit per worker (fix_ph: per stage)
-        auto issue_qk = [&](int w) {
-          const uint64_t a0 = q_desc0 + ((w * C::kTileBytes) >> 4);
+        uint32_t pph = 0, oph = 0, fix_ph = 0;  // parities, one bit per worker (fix_ph: per stage)
+        uint32_t n_q0 = 0, n_q1 = 0;            // pieces begun by each worker
+        // Q K of worker w's next tile; new_piece: its query rows have to be there first
+        auto issue_qk = [&](int w, bool new_piece, uint32_t q_off) -> bool {
+          if (new_piece) {
+            const uint32_t n = w ? n_q1++ : n_q0++;
+            if (!mbar_wait(&bars->q_ready[w][n & 1u], (n >> 1) & 1u, wc)) return false;
+          }
+          tc_fence_after();
+          const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + q_off) >> 4);
           const uint64_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -453,20 +502,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ss(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
           }
           mma_commit(&bars->s_full[w]);
+          return true;
         };
-        auto issue_pv = [&](int w, bool accumulate) {
+        // P V of worker w's tile, once its P is there (and, for a piece's first tile, O is free)
+        auto issue_pv = [&](int w, bool first, bool last) -> bool {
+          if (!mbar_wait(&bars->p_full[w], (pph >> w) & 1u, wc)) return false;
+          pph ^= 1u << w;
+          if (first) {
+            if (!mbar_wait(&bars->o_empty[w], ((oph >> w) & 1u) ^ 1u, wc)) return false;
+            oph ^= 1u << w;
+          }
+          tc_fence_after();
           const uint64_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             mma_ts(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
-                   (accumulate || kk > 0) ? 1u : 0u);
-        };
-        auto wait_q = [&](int w) -> bool {
-          const bool ok = mbar_wait(&bars->q_ready[w], (qph >> w) & 1u, wc);
-          qph ^= 1u << w;
-          return ok;
+                   (!first || kk > 0) ? 1u : 0u);
+          if (last) mma_commit(&bars->o_done[w]);
+          return true;
         };
         auto wait_k = [&]() -> bool { return mbar_wait(&bars->k_full[kr.st], kr.ph, wc); };
+        auto done_k = [&]() {
+          mma_commit(&bars->k_empty[kr.st]);
+          kr.next(C::kKStages);
+        };
         auto wait_v = [&](int n) -> bool {  // n keys of the tile are real; fewer than 128: the rest is cleared first
           if (!mbar_wait(&bars->v_full[vr.st], vr.ph, wc)) return false;
           if (n == BN) return true;
@@ -474,107 +533,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           fix_ph ^= 1u << vr.st;
           return ok;
         };
-        auto wait_p = [&](int w, bool first) -> bool {  // P of the tile, and a free O for a piece's first
-          if (!mbar_wait(&bars->p_full[w], (pph >> w) & 1u, wc)) return false;
-          pph ^= 1u << w;
-          if (first) {
-            if (!mbar_wait(&bars->o_empty[w], ((oph >> w) & 1u) ^ 1u, wc)) return false;
-            oph ^= 1u << w;
-          }
-          return true;
+        auto done_v = [&]() {
+          mma_commit(&bars->v_empty[vr.st]);
+          vr.next(C::kVStages);
         };
-        {
+        if (!cur.take(bars, wc, false) || !oth.take(bars, wc, false)) goto mma_done;
+        if (cur.u.kind == kPair) {
           // pair tiles: both workers' rows on each K/V tile
-          Walk wk = walk[0];
-          Piece u;
-          bool live = next_piece<true>(a, pl, wk, u);
-          int t = live ? u.t : 0;
-          bool first = true;  // t is its piece's first tile
-          if (live) {
-            if (!wait_k()) goto mma_done;
+          if (!wait_k()) goto mma_done;
+          for (int w = 0; w < 2; ++w)
+            if (!issue_qk(w, true, 0)) goto mma_done;
+          done_k();
+          bool first = true;  // the tile is its piece's first
+          while (cur.u.kind == kPair) {
+            const bool last = cur.t + 1 == cur.u.t_end;
+            if (!wait_v(tile_keys(cur.u, cur.t))) goto mma_done;
+            ++cur.t;
+            if (last && (!cur.take(bars, wc, false) || !oth.take(bars, wc, false))) goto mma_done;
+            const bool more = cur.u.kind == kPair;
             for (int w = 0; w < 2; ++w) {
-              if (!wait_q(w)) goto mma_done;
-              tc_fence_after();
-              issue_qk(w);
-            }
-            mma_commit(&bars->k_empty[kr.st]);
-            kr.next(C::kKStages);
-          }
-          while (live) {
-            const bool last = t + 1 == u.t_end;
-            const int n = tile_keys(u, t);
-            bool more = !last;
-            Piece nu = u;
-            if (last) more = next_piece<true>(a, pl, wk, nu);
-            if (!wait_v(n)) goto mma_done;
-            for (int w = 0; w < 2; ++w) {
-              if (!wait_p(w, first)) goto mma_done;
-              tc_fence_after();
-              issue_pv(w, !first);
-              if (last) mma_commit(&bars->o_done[w]);
-              if (w == 1) {
-                mma_commit(&bars->v_empty[vr.st]);
-                vr.next(C::kVStages);
-              }
+              if (!issue_pv(w, first, last)) goto mma_done;
+              if (w == 1) done_v();
               if (more) {
                 if (w == 0 && !wait_k()) goto mma_done;
-                if (last && !wait_q(w)) goto mma_done;
-                tc_fence_after();
-                issue_qk(w);
+                if (!issue_qk(w, last, 0)) goto mma_done;
               }
             }
-            if (more) {
-              mma_commit(&bars->k_empty[kr.st]);
-              kr.next(C::kKStages);
-            }
-            live = more;
+            if (more) done_k();
             first = last;
-            if (last) {
-              u = nu;
-              t = u.t;
-            } else {
-              ++t;
-            }
           }
         }
         {
           // single tiles: the workers take turns, each P V followed by its next Q K
-          Walk w0 = walk[0], w1 = walk[1];
-          Piece u0, u1;
-          bool live0 = next_piece<false>(a, pl, w0, u0), live1 = next_piece<false>(a, pl, w1, u1);
-          int t0 = live0 ? u0.t : 0, t1 = live1 ? u1.t : 0;
-          bool first0 = true, first1 = true;
-          auto qk_turn = [&](int w, bool new_piece) -> bool {
-            if (!wait_k()) return false;
-            if (new_piece && !wait_q(w)) return false;
-            tc_fence_after();
-            issue_qk(w);
-            mma_commit(&bars->k_empty[kr.st]);
-            kr.next(C::kKStages);
-            return true;
-          };
-          auto turn = [&](int w, Walk& wk, Piece& u, int& t, bool& live, bool& first) -> bool {
-            const bool last = t + 1 == u.t_end;
-            if (!wait_v(tile_keys(u, t))) return false;
-            if (!wait_p(w, first)) return false;
-            tc_fence_after();
-            issue_pv(w, !first);
-            if (last) mma_commit(&bars->o_done[w]);
-            mma_commit(&bars->v_empty[vr.st]);
-            vr.next(C::kVStages);
-            ++t;
-            if (last) {
-              live = next_piece<false>(a, pl, wk, u);
-              t = live ? u.t : 0;
+          bool first_cur = true, first_oth = true;
+          uint32_t off_cur = 0, off_oth = 0;  // Q rows of each worker's piece (next_q_off)
+          for (int w = 0; w < 2; ++w)
+            if ((w ? oth : cur).live()) {
+              if (!wait_k() || !issue_qk(w, true, 0)) goto mma_done;
+              done_k();
             }
-            first = last;
-            return !live || qk_turn(w, last);
-          };
-          if (live0 && !qk_turn(0, true)) goto mma_done;
-          if (live1 && !qk_turn(1, true)) goto mma_done;
-          while (live0 || live1) {
-            if (live0 && !turn(0, w0, u0, t0, live0, first0)) goto mma_done;
-            if (live1 && !turn(1, w1, u1, t1, live1, first1)) goto mma_done;
+          while (cur.live() || oth.live()) {
+            if (cur.live()) {
+              const bool last = cur.t + 1 == cur.u.t_end;
+              if (!wait_v(tile_keys(cur.u, cur.t))) goto mma_done;
+              if (!issue_pv(cur.w, first_cur, last)) goto mma_done;
+              done_v();
+              ++cur.t;
+              if (last) {
+                const int rows = q_rows(a, pl, cur.u);
+                if (!cur.take(bars, wc, false)) goto mma_done;
+                off_cur = next_q_off(rows, off_cur, q_rows(a, pl, cur.u));
+              }
+              first_cur = last;
+              if (cur.live()) {
+                if (!wait_k() || !issue_qk(cur.w, last, off_cur)) goto mma_done;
+                done_k();
+              }
+            }
+            if (oth.live()) {
+              const Cursor<D> x = cur;
+              cur = oth;
+              oth = x;
+              const bool y = first_cur;
+              first_cur = first_oth;
+              first_oth = y;
+              const uint32_t z = off_cur;
+              off_cur = off_oth;
+              off_oth = z;
+            }
           }
         }
       mma_done:
@@ -584,48 +610,154 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else {
-      // ------------------------------------------------------------ value rows behind a segment's end
-      Ring r;
-      auto pass = [&](int n) -> bool {
-        if (!warp_wait(&bars->v_full[r.st], r.ph, wc)) return false;
-        if (n < BN) {
-          // rows n.. were not loaded or hold no token: their weights are 0, and 0 times anything must be 0
-          uint8_t* const v = smem + C::kVOff + r.st * C::kTileBytes;
-          for (int i = lane; i < (BN - n) * 8; i += 32) {
-            const int row = n + (i >> 3);
+      // ------------------------------------------------------------ the walk, and value rows behind a segment's end
+      Walk walk[2];
+      {
+        // lane i sums the points of requests [i s, (i + 1) s)
+        const int strip = (a.B + 31) / 32;
+        const int b_lo = min(a.B, lane * strip), b_hi = min(a.B, b_lo + strip);
+        int mine = 0;
+#pragma unroll 4
+        for (int b = b_lo; b < b_hi; ++b) mine += seg_points(own_tiles(a, b), kSingleCost);
+        int before = mine;
 #pragma unroll
-            for (int blk = 0; blk < C::kBlocks; ++blk)
-              *reinterpret_cast<uint4*>(v + blk * C::kBlockBytes + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->v_fixed[r.st]);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += x;
         }
-        if (lane == 0) mbar_arrive(&bars->v_empty[r.st]);
-        r.next(C::kVStages);
-        return true;
-      };
-      bool ok = true;
-      Walk w0 = walk[0], w1 = walk[1];
-      Piece u0, u1;
-      while (ok && next_piece<true>(a, pl, w0, u0))
-        for (int t = u0.t; ok && t < u0.t_end; ++t) ok = pass(tile_keys(u0, t));
-      bool live0 = next_piece<false>(a, pl, w0, u0), live1 = next_piece<false>(a, pl, w1, u1);
-      int t0 = live0 ? u0.t : 0, t1 = live1 ? u1.t : 0;
-      while (ok && (live0 || live1)) {
-        if (live0) {
-          ok = pass(tile_keys(u0, t0));
-          if (++t0 == u0.t_end) {
-            live0 = next_piece<false>(a, pl, w0, u0);
-            t0 = live0 ? u0.t : 0;
+        const int own = __shfl_sync(0xffffffffu, before, 31);
+        before -= mine;
+        const Line line(pl, a.n_kv, own);
+        const int cta = blockIdx.x;
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          Walk k;
+          int lo, hi;
+          line.single_part(cta, w, &lo, &hi);
+          // where the single tiles begin
+          k.rest_end = lo < hi ? hi : 0;  // an empty part: no tile starts before point 0
+          k.rest_kind = kOwn;
+          k.rest_g = k.rest_b = k.rest_t = 0;
+          k.rest_s0 = line.prefix_end;
+          if (lo < line.prefix_end) {
+            const int len = seg_points(pl.prefix_tiles, kSingleCost);
+            k.rest_kind = kPrefix;
+            k.rest_g = (lo - line.pair_end) / len;
+            k.rest_s0 = line.pair_end + k.rest_g * len;
+            k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, kSingleCost, pl.prefix_tiles);
+          } else if (lo < hi) {
+            // the lane whose requests hold the part's first point finds the tile there
+            const int x = lo - line.prefix_end;
+            const bool here = x >= before * a.n_kv && x < (before + mine) * a.n_kv;
+            if (here) {
+              int at = before;
+              int b = b_lo;
+              int len = seg_points(own_tiles(a, b), kSingleCost);
+              while (x >= (at + len) * a.n_kv) {
+                at += len;
+                len = seg_points(own_tiles(a, ++b), kSingleCost);
+              }
+              k.rest_b = b;
+              k.rest_g = (x - at * a.n_kv) / len;
+              k.rest_s0 = line.prefix_end + at * a.n_kv + k.rest_g * len;
+              k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, kSingleCost, own_tiles(a, b));
+            }
+            const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+            k.rest_b = __shfl_sync(0xffffffffu, k.rest_b, src);
+            k.rest_g = __shfl_sync(0xffffffffu, k.rest_g, src);
+            k.rest_t = __shfl_sync(0xffffffffu, k.rest_t, src);
+            k.rest_s0 = __shfl_sync(0xffffffffu, k.rest_s0, src);
           }
+          // and the pairs before them
+          const int x0 = line.cut(cta);
+          k.kind = kPair;
+          k.g = k.b = k.t = 0;
+          k.s0 = 0;
+          k.end = 0;
+          if (x0 < line.pair_end) {
+            const int len = seg_points(pl.prefix_tiles, kPairCost);
+            const int seg = x0 / len;
+            k.end = min(line.cut(cta + 1), line.pair_end);
+            k.s0 = seg * len;
+            k.t = tile_at(x0, k.s0 + kPieceCost, kPairCost, pl.prefix_tiles);
+            k.g = seg / pl.n_pairs;
+            k.b = seg - k.g * pl.n_pairs;
+            if (k.t == pl.prefix_tiles) {  // behind the segment's last tile
+              k.t = 0;
+              k.s0 += len;
+              if (++k.b == pl.n_pairs) {
+                k.b = 0;
+                ++k.g;
+              }
+            }
+          }
+          walk[w] = k;
         }
-        if (ok && live1) {
-          ok = pass(tile_keys(u1, t1));
-          if (++t1 == u1.t_end) {
-            live1 = next_piece<false>(a, pl, w1, u1);
-            t1 = live1 ? u1.t : 0;
+        if (cta == 0) {
+          int* const sums = static_cast<int*>(a.workspace) + pl.sums;
+          int at = before;
+          for (int b = b_lo; b < b_hi; ++b) {
+            sums[b] = at;
+            at += seg_points(own_tiles(a, b), kSingleCost);
           }
+          if (lane == 0) sums[a.B] = own;
+        }
+      }
+      uint32_t n_pub[2] = {0, 0}, n_end[2] = {C::kAhead, C::kAhead};  // pieces handed out; and to be, so far
+      Ring r;
+      bool ok = true, take_cur = true, take_oth = true;
+      for (;;) {
+        // hand out pieces, kAhead in front of the one this warp is in
+        for (;;) {
+          const int w = n_pub[0] < n_end[0] ? 0 : 1;
+          if (n_pub[w] >= n_end[w]) break;
+          const Piece u = next_piece(a, pl, walk[w]);
+          if (lane == 0) {
+            bars->piece[w][n_pub[w] % C::kQueue] = u;
+            mbar_arrive(&bars->piece_full[w][n_pub[w] % C::kQueue]);
+          }
+          ++n_pub[w];
+          if (u.kind == kNone) n_end[w] = 0;  // the last one
+        }
+        if (take_cur) ok = cur.take(bars, wc, true);
+        if (take_oth) ok = ok && oth.take(bars, wc, true);
+        take_cur = take_oth = false;
+        if (!ok || !(cur.live() || oth.live())) break;
+        if (cur.live()) {
+          if (!warp_wait(&bars->v_full[r.st], r.ph, wc)) break;
+          const int n = tile_keys(cur.u, cur.t);
+          if (n < BN) {
+            // rows n.. were not loaded or hold no token: their weights are 0, and 0 times anything must be 0
+            uint8_t* const v = smem + C::kVOff + r.st * C::kTileBytes + n * 128;
+#pragma unroll 1
+            for (int i = lane; i < (BN - n) * 8; i += 32) {
+#pragma unroll
+              for (int blk = 0; blk < C::kBlocks; ++blk)
+                *reinterpret_cast<uint4*>(v + blk * C::kBlockBytes + i * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->v_fixed[r.st]);
+          }
+          if (lane == 0) mbar_arrive(&bars->v_empty[r.st]);
+          r.next(C::kVStages);
+          const bool pair = cur.u.kind == kPair;
+          if (++cur.t == cur.u.t_end) {
+            take_cur = true;
+            take_oth = pair;
+            if (n_end[cur.w]) ++n_end[cur.w];
+            if (pair && n_end[oth.w]) ++n_end[oth.w];
+          }
+          // on pair tiles worker 0 goes on until its first single tile; a finished piece is replaced first
+          if (pair) continue;
+        }
+        if (take_cur ? true : oth.live()) {
+          if (!oth.live()) continue;
+          const Cursor<D> x = cur;
+          cur = oth;
+          oth = x;
+          take_oth = take_cur;
+          take_cur = false;
         }
       }
       __syncwarp();
@@ -633,67 +765,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
     // ------------------------------------------------------------ softmax warpgroups (workers)
-    const int w = (warp - 4) >> 2;
+    Cursor<D> cur;
+    cur.w = (warp - 4) >> 2;
+    cur.n = 0;
+    const int w = cur.w;
     const int quad = warp & 3;       // TMEM lane quadrant
     const int r = quad * 32 + lane;  // row within the tile
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + (w ? 128u : 0u);
     const uint32_t o_addr = tmem + lane_off + C::kOCol + (w ? D : 0);
-    uint8_t* const q_smem = smem + C::kQOff + w * C::kTileBytes;
     const int G = a.n_h / a.n_kv;
-    float* const ws = static_cast<float*>(a.workspace);
-    Walk wk = w ? walk[1] : walk[0];
-    uint32_t sph = 0, n_done = 0;
+    uint32_t sph = 0, n_done = 0, n_q = 0, q_off = 0;
 
-    auto next = [&](Piece& u) -> bool {
-      return next_piece<true>(a, pl, wk, u) || next_piece<false>(a, pl, wk, u);
+    // the first of a piece's rows among its KV head's prefix rows (row r: request r / G), and how many it has
+    auto first_row = [&](const Piece& u) {
+      return u.kind == kOwn ? u.b * G : (u.kind == kPair ? u.b * 2 * BM + w * BM : pl.n_pairs * 2 * BM);
     };
-    // The piece's query rows into shared memory, each rotated at its request's last position; the
-    // last piece's Q K have completed.  One thread per (row, chunks c and c + D / 16).
-    auto prepare_q = [&](const Piece& u) {
-      constexpr int kPairsOfChunks = D / 16;
-      for (int idx = r; idx < u.n_rows * kPairsOfChunks; idx += 128) {
-        const int i = idx / kPairsOfChunks, c = idx % kPairsOfChunks;
-        const int b = u.kind == kOwn ? u.b : (u.row0 + i) / G;
-        const int h = u.g * G + (u.kind == kOwn ? i : (u.row0 + i) % G);
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<long long>(b) * a.n_h + h) * D;
-        float x0[8], x1[8];
-        bf16x8_to_f32(*reinterpret_cast<const uint4*>(q + c * 8), x0);
-        bf16x8_to_f32(*reinterpret_cast<const uint4*>(q + D / 2 + c * 8), x1);
-        if (f.n_pairs) {  // the rotated span is the whole head (decode_paged_tc_supported)
-          const int pos = max(paged_len(a, b), 1) - 1;
-          if (f.half) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float sn, cs;
-              rope_sincos_fast(pos, f_hi[c * 8 + e], f_lo[c * 8 + e], &sn, &cs);
-              rotate_pair(x0[e], x1[e], sn, cs);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float sn, cs;
-              rope_sincos_fast(pos, f_hi[c * 4 + e], f_lo[c * 4 + e], &sn, &cs);
-              rotate_pair(x0[2 * e], x0[2 * e + 1], sn, cs);
-              rope_sincos_fast(pos, f_hi[D / 4 + c * 4 + e], f_lo[D / 4 + c * 4 + e], &sn, &cs);
-              rotate_pair(x1[2 * e], x1[2 * e + 1], sn, cs);
-            }
-          }
-        }
-        *reinterpret_cast<uint4*>(q_smem + chunk_off(i, c)) = f32_to_bf16x8(x0);
-        *reinterpret_cast<uint4*>(q_smem + chunk_off(i, c + kPairsOfChunks)) = f32_to_bf16x8(x1);
+    auto rows_of = [&](const Piece& u) {
+      return u.kind == kOwn ? G : u.kind == kPrefix ? pl.rows1 : min(BM, a.B * G - first_row(u));
+    };
+    // the query rows of the piece in cur; what the place held before has been read by its Q K
+    auto prepare_q = [&]() {
+      load_q_rows<D>(&a, smem + C::kQOff + w * C::kTileBytes + q_off, f_hi, f_lo, f.n_pairs, f.half, cur.u.g,
+                     first_row(cur.u), rows_of(cur.u), r);
+      mbar_arrive(&bars->q_ready[w][n_q & 1u]);
+      ++n_q;
+    };
+
+    bool ok = cur.take(bars, wc, true);
+    bool prepared = false;
+    while (ok && cur.live()) {
+      // the first piece's rows, or those that could not be written while the piece before ran
+      if (!prepared) prepare_q();
+      const Piece u = cur.u;
+      const int n_rows = rows_of(u);
+      const bool active = quad * 32 < n_rows;  // this warp holds rows of the piece
+      // the next piece's rows go to the tile's other half while this piece runs, if both fit a half
+      if (!cur.take(bars, wc, true)) break;
+      prepared = false;
+      if (cur.live()) {
+        const int p = q_rows(a, pl, u), q = q_rows(a, pl, cur.u);
+        q_off = next_q_off(p, q_off, q);
+        prepared = p <= kHalfRows && q <= kHalfRows;
+        if (prepared) prepare_q();
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&bars->q_ready[w]);
-    };
-
-    Piece u;
-    bool live = next(u);
-    if (live) prepare_q(u);
-    while (live) {
-      const bool active = quad * 32 < u.n_rows;  // this warp holds rows of the piece
       float m_run = -INFINITY, l_run = 0.f;
-      bool ok = true;
       for (int t = u.t; t < u.t_end; ++t) {
         if (!warp_wait(&bars->s_full[w], sph, wc)) { ok = false; break; }
         sph ^= 1;
@@ -729,10 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          a.scale_log2;
         // the reference maximum moves only when the row's grew by more than the threshold
         const bool need = mx > m_run + kRescaleThreshold;
-        const bool seen = m_run != -INFINITY;
         float alpha = 1.f;
         if (need) {
-          if (seen) alpha = fast_exp2(m_run - mx);
+          if (m_run != -INFINITY) alpha = fast_exp2(m_run - mx);
           l_run *= alpha;
           m_run = mx;
         }
@@ -777,25 +892,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bars->p_full[w]);
       }
       if (!__all_sync(0xffffffffu, ok)) break;
-      Piece nu = u;
-      const bool more = next(nu);
-      if (more) prepare_q(nu);
+      // rows of the next piece that take the whole tile: the Q K of this piece have completed
+      if (cur.live() && !prepared) {
+        prepare_q();
+        prepared = true;
+      }
 
       // epilogue: the piece's normalised partial and its log-sum-exp
       if (!warp_wait(&bars->o_done[w], n_done & 1, wc)) break;
       ++n_done;
       if (active) {
         tc_fence_after();
-        const int rows = u.kind == kPair ? 2 * BM : u.kind == kPrefix ? pl.rows1 : G;
-        const long long row = u.slot * rows + (u.kind == kPair ? w * BM : 0) + r;
-        float* const po = ws + (u.kind == kPair ? pl.o2 : u.kind == kPrefix ? pl.o1 : pl.o0) + row * D;
-        const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+        float* const ws = static_cast<float*>(a.workspace);
+        const long long worker = 2 * static_cast<long long>(blockIdx.x) + w;
+        long long row, o_at, l_at;
+        if (u.kind == kOwn) {
+          row = (worker + static_cast<long long>(u.b) * a.n_kv + u.g) * G;
+          o_at = pl.o0;
+          l_at = pl.l0;
+        } else if (u.kind == kPrefix) {
+          row = (worker + u.g) * pl.rows1;
+          o_at = pl.o1;
+          l_at = pl.l1;
+        } else {
+          row = (blockIdx.x + static_cast<long long>(u.g) * pl.n_pairs + u.b) * (2 * BM) + w * BM;
+          o_at = pl.o2;
+          l_at = pl.l2;
+        }
+        row += r;
+        float* const po = ws + o_at + row * D;
+        const float inv_l = l_run > 0.f ? 1.f / l_run : l_run;  // 0: every score is -inf; NaN stays
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t orow[32];
           tmem_ld32(o_addr + c * 32, orow);
           tmem_wait_ld();
-          if (r < u.n_rows) {
+          if (r < n_rows) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<float4*>(po + c * 32 + e) =
@@ -803,13 +935,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                               __uint_as_float(orow[e + 2]) * inv_l, __uint_as_float(orow[e + 3]) * inv_l);
           }
         }
-        if (r < u.n_rows)
-          ws[(u.kind == kPair ? pl.l2 : u.kind == kPrefix ? pl.l1 : pl.l0) + row] = m_run + log2f(l_run);
+        if (r < n_rows) ws[l_at + row] = m_run + log2f(l_run);
         tc_fence_before();
       }
       mbar_arrive(&bars->o_empty[w]);
-      u = nu;
-      live = more;
     }
   }
 
@@ -823,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // One warp per (request b, head h): its row's pieces are those of the CTAs (pair tiles) or workers
 // (single tiles) between the one that holds the segment's first tile and the one that holds its
-// last; a CTA or worker between them whose part of the line holds no tile wrote none.
+// last; a CTA or worker between them in whose part no tile starts wrote none.
 constexpr int kCombineWarps = 4;
 
 template <int D>
@@ -842,35 +971,25 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     return;
   }
   const float* const ws = static_cast<const float*>(a.workspace);
-  const long long* const sums = reinterpret_cast<const long long*>(ws + pl.sums);
+  const int* const sums = reinterpret_cast<const int*>(ws + pl.sums);
+  const int sum_b = sums[b];
   const Line line(pl, a.n_kv, sums[a.B]);
-  // the row's segments: [first, last] tile of the prefix (pair or single) and of its own keys
-  const long long row = static_cast<long long>(b) * G + i;  // among the KV head's prefix rows
-  const bool pair = row < static_cast<long long>(pl.n_pairs) * 2 * BM;
-  long long pf = 0, own_f;
+  // the row's two segments, each from its first tile's point p0: the prefix (pair or single) and its own keys
+  const int row = b * G + i;  // among the KV head's prefix rows
+  const bool pair = row < pl.n_pairs * 2 * BM;
+  const int seg = pair ? g * pl.n_pairs + row / (2 * BM) : g;
+  const int pre_cost = pair ? kPairCost : kSingleCost;
+  const int pre_p0 = (pair ? 0 : line.pair_end) + kPieceCost + seg * seg_points(pl.prefix_tiles, pre_cost);
   int c0 = 0, n_pre = 0;  // first CTA (pair) or worker (single) of the prefix pieces, and how many to look at
-  auto worker_of = [&](long long j) {  // the worker that holds single tile j
-    const int c = line.cta_of(line.pair_tiles * kPairCost + j * kSingleCost, pl.ctas);
-    long long lo, hi;
-    line.singles(c, 1, pl.ctas, &lo, &hi);
-    return 2 * c + (j >= lo ? 1 : 0);
-  };
   if (pl.prefix_tiles > 0) {
-    const long long seg = pair ? static_cast<long long>(g) * pl.n_pairs + row / (2 * BM) : g;
-    pf = seg * pl.prefix_tiles;
-    const long long pe = pf + pl.prefix_tiles - 1;
-    if (pair) {
-      c0 = line.cta_of(pf * kPairCost, pl.ctas);
-      n_pre = line.cta_of(pe * kPairCost, pl.ctas) - c0 + 1;
-    } else {
-      c0 = worker_of(pf);
-      n_pre = worker_of(pe) - c0 + 1;
-    }
+    const int last = pre_p0 + (pl.prefix_tiles - 1) * pre_cost;
+    c0 = pair ? line.cta_of(pre_p0) : line.worker_of(pre_p0);
+    n_pre = (pair ? line.cta_of(last) : line.worker_of(last)) - c0 + 1;
   }
-  const long long nt = (L - a.prefix_len + BN - 1) / BN;
-  own_f = line.single_prefix + sums[b] * a.n_kv + g * nt;
-  const int w0 = worker_of(own_f);
-  const int n = n_pre + worker_of(own_f + nt - 1) - w0 + 1;
+  const int nt = own_tiles(a, b);
+  const int own_p0 = line.prefix_end + sum_b * a.n_kv + g * seg_points(nt, kSingleCost) + kPieceCost;
+  const int w0 = line.worker_of(own_p0);
+  const int n = n_pre + line.worker_of(own_p0 + (nt - 1) * kSingleCost) - w0 + 1;
 
   float M = -INFINITY, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -878,26 +997,32 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     // lane j looks at piece j0 + j: its place in the workspace and its log-sum-exp
     long long at = -1, l_at = 0;
     const int j = j0 + lane;
-    if (j < n_pre && pair) {
-      const int c = c0 + j;
-      const long long lo = line.pair_at(line.cut(c, pl.ctas)), hi = line.pair_at(line.cut(c + 1, pl.ctas));
-      if (max(lo, pf) < min(hi, pf + pl.prefix_tiles)) {
-        const long long seg = pf / pl.prefix_tiles;
-        l_at = (c + seg) * (2 * BM) + row % (2 * BM);
-        at = pl.o2 + l_at * D;
-        l_at += pl.l2;
-      }
-    } else if (j < n) {
+    if (j < n) {
       const bool pre = j < n_pre;
       const int w = pre ? c0 + j : w0 + j - n_pre;
-      const long long f = pre ? pf : own_f, e = f + (pre ? pl.prefix_tiles : nt);
-      long long lo, hi;
-      line.singles(w >> 1, w & 1, pl.ctas, &lo, &hi);
-      if (max(lo, f) < min(hi, e)) {
-        l_at = pre ? (static_cast<long long>(w) + g) * pl.rows1 + row - static_cast<long long>(pl.n_pairs) * 2 * BM
-                   : (static_cast<long long>(w) + static_cast<long long>(b) * a.n_kv + g) * G + i;
-        at = (pre ? pl.o1 : pl.o0) + l_at * D;
-        l_at += pre ? pl.l1 : pl.l0;
+      int lo, hi;
+      if (pre && pair) {
+        lo = line.cut(w);
+        hi = min(line.cut(w + 1), line.pair_end);
+      } else {
+        line.single_part(w >> 1, w & 1, &lo, &hi);
+      }
+      const int p0 = pre ? pre_p0 : own_p0;
+      const int cost = pre ? pre_cost : kSingleCost, tiles = pre ? pl.prefix_tiles : nt;
+      if (tile_at(lo, p0, cost, tiles) < tile_at(hi, p0, cost, tiles)) {
+        if (!pre) {
+          l_at = (static_cast<long long>(w) + static_cast<long long>(b) * a.n_kv + g) * G + i;
+          at = pl.o0 + l_at * D;
+          l_at += pl.l0;
+        } else if (pair) {
+          l_at = (static_cast<long long>(w) + seg) * (2 * BM) + row % (2 * BM);
+          at = pl.o2 + l_at * D;
+          l_at += pl.l2;
+        } else {
+          l_at = (static_cast<long long>(w) + seg) * pl.rows1 + row - pl.n_pairs * 2 * BM;
+          at = pl.o1 + l_at * D;
+          l_at += pl.l1;
+        }
       }
     }
     const float l = at >= 0 ? ws[l_at] : -INFINITY;
@@ -909,13 +1034,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     const float alpha = exp2f(M - m_ref);
     const float wl = at >= 0 ? exp2f(l - m_ref) : 0.f;
     M = m_new;
-    den = den * alpha + wl;
+    den = den * alpha + wl;  // of this lane's pieces
     acc.x *= alpha;
     acc.y *= alpha;
     acc.z *= alpha;
     acc.w *= alpha;
     const int nj = min(32, n - j0);
-#pragma unroll 4
+#pragma unroll 8
     for (int jj = 0; jj < nj; ++jj) {
       const long long p = __shfl_sync(0xffffffffu, at, jj);
       const float wj = __shfl_sync(0xffffffffu, wl, jj);
@@ -928,7 +1053,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       }
     }
   }
-  // (den of a lane holds only its own pieces' weights, rescaled alike)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   const float inv = 1.f / den;
@@ -941,7 +1065,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
 // CTAs at most: the workspace is sized for this many (a GB300 has 152 SMs).
 constexpr int kMaxCtas = 160;
 
-// False if the sizes pass what the kernel's indices hold.
 PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
   PagedTcPlan p{};
   const int G = a.n_h / a.n_kv;
@@ -951,7 +1074,7 @@ PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
   p.n_pairs = row_tiles / 2;
   p.odd = row_tiles & 1;
   p.rows1 = p.odd ? static_cast<int>(rows - static_cast<long long>(p.n_pairs) * 2 * BM) : 0;
-  p.prefix_tiles = (a.prefix_len + BN - 1) / BN;
+  p.prefix_tiles = static_cast<int>((static_cast<long long>(a.prefix_len) + BN - 1) / BN);
   const long long pieces2 = p.n_pairs ? kMaxCtas + static_cast<long long>(p.n_pairs) * a.n_kv : 0;
   const long long pieces1 = p.odd ? 2 * kMaxCtas + static_cast<long long>(a.n_kv) : 0;
   const long long pieces0 = 2 * kMaxCtas + static_cast<long long>(a.B) * a.n_kv;
@@ -962,7 +1085,7 @@ PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
   p.l1 = p.l2 + pieces2 * 2 * BM;
   p.l0 = p.l1 + pieces1 * p.rows1;
   p.sums = (p.l0 + pieces0 * G + 3) & ~3LL;  // 16-byte aligned
-  p.end = p.sums + 2 * (static_cast<long long>(a.B) + 1);
+  p.end = p.sums + a.B + 1;
   return p;
 }
 
@@ -1003,8 +1126,17 @@ cudaError_t launch(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtenso
 
 bool decode_paged_tc_supported(const PagedDecodeArgs& a, bool bf16, int rope_offset, int rope_dims, bool rope) {
   const int G = a.n_h / a.n_kv;
-  return bf16 && a.D_qk == a.D_v && (a.D_qk == 64 || a.D_qk == 128) && G <= BM &&
-         (!rope || (rope_offset == 0 && rope_dims == a.D_qk));
+  if (!(bf16 && a.D_qk == a.D_v && (a.D_qk == 64 || a.D_qk == 128) && G <= BM &&
+        (!rope || (rope_offset == 0 && rope_dims == a.D_qk))))
+    return false;
+  // the line of tiles in 32-bit points: B * n_kv * keys up to some 3e10 (a table far wider than a cache's pages)
+  const PagedTcPlan p = make_plan(a, 1);
+  const long long own = ((static_cast<long long>(a.max_blocks) << a.page_shift) - a.prefix_len + BN - 1) / BN;
+  const double points = static_cast<double>(a.n_kv) *
+                        ((static_cast<double>(p.n_pairs) * kPairCost + p.odd * kSingleCost) * p.prefix_tiles +
+                         (p.n_pairs + p.odd + static_cast<double>(a.B)) * kPieceCost +
+                         static_cast<double>(a.B) * own * kSingleCost);
+  return points < 2147483647.0;
 }
 
 size_t decode_paged_tc_workspace(const PagedDecodeArgs& a) {
