@@ -105,15 +105,7 @@ int decode_impl(const void* q, const void* k_pages, const void* v_pages, int v_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!decode_paged_tc_supported(a, bf16, rope_offset, rope_dims, rope))
     return finish(launch_decode_paged(a, rf, bf16, st, &launches), launches);
-  // one box: 64 dims of one head, the rows of a page (half of them where a page is two tiles)
-  CUtensorMap maps[2];
-  const unsigned long long hs = static_cast<unsigned long long>(D_qk) * 2;
-  const unsigned long long ks = hs * n_kv, vs = static_cast<unsigned long long>(ldv) * 2;
-  const int box_rows = page_size < 128 ? page_size : 128;
-  if (!make_map4(&maps[0], k_pages, D_qk, n_kv, page_size, n_pages, hs, ks, ks * page_size, box_rows) ||
-      !make_map4(&maps[1], v_pages, D_v, n_kv, page_size, n_pages, hs, vs, vs * page_size, box_rows))
-    return finish(cudaErrorInvalidValue, launches);
-  return finish(launch_decode_paged_tc(a, rf, maps, dev.sms, st, &launches), launches);
+  return finish(launch_decode_paged_tc(a, rf, dev.sms, st, &launches), launches);
 }
 
 }  // namespace

@@ -33,33 +33,38 @@
 // points at its start; CTA 0's leaves the sums for the combine kernel) and hands the
 // pieces to the other roles through two small queues in shared memory, a few pieces
 // ahead; it also clears value rows behind a segment's last key, which may hold anything.
-// Warps 0 and 2 load K and V tiles by TMA, one box per page and 64 dims (a page is part
-// of a tile, the tile, or twice the tile), the lanes of the warp issuing one box each;
-// warp 1 issues the MMAs; warps 4-7 and 8-11 are the two workers' softmax.  The workers
-// run separate pieces (their tiles alternate in the K and V rings), so that one's MMAs
-// and loads fill the other's softmax and piece ends; on pair tiles they hold the two
-// row tiles.  Every role's code at a piece's boundary is kept small, one copy of each
-// part: with the walk inlined into every role a one-tile piece took 7 us, most of it
-// instruction fetches.
+// Warps 0 and 2 load the query rows, K and V tiles by TMA - K and V one box per page and
+// 64 dims (a page is part of a tile, the tile, or twice the tile), the lanes of the warp
+// issuing one box each; warp 1 issues the MMAs; warps 4-7 and 8-11 are the two workers'
+// softmax.  The workers run separate pieces (their tiles alternate in the K and V rings),
+// so that one's MMAs and loads fill the other's softmax and piece ends; on pair tiles
+// they hold the two row tiles and share each K/V tile.
+// A role's code is one small loop, the same for pair and single tiles: with the walk, the
+// query rotation and the two cases written out in each role (120 KB of instructions) a
+// one-tile piece took 10 us, the instruction fetches of the SMs saturating their shared
+// caches.  For the same reason the queries are rotated before, by a kernel of their own
+// that this one overlaps with its start (programmatic launch).
 // TMEM: S/P of the workers in columns [0, 128) and [128, 256), O behind them.
 #include <math.h>
 
 #include <atomic>
 
-#include "kernels.h"
+#include "api.h"
 
 namespace attn {
 
 // The cut of a call that does not depend on the lengths, and the layout of its workspace.
 struct PagedTcPlan {
   int ctas;
-  int n_pairs;       // pairs of 128-row tiles of a KV head's prefix rows
-  int odd;           // 1: one more row tile, of rows1 rows
-  int rows1;
+  int row_reqs;      // requests per row tile: 128 / G
+  int rows;          // rows per row tile: row_reqs * G
+  int n_pairs;       // pairs of row tiles of a KV head's prefix rows
+  int odd;           // 1: one more row tile
   int prefix_tiles;  // key tiles of the prefix
-  // float offsets into the workspace: partial outputs and log-sum-exps of pair pieces [256 rows],
-  // single prefix pieces [rows1] and own pieces [G]; then (int) B + 1 sums of points
-  long long o2, o1, o0, l2, l1, l0, sums, end;
+  // float offsets into the workspace: partial outputs and log-sum-exps of pair pieces [2 * rows],
+  // single prefix pieces [rows] and own pieces [G]; then (int) B + 1 sums of points and the rotated
+  // queries (bf16 [B, n_h, D])
+  long long o2, o1, o0, l2, l1, l0, sums, q, end;
 };
 
 namespace {
@@ -84,6 +89,8 @@ struct Piece {
   int b;         // own: the request; pair: the pair of row tiles
   int t, t_end;
   int keys;      // keys of the whole segment: tile t holds min(128, keys - 128 t) of them
+  int q_alt;     // 1: the query rows lie in the second half of the worker's Q tile
+  int q_back;    // they may be loaded when the Q K of this many pieces before are done
 };
 
 template <int D>
@@ -106,8 +113,7 @@ struct Cfg {
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
   static constexpr int kBarOff = kVOff + kVStages * kTileBytes;
   static constexpr int kBarBytes = D == 128 ? 1024 : 2048;
-  static constexpr int kFreqOff = kBarOff + kBarBytes;  // RoPE frequencies, hi then lo words
-  static constexpr int kSmemBytes = kFreqOff + D * 4 + 1024;  // + alignment slack
+  static constexpr int kSmemBytes = kBarOff + kBarBytes + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kOCol = 256;             // O of worker w at kOCol + w D
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(BM, BN, false);
@@ -119,11 +125,12 @@ struct Bars {
   using C = Cfg<D>;
   uint64_t k_full[C::kKStages], k_empty[C::kKStages];
   uint64_t v_full[C::kVStages], v_empty[C::kVStages], v_fixed[C::kVStages];
-  uint64_t q_ready[2][2];  // per worker, alternating between its pieces: the next one's rows may be ready early
+  uint64_t q_full[2][2], q_free[2][2];  // per worker, alternating between its pieces
   uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
   uint64_t piece_full[2][C::kQueue];
   uint64_t fin;
   Piece piece[2][C::kQueue];
+  WaitCtl wc;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -178,12 +185,20 @@ struct Line {
   }
 };
 
+// Where a piece's query rows lie in its worker's Q tile: own pieces of at most 64 rows alternate
+// between the tile's halves, so that the next piece's rows load while this one's are read (an MMA
+// reads 128 rows from either; what lies behind a piece's rows reaches only lanes that nobody reads).
+// A piece whose rows alternate waits for the Q K of the piece two before it, any other for those of
+// the piece before.
+constexpr int kHalfRows = 64;
+
 // A walk along one worker's part of the line: the next segment, its first point, its next tile, and
 // where the part ends.  Pair pieces come first (in both workers' walks), then single prefix pieces,
 // then own ones.
 struct Walk {
   int kind, g, b, t, s0, end;                                   // of the pairs, then of the rest
   int rest_kind, rest_g, rest_b, rest_t, rest_s0, rest_end;  // where the single tiles begin
+  int q_alt;  // Piece::q_alt of the last piece; -1: that piece's rows fill more than half a Q tile
 };
 
 // The next piece of a walk; kind kNone at its end.
@@ -192,7 +207,7 @@ __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const Page
   if (w.kind == kPair) {
     const int t_end = tile_at(w.end, w.s0 + kPieceCost, kPairCost, pl.prefix_tiles);
     if (w.g < a.n_kv && w.t < t_end) {
-      u = Piece{kPair, w.g, w.b, w.t, t_end, a.prefix_len};
+      u = Piece{kPair, w.g, w.b, w.t, t_end, a.prefix_len, 0, 1};
       w.t = t_end;
       if (t_end == pl.prefix_tiles) {
         w.t = 0;
@@ -228,7 +243,12 @@ __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const Page
     if (w.t >= t_end) {
       if (w.t < nt) return u;  // the part ends here
     } else {
-      u = Piece{w.kind, w.g, w.b, w.t, t_end, keys};
+      // own pieces of at most kHalfRows rows alternate between the halves of their Q tile
+      const bool half = w.kind == kOwn && a.n_h / a.n_kv <= kHalfRows;
+      const bool turn = half && w.q_alt >= 0;
+      const int alt = turn ? w.q_alt ^ 1 : 0;
+      w.q_alt = half ? alt : -1;
+      u = Piece{w.kind, w.g, w.b, w.t, t_end, keys, alt, turn ? 2 : 1};
       w.t = t_end;
     }
     if (w.t == nt) {
@@ -247,12 +267,24 @@ __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const Page
 __device__ __forceinline__ int tile_keys(const Piece& u, int t) { return min(BN, u.keys - t * BN); }
 
 // ------------------------------------------------------------------------------------- waits
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
-  const bool ok = mbar_wait(bar, parity, w);
+// A wait whose slow part is out of line: two dozen inlined copies of it were a quarter of the code.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, const WaitCtl* w) {
+  return mbar_wait(bar, parity, *w);
+}
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, const WaitCtl* w) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, w);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl* w) {
+  const bool ok = lane_wait(bar, parity, w);
+  return __all_sync(0xffffffffu, ok);
+}
+// In line, for the softmax warps (beside their tile loops the compiler finds no registers for a call).
+__device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, const WaitCtl* w) {
+  const bool ok = mbar_wait(bar, parity, *w);
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+__device__ __noinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (globaltimer_ns() - t0 > limit_ns) return;
@@ -275,11 +307,13 @@ struct Cursor {
   Piece u;
   int t, w;
   uint32_t n;  // pieces taken
-  __device__ __forceinline__ bool take(Bars<D>* bars, const WaitCtl& wc, bool whole_warp) {
+  enum { kLane, kWarp, kRow };  // who waits: one lane, a warp, a softmax warp
+  template <int WHO>
+  __device__ __forceinline__ bool take(Bars<D>* bars, const WaitCtl* wc) {
     constexpr uint32_t kQueue = Cfg<D>::kQueue;
     uint64_t* bar = &bars->piece_full[w][n % kQueue];
     const uint32_t par = (n / kQueue) & 1u;
-    const bool ok = whole_warp ? warp_wait(bar, par, wc) : mbar_wait(bar, par, wc);
+    const bool ok = WHO == kWarp ? warp_wait(bar, par, wc) : WHO == kRow ? row_wait(bar, par, wc) : lane_wait(bar, par, wc);
     if (ok) u = bars->piece[w][n % kQueue];
     else u.kind = kNone;
     t = u.t;
@@ -289,93 +323,212 @@ struct Cursor {
   __device__ __forceinline__ bool live() const { return u.kind != kNone; }
 };
 
-// ------------------------------------------------------------------------------------- query rows
-// Byte offset of the 16-byte chunk c (dims 8 c ..) of row r of a K-major, 128-byte-swizzled tile.
-__device__ __forceinline__ uint32_t chunk_off(int r, int c) {
-  return (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+// ------------------------------------------------------------------------------------- softmax of a tile
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
-// Where a piece's query rows lie in its worker's Q tile: pieces of at most 64 rows alternate between
-// the tile's halves, so that the next piece's rows are written while this one's are read (an MMA reads
-// 128 rows from either; what lies behind a piece's rows reaches only lanes that nobody reads).
-constexpr int kHalfRows = 64;
-__device__ __forceinline__ uint32_t next_q_off(int prev_rows, uint32_t prev_off, int rows) {
-  return prev_rows <= kHalfRows && rows <= kHalfRows ? prev_off ^ (kHalfRows * 128u) : 0u;
-}
-// Rows that a piece's Q tile is counted with there (a pair's tiles as full ones).
-__device__ __forceinline__ int q_rows(const PagedDecodeArgs& a, const PagedTcPlan& pl, const Piece& u) {
-  return u.kind == kPair ? BM : u.kind == kPrefix ? pl.rows1 : a.n_h / a.n_kv;
-}
-
-// Query rows row0 .. row0 + n_rows - 1 of KV head g (row r: head r mod G of request r / G) into the
-// swizzled tile at dst, rotated at their requests' last positions.  Thread r of 128 copies and
-// rotates the chunk pairs (c, c + D / 16) of row i with i D / 16 + c = r mod 128.  One copy of this
-// code, out of line, with the frequencies in shared memory.
+// This thread's row of O times alpha, before the tile's P V; the P V before has completed (the
+// tile's scores were committed after it).
 template <int D>
-__device__ __noinline__ void load_q_rows(const PagedDecodeArgs* ap, uint8_t* dst, const float* f_hi, const float* f_lo,
-                                         int n_pairs, int half, int g, int row0, int n_rows, int r) {
-  constexpr int kCP = D / 16;
-  const int G = ap->n_h / ap->n_kv, n_h = ap->n_h;
-  const __nv_bfloat16* const q0 = static_cast<const __nv_bfloat16*>(ap->q) + static_cast<long long>(g) * G * D;
-  const int n_items = n_rows * kCP;
-#pragma unroll 4
-  for (int idx = r; idx < n_items; idx += 128) {
-    const int i = idx / kCP, c = idx % kCP;
-    const int b = (row0 + i) / G, h = row0 + i - b * G;
-    const uint4* q = reinterpret_cast<const uint4*>(q0 + (static_cast<long long>(b) * n_h + h) * D) + c;
-    const uint4 lo = __ldg(q), hi = __ldg(q + kCP);
-    *reinterpret_cast<uint4*>(dst + chunk_off(i, c)) = lo;
-    *reinterpret_cast<uint4*>(dst + chunk_off(i, c + kCP)) = hi;
-  }
-  if (n_pairs) {
+__device__ __forceinline__ void rescale_o(uint32_t o_addr, float alpha) {
 #pragma unroll 1
-    for (int idx = r; idx < n_items; idx += 128) {
-      const int i = idx / kCP, c = idx % kCP;
-      const int pos = max(paged_len(*ap, (row0 + i) / G), 1) - 1;
-      uint4* const p0 = reinterpret_cast<uint4*>(dst + chunk_off(i, c));
-      uint4* const p1 = reinterpret_cast<uint4*>(dst + chunk_off(i, c + kCP));
-      float x0[8], x1[8], sn[8], cs[8];
-      bf16x8_to_f32(*p0, x0);
-      bf16x8_to_f32(*p1, x1);
-      // split halves: pair c 8 + e is (x0[e], x1[e]); adjacent: the chunks hold four whole pairs each
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t orow[32];
+    tmem_ld32(o_addr + c * 32, orow);
+    tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = half ? c * 8 + e : (e < 4 ? c * 4 + e : D / 4 + c * 4 + e - 4);
-        rope_sincos_fast(pos, f_hi[j], f_lo[j], &sn[e], &cs[e]);
-      }
-      if (half) {
+    for (int e = 0; e < 32; ++e) orow[e] = __float_as_uint(__uint_as_float(orow[e]) * alpha);
+    tmem_st32(o_addr + c * 32, orow);
+  }
+}
+
+// The scores of one tile (n real keys) in this thread's TMEM row become the weights P, written over
+// them as bf16: p = 2^(s * scale*log2e - m).  m moves only when the row maximum grew by more than the
+// threshold; O and l are then scaled by 2^(m_old - m_new), exactly (l and O share their reference).
+// This form takes 32 scores at a time, reading them twice: a quarter of the code of the form below,
+// which counts where pieces are short and every role's code has to stay cached.
+template <int D>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, int n, bool rescale, float scale_log2,
+                                             float& m_run, float& l_run) {
+  float m8[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rotate_pair(x0[e], x1[e], sn[e], cs[e]);
-      } else {
+  for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t v[32];
+    tmem_ld32(s_addr + c * 32, v);
+    tmem_wait_ld();
+    if (n < c * 32 + 32) {  // keys behind the segment's end
+      const uint32_t keep = n > c * 32 ? (1u << (n - c * 32)) - 1u : 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          rotate_pair(x0[2 * e], x0[2 * e + 1], sn[e], cs[e]);
-          rotate_pair(x1[2 * e], x1[2 * e + 1], sn[4 + e], cs[4 + e]);
-        }
-      }
-      *p0 = f32_to_bf16x8(x0);
-      *p1 = f32_to_bf16x8(x1);
+      for (int e = 0; e < 32; ++e)
+        if (!(keep & (1u << e))) v[e] = __float_as_uint(-INFINITY);
+      tmem_st32(s_addr + c * 32, v);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      m8[e] = fmax3(m8[e], __uint_as_float(v[e]), __uint_as_float(v[8 + e]));
+      m8[e] = fmax3(m8[e], __uint_as_float(v[16 + e]), __uint_as_float(v[24 + e]));
     }
   }
-  fence_proxy_async_smem();
+  if (n < BN) tmem_wait_st();
+  const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7])) *
+                   scale_log2;
+  const bool need = mx > m_run + kRescaleThreshold;
+  float alpha = 1.f;
+  if (need) {
+    if (m_run != -INFINITY) alpha = fast_exp2(m_run - mx);
+    l_run *= alpha;
+    m_run = mx;
+  }
+  if (__any_sync(0xffffffffu, need && rescale)) rescale_o<D>(o_addr, alpha);
+  const float2 sl2 = make_float2(scale_log2, scale_log2);
+  const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
+  const float2 nm2 = make_float2(-m_ref, -m_ref);
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t v[32], p[16];
+    tmem_ld32(s_addr + c * 32, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2, nm2);
+      const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      acc[e & 1] = __fadd2_rn(acc[e & 1], pp);
+      p[e] = pack_bf16x2(pp.x, pp.y);
+    }
+    tmem_st16(s_addr + c * 16, p);  // over scores already taken
+  }
+  acc[0] = __fadd2_rn(acc[0], acc[1]);
+  l_run += acc[0].x + acc[0].y;
 }
 
+// The same with the whole row in registers, each score read once and the chains independent: for pair
+// tiles, which both workers' rows fill and the tensor pipe waits for.
+template <int D>
+__device__ __forceinline__ void softmax_tile_wide(uint32_t s_addr, uint32_t o_addr, int n, bool rescale,
+                                                  float scale_log2, float& m_run, float& l_run) {
+  uint32_t sr[BN];
+#pragma unroll
+  for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_addr + c * 32, sr + c * 32);
+  tmem_wait_ld();
+  float s[BN];
+#pragma unroll
+  for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(sr[c]);
+  if (n < BN) {
+#pragma unroll
+    for (int c = 0; c < BN; ++c)
+      if (c >= n) s[c] = -INFINITY;
+  }
+  // row maximum: 8 independent chains of three-input max, then a tree
+  float m8[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m8[e] = s[e];
+#pragma unroll
+  for (int c = 8; c + 16 <= BN; c += 16)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m8[e] = fmax3(m8[e], s[c + e], s[c + 8 + e]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[BN - 8 + e]);
+  const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7])) *
+                   scale_log2;
+  // the reference maximum moves only when the row's grew by more than the threshold
+  const bool need = mx > m_run + kRescaleThreshold;
+  float alpha = 1.f;
+  if (need) {
+    if (m_run != -INFINITY) alpha = fast_exp2(m_run - mx);
+    l_run *= alpha;
+    m_run = mx;
+  }
+  uint32_t pr[BN / 2];
+  const float2 sl2 = make_float2(scale_log2, scale_log2);
+  const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
+  const float2 nm2 = make_float2(-m_ref, -m_ref);
+  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < BN / 4; ++c) {
+    const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sl2, nm2);
+    const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+    acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
+    pr[c] = pack_bf16x2(pp.x, pp.y);
+  }
+  tmem_st32(s_addr, pr);
+  if (__any_sync(0xffffffffu, need && rescale)) rescale_o<D>(o_addr, alpha);
+#pragma unroll
+  for (int c = BN / 4; c < BN / 2; ++c) {
+    const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sl2, nm2);
+    const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+    acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
+    pr[c] = pack_bf16x2(pp.x, pp.y);
+  }
+  acc[0] = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+  l_run += acc[0].x + acc[0].y;
+  tmem_st32(s_addr + 32, pr + 32);
+}
+
+// The new tokens' queries rotated at their positions, bf16 [B, n_h, D]: one thread per (row, chunks
+// of 8 dims c and c + D / 16).  The decode kernel may start as soon as this one has.
+template <int D>
+__global__ void __launch_bounds__(256) paged_rope_q_kernel(const __grid_constant__ PagedDecodeArgs a,
+                                                           const __grid_constant__ RopeFreq f, __nv_bfloat16* out) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int kCP = D / 16;
+  __shared__ float f_hi[D / 2], f_lo[D / 2];
+  for (int i = threadIdx.x; i < f.n_pairs; i += 256) {
+    f_hi[i] = f.hi[i];
+    f_lo[i] = f.lo[i];
+  }
+  __syncthreads();
+  const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long row = idx / kCP;
+  if (row >= static_cast<long long>(a.B) * a.n_h) return;
+  const int c = static_cast<int>(idx % kCP);
+  const int pos = max(paged_len(a, static_cast<int>(row / a.n_h)), 1) - 1;
+  const uint4* const q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D) + c;
+  uint4* const o = reinterpret_cast<uint4*>(out + row * D) + c;
+  float x0[8], x1[8];
+  bf16x8_to_f32(q[0], x0);
+  bf16x8_to_f32(q[kCP], x1);
+  if (f.half) {  // pair 8 c + e is (x0[e], x1[e])
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float sn, cs;
+      rope_sincos(pos, f_hi[c * 8 + e], f_lo[c * 8 + e], &sn, &cs);
+      rotate_pair(x0[e], x1[e], sn, cs);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float sn, cs;
+      rope_sincos(pos, f_hi[c * 4 + e], f_lo[c * 4 + e], &sn, &cs);
+      rotate_pair(x0[2 * e], x0[2 * e + 1], sn, cs);
+      rope_sincos(pos, f_hi[D / 4 + c * 4 + e], f_lo[D / 4 + c * 4 + e], &sn, &cs);
+      rotate_pair(x1[2 * e], x1[2 * e + 1], sn, cs);
+    }
+  }
+  o[0] = f32_to_bf16x8(x0);
+  o[kCP] = f32_to_bf16x8(x1);
+}
+
+// tm_q: the query rows of one request and KV head per box; tm_qn: of row_reqs requests.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ RopeFreq f,
-                    const __grid_constant__ PagedTcPlan pl, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v) {
+    paged_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ PagedTcPlan pl,
+                    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qn,
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars<D>* bars = reinterpret_cast<Bars<D>*>(smem + C::kBarOff);
-  float* const f_hi = reinterpret_cast<float*>(smem + C::kFreqOff);
-  float* const f_lo = f_hi + D / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < f.n_pairs; i += kThreads) {
-    f_hi[i] = f.hi[i];
-    f_lo[i] = f.lo[i];
-  }
+  asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may start to wait
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
@@ -387,8 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->v_fixed[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&bars->q_ready[w][0], 128);
-      mbar_init(&bars->q_ready[w][1], 128);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars->q_full[w][i], 1);
+        mbar_init(&bars->q_free[w][i], 1);
+      }
       mbar_init(&bars->s_full[w], 1);
       mbar_init(&bars->p_full[w], 128);
       mbar_init(&bars->o_done[w], 1);
@@ -397,6 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bars->fin, 1);
     bars->abort_flag = 0;
+    bars->wc.abort_flag = &bars->abort_flag;
+    bars->wc.status = a.status;
+    bars->wc.limit_ns = a.wait_limit_ns;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -407,10 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const WaitCtl wc{&bars->abort_flag, a.status, a.wait_limit_ns};
+  const WaitCtl* const wc = &bars->wc;
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsCtl>();
+    // Every role visits the two workers' tiles in turns, worker 0 first, one worker alone when the
+    // other is done.  A pair tile is in both workers' queues: its K and V belong to worker 0's visit.
     Cursor<D> cur, oth;  // the worker whose turn it is, and the other one
     cur.w = 0;
     oth.w = 1;
@@ -427,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box_shift = min(a.page_shift, 7);  // rows per box: a page, or half of a 256-token page
       const int boxes = BN >> box_shift;            // per column block of a tile
       const int box = lane & (boxes - 1), blk = lane / boxes;  // lane l loads block l / boxes of page l mod boxes
+      const int G = a.n_h / a.n_kv;
       Ring r;
       uint32_t issued = 0, last_ph = 0;
       int id_cur = -1, id_oth = -1;  // the lane's page of each worker's next tile
@@ -437,32 +598,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key = s.t * BN + (box << box_shift);
         return s.live() && blk < C::kBlocks && key < s.u.keys ? tbl[key >> a.page_shift] : -1;
       };
-      bool ok = cur.take(bars, wc, true) && oth.take(bars, wc, true);
+      bool ok = cur.template take<Cursor<D>::kWarp>(bars, wc) && oth.template take<Cursor<D>::kWarp>(bars, wc);
       id_cur = fetch(cur);
       id_oth = fetch(oth);
+      if (!is_v) {  // the rotated queries come from the kernel before
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+      }
       while (ok && (cur.live() || oth.live())) {
         if (cur.live()) {
-          if (!warp_wait(&empty[r.st], r.ph ^ 1, wc)) break;
-          const int n_boxes = (tile_keys(cur.u, cur.t) + (1 << box_shift) - 1) >> box_shift;  // others hold no key
-          if (lane == 0)
-            mbar_arrive_expect_tx(&full[r.st], static_cast<uint32_t>(n_boxes * C::kBlocks) << (box_shift + 7));
-          __syncwarp();
-          if (blk < C::kBlocks && box < n_boxes)
-            tma_load_4d(ring + r.st * C::kTileBytes + blk * C::kBlockBytes + (box << (box_shift + 7)), map,
-                        &full[r.st], blk * 64, cur.u.g, (cur.t * BN) & ((1 << a.page_shift) - 1), id_cur);
-          issued |= 1u << r.st;
-          last_ph = (last_ph & ~(1u << r.st)) | (r.ph << r.st);
-          r.next(n_stages);
-          const bool pair = cur.u.kind == kPair;
-          if (++cur.t == cur.u.t_end) {
-            ok = cur.take(bars, wc, true);
-            if (ok && pair) {  // a pair piece stands in both queues
-              ok = oth.take(bars, wc, true);
-              id_oth = fetch(oth);
+          if (!is_v && cur.t == cur.u.t) {
+            // the piece's query rows
+            const uint32_t n = cur.n - 1;
+            const bool own = cur.u.kind == kOwn;
+            const uint32_t back = cur.u.q_back;
+            if (n >= back) {
+              const uint32_t m = n - back;
+              if (!warp_wait(&bars->q_free[cur.w][m & 1u], (m >> 1) & 1u, wc)) break;
             }
+            if (lane == 0) {
+              const int tile = cur.u.kind == kPair ? 2 * cur.u.b + cur.w : 2 * pl.n_pairs;  // row tile of the prefix
+              uint8_t* const dst = smem + C::kQOff + cur.w * C::kTileBytes + cur.u.q_alt * (kHalfRows * 128);
+              uint64_t* const bar = &bars->q_full[cur.w][n & 1u];
+              mbar_arrive_expect_tx(bar, (own ? G : pl.rows) * 128 * C::kBlocks);
+              for (int i = 0; i < C::kBlocks; ++i)
+                tma_load_4d(dst + i * C::kBlockBytes, own ? &tm_q : &tm_qn, bar, i * 64, 0, cur.u.g,
+                            own ? cur.u.b : tile * pl.row_reqs);
+            }
+            __syncwarp();
           }
+          if (cur.u.kind != kPair || cur.w == 0) {
+            if (!warp_wait(&empty[r.st], r.ph ^ 1, wc)) break;
+            const int n_boxes = (tile_keys(cur.u, cur.t) + (1 << box_shift) - 1) >> box_shift;  // others hold no key
+            if (lane == 0)
+              mbar_arrive_expect_tx(&full[r.st], static_cast<uint32_t>(n_boxes * C::kBlocks) << (box_shift + 7));
+            __syncwarp();
+            if (blk < C::kBlocks && box < n_boxes)
+              tma_load_4d(ring + r.st * C::kTileBytes + blk * C::kBlockBytes + (box << (box_shift + 7)), map,
+                          &full[r.st], blk * 64, cur.u.g, (cur.t * BN) & ((1 << a.page_shift) - 1), id_cur);
+            issued |= 1u << r.st;
+            last_ph = (last_ph & ~(1u << r.st)) | (r.ph << r.st);
+            r.next(n_stages);
+          }
+          if (++cur.t == cur.u.t_end) ok = cur.template take<Cursor<D>::kWarp>(bars, wc);
           id_cur = fetch(cur);
-          if (pair) continue;  // the first single tile is worker 0's
         }
         if (oth.live()) {
           const Cursor<D> x = cur;
@@ -476,6 +655,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bars->abort_flag) {  // let every copy in flight land before shared memory goes away
         for (uint32_t s = 0; s < n_stages; ++s)
           if (issued & (1u << s)) drain_wait(&full[s], (last_ph >> s) & 1, a.wait_limit_ns);
+        if (!is_v)  // query rows of the piece a worker is in, or before it
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t n = ((i & 1) ? oth.n : cur.n) - 1 - (i >> 1);
+            const int w = (i & 1) ? oth.w : cur.w;
+            if (static_cast<int>(n) >= 0) drain_wait(&bars->q_full[w][n & 1u], (n >> 1) & 1u, 1000000ull);
+          }
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -486,124 +671,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t v_desc0 = sdesc_sw128(smem_u32(smem + C::kVOff), C::kBlockBytes, 1024);
         Ring kr, vr;
         uint32_t pph = 0, oph = 0, fix_ph = 0;  // parities, one bit per worker (fix_ph: per stage)
-        uint32_t n_q0 = 0, n_q1 = 0;            // pieces begun by each worker
-        // Q K of worker w's next tile; new_piece: its query rows have to be there first
-        auto issue_qk = [&](int w, bool new_piece, uint32_t q_off) -> bool {
-          if (new_piece) {
-            const uint32_t n = w ? n_q1++ : n_q0++;
-            if (!mbar_wait(&bars->q_ready[w][n & 1u], (n >> 1) & 1u, wc)) return false;
-          }
-          tc_fence_after();
-          const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + q_off) >> 4);
-          const uint64_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&bars->s_full[w]);
-          return true;
-        };
-        // P V of worker w's tile, once its P is there (and, for a piece's first tile, O is free)
-        auto issue_pv = [&](int w, bool first, bool last) -> bool {
-          if (!mbar_wait(&bars->p_full[w], (pph >> w) & 1u, wc)) return false;
-          pph ^= 1u << w;
-          if (first) {
-            if (!mbar_wait(&bars->o_empty[w], ((oph >> w) & 1u) ^ 1u, wc)) return false;
-            oph ^= 1u << w;
-          }
-          tc_fence_after();
-          const uint64_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
-                   (!first || kk > 0) ? 1u : 0u);
-          if (last) mma_commit(&bars->o_done[w]);
-          return true;
-        };
-        auto wait_k = [&]() -> bool { return mbar_wait(&bars->k_full[kr.st], kr.ph, wc); };
-        auto done_k = [&]() {
-          mma_commit(&bars->k_empty[kr.st]);
-          kr.next(C::kKStages);
-        };
-        auto wait_v = [&](int n) -> bool {  // n keys of the tile are real; fewer than 128: the rest is cleared first
-          if (!mbar_wait(&bars->v_full[vr.st], vr.ph, wc)) return false;
-          if (n == BN) return true;
-          const bool ok = mbar_wait(&bars->v_fixed[vr.st], (fix_ph >> vr.st) & 1u, wc);
-          fix_ph ^= 1u << vr.st;
-          return ok;
-        };
-        auto done_v = [&]() {
-          mma_commit(&bars->v_empty[vr.st]);
-          vr.next(C::kVStages);
-        };
-        if (!cur.take(bars, wc, false) || !oth.take(bars, wc, false)) goto mma_done;
-        if (cur.u.kind == kPair) {
-          // pair tiles: both workers' rows on each K/V tile
-          if (!wait_k()) goto mma_done;
-          for (int w = 0; w < 2; ++w)
-            if (!issue_qk(w, true, 0)) goto mma_done;
-          done_k();
-          bool first = true;  // the tile is its piece's first
-          while (cur.u.kind == kPair) {
-            const bool last = cur.t + 1 == cur.u.t_end;
-            if (!wait_v(tile_keys(cur.u, cur.t))) goto mma_done;
-            ++cur.t;
-            if (last && (!cur.take(bars, wc, false) || !oth.take(bars, wc, false))) goto mma_done;
-            const bool more = cur.u.kind == kPair;
-            for (int w = 0; w < 2; ++w) {
-              if (!issue_pv(w, first, last)) goto mma_done;
-              if (w == 1) done_v();
-              if (more) {
-                if (w == 0 && !wait_k()) goto mma_done;
-                if (!issue_qk(w, last, 0)) goto mma_done;
+        uint32_t pending = 0;                   // bit w: worker w's Q K is out, its P V not yet
+        bool ok = cur.template take<Cursor<D>::kLane>(bars, wc) && oth.template take<Cursor<D>::kLane>(bars, wc);
+        // one visit: P V of the worker's tile, then Q K of its next one
+        while (ok && (cur.live() || oth.live())) {
+          if (cur.live()) {
+            const uint32_t w = cur.w, bit = 1u << w;
+            if (pending & bit) {
+              const bool pair = cur.u.kind == kPair, first = cur.t == cur.u.t, last = cur.t + 1 == cur.u.t_end;
+              if (!pair || w == 0) {
+                if (!lane_wait(&bars->v_full[vr.st], vr.ph, wc)) break;
+                if (tile_keys(cur.u, cur.t) < BN) {  // the rows behind the last key are cleared first
+                  if (!lane_wait(&bars->v_fixed[vr.st], (fix_ph >> vr.st) & 1u, wc)) break;
+                  fix_ph ^= 1u << vr.st;
+                }
               }
-            }
-            if (more) done_k();
-            first = last;
-          }
-        }
-        {
-          // single tiles: the workers take turns, each P V followed by its next Q K
-          bool first_cur = true, first_oth = true;
-          uint32_t off_cur = 0, off_oth = 0;  // Q rows of each worker's piece (next_q_off)
-          for (int w = 0; w < 2; ++w)
-            if ((w ? oth : cur).live()) {
-              if (!wait_k() || !issue_qk(w, true, 0)) goto mma_done;
-              done_k();
-            }
-          while (cur.live() || oth.live()) {
-            if (cur.live()) {
-              const bool last = cur.t + 1 == cur.u.t_end;
-              if (!wait_v(tile_keys(cur.u, cur.t))) goto mma_done;
-              if (!issue_pv(cur.w, first_cur, last)) goto mma_done;
-              done_v();
+              if (!lane_wait(&bars->p_full[w], (pph >> w) & 1u, wc)) break;
+              pph ^= bit;
+              if (first) {  // O has been read
+                if (!lane_wait(&bars->o_empty[w], ((oph >> w) & 1u) ^ 1u, wc)) break;
+                oph ^= bit;
+              }
+              tc_fence_after();
+              const uint64_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < BN / 16; ++kk)
+                mma_ts(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
+                       (!first || kk > 0) ? 1u : 0u);
+              if (last) mma_commit(&bars->o_done[w]);
+              if (!pair || w == 1) {
+                mma_commit(&bars->v_empty[vr.st]);
+                vr.next(C::kVStages);
+              }
               ++cur.t;
-              if (last) {
-                const int rows = q_rows(a, pl, cur.u);
-                if (!cur.take(bars, wc, false)) goto mma_done;
-                off_cur = next_q_off(rows, off_cur, q_rows(a, pl, cur.u));
-              }
-              first_cur = last;
-              if (cur.live()) {
-                if (!wait_k() || !issue_qk(cur.w, last, off_cur)) goto mma_done;
-                done_k();
-              }
+              if (last && !cur.template take<Cursor<D>::kLane>(bars, wc)) break;
+              pending &= ~bit;
             }
-            if (oth.live()) {
-              const Cursor<D> x = cur;
-              cur = oth;
-              oth = x;
-              const bool y = first_cur;
-              first_cur = first_oth;
-              first_oth = y;
-              const uint32_t z = off_cur;
-              off_cur = off_oth;
-              off_oth = z;
+            if (cur.live()) {
+              const bool pair = cur.u.kind == kPair;
+              if (!pair || w == 0) {
+                if (!lane_wait(&bars->k_full[kr.st], kr.ph, wc)) break;
+              }
+              const uint32_t n = cur.n - 1;
+              if (cur.t == cur.u.t && !lane_wait(&bars->q_full[w][n & 1u], (n >> 1) & 1u, wc)) break;
+              tc_fence_after();
+              const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + cur.u.q_alt * (kHalfRows * 128)) >> 4);
+              const uint64_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&bars->s_full[w]);
+              if (cur.t + 1 == cur.u.t_end) mma_commit(&bars->q_free[w][n & 1u]);
+              if (!pair || w == 1) {
+                mma_commit(&bars->k_empty[kr.st]);
+                kr.next(C::kKStages);
+              }
+              pending |= bit;
             }
           }
+          if (oth.live()) {
+            const Cursor<D> x = cur;
+            cur = oth;
+            oth = x;
+          }
         }
-      mma_done:
         // every MMA issued so far completes before TMEM is released
         mma_commit(&bars->fin);
         drain_wait(&bars->fin, 0, a.wait_limit_ns);
@@ -674,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           k.g = k.b = k.t = 0;
           k.s0 = 0;
           k.end = 0;
+          k.q_alt = -1;
           if (x0 < line.pair_end) {
             const int len = seg_points(pl.prefix_tiles, kPairCost);
             const int seg = x0 / len;
@@ -719,40 +853,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n_pub[w];
           if (u.kind == kNone) n_end[w] = 0;  // the last one
         }
-        if (take_cur) ok = cur.take(bars, wc, true);
-        if (take_oth) ok = ok && oth.take(bars, wc, true);
+        if (take_cur) ok = cur.template take<Cursor<D>::kWarp>(bars, wc);
+        if (take_oth) ok = ok && oth.template take<Cursor<D>::kWarp>(bars, wc);
         take_cur = take_oth = false;
         if (!ok || !(cur.live() || oth.live())) break;
         if (cur.live()) {
-          if (!warp_wait(&bars->v_full[r.st], r.ph, wc)) break;
-          const int n = tile_keys(cur.u, cur.t);
-          if (n < BN) {
-            // rows n.. were not loaded or hold no token: their weights are 0, and 0 times anything must be 0
-            uint8_t* const v = smem + C::kVOff + r.st * C::kTileBytes + n * 128;
+          if (cur.u.kind != kPair || cur.w == 0) {
+            if (!warp_wait(&bars->v_full[r.st], r.ph, wc)) break;
+            const int n = tile_keys(cur.u, cur.t);
+            if (n < BN) {
+              // rows n.. were not loaded or hold no token: their weights are 0, and 0 times anything must be 0
+              uint8_t* const v = smem + C::kVOff + r.st * C::kTileBytes + n * 128;
 #pragma unroll 1
-            for (int i = lane; i < (BN - n) * 8; i += 32) {
+              for (int i = lane; i < (BN - n) * 8; i += 32) {
 #pragma unroll
-              for (int blk = 0; blk < C::kBlocks; ++blk)
-                *reinterpret_cast<uint4*>(v + blk * C::kBlockBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                for (int blk = 0; blk < C::kBlocks; ++blk)
+                  *reinterpret_cast<uint4*>(v + blk * C::kBlockBytes + i * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->v_fixed[r.st]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->v_fixed[r.st]);
+            if (lane == 0) mbar_arrive(&bars->v_empty[r.st]);
+            r.next(C::kVStages);
           }
-          if (lane == 0) mbar_arrive(&bars->v_empty[r.st]);
-          r.next(C::kVStages);
-          const bool pair = cur.u.kind == kPair;
           if (++cur.t == cur.u.t_end) {
             take_cur = true;
-            take_oth = pair;
             if (n_end[cur.w]) ++n_end[cur.w];
-            if (pair && n_end[oth.w]) ++n_end[oth.w];
           }
-          // on pair tiles worker 0 goes on until its first single tile; a finished piece is replaced first
-          if (pair) continue;
         }
-        if (take_cur ? true : oth.live()) {
-          if (!oth.live()) continue;
+        // the finished piece's successor is taken before its worker's next turn
+        if (oth.live()) {
           const Cursor<D> x = cur;
           cur = oth;
           oth = x;
@@ -775,147 +906,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + lane_off + (w ? 128u : 0u);
     const uint32_t o_addr = tmem + lane_off + C::kOCol + (w ? D : 0);
     const int G = a.n_h / a.n_kv;
-    uint32_t sph = 0, n_done = 0, n_q = 0, q_off = 0;
-
-    // the first of a piece's rows among its KV head's prefix rows (row r: request r / G), and how many it has
-    auto first_row = [&](const Piece& u) {
-      return u.kind == kOwn ? u.b * G : (u.kind == kPair ? u.b * 2 * BM + w * BM : pl.n_pairs * 2 * BM);
-    };
-    auto rows_of = [&](const Piece& u) {
-      return u.kind == kOwn ? G : u.kind == kPrefix ? pl.rows1 : min(BM, a.B * G - first_row(u));
-    };
-    // the query rows of the piece in cur; what the place held before has been read by its Q K
-    auto prepare_q = [&]() {
-      load_q_rows<D>(&a, smem + C::kQOff + w * C::kTileBytes + q_off, f_hi, f_lo, f.n_pairs, f.half, cur.u.g,
-                     first_row(cur.u), rows_of(cur.u), r);
-      mbar_arrive(&bars->q_ready[w][n_q & 1u]);
-      ++n_q;
-    };
-
-    bool ok = cur.take(bars, wc, true);
-    bool prepared = false;
-    while (ok && cur.live()) {
-      // the first piece's rows, or those that could not be written while the piece before ran
-      if (!prepared) prepare_q();
-      const Piece u = cur.u;
-      const int n_rows = rows_of(u);
+    uint32_t sph = 0, n_done = 0;
+    bool ok = true;
+    while (ok && cur.template take<Cursor<D>::kRow>(bars, wc) && cur.live()) {
+      const Piece& u = cur.u;
+      const int tile = u.kind == kPair ? 2 * u.b + w : 2 * pl.n_pairs;  // row tile of the prefix
+      const int n_rows = u.kind == kOwn ? G : min(pl.row_reqs, a.B - tile * pl.row_reqs) * G;
       const bool active = quad * 32 < n_rows;  // this warp holds rows of the piece
-      // the next piece's rows go to the tile's other half while this piece runs, if both fit a half
-      if (!cur.take(bars, wc, true)) break;
-      prepared = false;
-      if (cur.live()) {
-        const int p = q_rows(a, pl, u), q = q_rows(a, pl, cur.u);
-        q_off = next_q_off(p, q_off, q);
-        prepared = p <= kHalfRows && q <= kHalfRows;
-        if (prepared) prepare_q();
-      }
       float m_run = -INFINITY, l_run = 0.f;
       for (int t = u.t; t < u.t_end; ++t) {
-        if (!warp_wait(&bars->s_full[w], sph, wc)) { ok = false; break; }
+        if (!row_wait(&bars->s_full[w], sph, wc)) { ok = false; break; }
         sph ^= 1;
         if (!active) {  // padding rows: whatever their P is, it reaches only their own O
           mbar_arrive(&bars->p_full[w]);
           continue;
         }
         tc_fence_after();
-        uint32_t sr[BN];
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_addr + c * 32, sr + c * 32);
-        tmem_wait_ld();
-        float s[BN];
-#pragma unroll
-        for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(sr[c]);
-        const int n = tile_keys(u, t);
-        if (n < BN) {
-#pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c >= n) s[c] = -INFINITY;
-        }
-        // row maximum: 8 independent chains of three-input max, then a tree
-        float m8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = s[e];
-#pragma unroll
-        for (int c = 8; c + 16 <= BN; c += 16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m8[e] = fmax3(m8[e], s[c + e], s[c + 8 + e]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[BN - 8 + e]);
-        const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7])) *
-                         a.scale_log2;
-        // the reference maximum moves only when the row's grew by more than the threshold
-        const bool need = mx > m_run + kRescaleThreshold;
-        float alpha = 1.f;
-        if (need) {
-          if (m_run != -INFINITY) alpha = fast_exp2(m_run - mx);
-          l_run *= alpha;
-          m_run = mx;
-        }
-        uint32_t pr[BN / 2];
-        const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-        const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
-        const float2 nm2 = make_float2(-m_ref, -m_ref);
-        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < BN / 4; ++c) {
-          const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sl2, nm2);
-          const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
-          pr[c] = pack_bf16x2(pp.x, pp.y);
-        }
-        tmem_st32(s_addr, pr);
-        // O rescale before this tile's P V; the P V before has completed (s_full of this tile was
-        // committed after it)
-        if (__any_sync(0xffffffffu, need && t > u.t)) {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t orow[32];
-            tmem_ld32(o_addr + c * 32, orow);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) orow[e] = __float_as_uint(__uint_as_float(orow[e]) * alpha);
-            tmem_st32(o_addr + c * 32, orow);
-          }
-        }
-#pragma unroll
-        for (int c = BN / 4; c < BN / 2; ++c) {
-          const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sl2, nm2);
-          const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
-          pr[c] = pack_bf16x2(pp.x, pp.y);
-        }
-        acc[0] = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-        l_run += acc[0].x + acc[0].y;
-        tmem_st32(s_addr + 32, pr + 32);
+        if (u.kind == kPair)
+          softmax_tile_wide<D>(s_addr, o_addr, tile_keys(u, t), t > u.t, a.scale_log2, m_run, l_run);
+        else
+          softmax_tile<D>(s_addr, o_addr, tile_keys(u, t), t > u.t, a.scale_log2, m_run, l_run);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars->p_full[w]);
       }
       if (!__all_sync(0xffffffffu, ok)) break;
-      // rows of the next piece that take the whole tile: the Q K of this piece have completed
-      if (cur.live() && !prepared) {
-        prepare_q();
-        prepared = true;
-      }
-
       // epilogue: the piece's normalised partial and its log-sum-exp
-      if (!warp_wait(&bars->o_done[w], n_done & 1, wc)) break;
+      if (!row_wait(&bars->o_done[w], n_done & 1, wc)) break;
       ++n_done;
       if (active) {
         tc_fence_after();
         float* const ws = static_cast<float*>(a.workspace);
         const long long worker = 2 * static_cast<long long>(blockIdx.x) + w;
-        long long row, o_at, l_at;
+        long long row = worker, o_at = pl.o0, l_at = pl.l0;
         if (u.kind == kOwn) {
-          row = (worker + static_cast<long long>(u.b) * a.n_kv + u.g) * G;
-          o_at = pl.o0;
-          l_at = pl.l0;
+          row = (row + static_cast<long long>(u.b) * a.n_kv + u.g) * G;
         } else if (u.kind == kPrefix) {
-          row = (worker + u.g) * pl.rows1;
+          row = (row + u.g) * pl.rows;
           o_at = pl.o1;
           l_at = pl.l1;
         } else {
-          row = (blockIdx.x + static_cast<long long>(u.g) * pl.n_pairs + u.b) * (2 * BM) + w * BM;
+          row = ((blockIdx.x + static_cast<long long>(u.g) * pl.n_pairs + u.b) * 2 + w) * pl.rows;
           o_at = pl.o2;
           l_at = pl.l2;
         }
@@ -959,12 +990,13 @@ template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     paged_tc_combine_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ PagedTcPlan pl) {
   const int lane = threadIdx.x & 31;
-  const long long bh = static_cast<long long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
-  if (bh >= static_cast<long long>(a.B) * a.n_h) return;  // whole warps only
-  const int b = static_cast<int>(bh / a.n_h), h = static_cast<int>(bh % a.n_h);
+  const unsigned bh = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);  // B * n_h < 2^31
+  const int b = static_cast<int>(bh / static_cast<unsigned>(a.n_h)), h = static_cast<int>(bh) - b * a.n_h;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
+  if (b >= a.B) return;  // whole warps only
   const int G = a.n_h / a.n_kv, g = h / G, i = h % G;
   const int L = paged_len(a, b);
-  __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + bh * D;
+  __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(bh) * D;
   if (L <= a.prefix_len) {  // an empty place of the batch
     if (lane < D / 4) *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0, 0);
     if (a.lse != nullptr && lane == 0) a.lse[bh] = -INFINITY;
@@ -975,9 +1007,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const int sum_b = sums[b];
   const Line line(pl, a.n_kv, sums[a.B]);
   // the row's two segments, each from its first tile's point p0: the prefix (pair or single) and its own keys
-  const int row = b * G + i;  // among the KV head's prefix rows
-  const bool pair = row < pl.n_pairs * 2 * BM;
-  const int seg = pair ? g * pl.n_pairs + row / (2 * BM) : g;
+  const int tile = b / pl.row_reqs;                // row tile of the prefix,
+  const int row = (b - tile * pl.row_reqs) * G + i;  // and the row there
+  const bool pair = tile < 2 * pl.n_pairs;
+  const int seg = pair ? g * pl.n_pairs + tile / 2 : g;
   const int pre_cost = pair ? kPairCost : kSingleCost;
   const int pre_p0 = (pair ? 0 : line.pair_end) + kPieceCost + seg * seg_points(pl.prefix_tiles, pre_cost);
   int c0 = 0, n_pre = 0;  // first CTA (pair) or worker (single) of the prefix pieces, and how many to look at
@@ -1015,11 +1048,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
           at = pl.o0 + l_at * D;
           l_at += pl.l0;
         } else if (pair) {
-          l_at = (static_cast<long long>(w) + seg) * (2 * BM) + row % (2 * BM);
+          l_at = ((static_cast<long long>(w) + seg) * 2 + (tile & 1)) * pl.rows + row;
           at = pl.o2 + l_at * D;
           l_at += pl.l2;
         } else {
-          l_at = (static_cast<long long>(w) + seg) * pl.rows1 + row - pl.n_pairs * 2 * BM;
+          l_at = (static_cast<long long>(w) + seg) * pl.rows + row;
           at = pl.o1 + l_at * D;
           l_at += pl.l1;
         }
@@ -1068,24 +1101,25 @@ constexpr int kMaxCtas = 160;
 PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
   PagedTcPlan p{};
   const int G = a.n_h / a.n_kv;
-  const long long rows = a.prefix_len > 0 ? static_cast<long long>(a.B) * G : 0;
-  const int row_tiles = static_cast<int>((rows + BM - 1) / BM);
   p.ctas = ctas;
+  p.row_reqs = BM / G;
+  p.rows = p.row_reqs * G;
+  const int row_tiles = a.prefix_len > 0 ? (a.B + p.row_reqs - 1) / p.row_reqs : 0;
   p.n_pairs = row_tiles / 2;
   p.odd = row_tiles & 1;
-  p.rows1 = p.odd ? static_cast<int>(rows - static_cast<long long>(p.n_pairs) * 2 * BM) : 0;
   p.prefix_tiles = static_cast<int>((static_cast<long long>(a.prefix_len) + BN - 1) / BN);
   const long long pieces2 = p.n_pairs ? kMaxCtas + static_cast<long long>(p.n_pairs) * a.n_kv : 0;
   const long long pieces1 = p.odd ? 2 * kMaxCtas + static_cast<long long>(a.n_kv) : 0;
   const long long pieces0 = 2 * kMaxCtas + static_cast<long long>(a.B) * a.n_kv;
   p.o2 = 0;
-  p.o1 = p.o2 + pieces2 * 2 * BM * a.D_v;
-  p.o0 = p.o1 + pieces1 * p.rows1 * a.D_v;
+  p.o1 = p.o2 + pieces2 * 2 * p.rows * a.D_v;
+  p.o0 = p.o1 + pieces1 * p.rows * a.D_v;
   p.l2 = p.o0 + pieces0 * G * a.D_v;
-  p.l1 = p.l2 + pieces2 * 2 * BM;
-  p.l0 = p.l1 + pieces1 * p.rows1;
-  p.sums = (p.l0 + pieces0 * G + 3) & ~3LL;  // 16-byte aligned
-  p.end = p.sums + a.B + 1;
+  p.l1 = p.l2 + pieces2 * 2 * p.rows;
+  p.l0 = p.l1 + pieces1 * p.rows;
+  p.sums = p.l0 + pieces0 * G;
+  p.q = (p.sums + a.B + 1 + 31) & ~31LL;  // 128-byte aligned
+  p.end = p.q + static_cast<long long>(a.B) * a.n_h * (a.D_qk / 2);
   return p;
 }
 
@@ -1108,18 +1142,44 @@ cudaError_t prepare() {
   return cudaSuccess;
 }
 
+// Launches a kernel that may start before the one in front of it has ended.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, bool early,
+                         A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D>
 cudaError_t launch(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtensorMap* maps, const PagedTcPlan& pl,
                    cudaStream_t st, int* launches) {
   cudaError_t e = prepare<D>();
   if (e != cudaSuccess) return e;
-  paged_tc_kernel<D><<<pl.ctas, kThreads, Cfg<D>::kSmemBytes, st>>>(a, rope, pl, maps[0], maps[1]);
+  const bool rotate = rope.n_pairs > 0;
+  if (rotate) {
+    const long long items = static_cast<long long>(a.B) * a.n_h * (D / 16);
+    __nv_bfloat16* const q = reinterpret_cast<__nv_bfloat16*>(static_cast<float*>(a.workspace) + pl.q);
+    paged_rope_q_kernel<D><<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(a, rope, q);
+    *launches += 1;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  e = launch_early(paged_tc_kernel<D>, pl.ctas, kThreads, Cfg<D>::kSmemBytes, st, rotate, a, pl, maps[0], maps[1],
+                   maps[2], maps[3]);
+  if (e != cudaSuccess) return e;
   *launches += 1;
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long grid = (static_cast<long long>(a.B) * a.n_h + kCombineWarps - 1) / kCombineWarps;
-  paged_tc_combine_kernel<D><<<static_cast<unsigned>(grid), kCombineWarps * 32, 0, st>>>(a, pl);
+  const unsigned grid = (static_cast<unsigned>(a.B) * a.n_h + kCombineWarps - 1) / kCombineWarps;
+  e = launch_early(paged_tc_combine_kernel<D>, grid, kCombineWarps * 32, 0, st, true, a, pl);
   *launches += 1;
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
@@ -1143,8 +1203,8 @@ size_t decode_paged_tc_workspace(const PagedDecodeArgs& a) {
   return static_cast<size_t>(make_plan(a, kMaxCtas).end) * sizeof(float);
 }
 
-cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtensorMap* maps,
-                                   int num_sms, cudaStream_t st, int* launches) {
+cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st,
+                                   int* launches) {
   // no more CTAs than the call can have tiles
   const long long own = ((static_cast<long long>(a.max_blocks) << a.page_shift) - a.prefix_len + BN - 1) / BN;
   const PagedTcPlan p = make_plan(a, 1);
@@ -1153,6 +1213,18 @@ cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rop
   long long ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   if (most < ctas) ctas = most > 0 ? most : 1;
   const PagedTcPlan pl = make_plan(a, static_cast<int>(ctas));
+  // query rows by (dim, head of the group, KV head, request); K and V by (dim, KV head, row in page, page),
+  // a page per box (half of a 256-token page)
+  const void* q = rope.n_pairs > 0 ? static_cast<const float*>(a.workspace) + pl.q : a.q;
+  const unsigned long long hs = static_cast<unsigned long long>(a.D_qk) * 2, page = 1ull << a.page_shift;
+  const unsigned long long ks = hs * a.n_kv, vs = static_cast<unsigned long long>(a.v_token_stride) * 2;
+  const int G = a.n_h / a.n_kv, box_rows = page < 128 ? static_cast<int>(page) : 128;
+  CUtensorMap maps[4];
+  if (!make_map_rows(&maps[0], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, 1) ||
+      !make_map_rows(&maps[1], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, pl.row_reqs) ||
+      !make_map4(&maps[2], a.k_pages, a.D_qk, a.n_kv, static_cast<int>(page), a.n_pages, hs, ks, ks * page, box_rows) ||
+      !make_map4(&maps[3], a.v_pages, a.D_v, a.n_kv, static_cast<int>(page), a.n_pages, hs, vs, vs * page, box_rows))
+    return cudaErrorInvalidValue;
   return a.D_qk == 64 ? launch<64>(a, rope, maps, pl, st, launches) : launch<128>(a, rope, maps, pl, st, launches);
 }
 

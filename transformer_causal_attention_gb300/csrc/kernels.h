@@ -159,11 +159,11 @@ size_t decode_paged_workspace(const PagedDecodeArgs& a);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
                                 int* launches);
 // The same on the tensor cores (bf16, D_qk = D_v = 64 or 128, RoPE over the whole head or none, at
-// most 128 query heads per KV head); maps: K and V pages, boxes of min(page_size, 128) rows.
+// most 128 query heads per KV head).
 bool decode_paged_tc_supported(const PagedDecodeArgs& a, bool bf16, int rope_offset, int rope_dims, bool rope);
 size_t decode_paged_tc_workspace(const PagedDecodeArgs& a);
-cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtensorMap* maps,
-                                   int num_sms, cudaStream_t st, int* launches);
+cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st,
+                                   int* launches);
 int decode_plan_splits(int B, int n_h, int n_kv, int D_qk, int D_v, int max_len, int* chunk);
 cudaError_t launch_decode(const DecodeArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
                           int* launches);
