@@ -981,34 +981,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One warp per (request b, head h): its row's pieces are those of the CTAs (pair tiles) or workers
-// (single tiles) between the one that holds the segment's first tile and the one that holds its
-// last; a CTA or worker between them in whose part no tile starts wrote none.
-constexpr int kCombineWarps = 4;
+// One block per (request b, KV head g): the pieces of its G rows are those of the CTAs (pair tiles) or
+// workers (single tiles) between the one that holds the segment's first tile and the one that holds
+// its last; a CTA or worker between them in whose part no tile starts wrote none.  The block lists
+// them, one thread per candidate; then each thread takes four dims of one row over every n-th piece
+// (n such groups of threads, where a row set has few dims), eight pieces' loads at a time, with a
+// running maximum of their log-sum-exps, and the groups merge in shared memory.
+constexpr int kCombineThreads = 256;
+constexpr int kMaxPieces = 4 * 160;  // prefix and own pieces of a row: at most every worker's, twice
 
 template <int D>
-__global__ void __launch_bounds__(kCombineWarps * 32)
+__global__ void __launch_bounds__(kCombineThreads)
     paged_tc_combine_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ PagedTcPlan pl) {
-  const int lane = threadIdx.x & 31;
-  const unsigned bh = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);  // B * n_h < 2^31
-  const int b = static_cast<int>(bh / static_cast<unsigned>(a.n_h)), h = static_cast<int>(bh) - b * a.n_h;
+  __shared__ long long base[kMaxPieces];  // first row of each piece's partials of this request, -1: none
+  __shared__ float4 red_acc[kCombineThreads];
+  __shared__ float2 red_ml[kCombineThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
-  if (b >= a.B) return;  // whole warps only
-  const int G = a.n_h / a.n_kv, g = h / G, i = h % G;
-  const int L = paged_len(a, b);
-  __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(bh) * D;
-  if (L <= a.prefix_len) {  // an empty place of the batch
-    if (lane < D / 4) *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(0, 0);
-    if (a.lse != nullptr && lane == 0) a.lse[bh] = -INFINITY;
+  const int b = blockIdx.x / a.n_kv, g = blockIdx.x - b * a.n_kv;
+  const int G = a.n_h / a.n_kv;
+  const int items = G * (D / 4);  // (row, four dims)
+  const int n_thr = blockDim.x;
+  const long long out_row = static_cast<long long>(b) * a.n_h + g * G;
+  __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + out_row * D;
+  const int nt = own_tiles(a, b);
+  if (nt == 0) {  // an empty place of the batch
+    for (int it = threadIdx.x; it < items; it += n_thr)
+      *reinterpret_cast<uint2*>(out + 4 * it) = make_uint2(0, 0);
+    if (a.lse != nullptr)
+      for (int i = threadIdx.x; i < G; i += n_thr) a.lse[out_row + i] = -INFINITY;
     return;
   }
   const float* const ws = static_cast<const float*>(a.workspace);
   const int* const sums = reinterpret_cast<const int*>(ws + pl.sums);
   const int sum_b = sums[b];
   const Line line(pl, a.n_kv, sums[a.B]);
-  // the row's two segments, each from its first tile's point p0: the prefix (pair or single) and its own keys
-  const int tile = b / pl.row_reqs;                // row tile of the prefix,
-  const int row = (b - tile * pl.row_reqs) * G + i;  // and the row there
+  // the rows' two segments, each from its first tile's point p0: the prefix (pair or single) and their own keys
+  const int tile = b / pl.row_reqs;  // row tile of the prefix
   const bool pair = tile < 2 * pl.n_pairs;
   const int seg = pair ? g * pl.n_pairs + tile / 2 : g;
   const int pre_cost = pair ? kPairCost : kSingleCost;
@@ -1019,84 +1027,103 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     c0 = pair ? line.cta_of(pre_p0) : line.worker_of(pre_p0);
     n_pre = (pair ? line.cta_of(last) : line.worker_of(last)) - c0 + 1;
   }
-  const int nt = own_tiles(a, b);
   const int own_p0 = line.prefix_end + sum_b * a.n_kv + g * seg_points(nt, kSingleCost) + kPieceCost;
   const int w0 = line.worker_of(own_p0);
   const int n = n_pre + line.worker_of(own_p0 + (nt - 1) * kSingleCost) - w0 + 1;
-
-  float M = -INFINITY, den = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    // lane j looks at piece j0 + j: its place in the workspace and its log-sum-exp
-    long long at = -1, l_at = 0;
-    const int j = j0 + lane;
-    if (j < n) {
-      const bool pre = j < n_pre;
-      const int w = pre ? c0 + j : w0 + j - n_pre;
-      int lo, hi;
-      if (pre && pair) {
-        lo = line.cut(w);
-        hi = min(line.cut(w + 1), line.pair_end);
-      } else {
-        line.single_part(w >> 1, w & 1, &lo, &hi);
-      }
-      const int p0 = pre ? pre_p0 : own_p0;
-      const int cost = pre ? pre_cost : kSingleCost, tiles = pre ? pl.prefix_tiles : nt;
-      if (tile_at(lo, p0, cost, tiles) < tile_at(hi, p0, cost, tiles)) {
-        if (!pre) {
-          l_at = (static_cast<long long>(w) + static_cast<long long>(b) * a.n_kv + g) * G + i;
-          at = pl.o0 + l_at * D;
-          l_at += pl.l0;
-        } else if (pair) {
-          l_at = ((static_cast<long long>(w) + seg) * 2 + (tile & 1)) * pl.rows + row;
-          at = pl.o2 + l_at * D;
-          l_at += pl.l2;
-        } else {
-          l_at = (static_cast<long long>(w) + seg) * pl.rows + row;
-          at = pl.o1 + l_at * D;
-          l_at += pl.l1;
+  for (int j = threadIdx.x; j < n; j += n_thr) {
+    const bool pre = j < n_pre;
+    const int w = pre ? c0 + j : w0 + j - n_pre;
+    int lo, hi;
+    if (pre && pair) {
+      lo = line.cut(w);
+      hi = min(line.cut(w + 1), line.pair_end);
+    } else {
+      line.single_part(w >> 1, w & 1, &lo, &hi);
+    }
+    const int p0 = pre ? pre_p0 : own_p0, cost = pre ? pre_cost : kSingleCost, tiles = pre ? pl.prefix_tiles : nt;
+    long long row = -1;
+    if (tile_at(lo, p0, cost, tiles) < tile_at(hi, p0, cost, tiles)) {
+      row = static_cast<long long>(w) + (pre ? seg : static_cast<long long>(b) * a.n_kv + g);
+      if (!pre) row *= G;
+      else row = (pair ? row * 2 + (tile & 1) : row) * pl.rows + (b - tile * pl.row_reqs) * G;
+    }
+    base[j] = row;
+  }
+  __syncthreads();
+  const long long pre_o = pair ? pl.o2 : pl.o1, pre_l = pair ? pl.l2 : pl.l1;
+  const int groups = items < n_thr ? n_thr / items : 1;
+  for (int it0 = 0; it0 < items; it0 += n_thr) {
+    const int grp = groups > 1 ? threadIdx.x / items : 0;
+    const int it = groups > 1 ? threadIdx.x - grp * items : it0 + threadIdx.x;
+    const bool mine = grp < groups && it < items;
+    const int i = it / (D / 4), d = (it - i * (D / 4)) * 4;
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine) {
+      for (int j0 = grp; j0 < n; j0 += 8 * groups) {
+        float l[8];
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int j = j0 + k * groups;
+          const long long row = j < n ? base[j] : -1;
+          const bool pre = j < n_pre;
+          l[k] = -INFINITY;
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row >= 0) {
+            l[k] = ws[(pre ? pre_l : pl.l0) + row + i];
+            v[k] = *reinterpret_cast<const float4*>(ws + (pre ? pre_o : pl.o0) + (row + i) * D + d);
+          }
+        }
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, l[k]);
+        const float m_ref = m == -INFINITY ? 0.f : m;
+        const float alpha = exp2f(M - m_ref);
+        M = m;
+        den *= alpha;
+        acc.x *= alpha;
+        acc.y *= alpha;
+        acc.z *= alpha;
+        acc.w *= alpha;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float w = exp2f(l[k] - m_ref);
+          den += w;
+          acc.x = fmaf(w, v[k].x, acc.x);
+          acc.y = fmaf(w, v[k].y, acc.y);
+          acc.z = fmaf(w, v[k].z, acc.z);
+          acc.w = fmaf(w, v[k].w, acc.w);
         }
       }
     }
-    const float l = at >= 0 ? ws[l_at] : -INFINITY;
-    float m = l;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float m_new = fmaxf(M, m);
-    const float m_ref = m_new == -INFINITY ? 0.f : m_new;
-    const float alpha = exp2f(M - m_ref);
-    const float wl = at >= 0 ? exp2f(l - m_ref) : 0.f;
-    M = m_new;
-    den = den * alpha + wl;  // of this lane's pieces
-    acc.x *= alpha;
-    acc.y *= alpha;
-    acc.z *= alpha;
-    acc.w *= alpha;
-    const int nj = min(32, n - j0);
-#pragma unroll 8
-    for (int jj = 0; jj < nj; ++jj) {
-      const long long p = __shfl_sync(0xffffffffu, at, jj);
-      const float wj = __shfl_sync(0xffffffffu, wl, jj);
-      if (p >= 0 && lane < D / 4) {
-        const float4 v = *reinterpret_cast<const float4*>(ws + p + 4 * lane);
-        acc.x = fmaf(wj, v.x, acc.x);
-        acc.y = fmaf(wj, v.y, acc.y);
-        acc.z = fmaf(wj, v.z, acc.z);
-        acc.w = fmaf(wj, v.w, acc.w);
+    if (groups > 1) {
+      red_acc[threadIdx.x] = acc;
+      red_ml[threadIdx.x] = make_float2(M, den);
+      __syncthreads();
+      if (grp == 0) {
+        for (int k = 1; k < groups; ++k) {
+          const float2 ml = red_ml[k * items + it];
+          const float4 v = red_acc[k * items + it];
+          const float m = fmaxf(M, ml.x), m_ref = m == -INFINITY ? 0.f : m;
+          const float x = exp2f(M - m_ref), y = exp2f(ml.x - m_ref);
+          M = m;
+          den = den * x + ml.y * y;
+          acc = make_float4(acc.x * x + v.x * y, acc.y * x + v.y * y, acc.z * x + v.z * y, acc.w * x + v.w * y);
+        }
       }
     }
+    if (mine && grp == 0) {
+      const float inv = 1.f / den;
+      *reinterpret_cast<uint2*>(out + static_cast<long long>(i) * D + d) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (a.lse != nullptr && d == 0) a.lse[out_row + i] = (M + log2f(den)) * 0.69314718055994530942f;
+    }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  const float inv = 1.f / den;
-  if (lane < D / 4)
-    *reinterpret_cast<uint2*>(out + 4 * lane) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (a.lse != nullptr && lane == 0) a.lse[bh] = (M + log2f(den)) * 0.69314718055994530942f;
 }
 
 // CTAs at most: the workspace is sized for this many (a GB300 has 152 SMs).
-constexpr int kMaxCtas = 160;
+constexpr int kMaxCtas = kMaxPieces / 4;
 
 PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
   PagedTcPlan p{};
@@ -1176,8 +1203,10 @@ cudaError_t launch(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtenso
                    maps[2], maps[3]);
   if (e != cudaSuccess) return e;
   *launches += 1;
-  const unsigned grid = (static_cast<unsigned>(a.B) * a.n_h + kCombineWarps - 1) / kCombineWarps;
-  e = launch_early(paged_tc_combine_kernel<D>, grid, kCombineWarps * 32, 0, st, true, a, pl);
+  // rows behind a prefix have dozens of pieces, others one to three: a thread per item is enough for these
+  const int items = (a.n_h / a.n_kv * (D / 4) + 31) / 32 * 32;
+  const int threads = a.prefix_len > 0 || items > kCombineThreads ? kCombineThreads : items;
+  e = launch_early(paged_tc_combine_kernel<D>, static_cast<unsigned>(a.B) * a.n_kv, threads, 0, st, true, a, pl);
   *launches += 1;
   return e;
 }
