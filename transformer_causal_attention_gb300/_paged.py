@@ -29,6 +29,7 @@ SIGNATURES = [
 ]
 
 _LIB = None
+_NO_SIZE = ctypes.c_size_t(-1).value
 
 
 def _lib() -> ctypes.CDLL:
@@ -43,59 +44,59 @@ def _lib() -> ctypes.CDLL:
     return _LIB
 
 
-def _tensors(dtype, **tensors) -> torch.device:
-    """Check that the given tensors are contiguous CUDA tensors of one device (and, unless None, of dtype)."""
-    device = None
-    for name, t in tensors.items():
+# A small call's time is its host time, so the checks below are written out: no dicts, and no stream or
+# device objects where the call runs on the current stream of the current device.
+def _cuda(t, name: str, dtype, device):
+    """Check that t is a contiguous CUDA tensor (of dtype, on device, unless these are None); its device."""
+    if not t.is_cuda or not t.is_contiguous():
         _b._dev(t, name)
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the tensors before it on {device}")
-        device = t.device
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if device is None:
+        return t.device
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
     return device
 
 
-def _ints(device, **tensors) -> None:
-    for name, (t, shape) in tensors.items():
-        if _tensors(torch.int32, **{name: t}) != device:
-            raise ValueError(f"{name} must be on {device}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be int32 {list(shape)}, not {list(t.shape)}")
+def _ints(t, name: str, shape: tuple, device) -> None:
+    _cuda(t, name, torch.int32, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, not {list(t.shape)}")
 
 
-@contextlib.contextmanager
+_HERE = contextlib.nullcontext()
+
+
 def _on(device, stream):
-    """The tensors' device made current, with the call's stream current on it; yields the stream's handle."""
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+    """(context, stream handle): the tensors' device made current, with the call's stream current on it."""
+    if stream is None:
+        index = device.index
+        if index == torch.cuda.current_device():
+            return _HERE, torch._C._cuda_getCurrentRawStream(index)
+        return torch.cuda.device(device), torch._C._cuda_getCurrentRawStream(index)
+    if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
-    if stream is not None and stream.device != device:
+    if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if stream is None and device.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream().cuda_stream
-    elif stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream().cuda_stream
-    else:
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
-def _page_dims(k_pages, v_pages):
+def _page_dims(k_pages, v_pages, device):
     """(n_pages, page_size, n_kv, D_qk, D_v, v_token_stride) of a cache; v_pages contiguous, or a leading slice of
     k_pages' last dim (MLA: the values are the first D_v latent dims)."""
-    if k_pages.dim() != 4 or v_pages.dim() != 4 or v_pages.shape[:3] != k_pages.shape[:3]:
+    ks, vs = k_pages.shape, v_pages.shape
+    if len(ks) != 4 or len(vs) != 4 or vs[:3] != ks[:3]:
         raise ValueError("k_pages and v_pages must be [n_pages, page_size, n_kv, D] with the same first three sizes")
-    if v_pages.dtype != k_pages.dtype or v_pages.device != k_pages.device:
+    if v_pages.dtype is not k_pages.dtype or v_pages.device != device:
         raise TypeError("k_pages and v_pages must share a dtype and a device")
-    D_qk, D_v = k_pages.shape[3], v_pages.shape[3]
     if v_pages.is_contiguous():
         ldv = 0
-    elif v_pages.data_ptr() == k_pages.data_ptr() and v_pages.stride() == k_pages.stride() and D_v <= D_qk:
+    elif v_pages.data_ptr() == k_pages.data_ptr() and v_pages.stride() == k_pages.stride() and vs[3] <= ks[3]:
         ldv = v_pages.stride(1)
     else:
         raise ValueError("v_pages must be contiguous or a leading slice of k_pages' last dim")
-    return (*k_pages.shape[:3], D_qk, D_v, ldv)
+    return ks[0], ks[1], ks[2], ks[3], vs[3], ldv
 
 
 def page_plan(lens, n_new, block_table, free_pages, n_free, *, page_size: int, n_pages: int, max_tokens: int,
@@ -109,23 +110,29 @@ def page_plan(lens, n_new, block_table, free_pages, n_free, *, page_size: int, n
     not fit keep their length and get slots of -1.  The outputs may be passed in (for a
     captured step), but none may overlap an input.
     """
-    device = _tensors(torch.int32, lens=lens, n_new=n_new, block_table=block_table, free_pages=free_pages,
-                      n_free=n_free)
-    if lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("lens must be [B], block_table [B, max_blocks] and free_pages [n]")
+    device = _cuda(lens, "lens", torch.int32, None)
+    _cuda(block_table, "block_table", torch.int32, device)
+    _cuda(free_pages, "free_pages", torch.int32, device)
+    if block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("block_table must be [B, max_blocks] and free_pages [n]")
     B, max_blocks = block_table.shape
-    _ints(device, lens=(lens, (B,)), n_new=(n_new, (B,)), n_free=(n_free, (1,)))
-    with _on(device, stream) as st:
-        def given(t, n):
-            return torch.empty(n, dtype=torch.int32, device=device) if t is None else t
-        seqlens, cu_new, n_left = given(seqlens, B), given(cu_new, B + 1), given(n_left, 1)
-        slots, positions = given(slots, max_tokens), given(positions, max_tokens)
-        _ints(device, seqlens=(seqlens, (B,)), cu_new=(cu_new, (B + 1,)), slots=(slots, (max_tokens,)),
-              positions=(positions, (max_tokens,)), n_left=(n_left, (1,)))
+    _ints(lens, "lens", (B,), device)
+    _ints(n_new, "n_new", (B,), device)
+    _ints(n_free, "n_free", (1,), device)
+    context, st = _on(device, stream)
+    with context:
+        def given(t, name, n):
+            if t is None:
+                return torch.empty(n, dtype=torch.int32, device=device)
+            _ints(t, name, (n,), device)
+            return t
+        seqlens, cu_new = given(seqlens, "seqlens", B), given(cu_new, "cu_new", B + 1)
+        slots, positions = given(slots, "slots", max_tokens), given(positions, "positions", max_tokens)
+        n_left = given(n_left, "n_left", 1)
         rc = _lib().attn_page_plan(lens.data_ptr(), n_new.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
                                    n_free.data_ptr(), seqlens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-                                   positions.data_ptr(), n_left.data_ptr(), B, max_blocks, int(page_size),
-                                   int(n_pages), free_pages.numel(), int(max_tokens), st)
+                                   positions.data_ptr(), n_left.data_ptr(), B, max_blocks, page_size, n_pages,
+                                   free_pages.shape[0], max_tokens, st)
     _b._check(rc, "attn_page_plan")
     return seqlens, cu_new, slots, positions, n_left
 
@@ -139,25 +146,28 @@ def kv_append_paged(k_new, v_new, k_pages, v_pages, slots, positions=None, *, ro
     [n_pages, page_size, n_kv, D_qk], v_pages [n_pages, page_size, n_kv, D_v], slots int32
     [T] (outside the cache: skipped), positions int32 [T] (needed when rope_base > 0).
     """
-    device = _tensors(None, k_new=k_new, k_pages=k_pages)
-    n_pages, page_size, n_kv, D_qk, D_v, ldv = _page_dims(k_pages, v_pages)
+    device = _cuda(k_new, "k_new", None, None)
+    _cuda(k_pages, "k_pages", k_new.dtype, device)
+    n_pages, page_size, n_kv, D_qk, D_v, ldv = _page_dims(k_pages, v_pages, device)
     T = k_new.shape[0]
-    if tuple(k_new.shape) != (T, n_kv, D_qk) or k_new.dtype != k_pages.dtype:
-        raise ValueError(f"k_new must be {k_pages.dtype} [T, {n_kv}, {D_qk}]")
+    if k_new.shape != (T, n_kv, D_qk):
+        raise ValueError(f"k_new must be [T, {n_kv}, {D_qk}]")
     if v_new is not None:
-        if _tensors(k_new.dtype, v_new=v_new) != device or tuple(v_new.shape) != (T, n_kv, D_v):
-            raise ValueError(f"v_new must be [{T}, {n_kv}, {D_v}] on {device}")
-    _ints(device, slots=(slots, (T,)))
+        _cuda(v_new, "v_new", k_new.dtype, device)
+        if v_new.shape != (T, n_kv, D_v):
+            raise ValueError(f"v_new must be [{T}, {n_kv}, {D_v}]")
+    _ints(slots, "slots", (T,), device)
     if positions is not None:
-        _ints(device, positions=(positions, (T,)))
+        _ints(positions, "positions", (T,), device)
     if T == 0:
         return
     rope_dims = (D_qk - rope_offset) if rope_dims is None else rope_dims
     code = _b._dtype_code(k_new, pairing)
-    with _on(device, stream) as st:
+    context, st = _on(device, stream)
+    with context:
         rc = _lib().attn_kv_append_paged(k_new.data_ptr(), _b._ptr(v_new), k_pages.data_ptr(), v_pages.data_ptr(),
                                          ldv, slots.data_ptr(), _b._ptr(positions), T, n_kv, D_qk, D_v, n_pages,
-                                         page_size, float(rope_base), rope_offset, rope_dims, code, st)
+                                         page_size, rope_base, rope_offset, rope_dims, code, st)
     _b._check(rc, "attn_kv_append_paged")
 
 
@@ -166,56 +176,64 @@ def decode_paged_workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, 
     """Bytes of scratch of decode_paged (prefix_len = 0) or decode_shared."""
     n = _lib().attn_decode_paged_workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len,
                                                 _b.ATTN_BF16 if dtype == torch.bfloat16 else _b.ATTN_F32)
-    if n == ctypes.c_size_t(-1).value:
+    if n == _NO_SIZE:
         raise ValueError("invalid paged decode sizes")
     return n
 
 
 def _decode(q, k_pages, v_pages, prefix_pages, block_table, seqlens, rope_base, rope_offset, rope_dims, scale, out,
             lse, workspace, pairing, stream):
-    device = _tensors(None, q=q, k_pages=k_pages)
-    n_pages, page_size, n_kv, D_qk, D_v, ldv = _page_dims(k_pages, v_pages)
-    if q.dim() != 3 or q.shape[2] != D_qk or q.dtype != k_pages.dtype:
-        raise ValueError(f"q must be {k_pages.dtype} [B, n_h, {D_qk}]")
+    device = _cuda(q, "q", None, None)
+    _cuda(k_pages, "k_pages", q.dtype, device)
+    n_pages, page_size, n_kv, D_qk, D_v, ldv = _page_dims(k_pages, v_pages, device)
+    if q.dim() != 3 or q.shape[2] != D_qk:
+        raise ValueError(f"q must be [B, n_h, {D_qk}]")
     B, n_h, _ = q.shape
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     max_blocks = block_table.shape[1]
-    _ints(device, block_table=(block_table, (B, max_blocks)), seqlens=(seqlens, (B,)))
+    _ints(block_table, "block_table", (B, max_blocks), device)
+    _ints(seqlens, "seqlens", (B,), device)
     prefix_len = 0
     if prefix_pages is not None:
-        _ints(device, prefix_pages=(prefix_pages, (prefix_pages.numel(),)))
-        prefix_len = prefix_pages.numel() * page_size
+        _ints(prefix_pages, "prefix_pages", (prefix_pages.numel(),), device)
+        prefix_len = prefix_pages.shape[0] * page_size
     rope_dims = (D_qk - rope_offset) if rope_dims is None else rope_dims
     code = _b._dtype_code(q, pairing)
-    need = _lib().attn_decode_paged_workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len,
-                                                   code & 0xff)
-    with _on(device, stream) as st:
+    lib = _lib()
+    context, st = _on(device, stream)
+    with context:
         if out is None:
             out = torch.empty((B, n_h, D_v), dtype=q.dtype, device=device)
-        elif _tensors(q.dtype, out=out) != device or tuple(out.shape) != (B, n_h, D_v):
-            raise ValueError(f"out must be [{B}, {n_h}, {D_v}] on {device}")
+        else:
+            _cuda(out, "out", q.dtype, device)
+            if out.shape != (B, n_h, D_v):
+                raise ValueError(f"out must be [{B}, {n_h}, {D_v}]")
         if isinstance(lse, torch.Tensor):
-            if _tensors(torch.float32, lse=lse) != device or tuple(lse.shape) != (B, n_h):
-                raise ValueError(f"lse must be fp32 [{B}, {n_h}] on {device}")
+            _cuda(lse, "lse", torch.float32, device)
+            if lse.shape != (B, n_h):
+                raise ValueError(f"lse must be fp32 [{B}, {n_h}]")
             lse_t = lse
         else:
             lse_t = torch.empty((B, n_h), dtype=torch.float32, device=device) if lse else None
-        if workspace is None:  # invalid sizes: the call itself says what is wrong with them
-            workspace = torch.empty(16 if need == ctypes.c_size_t(-1).value else need, dtype=torch.uint8,
-                                    device=device)
-        elif _tensors(None, workspace=workspace) != device:
-            raise ValueError(f"workspace must be on {device}")
-        dims = (B, n_h, n_kv, D_qk, D_v, n_pages, page_size, max_blocks, float(rope_base), rope_offset, rope_dims,
-                float(scale), code, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
-        if prefix_pages is None:
-            rc = _lib().attn_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ldv,
-                                          block_table.data_ptr(), seqlens.data_ptr(), out.data_ptr(),
-                                          _b._ptr(lse_t), *dims)
+        if workspace is None:
+            need = lib.attn_decode_paged_workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len,
+                                                        code & 0xff)
+            # invalid sizes: the call itself says what is wrong with them
+            workspace = torch.empty(16 if need == _NO_SIZE else need, dtype=torch.uint8, device=device)
         else:
-            rc = _lib().attn_decode_shared(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ldv,
-                                           prefix_pages.data_ptr(), prefix_len, block_table.data_ptr(),
-                                           seqlens.data_ptr(), out.data_ptr(), _b._ptr(lse_t), *dims)
+            _cuda(workspace, "workspace", None, device)
+        if prefix_pages is None:
+            rc = lib.attn_decode_paged(
+                q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ldv, block_table.data_ptr(), seqlens.data_ptr(),
+                out.data_ptr(), _b._ptr(lse_t), B, n_h, n_kv, D_qk, D_v, n_pages, page_size, max_blocks, rope_base,
+                rope_offset, rope_dims, scale, code, workspace.data_ptr(), workspace.nbytes, st)
+        else:
+            rc = lib.attn_decode_shared(
+                q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ldv, prefix_pages.data_ptr(), prefix_len,
+                block_table.data_ptr(), seqlens.data_ptr(), out.data_ptr(), _b._ptr(lse_t), B, n_h, n_kv, D_qk, D_v,
+                n_pages, page_size, max_blocks, rope_base, rope_offset, rope_dims, scale, code, workspace.data_ptr(),
+                workspace.nbytes, st)
     _b._check(rc, "attn_decode_paged" if prefix_pages is None else "attn_decode_shared")
     return out, lse_t
 

@@ -130,7 +130,11 @@ bool parse_dtype(attn_dtype_t dtype, bool* bf16, bool* half) {
 }
 
 // theta_i = base^(-2i/dims) expressed in turns per position, split hi + lo.
+// The last table is kept per thread: its powers take microseconds, and a model's calls share one table.
 RopeFreq make_rope(float base, int dims, bool half) {
+  static thread_local RopeFreq last{};
+  static thread_local float last_base = 0.f;
+  if (base > 0.f && base == last_base && last.n_pairs == dims / 2 && last.half == (half ? 1 : 0)) return last;
   RopeFreq f;
   memset(&f, 0, sizeof(f));
   if (!(base > 0.f) || dims <= 0) return f;
@@ -142,6 +146,8 @@ RopeFreq make_rope(float base, int dims, bool half) {
     f.hi[i] = static_cast<float>(turns);
     f.lo[i] = static_cast<float>(turns - static_cast<double>(f.hi[i]));
   }
+  last = f;
+  last_base = base;
   return f;
 }
 

@@ -16,15 +16,18 @@
 // with 1024 pipe cycles per 64 KB tile (D = 128) against ~2800 cycles for which an SM
 // waits for those bytes at HBM speed, padding a request's rows to 128 costs nothing.
 //
-// Work split.  All tiles of the call lie on one line - first the pair tiles, KV head by
-// KV head, then the single ones (prefix tiles of an odd last row tile, then request
-// after request, KV head fastest).  A tile is a few points long (kPairCost, kSingleCost)
-// and each segment is led by kPieceCost points for what starting it costs; the line is
-// cut into equal parts, one per CTA (one persistent CTA per SM), and the single tiles of
-// a CTA's part once more, into halves for its two workers.  Cuts fall anywhere, also
-// inside a request: each (worker, segment) piece writes one normalised partial and its
-// log-sum-exp, and the combine kernel merges the pieces of a row.  So the SMs finish
-// together whatever the lengths are, without a counter in memory, and partials are few.
+// Work split.  The pair tiles lie on one line, KV head by KV head, and the single ones on
+// another: prefix tiles of an odd last row tile, then request after request, KV head
+// fastest.  A tile is a few points long and each segment is led by kPieceCost points for
+// what starting it costs; the first line is cut into equal parts, one per CTA (one
+// persistent CTA per SM), the second into twice as many, one per worker (a CTA has two).
+// A CTA does its pair tiles, then its workers their single ones.  (Cut as one line, so
+// that some CTAs got pairs and others single tiles, the shares hung on how well the costs
+// of the two were guessed: of 256 requests behind 16384 shared tokens the first CTA ended
+// after 80 us and the last after 137.)  Cuts fall anywhere, also inside a request: each
+// (worker, segment) piece writes one normalised partial and its log-sum-exp, and the
+// combine kernel merges the pieces of a row.  So the SMs finish together whatever the
+// lengths are, without a counter in memory, and partials are few.
 // Where a piece's partial goes needs no table either: walking the line, each step to
 // the next piece raises the worker's index or the segment's, so their sum numbers the
 // pieces.
@@ -73,8 +76,8 @@ constexpr int BM = 128;  // rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// Points on the line: a pair tile, a single tile, the start of a segment.
-constexpr int kPairCost = 14, kSingleCost = 8, kPieceCost = 8;
+// Points on the lines: a tile, the start of a segment.
+constexpr int kTileCost = 8, kPieceCost = 8;
 
 // Register split as in prefill_tc.cu: a softmax thread holds a row of 128 scores.
 constexpr int kLaunchRegs = 168;
@@ -138,51 +141,43 @@ static_assert(sizeof(Bars<64>) <= Cfg<64>::kBarBytes && sizeof(Bars<128>) <= Cfg
 
 // ------------------------------------------------------------------------------------- the line
 // Points are 32-bit: decode_paged_tc_supported bounds the line.
-// The first tile of a segment (n tiles of `cost` points each, its first one at point p0) that starts
-// at or behind point x.
-__device__ __forceinline__ int tile_at(int x, int p0, int cost, int n) {
+// The first tile of a segment (n tiles, the first one at point p0) that starts at or behind point x.
+__device__ __forceinline__ int tile_at(int x, int p0, int n) {
   const int d = x - p0;
-  return d <= 0 ? 0 : min(n, static_cast<int>((static_cast<unsigned>(d) + cost - 1) / static_cast<unsigned>(cost)));
+  return d <= 0 ? 0 : min(n, static_cast<int>((static_cast<unsigned>(d) + kTileCost - 1) / kTileCost));
 }
-__device__ __forceinline__ int seg_points(int tiles, int cost) { return tiles > 0 ? tiles * cost + kPieceCost : 0; }
+__device__ __forceinline__ int seg_points(int tiles) { return tiles > 0 ? tiles * kTileCost + kPieceCost : 0; }
 __device__ __forceinline__ int own_tiles(const PagedDecodeArgs& a, int b) {
   const int L = paged_len(a, b);
   return L > a.prefix_len ? static_cast<int>((static_cast<unsigned>(L - a.prefix_len) + BN - 1) / BN) : 0;
 }
 
-// The line and its cut, once the sum of the requests' own points (of one KV head) is known.
-struct Line {
-  int pair_end, prefix_end, total;  // [0, pair_end) pairs, [.., prefix_end) single prefix tiles, own tiles
-  int part, extra, ctas;            // points per CTA, one more for the first `extra` CTAs
-  __device__ __forceinline__ Line(const PagedTcPlan& p, int n_kv, int own) {
-    pair_end = p.n_pairs * n_kv * seg_points(p.prefix_tiles, kPairCost);
-    prefix_end = pair_end + p.odd * n_kv * seg_points(p.prefix_tiles, kSingleCost);
-    total = prefix_end + own * n_kv;
-    ctas = p.ctas;
-    part = static_cast<int>(static_cast<unsigned>(total) / static_cast<unsigned>(ctas));
-    extra = total - part * ctas;
+// [0, total) cut into n equal parts, the first `extra` of them one point longer.
+struct Cut {
+  int part, extra;
+  __device__ __forceinline__ Cut(int total, int n) {
+    part = static_cast<int>(static_cast<unsigned>(total) / static_cast<unsigned>(n));
+    extra = total - part * n;
   }
-  __device__ __forceinline__ int cut(int c) const { return part * c + min(c, extra); }
-  // The CTA whose part holds point x.
-  __device__ __forceinline__ int cta_of(int x) const {
-    const int wide = extra * (part + 1);  // the end of the parts that are one point longer
+  __device__ __forceinline__ int at(int k) const { return part * k + min(k, extra); }
+  __device__ __forceinline__ int holder(int x) const {  // the part that holds point x
+    const int wide = extra * (part + 1);                // the end of the longer parts
     const bool in_wide = x < wide;
-    const unsigned len = in_wide ? part + 1 : part;  // part > 0 behind `wide`
+    const unsigned len = in_wide ? part + 1 : part;     // part > 0 behind `wide`
     return (in_wide ? 0 : extra) + static_cast<int>(static_cast<unsigned>(in_wide ? x : x - wide) / len);
   }
-  // Worker w of CTA c takes the single tiles that start in [lo, hi).
-  __device__ __forceinline__ void single_part(int c, int w, int* lo, int* hi) const {
-    const int a = max(cut(c), pair_end), b = max(cut(c + 1), pair_end);
-    const int mid = a + (b - a + 1) / 2;
-    *lo = w ? mid : a;
-    *hi = w ? b : mid;
-  }
-  __device__ __forceinline__ int worker_of(int x) const {  // x >= pair_end
-    const int c = cta_of(x);
-    int lo, hi;
-    single_part(c, 1, &lo, &hi);
-    return 2 * c + (x >= lo ? 1 : 0);
-  }
+};
+
+// The two lines, once the sum of the requests' own points (of one KV head) is known: pair tiles on
+// [0, pair_end); single prefix tiles on [0, prefix_end), then own tiles.
+struct Lines {
+  int pair_end, prefix_end;
+  Cut pairs, singles;
+  __device__ __forceinline__ Lines(const PagedTcPlan& p, int n_kv, int own)
+      : pair_end(p.n_pairs * n_kv * seg_points(p.prefix_tiles)),
+        prefix_end(p.odd * n_kv * seg_points(p.prefix_tiles)),
+        pairs(pair_end, p.ctas),
+        singles(prefix_end + own * n_kv, 2 * p.ctas) {}
 };
 
 // Where a piece's query rows lie in its worker's Q tile: own pieces of at most 64 rows alternate
@@ -192,7 +187,7 @@ struct Line {
 // the piece before.
 constexpr int kHalfRows = 64;
 
-// A walk along one worker's part of the line: the next segment, its first point, its next tile, and
+// A walk along one worker's parts of the lines: the next segment, its first point, its next tile, and
 // where the part ends.  Pair pieces come first (in both workers' walks), then single prefix pieces,
 // then own ones.
 struct Walk {
@@ -205,13 +200,13 @@ struct Walk {
 __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const PagedTcPlan& pl, Walk& w) {
   Piece u;
   if (w.kind == kPair) {
-    const int t_end = tile_at(w.end, w.s0 + kPieceCost, kPairCost, pl.prefix_tiles);
+    const int t_end = tile_at(w.end, w.s0 + kPieceCost, pl.prefix_tiles);
     if (w.g < a.n_kv && w.t < t_end) {
       u = Piece{kPair, w.g, w.b, w.t, t_end, a.prefix_len, 0, 1};
       w.t = t_end;
       if (t_end == pl.prefix_tiles) {
         w.t = 0;
-        w.s0 += seg_points(pl.prefix_tiles, kPairCost);
+        w.s0 += seg_points(pl.prefix_tiles);
         if (++w.b == pl.n_pairs) {
           w.b = 0;
           ++w.g;
@@ -239,7 +234,7 @@ __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const Page
       continue;
     }
     const int nt = static_cast<int>((static_cast<unsigned>(keys) + BN - 1) / BN);
-    const int t_end = tile_at(w.end, w.s0 + kPieceCost, kSingleCost, nt);
+    const int t_end = tile_at(w.end, w.s0 + kPieceCost, nt);
     if (w.t >= t_end) {
       if (w.t < nt) return u;  // the part ends here
     } else {
@@ -253,7 +248,7 @@ __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const Page
     }
     if (w.t == nt) {
       w.t = 0;
-      w.s0 += seg_points(nt, kSingleCost);
+      w.s0 += seg_points(nt);
       if (++w.g == a.n_kv && w.kind == kOwn) {
         w.g = 0;
         ++w.b;
@@ -500,16 +495,16 @@ __global__ void __launch_bounds__(256) paged_rope_q_kernel(const __grid_constant
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float sn, cs;
-      rope_sincos(pos, f_hi[c * 8 + e], f_lo[c * 8 + e], &sn, &cs);
+      rope_sincos_fast(pos, f_hi[c * 8 + e], f_lo[c * 8 + e], &sn, &cs);
       rotate_pair(x0[e], x1[e], sn, cs);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float sn, cs;
-      rope_sincos(pos, f_hi[c * 4 + e], f_lo[c * 4 + e], &sn, &cs);
+      rope_sincos_fast(pos, f_hi[c * 4 + e], f_lo[c * 4 + e], &sn, &cs);
       rotate_pair(x0[2 * e], x0[2 * e + 1], sn, cs);
-      rope_sincos(pos, f_hi[D / 4 + c * 4 + e], f_lo[D / 4 + c * 4 + e], &sn, &cs);
+      rope_sincos_fast(pos, f_hi[D / 4 + c * 4 + e], f_lo[D / 4 + c * 4 + e], &sn, &cs);
       rotate_pair(x1[2 * e], x1[2 * e + 1], sn, cs);
     }
   }
@@ -751,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b_lo = min(a.B, lane * strip), b_hi = min(a.B, b_lo + strip);
         int mine = 0;
 #pragma unroll 4
-        for (int b = b_lo; b < b_hi; ++b) mine += seg_points(own_tiles(a, b), kSingleCost);
+        for (int b = b_lo; b < b_hi; ++b) mine += seg_points(own_tiles(a, b));
         int before = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -760,40 +755,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int own = __shfl_sync(0xffffffffu, before, 31);
         before -= mine;
-        const Line line(pl, a.n_kv, own);
+        const Lines lines(pl, a.n_kv, own);
         const int cta = blockIdx.x;
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
           Walk k;
-          int lo, hi;
-          line.single_part(cta, w, &lo, &hi);
+          const int lo = lines.singles.at(2 * cta + w), hi = lines.singles.at(2 * cta + w + 1);
           // where the single tiles begin
           k.rest_end = lo < hi ? hi : 0;  // an empty part: no tile starts before point 0
           k.rest_kind = kOwn;
           k.rest_g = k.rest_b = k.rest_t = 0;
-          k.rest_s0 = line.prefix_end;
-          if (lo < line.prefix_end) {
-            const int len = seg_points(pl.prefix_tiles, kSingleCost);
+          k.rest_s0 = lines.prefix_end;
+          if (lo < lines.prefix_end) {
+            const int len = seg_points(pl.prefix_tiles);
             k.rest_kind = kPrefix;
-            k.rest_g = (lo - line.pair_end) / len;
-            k.rest_s0 = line.pair_end + k.rest_g * len;
-            k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, kSingleCost, pl.prefix_tiles);
+            k.rest_g = lo / len;
+            k.rest_s0 = k.rest_g * len;
+            k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, pl.prefix_tiles);
           } else if (lo < hi) {
             // the lane whose requests hold the part's first point finds the tile there
-            const int x = lo - line.prefix_end;
+            const int x = lo - lines.prefix_end;
             const bool here = x >= before * a.n_kv && x < (before + mine) * a.n_kv;
             if (here) {
               int at = before;
               int b = b_lo;
-              int len = seg_points(own_tiles(a, b), kSingleCost);
+              int len = seg_points(own_tiles(a, b));
               while (x >= (at + len) * a.n_kv) {
                 at += len;
-                len = seg_points(own_tiles(a, ++b), kSingleCost);
+                len = seg_points(own_tiles(a, ++b));
               }
               k.rest_b = b;
               k.rest_g = (x - at * a.n_kv) / len;
-              k.rest_s0 = line.prefix_end + at * a.n_kv + k.rest_g * len;
-              k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, kSingleCost, own_tiles(a, b));
+              k.rest_s0 = lines.prefix_end + at * a.n_kv + k.rest_g * len;
+              k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, own_tiles(a, b));
             }
             const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
             k.rest_b = __shfl_sync(0xffffffffu, k.rest_b, src);
@@ -802,18 +796,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             k.rest_s0 = __shfl_sync(0xffffffffu, k.rest_s0, src);
           }
           // and the pairs before them
-          const int x0 = line.cut(cta);
+          const int x0 = lines.pairs.at(cta);
           k.kind = kPair;
           k.g = k.b = k.t = 0;
           k.s0 = 0;
           k.end = 0;
           k.q_alt = -1;
-          if (x0 < line.pair_end) {
-            const int len = seg_points(pl.prefix_tiles, kPairCost);
+          if (x0 < lines.pair_end) {
+            const int len = seg_points(pl.prefix_tiles);
             const int seg = x0 / len;
-            k.end = min(line.cut(cta + 1), line.pair_end);
+            k.end = lines.pairs.at(cta + 1);
             k.s0 = seg * len;
-            k.t = tile_at(x0, k.s0 + kPieceCost, kPairCost, pl.prefix_tiles);
+            k.t = tile_at(x0, k.s0 + kPieceCost, pl.prefix_tiles);
             k.g = seg / pl.n_pairs;
             k.b = seg - k.g * pl.n_pairs;
             if (k.t == pl.prefix_tiles) {  // behind the segment's last tile
@@ -832,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int at = before;
           for (int b = b_lo; b < b_hi; ++b) {
             sums[b] = at;
-            at += seg_points(own_tiles(a, b), kSingleCost);
+            at += seg_points(own_tiles(a, b));
           }
           if (lane == 0) sums[a.B] = own;
         }
@@ -981,135 +975,148 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// One block per (request b, KV head g): the pieces of its G rows are those of the CTAs (pair tiles) or
-// workers (single tiles) between the one that holds the segment's first tile and the one that holds
-// its last; a CTA or worker between them in whose part no tile starts wrote none.  The block lists
-// them, one thread per candidate; then each thread takes four dims of one row over every n-th piece
-// (n such groups of threads, where a row set has few dims), eight pieces' loads at a time, with a
-// running maximum of their log-sum-exps, and the groups merge in shared memory.
+// The rows of one (request b, KV head g): their pieces are those of the CTAs (pair tiles) or workers
+// (single tiles) between the one that holds the segment's first tile and the one that holds its last;
+// a CTA or worker between them in whose part no tile starts wrote none.  T threads (a block; a
+// warp, where there are many row sets of one to three pieces) list the pieces, one thread per candidate; then each thread takes four dims of one row over every n-th piece (n such
+// groups of threads, where a row set has few dims), kBatch pieces' loads at a time, with a running
+// maximum of their log-sum-exps, and the groups merge in shared memory.
 constexpr int kCombineThreads = 256;
 constexpr int kMaxPieces = 4 * 160;  // prefix and own pieces of a row: at most every worker's, twice
 
-template <int D>
+template <int D, int T>
 __global__ void __launch_bounds__(kCombineThreads)
     paged_tc_combine_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ PagedTcPlan pl) {
-  __shared__ long long base[kMaxPieces];  // first row of each piece's partials of this request, -1: none
-  __shared__ float4 red_acc[kCombineThreads];
-  __shared__ float2 red_ml[kCombineThreads];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
-  const int b = blockIdx.x / a.n_kv, g = blockIdx.x - b * a.n_kv;
-  const int G = a.n_h / a.n_kv;
-  const int items = G * (D / 4);  // (row, four dims)
-  const int n_thr = blockDim.x;
-  const long long out_row = static_cast<long long>(b) * a.n_h + g * G;
-  __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + out_row * D;
+  constexpr bool kBlock = T == kCombineThreads;
+  constexpr int kBatch = kBlock ? 8 : 4;
+  constexpr int kList = kBlock ? kMaxPieces : 32;  // a warp lists 32 pieces at a time
+  __shared__ long long list[kCombineThreads / T][kList];  // first row of each piece's partials of this request, -1: none
+  __shared__ float4 red_acc[kBlock ? kCombineThreads : 1];
+  __shared__ float2 red_ml[kBlock ? kCombineThreads : 1];
+  const int tid = kBlock ? threadIdx.x : threadIdx.x & (T - 1);
+  const unsigned bg = kBlock ? blockIdx.x : blockIdx.x * (kCombineThreads / T) + threadIdx.x / T;
+  const int b = static_cast<int>(bg / static_cast<unsigned>(a.n_kv)), g = static_cast<int>(bg) - b * a.n_kv;
+  long long* const base = list[kBlock ? 0 : threadIdx.x / T];
+  auto sync = [] { if constexpr (kBlock) __syncthreads(); else __syncwarp(); };
+  if (b >= a.B) return;  // whole warps only
   const int nt = own_tiles(a, b);
-  if (nt == 0) {  // an empty place of the batch
-    for (int it = threadIdx.x; it < items; it += n_thr)
-      *reinterpret_cast<uint2*>(out + 4 * it) = make_uint2(0, 0);
-    if (a.lse != nullptr)
-      for (int i = threadIdx.x; i < G; i += n_thr) a.lse[out_row + i] = -INFINITY;
-    return;
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
   const float* const ws = static_cast<const float*>(a.workspace);
   const int* const sums = reinterpret_cast<const int*>(ws + pl.sums);
-  const int sum_b = sums[b];
-  const Line line(pl, a.n_kv, sums[a.B]);
-  // the rows' two segments, each from its first tile's point p0: the prefix (pair or single) and their own keys
+  const int sum_b = sums[b], sum_all = sums[a.B];
+  const int G = a.n_h / a.n_kv;
+  const int items = G * (D / 4);  // (row, four dims)
+  const long long out_row = static_cast<long long>(b) * a.n_h + g * G;
+  __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + out_row * D;
+  if (nt == 0) {  // an empty place of the batch
+    for (int it = tid; it < items; it += T) *reinterpret_cast<uint2*>(out + 4 * it) = make_uint2(0, 0);
+    if (a.lse != nullptr)
+      for (int i = tid; i < G; i += T) a.lse[out_row + i] = -INFINITY;
+    return;
+  }
+  const Lines lines(pl, a.n_kv, sum_all);
+  // the rows' two segments, each from its first tile's point: the prefix (pair or single) and their own keys;
+  // lanes 0 to 3 of each warp find who holds the first and the last tile of each
   const int tile = b / pl.row_reqs;  // row tile of the prefix
   const bool pair = tile < 2 * pl.n_pairs;
   const int seg = pair ? g * pl.n_pairs + tile / 2 : g;
-  const int pre_cost = pair ? kPairCost : kSingleCost;
-  const int pre_p0 = (pair ? 0 : line.pair_end) + kPieceCost + seg * seg_points(pl.prefix_tiles, pre_cost);
-  int c0 = 0, n_pre = 0;  // first CTA (pair) or worker (single) of the prefix pieces, and how many to look at
-  if (pl.prefix_tiles > 0) {
-    const int last = pre_p0 + (pl.prefix_tiles - 1) * pre_cost;
-    c0 = pair ? line.cta_of(pre_p0) : line.worker_of(pre_p0);
-    n_pre = (pair ? line.cta_of(last) : line.worker_of(last)) - c0 + 1;
+  const int pre_p0 = kPieceCost + seg * seg_points(pl.prefix_tiles);
+  const int own_p0 = lines.prefix_end + sum_b * a.n_kv + g * seg_points(nt) + kPieceCost;
+  int held;
+  {
+    const int lane = threadIdx.x & 31;
+    const bool own = lane & 2;
+    const int x = (own ? own_p0 : pre_p0) + ((lane & 1) ? ((own ? nt : pl.prefix_tiles) - 1) * kTileCost : 0);
+    const Cut& c = pair && !own ? lines.pairs : lines.singles;
+    held = pl.prefix_tiles > 0 || own ? c.holder(x) : 0;
   }
-  const int own_p0 = line.prefix_end + sum_b * a.n_kv + g * seg_points(nt, kSingleCost) + kPieceCost;
-  const int w0 = line.worker_of(own_p0);
-  const int n = n_pre + line.worker_of(own_p0 + (nt - 1) * kSingleCost) - w0 + 1;
-  for (int j = threadIdx.x; j < n; j += n_thr) {
+  const int c0 = __shfl_sync(0xffffffffu, held, 0), w0 = __shfl_sync(0xffffffffu, held, 2);
+  const int n_pre = pl.prefix_tiles > 0 ? __shfl_sync(0xffffffffu, held, 1) - c0 + 1 : 0;
+  const int n = n_pre + __shfl_sync(0xffffffffu, held, 3) - w0 + 1;
+  auto find = [&](int j) -> long long {  // candidate j's rows
     const bool pre = j < n_pre;
     const int w = pre ? c0 + j : w0 + j - n_pre;
-    int lo, hi;
-    if (pre && pair) {
-      lo = line.cut(w);
-      hi = min(line.cut(w + 1), line.pair_end);
-    } else {
-      line.single_part(w >> 1, w & 1, &lo, &hi);
-    }
-    const int p0 = pre ? pre_p0 : own_p0, cost = pre ? pre_cost : kSingleCost, tiles = pre ? pl.prefix_tiles : nt;
-    long long row = -1;
-    if (tile_at(lo, p0, cost, tiles) < tile_at(hi, p0, cost, tiles)) {
-      row = static_cast<long long>(w) + (pre ? seg : static_cast<long long>(b) * a.n_kv + g);
-      if (!pre) row *= G;
-      else row = (pair ? row * 2 + (tile & 1) : row) * pl.rows + (b - tile * pl.row_reqs) * G;
-    }
-    base[j] = row;
+    const Cut& c = pair && pre ? lines.pairs : lines.singles;
+    const int p0 = pre ? pre_p0 : own_p0, tiles = pre ? pl.prefix_tiles : nt;
+    if (tile_at(c.at(w), p0, tiles) >= tile_at(c.at(w + 1), p0, tiles)) return -1;
+    if (!pre) return (w + static_cast<long long>(b) * a.n_kv + g) * G;
+    const long long slot = static_cast<long long>(w) + seg;
+    return (pair ? slot * 2 + (tile & 1) : slot) * pl.rows + (b - tile * pl.row_reqs) * G;
+  };
+  if constexpr (kBlock) {
+    for (int j = tid; j < n; j += T) base[j] = find(j);
+    sync();
   }
-  __syncthreads();
   const long long pre_o = pair ? pl.o2 : pl.o1, pre_l = pair ? pl.l2 : pl.l1;
-  const int groups = items < n_thr ? n_thr / items : 1;
-  for (int it0 = 0; it0 < items; it0 += n_thr) {
-    const int grp = groups > 1 ? threadIdx.x / items : 0;
-    const int it = groups > 1 ? threadIdx.x - grp * items : it0 + threadIdx.x;
+  const int groups = kBlock && items < T ? T / items : 1;
+  for (int it0 = 0; it0 < items; it0 += T) {
+    const int grp = groups > 1 ? tid / items : 0;
+    const int it = groups > 1 ? tid - grp * items : it0 + tid;
     const bool mine = grp < groups && it < items;
     const int i = it / (D / 4), d = (it - i * (D / 4)) * 4;
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mine) {
-      for (int j0 = grp; j0 < n; j0 += 8 * groups) {
-        float l[8];
-        float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = j0 + k * groups;
-          const long long row = j < n ? base[j] : -1;
-          const bool pre = j < n_pre;
-          l[k] = -INFINITY;
-          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (row >= 0) {
-            l[k] = ws[(pre ? pre_l : pl.l0) + row + i];
-            v[k] = *reinterpret_cast<const float4*>(ws + (pre ? pre_o : pl.o0) + (row + i) * D + d);
-          }
+    for (int n0 = 0; n0 < n; n0 += kList) {
+      if constexpr (!kBlock) {
+        if (it0 == 0 || n > kList) {
+          sync();
+          if (n0 + tid < n) base[tid] = find(n0 + tid);
+          sync();
         }
-        float m = M;
+      }
+      const int n1 = min(n - n0, kList);
+      if (mine) {
+#pragma unroll 1
+        for (int j0 = grp; j0 < n1; j0 += kBatch * groups) {
+          float l[kBatch];
+          float4 v[kBatch];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, l[k]);
-        const float m_ref = m == -INFINITY ? 0.f : m;
-        const float alpha = exp2f(M - m_ref);
-        M = m;
-        den *= alpha;
-        acc.x *= alpha;
-        acc.y *= alpha;
-        acc.z *= alpha;
-        acc.w *= alpha;
+          for (int k = 0; k < kBatch; ++k) {
+            const int j = j0 + k * groups;
+            const long long row = j < n1 ? base[j] : -1;
+            const bool pre = n0 + j < n_pre;
+            l[k] = -INFINITY;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row >= 0) {
+              l[k] = ws[(pre ? pre_l : pl.l0) + row + i];
+              v[k] = *reinterpret_cast<const float4*>(ws + (pre ? pre_o : pl.o0) + (row + i) * D + d);
+            }
+          }
+          float m = M;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float w = exp2f(l[k] - m_ref);
-          den += w;
-          acc.x = fmaf(w, v[k].x, acc.x);
-          acc.y = fmaf(w, v[k].y, acc.y);
-          acc.z = fmaf(w, v[k].z, acc.z);
-          acc.w = fmaf(w, v[k].w, acc.w);
+          for (int k = 0; k < kBatch; ++k) m = fmaxf(m, l[k]);
+          const float m_ref = m == -INFINITY ? 0.f : m;
+          const float alpha = exp2f(M - m_ref);
+          M = m;
+          den *= alpha;
+          acc = make_float4(acc.x * alpha, acc.y * alpha, acc.z * alpha, acc.w * alpha);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const float w = exp2f(l[k] - m_ref);
+            den += w;
+            acc.x = fmaf(w, v[k].x, acc.x);
+            acc.y = fmaf(w, v[k].y, acc.y);
+            acc.z = fmaf(w, v[k].z, acc.z);
+            acc.w = fmaf(w, v[k].w, acc.w);
+          }
         }
       }
     }
-    if (groups > 1) {
-      red_acc[threadIdx.x] = acc;
-      red_ml[threadIdx.x] = make_float2(M, den);
-      __syncthreads();
-      if (grp == 0) {
-        for (int k = 1; k < groups; ++k) {
-          const float2 ml = red_ml[k * items + it];
-          const float4 v = red_acc[k * items + it];
-          const float m = fmaxf(M, ml.x), m_ref = m == -INFINITY ? 0.f : m;
-          const float x = exp2f(M - m_ref), y = exp2f(ml.x - m_ref);
-          M = m;
-          den = den * x + ml.y * y;
-          acc = make_float4(acc.x * x + v.x * y, acc.y * x + v.y * y, acc.z * x + v.z * y, acc.w * x + v.w * y);
+    if constexpr (kBlock) {
+      if (groups > 1) {
+        red_acc[tid] = acc;
+        red_ml[tid] = make_float2(M, den);
+        __syncthreads();
+        if (grp == 0) {
+          for (int k = 1; k < groups; ++k) {
+            const float2 ml = red_ml[k * items + it];
+            const float4 v = red_acc[k * items + it];
+            const float m = fmaxf(M, ml.x), m_ref = m == -INFINITY ? 0.f : m;
+            const float x = exp2f(M - m_ref), y = exp2f(ml.x - m_ref);
+            M = m;
+            den = den * x + ml.y * y;
+            acc = make_float4(acc.x * x + v.x * y, acc.y * x + v.y * y, acc.z * x + v.z * y, acc.w * x + v.w * y);
+          }
         }
       }
     }
@@ -1203,10 +1210,13 @@ cudaError_t launch(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtenso
                    maps[2], maps[3]);
   if (e != cudaSuccess) return e;
   *launches += 1;
-  // rows behind a prefix have dozens of pieces, others one to three: a thread per item is enough for these
-  const int items = (a.n_h / a.n_kv * (D / 4) + 31) / 32 * 32;
-  const int threads = a.prefix_len > 0 || items > kCombineThreads ? kCombineThreads : items;
-  e = launch_early(paged_tc_combine_kernel<D>, static_cast<unsigned>(a.B) * a.n_kv, threads, 0, st, true, a, pl);
+  const unsigned teams = static_cast<unsigned>(a.B) * a.n_kv;
+  // a warp per row set once there are two waves of blocks' worth of them
+  if (a.prefix_len > 0 || teams < 2432)
+    e = launch_early(paged_tc_combine_kernel<D, kCombineThreads>, teams, kCombineThreads, 0, st, true, a, pl);
+  else
+    e = launch_early(paged_tc_combine_kernel<D, 32>, (teams + kCombineThreads / 32 - 1) / (kCombineThreads / 32),
+                     kCombineThreads, 0, st, true, a, pl);
   *launches += 1;
   return e;
 }
@@ -1222,9 +1232,8 @@ bool decode_paged_tc_supported(const PagedDecodeArgs& a, bool bf16, int rope_off
   const PagedTcPlan p = make_plan(a, 1);
   const long long own = ((static_cast<long long>(a.max_blocks) << a.page_shift) - a.prefix_len + BN - 1) / BN;
   const double points = static_cast<double>(a.n_kv) *
-                        ((static_cast<double>(p.n_pairs) * kPairCost + p.odd * kSingleCost) * p.prefix_tiles +
-                         (p.n_pairs + p.odd + static_cast<double>(a.B)) * kPieceCost +
-                         static_cast<double>(a.B) * own * kSingleCost);
+                        ((static_cast<double>(p.n_pairs) + p.odd) * (static_cast<double>(p.prefix_tiles) * kTileCost + kPieceCost) +
+                         static_cast<double>(a.B) * (static_cast<double>(own) * kTileCost + kPieceCost));
   return points < 2147483647.0;
 }
 

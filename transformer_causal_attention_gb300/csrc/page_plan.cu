@@ -143,9 +143,11 @@ __global__ void __launch_bounds__(1024) page_plan_kernel(PagePlanArgs a) {
 
 cudaError_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st, int* launches) {
   const size_t smem = 2 * sizeof(unsigned) * (static_cast<size_t>(a.B) + 1);
-  const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             2 * static_cast<int>(sizeof(unsigned)) * (kMaxPlanRequests + 1));
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {  // above the default: opt in
+    const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               2 * static_cast<int>(sizeof(unsigned)) * (kMaxPlanRequests + 1));
+    if (e != cudaSuccess) return e;
+  }
   const int threads = a.B <= 256 && a.max_tokens <= 1024 ? 256 : 1024;
   long long blocks = (static_cast<long long>(a.max_tokens) + 2 * threads - 1) / (2 * threads);
   if (a.max_tokens <= 1024) blocks = 1;
