@@ -343,6 +343,21 @@ __device__ __forceinline__ void rescale_o(uint32_t o_addr, float alpha) {
   }
 }
 
+// Among four lanes (lj = lane & 3): piece e of lane k becomes piece k of lane e.
+__device__ __forceinline__ void transpose_pieces(uint4* pc, int lj) {
+  const bool b1 = (lj & 2) != 0, b0 = (lj & 1) != 0;
+  const uint4 r0 = shfl_xor_u4(b1 ? pc[0] : pc[2], 2), r1 = shfl_xor_u4(b1 ? pc[1] : pc[3], 2);
+  pc[0] = b1 ? r0 : pc[0];
+  pc[1] = b1 ? r1 : pc[1];
+  pc[2] = b1 ? pc[2] : r0;
+  pc[3] = b1 ? pc[3] : r1;
+  const uint4 q0 = shfl_xor_u4(b0 ? pc[0] : pc[1], 1), q1 = shfl_xor_u4(b0 ? pc[2] : pc[3], 1);
+  pc[0] = b0 ? q0 : pc[0];
+  pc[1] = b0 ? pc[1] : q0;
+  pc[2] = b0 ? q1 : pc[2];
+  pc[3] = b0 ? pc[3] : q1;
+}
+
 // The scores of one tile (n real keys) in this thread's TMEM row become the weights P, written over
 // them as bf16: p = 2^(s * scale*log2e - m).  m moves only when the row maximum grew by more than the
 // threshold; O and l are then scaled by 2^(m_old - m_new), exactly (l and O share their reference).
@@ -668,8 +683,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pph = 0, oph = 0, fix_ph = 0;  // parities, one bit per worker (fix_ph: per stage)
         uint32_t pending = 0;                   // bit w: worker w's Q K is out, its P V not yet
         bool ok = cur.template take<Cursor<D>::kLane>(bars, wc) && oth.template take<Cursor<D>::kLane>(bars, wc);
+        auto issue_qk = [&](uint32_t w, uint32_t alt, int from, int to) {
+          const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + alt * (kHalfRows * 128)) >> 4);
+          const uint64_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+#pragma unroll
+          for (int kk = from; kk < to; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+          }
+        };
+        auto issue_pv = [&](uint32_t w, bool first) {
+          const uint64_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
+                   (!first || kk > 0) ? 1u : 0u);
+        };
         // one visit: P V of the worker's tile, then Q K of its next one
         while (ok && (cur.live() || oth.live())) {
+          if (cur.u.kind == kPair && cur.w == 0 && pending == 3u && cur.t > cur.u.t && cur.t + 2 < cur.u.t_end) {
+            // inside a pair piece, both workers at tile t: no piece begins or ends before t_end - 2, and the tiles
+            // are whole (only a segment's last one may not be).  What the next turn needs is waited for in front
+            // of this turn's last MMAs, so that the tensor pipe does not run dry.
+            if (!lane_wait(&bars->v_full[vr.st], vr.ph, wc) || !lane_wait(&bars->k_full[kr.st], kr.ph, wc)) break;
+            for (; cur.t + 2 < cur.u.t_end; ++cur.t) {
+              if (!(ok = lane_wait(&bars->p_full[0], pph & 1u, wc))) break;
+              pph ^= 1u;
+              tc_fence_after();
+              issue_pv(0, false);
+              issue_qk(0, 0, 0, D / 16);
+              mma_commit(&bars->s_full[0]);
+              if (!(ok = lane_wait(&bars->p_full[1], (pph >> 1) & 1u, wc))) break;
+              pph ^= 2u;
+              tc_fence_after();
+              issue_pv(1, false);
+              mma_commit(&bars->v_empty[vr.st]);
+              vr.next(C::kVStages);
+              issue_qk(1, 0, 0, D / 32);
+              Ring kn = kr;
+              kn.next(C::kKStages);
+              if (!(ok = lane_wait(&bars->v_full[vr.st], vr.ph, wc) && lane_wait(&bars->k_full[kn.st], kn.ph, wc))) break;
+              tc_fence_after();
+              issue_qk(1, 0, D / 32, D / 16);
+              mma_commit(&bars->s_full[1]);
+              mma_commit(&bars->k_empty[kr.st]);
+              kr = kn;
+            }
+            oth.t = cur.t;
+            if (!ok) break;
+          }
           if (cur.live()) {
             const uint32_t w = cur.w, bit = 1u << w;
             if (pending & bit) {
@@ -688,11 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 oph ^= bit;
               }
               tc_fence_after();
-              const uint64_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                mma_ts(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
-                       (!first || kk > 0) ? 1u : 0u);
+              issue_pv(w, first);
               if (last) mma_commit(&bars->o_done[w]);
               if (!pair || w == 1) {
                 mma_commit(&bars->v_empty[vr.st]);
@@ -710,13 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t n = cur.n - 1;
               if (cur.t == cur.u.t && !lane_wait(&bars->q_full[w][n & 1u], (n >> 1) & 1u, wc)) break;
               tc_fence_after();
-              const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + cur.u.q_alt * (kHalfRows * 128)) >> 4);
-              const uint64_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-                mma_ss(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
-              }
+              issue_qk(w, cur.u.q_alt, 0, D / 16);
               mma_commit(&bars->s_full[w]);
               if (cur.t + 1 == cur.u.t_end) mma_commit(&bars->q_free[w][n & 1u]);
               if (!pair || w == 1) {
@@ -739,7 +791,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ------------------------------------------------------------ the walk, and value rows behind a segment's end
-      Walk walk[2];
+      // lanes 0-15 walk for worker 0, lanes 16-31 for worker 1, each half all alike
+      const int me = lane >> 4;
+      Walk walk;
+      int own_sum, before_sum;
       {
         // lane i sums the points of requests [i s, (i + 1) s)
         const int strip = (a.B + 31) / 32;
@@ -757,95 +812,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         before -= mine;
         const Lines lines(pl, a.n_kv, own);
         const int cta = blockIdx.x;
+        const int lo = lines.singles.at(2 * cta + me), hi = lines.singles.at(2 * cta + me + 1);
+        // where the single tiles begin
+        walk.rest_end = lo < hi ? hi : 0;  // an empty part: no tile starts before point 0
+        walk.rest_kind = kOwn;
+        walk.rest_g = walk.rest_b = walk.rest_t = 0;
+        walk.rest_s0 = lines.prefix_end;
+        if (lo < lines.prefix_end) {
+          const int len = seg_points(pl.prefix_tiles);
+          walk.rest_kind = kPrefix;
+          walk.rest_g = lo / len;
+          walk.rest_s0 = walk.rest_g * len;
+          walk.rest_t = tile_at(lo, walk.rest_s0 + kPieceCost, pl.prefix_tiles);
+        }
+        // own tiles: the lane whose requests hold the part's first point finds the tile there (for each worker)
+        const bool own_start = lo < hi && lo >= lines.prefix_end;
+        const int first = own_start ? lo - lines.prefix_end : -1;
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
-          Walk k;
-          const int lo = lines.singles.at(2 * cta + w), hi = lines.singles.at(2 * cta + w + 1);
-          // where the single tiles begin
-          k.rest_end = lo < hi ? hi : 0;  // an empty part: no tile starts before point 0
-          k.rest_kind = kOwn;
-          k.rest_g = k.rest_b = k.rest_t = 0;
-          k.rest_s0 = lines.prefix_end;
-          if (lo < lines.prefix_end) {
-            const int len = seg_points(pl.prefix_tiles);
-            k.rest_kind = kPrefix;
-            k.rest_g = lo / len;
-            k.rest_s0 = k.rest_g * len;
-            k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, pl.prefix_tiles);
-          } else if (lo < hi) {
-            // the lane whose requests hold the part's first point finds the tile there
-            const int x = lo - lines.prefix_end;
-            const bool here = x >= before * a.n_kv && x < (before + mine) * a.n_kv;
-            if (here) {
-              int at = before;
-              int b = b_lo;
-              int len = seg_points(own_tiles(a, b));
-              while (x >= (at + len) * a.n_kv) {
-                at += len;
-                len = seg_points(own_tiles(a, ++b));
-              }
-              k.rest_b = b;
-              k.rest_g = (x - at * a.n_kv) / len;
-              k.rest_s0 = lines.prefix_end + at * a.n_kv + k.rest_g * len;
-              k.rest_t = tile_at(lo, k.rest_s0 + kPieceCost, own_tiles(a, b));
+          const int x = __shfl_sync(0xffffffffu, first, 16 * w);
+          int fb = 0, fat = 0;
+          const bool here = x >= before * a.n_kv && x < (before + mine) * a.n_kv;
+          if (here) {
+            int b = b_lo, at = before, len = seg_points(own_tiles(a, b));
+            while (x >= (at + len) * a.n_kv) {
+              at += len;
+              len = seg_points(own_tiles(a, ++b));
             }
-            const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-            k.rest_b = __shfl_sync(0xffffffffu, k.rest_b, src);
-            k.rest_g = __shfl_sync(0xffffffffu, k.rest_g, src);
-            k.rest_t = __shfl_sync(0xffffffffu, k.rest_t, src);
-            k.rest_s0 = __shfl_sync(0xffffffffu, k.rest_s0, src);
+            fb = b;
+            fat = at;
           }
-          // and the pairs before them
-          const int x0 = lines.pairs.at(cta);
-          k.kind = kPair;
-          k.g = k.b = k.t = 0;
-          k.s0 = 0;
-          k.end = 0;
-          k.q_alt = -1;
-          if (x0 < lines.pair_end) {
-            const int len = seg_points(pl.prefix_tiles);
-            const int seg = x0 / len;
-            k.end = lines.pairs.at(cta + 1);
-            k.s0 = seg * len;
-            k.t = tile_at(x0, k.s0 + kPieceCost, pl.prefix_tiles);
-            k.g = seg / pl.n_pairs;
-            k.b = seg - k.g * pl.n_pairs;
-            if (k.t == pl.prefix_tiles) {  // behind the segment's last tile
-              k.t = 0;
-              k.s0 += len;
-              if (++k.b == pl.n_pairs) {
-                k.b = 0;
-                ++k.g;
-              }
+          const int src = max(__ffs(__ballot_sync(0xffffffffu, here)) - 1, 0);
+          fb = __shfl_sync(0xffffffffu, fb, src);
+          fat = __shfl_sync(0xffffffffu, fat, src);
+          if (own_start && me == w) {
+            const int nt = own_tiles(a, fb), len = seg_points(nt);
+            walk.rest_b = fb;
+            walk.rest_g = (x - fat * a.n_kv) / len;
+            walk.rest_s0 = lines.prefix_end + fat * a.n_kv + walk.rest_g * len;
+            walk.rest_t = tile_at(lo, walk.rest_s0 + kPieceCost, nt);
+          }
+          __syncwarp();
+        }
+        // and the pairs before them
+        const int x0 = lines.pairs.at(cta);
+        walk.kind = kPair;
+        walk.g = walk.b = walk.t = 0;
+        walk.s0 = 0;
+        walk.end = 0;
+        walk.q_alt = -1;
+        if (x0 < lines.pair_end) {
+          const int len = seg_points(pl.prefix_tiles);
+          const int seg = x0 / len;
+          walk.end = lines.pairs.at(cta + 1);
+          walk.s0 = seg * len;
+          walk.t = tile_at(x0, walk.s0 + kPieceCost, pl.prefix_tiles);
+          walk.g = seg / pl.n_pairs;
+          walk.b = seg - walk.g * pl.n_pairs;
+          if (walk.t == pl.prefix_tiles) {  // behind the segment's last tile
+            walk.t = 0;
+            walk.s0 += len;
+            if (++walk.b == pl.n_pairs) {
+              walk.b = 0;
+              ++walk.g;
             }
           }
-          walk[w] = k;
         }
-        if (cta == 0) {
-          int* const sums = static_cast<int*>(a.workspace) + pl.sums;
-          int at = before;
-          for (int b = b_lo; b < b_hi; ++b) {
-            sums[b] = at;
-            at += seg_points(own_tiles(a, b));
-          }
-          if (lane == 0) sums[a.B] = own;
-        }
+        own_sum = own;
+        before_sum = before;
       }
-      uint32_t n_pub[2] = {0, 0}, n_end[2] = {C::kAhead, C::kAhead};  // pieces handed out; and to be, so far
+      uint32_t n_pub = 0, n_end = C::kAhead;  // pieces handed out by this half; and to be, so far
       Ring r;
-      bool ok = true, take_cur = true, take_oth = true;
+      bool ok = true, take_cur = true, take_oth = true, first_round = true;
       for (;;) {
-        // hand out pieces, kAhead in front of the one this warp is in
-        for (;;) {
-          const int w = n_pub[0] < n_end[0] ? 0 : 1;
-          if (n_pub[w] >= n_end[w]) break;
-          const Piece u = next_piece(a, pl, walk[w]);
-          if (lane == 0) {
-            bars->piece[w][n_pub[w] % C::kQueue] = u;
-            mbar_arrive(&bars->piece_full[w][n_pub[w] % C::kQueue]);
+        // hand out pieces, kAhead in front of the ones this warp is in
+        while (__any_sync(0xffffffffu, n_pub < n_end)) {
+          if (n_pub < n_end) {
+            const Piece u = next_piece(a, pl, walk);
+            if ((lane & 15) == 0) {
+              bars->piece[me][n_pub % C::kQueue] = u;
+              mbar_arrive(&bars->piece_full[me][n_pub % C::kQueue]);
+            }
+            ++n_pub;
+            if (u.kind == kNone) n_end = 0;  // the last one
           }
-          ++n_pub[w];
-          if (u.kind == kNone) n_end[w] = 0;  // the last one
+        }
+        if (first_round) {  // CTA 0 leaves the sums of points for the combine kernel
+          first_round = false;
+          if (blockIdx.x == 0) {
+            int* const sums = static_cast<int*>(a.workspace) + pl.sums;
+            const int strip = (a.B + 31) / 32;
+            for (int b = min(a.B, lane * strip), e = min(a.B, b + strip); b < e; ++b) {
+              sums[b] = before_sum;
+              before_sum += seg_points(own_tiles(a, b));
+            }
+            if (lane == 0) sums[a.B] = own_sum;
+          }
         }
         if (take_cur) ok = cur.template take<Cursor<D>::kWarp>(bars, wc);
         if (take_oth) ok = ok && oth.template take<Cursor<D>::kWarp>(bars, wc);
@@ -873,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (++cur.t == cur.u.t_end) {
             take_cur = true;
-            if (n_end[cur.w]) ++n_end[cur.w];
+            if (me == cur.w && n_end) ++n_end;
           }
         }
         // the finished piece's successor is taken before its worker's next turn
@@ -947,17 +1009,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         row += r;
         float* const po = ws + o_at + row * D;
         const float inv_l = l_run > 0.f ? 1.f / l_run : l_run;  // 0: every score is -inf; NaN stays
+        // four lanes exchange their rows' 16-byte pieces, so that a store writes 64 contiguous bytes of each
+        // of eight rows
+        const int lj = lane & 3;
+        float* const pg = po - static_cast<long long>(lj) * D + lj * 4;  // the group's first row, this lane's piece
+        const int left = n_rows - (r - lj);                             // rows of the group that exist
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t orow[32];
           tmem_ld32(o_addr + c * 32, orow);
           tmem_wait_ld();
-          if (r < n_rows) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(po + c * 32 + e) =
-                  make_float4(__uint_as_float(orow[e]) * inv_l, __uint_as_float(orow[e + 1]) * inv_l,
-                              __uint_as_float(orow[e + 2]) * inv_l, __uint_as_float(orow[e + 3]) * inv_l);
+          for (int h = 0; h < 2; ++h) {
+            uint4 pc[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* o4 = orow + 16 * h + 4 * e;
+              pc[e] = make_uint4(__float_as_uint(__uint_as_float(o4[0]) * inv_l), __float_as_uint(__uint_as_float(o4[1]) * inv_l),
+                                 __float_as_uint(__uint_as_float(o4[2]) * inv_l), __float_as_uint(__uint_as_float(o4[3]) * inv_l));
+            }
+            transpose_pieces(pc, lj);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < left) *reinterpret_cast<uint4*>(pg + k * D + c * 32 + h * 16) = pc[k];
           }
         }
         if (r < n_rows) ws[l_at + row] = m_run + log2f(l_run);
