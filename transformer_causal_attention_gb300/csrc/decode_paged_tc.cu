@@ -273,9 +273,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   const bool ok = lane_wait(bar, parity, w);
   return __all_sync(0xffffffffu, ok);
 }
-// In line, for the softmax warps (beside their tile loops the compiler finds no registers for a call).
+// In line, for the softmax warps (beside their tile loops the compiler finds no registers for a call),
+// and short: what they wait for comes from the other roles, whose waits keep the time and raise the
+// abort flag; the count only bounds the loop should none of them be left.
 __device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, const WaitCtl* w) {
-  const bool ok = mbar_wait(bar, parity, *w);
+  bool ok = false;
+#pragma unroll 1
+  for (uint32_t it = 0; it < (1u << 26) && !(ok = mbar_try_wait(bar, parity)) && !*w->abort_flag; ++it) {
+  }
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -1009,6 +1014,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         row += r;
         float* const po = ws + o_at + row * D;
         const float inv_l = l_run > 0.f ? 1.f / l_run : l_run;  // 0: every score is -inf; NaN stays
+        if (u.kind == kOwn) {  // mostly few rows: written row by row
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t orow[32];
+            tmem_ld32(o_addr + c * 32, orow);
+            tmem_wait_ld();
+            if (r < n_rows) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(po + c * 32 + e) =
+                    make_float4(__uint_as_float(orow[e]) * inv_l, __uint_as_float(orow[e + 1]) * inv_l,
+                                __uint_as_float(orow[e + 2]) * inv_l, __uint_as_float(orow[e + 3]) * inv_l);
+            }
+          }
+        } else {
         // four lanes exchange their rows' 16-byte pieces, so that a store writes 64 contiguous bytes of each
         // of eight rows
         const int lj = lane & 3;
@@ -1033,6 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k)
               if (k < left) *reinterpret_cast<uint4*>(pg + k * D + c * 32 + h * 16) = pc[k];
           }
+        }
         }
         if (r < n_rows) ws[l_at + row] = m_run + log2f(l_run);
         tc_fence_before();

@@ -133,8 +133,7 @@ struct PagedDecodeArgs {
 
 // Keys of request b; at most prefix_len (0 without a prefix) for an empty place of the batch.
 __device__ __forceinline__ int paged_len(const PagedDecodeArgs& a, int b) {
-  const long long cap = static_cast<long long>(a.max_blocks) << a.page_shift;
-  return static_cast<int>(min(static_cast<long long>(a.seqlens[b]), cap));
+  return min(a.seqlens[b], a.max_blocks << a.page_shift);  // the table's tokens fit 32 bits (checked by the caller)
 }
 
 // Each launcher returns the launch error (cudaSuccess when enqueued) and adds
