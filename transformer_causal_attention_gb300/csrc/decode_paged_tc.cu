@@ -1072,27 +1072,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The rows of one (request b, KV head g): their pieces are those of the CTAs (pair tiles) or workers
 // (single tiles) between the one that holds the segment's first tile and the one that holds its last;
-// a CTA or worker between them in whose part no tile starts wrote none.  T threads (a block; a
-// warp, where there are many row sets of one to three pieces) list the pieces, one thread per candidate; then each thread takes four dims of one row over every n-th piece (n such
-// groups of threads, where a row set has few dims), kBatch pieces' loads at a time, with a running
-// maximum of their log-sum-exps, and the groups merge in shared memory.
-constexpr int kCombineThreads = 256;
-constexpr int kMaxPieces = 4 * 160;  // prefix and own pieces of a row: at most every worker's, twice
+// a CTA or worker between them in whose part no tile starts wrote none.  A warp lists 32 candidates at
+// a time, one per lane, then takes the pieces two by two: each lane four dims of up to four rows
+// (kItems), all loads of the two pieces in flight, with a running maximum of their log-sum-exps.
+// SPLIT: the eight warps of a block take every eighth candidate of one (b, g) each and merge in shared
+// memory, for few rows in many pieces; otherwise each warp has its own (b, g).
+constexpr int kCombineWarps = 8;
+constexpr int kItems = 4;
 
-template <int D, int T>
-__global__ void __launch_bounds__(kCombineThreads)
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kCombineWarps * 32)
     paged_tc_combine_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ PagedTcPlan pl) {
-  constexpr bool kBlock = T == kCombineThreads;
-  constexpr int kBatch = kBlock ? 8 : 4;
-  constexpr int kList = kBlock ? kMaxPieces : 32;  // a warp lists 32 pieces at a time
-  __shared__ long long list[kCombineThreads / T][kList];  // first row of each piece's partials of this request, -1: none
-  __shared__ float4 red_acc[kBlock ? kCombineThreads : 1];
-  __shared__ float2 red_ml[kBlock ? kCombineThreads : 1];
-  const int tid = kBlock ? threadIdx.x : threadIdx.x & (T - 1);
-  const unsigned bg = kBlock ? blockIdx.x : blockIdx.x * (kCombineThreads / T) + threadIdx.x / T;
+  constexpr int kChunk = 32 * kItems;  // items (row, four dims) per pass
+  __shared__ float4 red_acc[SPLIT ? kCombineWarps * kChunk : 1];
+  __shared__ float2 red_ml[SPLIT ? kCombineWarps * kChunk : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned bg = SPLIT ? blockIdx.x : blockIdx.x * kCombineWarps + warp;
   const int b = static_cast<int>(bg / static_cast<unsigned>(a.n_kv)), g = static_cast<int>(bg) - b * a.n_kv;
-  long long* const base = list[kBlock ? 0 : threadIdx.x / T];
-  auto sync = [] { if constexpr (kBlock) __syncthreads(); else __syncwarp(); };
   if (b >= a.B) return;  // whole warps only
   const int nt = own_tiles(a, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
@@ -1100,18 +1096,19 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int* const sums = reinterpret_cast<const int*>(ws + pl.sums);
   const int sum_b = sums[b], sum_all = sums[a.B];
   const int G = a.n_h / a.n_kv;
-  const int items = G * (D / 4);  // (row, four dims)
+  const int items = G * (D / 4);
   const long long out_row = static_cast<long long>(b) * a.n_h + g * G;
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + out_row * D;
   if (nt == 0) {  // an empty place of the batch
-    for (int it = tid; it < items; it += T) *reinterpret_cast<uint2*>(out + 4 * it) = make_uint2(0, 0);
+    const int first = SPLIT ? threadIdx.x : lane, step = SPLIT ? kCombineWarps * 32 : 32;
+    for (int it = first; it < items; it += step) *reinterpret_cast<uint2*>(out + 4 * it) = make_uint2(0, 0);
     if (a.lse != nullptr)
-      for (int i = tid; i < G; i += T) a.lse[out_row + i] = -INFINITY;
+      for (int i = first; i < G; i += step) a.lse[out_row + i] = -INFINITY;
     return;
   }
   const Lines lines(pl, a.n_kv, sum_all);
   // the rows' two segments, each from its first tile's point: the prefix (pair or single) and their own keys;
-  // lanes 0 to 3 of each warp find who holds the first and the last tile of each
+  // lanes 0 to 3 find who holds the first and the last tile of each
   const int tile = b / pl.row_reqs;  // row tile of the prefix
   const bool pair = tile < 2 * pl.n_pairs;
   const int seg = pair ? g * pl.n_pairs + tile / 2 : g;
@@ -1119,16 +1116,17 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int own_p0 = lines.prefix_end + sum_b * a.n_kv + g * seg_points(nt) + kPieceCost;
   int held;
   {
-    const int lane = threadIdx.x & 31;
     const bool own = lane & 2;
     const int x = (own ? own_p0 : pre_p0) + ((lane & 1) ? ((own ? nt : pl.prefix_tiles) - 1) * kTileCost : 0);
-    const Cut& c = pair && !own ? lines.pairs : lines.singles;
-    held = pl.prefix_tiles > 0 || own ? c.holder(x) : 0;
+    held = pl.prefix_tiles > 0 || own ? (pair && !own ? lines.pairs : lines.singles).holder(x) : 0;
   }
   const int c0 = __shfl_sync(0xffffffffu, held, 0), w0 = __shfl_sync(0xffffffffu, held, 2);
-  const int n_pre = pl.prefix_tiles > 0 ? __shfl_sync(0xffffffffu, held, 1) - c0 + 1 : 0;
-  const int n = n_pre + __shfl_sync(0xffffffffu, held, 3) - w0 + 1;
-  auto find = [&](int j) -> long long {  // candidate j's rows
+  const int c1 = __shfl_sync(0xffffffffu, held, 1), w1 = __shfl_sync(0xffffffffu, held, 3);
+  const int n_pre = pl.prefix_tiles > 0 ? c1 - c0 + 1 : 0;
+  const int n = n_pre + w1 - w0 + 1;
+  const long long pre_o = pair ? pl.o2 : pl.o1, pre_l = pair ? pl.l2 : pl.l1;
+  auto find = [&](int j) -> long long {  // the first row of candidate j's partials of this request, -1: none
+    if (j >= n) return -1;
     const bool pre = j < n_pre;
     const int w = pre ? c0 + j : w0 + j - n_pre;
     const Cut& c = pair && pre ? lines.pairs : lines.singles;
@@ -1138,94 +1136,101 @@ __global__ void __launch_bounds__(kCombineThreads)
     const long long slot = static_cast<long long>(w) + seg;
     return (pair ? slot * 2 + (tile & 1) : slot) * pl.rows + (b - tile * pl.row_reqs) * G;
   };
-  if constexpr (kBlock) {
-    for (int j = tid; j < n; j += T) base[j] = find(j);
-    sync();
-  }
-  const long long pre_o = pair ? pl.o2 : pl.o1, pre_l = pair ? pl.l2 : pl.l1;
-  const int groups = kBlock && items < T ? T / items : 1;
-  for (int it0 = 0; it0 < items; it0 += T) {
-    const int grp = groups > 1 ? tid / items : 0;
-    const int it = groups > 1 ? tid - grp * items : it0 + tid;
-    const bool mine = grp < groups && it < items;
-    const int i = it / (D / 4), d = (it - i * (D / 4)) * 4;
-    float M = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int n0 = 0; n0 < n; n0 += kList) {
-      if constexpr (!kBlock) {
-        if (it0 == 0 || n > kList) {
-          sync();
-          if (n0 + tid < n) base[tid] = find(n0 + tid);
-          sync();
-        }
-      }
-      const int n1 = min(n - n0, kList);
-      if (mine) {
-#pragma unroll 1
-        for (int j0 = grp; j0 < n1; j0 += kBatch * groups) {
-          float l[kBatch];
-          float4 v[kBatch];
+  constexpr int kStep = SPLIT ? kCombineWarps : 1;  // this warp's candidates: every kStep-th
+  for (int it0 = 0; it0 < items; it0 += kChunk) {
+    float M[kItems], den[kItems];
+    float4 acc[kItems];
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int j = j0 + k * groups;
-            const long long row = j < n1 ? base[j] : -1;
-            const bool pre = n0 + j < n_pre;
-            l[k] = -INFINITY;
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row >= 0) {
-              l[k] = ws[(pre ? pre_l : pl.l0) + row + i];
-              v[k] = *reinterpret_cast<const float4*>(ws + (pre ? pre_o : pl.o0) + (row + i) * D + d);
+    for (int k = 0; k < kItems; ++k) {
+      M[k] = -INFINITY;
+      den[k] = 0.f;
+      acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int j0 = SPLIT ? warp : 0; j0 < n; j0 += 32 * kStep) {
+      const int j = j0 + kStep * lane;
+      const long long mine = find(j);
+      uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
+      const uint32_t pre_mask = __ballot_sync(0xffffffffu, j < n_pre);
+#pragma unroll 1
+      while (left) {
+        float l[2][kItems];
+        float4 v[2][kItems];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const bool any = left != 0;
+          const int from = any ? __ffs(left) - 1 : 0;
+          left &= left - 1;
+          const long long row = __shfl_sync(0xffffffffu, mine, from);
+          const bool pre = (pre_mask >> from) & 1u;
+          const float* const o = ws + (pre ? pre_o : pl.o0) + row * D + 4 * it0;
+          const float* const ll = ws + (pre ? pre_l : pl.l0) + row;
+#pragma unroll
+          for (int k = 0; k < kItems; ++k) {
+            const int it = it0 + 32 * k + lane;
+            l[q][k] = -INFINITY;
+            v[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (any && it < items) {
+              l[q][k] = ll[it / (D / 4)];
+              v[q][k] = *reinterpret_cast<const float4*>(o + 4 * (32 * k + lane));
             }
           }
-          float m = M;
+        }
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) m = fmaxf(m, l[k]);
+        for (int k = 0; k < kItems; ++k) {
+          const float m = fmax3(M[k], l[0][k], l[1][k]);
           const float m_ref = m == -INFINITY ? 0.f : m;
-          const float alpha = exp2f(M - m_ref);
-          M = m;
-          den *= alpha;
-          acc = make_float4(acc.x * alpha, acc.y * alpha, acc.z * alpha, acc.w * alpha);
+          const float x = exp2f(M[k] - m_ref), y = exp2f(l[0][k] - m_ref), z = exp2f(l[1][k] - m_ref);
+          M[k] = m;
+          den[k] = fmaf(den[k], x, y + z);
+          acc[k].x = fmaf(z, v[1][k].x, fmaf(y, v[0][k].x, acc[k].x * x));
+          acc[k].y = fmaf(z, v[1][k].y, fmaf(y, v[0][k].y, acc[k].y * x));
+          acc[k].z = fmaf(z, v[1][k].z, fmaf(y, v[0][k].z, acc[k].z * x));
+          acc[k].w = fmaf(z, v[1][k].w, fmaf(y, v[0][k].w, acc[k].w * x));
+        }
+      }
+    }
+    if constexpr (SPLIT) {
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const float w = exp2f(l[k] - m_ref);
-            den += w;
-            acc.x = fmaf(w, v[k].x, acc.x);
-            acc.y = fmaf(w, v[k].y, acc.y);
-            acc.z = fmaf(w, v[k].z, acc.z);
-            acc.w = fmaf(w, v[k].w, acc.w);
-          }
+      for (int k = 0; k < kItems; ++k) {
+        red_acc[warp * kChunk + 32 * k + lane] = acc[k];
+        red_ml[warp * kChunk + 32 * k + lane] = make_float2(M[k], den[k]);
+      }
+      __syncthreads();
+      if (threadIdx.x < kChunk) {  // thread t merges item t
+        M[0] = -INFINITY;
+        den[0] = 0.f;
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < kCombineWarps; ++q) M[0] = fmaxf(M[0], red_ml[q * kChunk + threadIdx.x].x);
+        const float m_ref = M[0] == -INFINITY ? 0.f : M[0];
+#pragma unroll
+        for (int q = 0; q < kCombineWarps; ++q) {
+          const float2 ml = red_ml[q * kChunk + threadIdx.x];
+          const float4 v = red_acc[q * kChunk + threadIdx.x];
+          const float x = exp2f(ml.x - m_ref);
+          den[0] = fmaf(ml.y, x, den[0]);
+          acc[0] = make_float4(fmaf(v.x, x, acc[0].x), fmaf(v.y, x, acc[0].y), fmaf(v.z, x, acc[0].z),
+                               fmaf(v.w, x, acc[0].w));
         }
       }
+      if (it0 + kChunk < items) __syncthreads();  // the next pass writes there again
     }
-    if constexpr (kBlock) {
-      if (groups > 1) {
-        red_acc[tid] = acc;
-        red_ml[tid] = make_float2(M, den);
-        __syncthreads();
-        if (grp == 0) {
-          for (int k = 1; k < groups; ++k) {
-            const float2 ml = red_ml[k * items + it];
-            const float4 v = red_acc[k * items + it];
-            const float m = fmaxf(M, ml.x), m_ref = m == -INFINITY ? 0.f : m;
-            const float x = exp2f(M - m_ref), y = exp2f(ml.x - m_ref);
-            M = m;
-            den = den * x + ml.y * y;
-            acc = make_float4(acc.x * x + v.x * y, acc.y * x + v.y * y, acc.z * x + v.z * y, acc.w * x + v.w * y);
-          }
-        }
+#pragma unroll
+    for (int k = 0; k < (SPLIT ? 1 : kItems); ++k) {
+      const int it = it0 + (SPLIT ? static_cast<int>(threadIdx.x) : 32 * k + lane);
+      if (it < items && (!SPLIT || threadIdx.x < kChunk)) {
+        const float inv = 1.f / den[k];
+        *reinterpret_cast<uint2*>(out + 4LL * it) =
+            make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+        if (a.lse != nullptr && it % (D / 4) == 0)
+          a.lse[out_row + it / (D / 4)] = (M[k] + log2f(den[k])) * 0.69314718055994530942f;
       }
-    }
-    if (mine && grp == 0) {
-      const float inv = 1.f / den;
-      *reinterpret_cast<uint2*>(out + static_cast<long long>(i) * D + d) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (a.lse != nullptr && d == 0) a.lse[out_row + i] = (M + log2f(den)) * 0.69314718055994530942f;
     }
   }
 }
 
 // CTAs at most: the workspace is sized for this many (a GB300 has 152 SMs).
-constexpr int kMaxCtas = kMaxPieces / 4;
+constexpr int kMaxCtas = 160;
 
 PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
   PagedTcPlan p{};
@@ -1306,12 +1311,13 @@ cudaError_t launch(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtenso
   if (e != cudaSuccess) return e;
   *launches += 1;
   const unsigned teams = static_cast<unsigned>(a.B) * a.n_kv;
-  // a warp per row set once there are two waves of blocks' worth of them
-  if (a.prefix_len > 0 || teams < 2432)
-    e = launch_early(paged_tc_combine_kernel<D, kCombineThreads>, teams, kCombineThreads, 0, st, true, a, pl);
+  // a warp per (b, g) where their rows have one to three pieces (no prefix, and rows enough for the workers) or
+  // there are more of them than blocks that run at a time
+  if (teams < (a.prefix_len > 0 ? 1216u : 152u))
+    e = launch_early(paged_tc_combine_kernel<D, true>, teams, kCombineWarps * 32, 0, st, true, a, pl);
   else
-    e = launch_early(paged_tc_combine_kernel<D, 32>, (teams + kCombineThreads / 32 - 1) / (kCombineThreads / 32),
-                     kCombineThreads, 0, st, true, a, pl);
+    e = launch_early(paged_tc_combine_kernel<D, false>, (teams + kCombineWarps - 1) / kCombineWarps, kCombineWarps * 32,
+                     0, st, true, a, pl);
   *launches += 1;
   return e;
 }
