@@ -59,18 +59,21 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-static bool make_map_4d(CUtensorMap* map, const void* base, int D, int n1, int n2, int n3, unsigned long long s1,
-                        unsigned long long s2, unsigned long long s3, const int* box_dims) {
+// The general form: rows of D bf16 indexed (d, i1, i2, i3) with the given byte strides, boxes of 64 dims x
+// box1 x box2 x box3; L2 fetches promote_256 ? 256 : 128 bytes for a missing row piece.
+bool make_map_box(CUtensorMap* map, const void* base, int D, int n1, int n2, int n3, unsigned long long s1,
+                  unsigned long long s2, unsigned long long s3, int box1, int box2, int box3, bool promote_256) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2),
                               static_cast<cuuint64_t>(n3)};
   const cuuint64_t strides[3] = {s1, s2, s3};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_dims[0]), static_cast<cuuint32_t>(box_dims[1]),
-                             static_cast<cuuint32_t>(box_dims[2]), static_cast<cuuint32_t>(box_dims[3])};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2),
+                             static_cast<cuuint32_t>(box3)};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             promote_256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -80,15 +83,7 @@ static bool make_map_4d(CUtensorMap* map, const void* base, int D, int n1, int n
 // layout of the tensor cores), zero fill outside the tensor.
 bool make_map4(CUtensorMap* map, const void* base, int D, int heads, int rows, int B, unsigned long long head_stride,
                unsigned long long row_stride, unsigned long long batch_stride, int box_rows) {
-  const int box[4] = {64, 1, box_rows, 1};
-  return make_map_4d(map, base, D, heads, rows, B, head_stride, row_stride, batch_stride, box);
-}
-
-// The same over rows indexed (d, i, g, b): boxes of 64 dims x box_i x 1 x box_b, box_i * box_b rows.
-bool make_map_rows(CUtensorMap* map, const void* base, int D, int n_i, int n_g, int n_b, unsigned long long i_stride,
-                   unsigned long long g_stride, unsigned long long b_stride, int box_i, int box_b) {
-  const int box[4] = {64, box_i, 1, box_b};
-  return make_map_4d(map, base, D, n_i, n_g, n_b, i_stride, g_stride, b_stride, box);
+  return make_map_box(map, base, D, heads, rows, B, head_stride, row_stride, batch_stride, 1, box_rows, 1, true);
 }
 
 // 3-D tensor map over a bf16 tensor indexed (d, row, batch): boxes of 64 dims x

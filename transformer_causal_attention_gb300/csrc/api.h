@@ -24,9 +24,9 @@ int device_info(DeviceInfo* out);
 bool make_map4(CUtensorMap* map, const void* base, int D, int heads, int rows, int B, unsigned long long head_stride,
                unsigned long long row_stride, unsigned long long batch_stride, int box_rows);
 
-// 4-D tensor map over bf16 rows indexed (d, i, g, b): boxes of 64 dims x box_i x 1 x box_b; see api.cu.
-bool make_map_rows(CUtensorMap* map, const void* base, int D, int n_i, int n_g, int n_b, unsigned long long i_stride,
-                   unsigned long long g_stride, unsigned long long b_stride, int box_i, int box_b);
+// 4-D tensor map over bf16 rows indexed (d, i1, i2, i3), boxes of 64 dims x box1 x box2 x box3; see api.cu.
+bool make_map_box(CUtensorMap* map, const void* base, int D, int n1, int n2, int n3, unsigned long long s1,
+                  unsigned long long s2, unsigned long long s3, int box1, int box2, int box3, bool promote_256);
 
 // The dtype argument: element type in the low byte, ATTN_ROPE_HALF optionally OR'd in.
 bool parse_dtype(attn_dtype_t dtype, bool* bf16, bool* half);

@@ -1359,10 +1359,13 @@ cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rop
   const unsigned long long ks = hs * a.n_kv, vs = static_cast<unsigned long long>(a.v_token_stride) * 2;
   const int G = a.n_h / a.n_kv, box_rows = page < 128 ? static_cast<int>(page) : 128;
   CUtensorMap maps[4];
-  if (!make_map_rows(&maps[0], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, 1) ||
-      !make_map_rows(&maps[1], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, pl.row_reqs) ||
-      !make_map4(&maps[2], a.k_pages, a.D_qk, a.n_kv, static_cast<int>(page), a.n_pages, hs, ks, ks * page, box_rows) ||
-      !make_map4(&maps[3], a.v_pages, a.D_v, a.n_kv, static_cast<int>(page), a.n_pages, hs, vs, vs * page, box_rows))
+  // (a head's row of 64 dims is 128 bytes: fetched with its neighbour's, half of the traffic would be wasted)
+  const bool wide = a.D_qk == 128;
+  const int rows = static_cast<int>(page);
+  if (!make_map_box(&maps[0], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, 1, 1, wide) ||
+      !make_map_box(&maps[1], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, 1, pl.row_reqs, wide) ||
+      !make_map_box(&maps[2], a.k_pages, a.D_qk, a.n_kv, rows, a.n_pages, hs, ks, ks * page, 1, box_rows, 1, wide) ||
+      !make_map_box(&maps[3], a.v_pages, a.D_v, a.n_kv, rows, a.n_pages, hs, vs, vs * page, 1, box_rows, 1, wide))
     return cudaErrorInvalidValue;
   return a.D_qk == 64 ? launch<64>(a, rope, maps, pl, st, launches) : launch<128>(a, rope, maps, pl, st, launches);
 }
