@@ -1075,19 +1075,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // a CTA or worker between them in whose part no tile starts wrote none.  A warp lists 32 candidates at
 // a time, one per lane, then takes the pieces two by two: each lane four dims of up to four rows
 // (kItems), all loads of the two pieces in flight, with a running maximum of their log-sum-exps.
-// SPLIT: the eight warps of a block take every eighth candidate of one (b, g) each and merge in shared
-// memory, for few rows in many pieces; otherwise each warp has its own (b, g).
-constexpr int kCombineWarps = 8;
+// SPLIT: the warps of a block share the candidates of one (b, g) and merge in shared memory, for rows in
+// many pieces; otherwise each warp has its own (b, g).
 constexpr int kItems = 4;
 
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kCombineWarps * 32)
+template <int D, int WARPS, bool SPLIT>
+__global__ void __launch_bounds__(WARPS * 32)
     paged_tc_combine_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ PagedTcPlan pl) {
   constexpr int kChunk = 32 * kItems;  // items (row, four dims) per pass
-  __shared__ float4 red_acc[SPLIT ? kCombineWarps * kChunk : 1];
-  __shared__ float2 red_ml[SPLIT ? kCombineWarps * kChunk : 1];
+  __shared__ float4 red_acc[SPLIT ? WARPS * kChunk : 1];
+  __shared__ float2 red_ml[SPLIT ? WARPS * kChunk : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned bg = SPLIT ? blockIdx.x : blockIdx.x * kCombineWarps + warp;
+  const unsigned bg = SPLIT ? blockIdx.x : blockIdx.x * WARPS + warp;
   const int b = static_cast<int>(bg / static_cast<unsigned>(a.n_kv)), g = static_cast<int>(bg) - b * a.n_kv;
   if (b >= a.B) return;  // whole warps only
   const int nt = own_tiles(a, b);
@@ -1100,7 +1099,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const long long out_row = static_cast<long long>(b) * a.n_h + g * G;
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out) + out_row * D;
   if (nt == 0) {  // an empty place of the batch
-    const int first = SPLIT ? threadIdx.x : lane, step = SPLIT ? kCombineWarps * 32 : 32;
+    const int first = SPLIT ? threadIdx.x : lane, step = SPLIT ? WARPS * 32 : 32;
     for (int it = first; it < items; it += step) *reinterpret_cast<uint2*>(out + 4 * it) = make_uint2(0, 0);
     if (a.lse != nullptr)
       for (int i = first; i < G; i += step) a.lse[out_row + i] = -INFINITY;
@@ -1136,7 +1135,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     const long long slot = static_cast<long long>(w) + seg;
     return (pair ? slot * 2 + (tile & 1) : slot) * pl.rows + (b - tile * pl.row_reqs) * G;
   };
-  constexpr int kStep = SPLIT ? kCombineWarps : 1;  // this warp's candidates: every kStep-th
+  constexpr int kStep = SPLIT ? WARPS : 1;  // this warp's candidates: every kStep-th
   for (int it0 = 0; it0 < items; it0 += kChunk) {
     float M[kItems], den[kItems];
     float4 acc[kItems];
@@ -1201,10 +1200,10 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
         den[0] = 0.f;
         acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int q = 0; q < kCombineWarps; ++q) M[0] = fmaxf(M[0], red_ml[q * kChunk + threadIdx.x].x);
+        for (int q = 0; q < WARPS; ++q) M[0] = fmaxf(M[0], red_ml[q * kChunk + threadIdx.x].x);
         const float m_ref = M[0] == -INFINITY ? 0.f : M[0];
 #pragma unroll
-        for (int q = 0; q < kCombineWarps; ++q) {
+        for (int q = 0; q < WARPS; ++q) {
           const float2 ml = red_ml[q * kChunk + threadIdx.x];
           const float4 v = red_acc[q * kChunk + threadIdx.x];
           const float x = exp2f(ml.x - m_ref);
@@ -1311,13 +1310,17 @@ cudaError_t launch(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtenso
   if (e != cudaSuccess) return e;
   *launches += 1;
   const unsigned teams = static_cast<unsigned>(a.B) * a.n_kv;
-  // a warp per (b, g) where their rows have one to three pieces (no prefix, and rows enough for the workers) or
-  // there are more of them than blocks that run at a time
-  if (teams < (a.prefix_len > 0 ? 1216u : 152u))
-    e = launch_early(paged_tc_combine_kernel<D, true>, teams, kCombineWarps * 32, 0, st, true, a, pl);
+  // A warp per (b, g) where its rows have one to three pieces (no prefix, and rows enough for the workers) or
+  // there are more (b, g) than blocks that run at a time.  Behind a prefix they have dozens of pieces: eight
+  // warps while two such blocks per SM hold all, else four (64 requests behind 32768 tokens, 512 (b, g):
+  // 58.4 us with four, 60.3 with eight; 8 behind 4096, 64 (b, g): 17.9 and 16.4).
+  const bool split = teams < (a.prefix_len > 0 ? 1216u : 152u);
+  if (split && teams <= 304)
+    e = launch_early(paged_tc_combine_kernel<D, 8, true>, teams, 8 * 32, 0, st, true, a, pl);
+  else if (split)
+    e = launch_early(paged_tc_combine_kernel<D, 4, true>, teams, 4 * 32, 0, st, true, a, pl);
   else
-    e = launch_early(paged_tc_combine_kernel<D, false>, (teams + kCombineWarps - 1) / kCombineWarps, kCombineWarps * 32,
-                     0, st, true, a, pl);
+    e = launch_early(paged_tc_combine_kernel<D, 8, false>, (teams + 7) / 8, 8 * 32, 0, st, true, a, pl);
   *launches += 1;
   return e;
 }
