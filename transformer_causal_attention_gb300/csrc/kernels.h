@@ -94,6 +94,7 @@ struct KvAppendArgs {
   const int* slots;
   const int* positions;  // nullable without RoPE
   int n_slots;
+  int lanes;  // set by the launcher: lanes per token of the row form
 };
 
 // One step's page plan (attn_page_plan).
