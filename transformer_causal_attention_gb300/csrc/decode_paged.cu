@@ -18,8 +18,9 @@
 // throughout); the 16 half-warps merge in shared memory and the block writes one
 // normalised partial per row.  The chunk's page indices are staged in shared
 // memory, so that a key row costs no dependent load from the table.
-// This is the path of the shapes the tensor cores do not take; it is bound by HBM
-// (few rows) or the fp32 pipes (many rows behind a prefix).
+// Behind a prefix with 16 rows or more (and head dims up to 128) the shared part is a
+// matrix product for the fp32 pipes instead: see paged_prefix_tile_kernel.
+// This is the path of the shapes the tensor cores do not take.
 #include <math.h>
 
 #include "kernels.h"
@@ -32,9 +33,10 @@ constexpr int kHalfWarps = kThreads / 16;
 constexpr int kMinPageShift = 4;
 constexpr int kMaxChunk = 4096;
 
-// How the call is cut: chunk keys per block, slots of partials per row.
+// How the call is cut: keys per block (of the prefix, of a request's own), slots of partials per row.
 struct Plan {
-  int chunk, n_pre, n_own;  // n_pre chunks of the prefix, then n_own of a request's own keys
+  int pre_chunk, own_chunk;
+  int n_pre, n_own;  // n_pre chunks of the prefix, then n_own of a request's own keys
   __host__ __device__ int slots() const { return n_pre + n_own; }
 };
 
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a
   float* red_o = q_s + HG * NQC * 128;                 // [16][HG][NVC*128]
   float* red_m = red_o + kHalfWarps * HG * NVC * 128;  // [16][HG]
   float* red_l = red_m + kHalfWarps * HG;              // [16][HG]
-  __shared__ int pages[kMaxChunk >> kMinPageShift];
+  __shared__ int pages[(kMaxChunk >> kMinPageShift) + 1];
 
   const int G = a.n_h / a.n_kv;
   const int n_rows = PREFIX ? a.B * G : G;  // rows of a KV head that see these keys
@@ -82,12 +84,13 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a
   const int split = static_cast<int>(PREFIX ? u : u / a.B);
   // keys [start, end): of the prefix, or of request b0's own
   const int lo = PREFIX ? 0 : a.prefix_len, hi = PREFIX ? a.prefix_len : paged_len(a, b0);
-  const long long start_ll = lo + static_cast<long long>(split) * plan.chunk;
+  const int chunk = PREFIX ? plan.pre_chunk : plan.own_chunk;
+  const long long start_ll = lo + static_cast<long long>(split) * chunk;
   if (start_ll >= hi) return;  // nothing here: the combine pass never reads this partial
   const int start = static_cast<int>(start_ll);
-  const int end = static_cast<int>(min(static_cast<long long>(hi), start_ll + plan.chunk));
+  const int end = static_cast<int>(min(static_cast<long long>(hi), start_ll + chunk));
   const int* table = PREFIX ? a.prefix_pages : a.block_table + static_cast<long long>(b0) * a.max_blocks;
-  const int page0 = start >> a.page_shift;  // start is the first token of a page
+  const int page0 = start >> a.page_shift;
   for (int i = threadIdx.x; i < ((end - 1) >> a.page_shift) - page0 + 1; i += kThreads) pages[i] = table[page0 + i];
 
   auto row_b = [&](int i) { return PREFIX ? (r0 + i) / G : b0; };
@@ -266,6 +269,203 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a
   }
 }
 
+// The shared part for many rows: one block per (64 rows of a KV head, chunk of keys), 64 keys at a time
+// through shared memory.  S = Q K^T and O += P V are register tiles of 4 x 4 and 4 x (DM / 16) per
+// thread, fed by 16-byte loads of transposed tiles (Q^T and K^T by dim, P^T by key), with packed fp32
+// FMAs; a row's 16 threads sit in one half-warp, so its maximum takes four shuffles.  K and V take turns
+// in one buffer, which lets two blocks share an SM and cover each other's loads.  Bound by the fp32 FMA
+// pipes: a shuffle per 8 FMAs and a load of every key per 4 rows made the split kernel above 6 to 8
+// times slower here (8 against ~50 TFLOP/s).
+constexpr int kTile = 64;           // rows and keys
+constexpr int kPad = kTile + 4;     // row stride of the transposed tiles, in floats
+constexpr int kTileMinRows = 16;    // below, the split kernel's 4 rows per block waste less
+
+template <int DM> constexpr int prefix_tile_smem() {
+  constexpr int kv = DM * kPad > kTile * (DM + 4) ? DM * kPad : kTile * (DM + 4);
+  return (DM * kPad + kv + kTile * kPad) * static_cast<int>(sizeof(float));
+}
+
+template <typename T, int DM>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_prefix_tile_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ RopeFreq f, Plan plan) {
+  constexpr int VD = DM / 16;  // value dims per thread
+  extern __shared__ float smem[];
+  float* const q_t = smem;                                  // [DM][kPad]: rotated, scaled queries by dim
+  float* const kv = q_t + DM * kPad;                        // K^T [DM][kPad], then V [64][DM + 4]
+  float* const p_t = kv + (DM * kPad > kTile * (DM + 4) ? DM * kPad : kTile * (DM + 4));  // P^T [64 keys][kPad]
+  __shared__ int pages[(kMaxChunk >> kMinPageShift) + 1];
+
+  const int G = a.n_h / a.n_kv, n_rows = a.B * G;
+  const int n_rt = (n_rows + kTile - 1) / kTile;
+  const int rt = blockIdx.x % n_rt, g = blockIdx.x / n_rt % a.n_kv, split = blockIdx.x / n_rt / a.n_kv;
+  const int r0 = rt * kTile;
+  const int start = split * plan.pre_chunk, end = min(a.prefix_len, start + plan.pre_chunk);
+  const int page0 = start >> a.page_shift;
+  for (int i = threadIdx.x; i < ((end - 1) >> a.page_shift) - page0 + 1; i += kThreads) pages[i] = a.prefix_pages[page0 + i];
+
+  for (int idx = threadIdx.x; idx < kTile * (DM / 2); idx += kThreads) {
+    const int i = idx % kTile, p = idx / kTile;
+    const int j = p - a.rope_offset / 2;
+    const bool rot = j >= 0 && j < f.n_pairs;
+    int2 d = make_int2(2 * p, 2 * p + 1);
+    if (rot) {
+      d = rope_pair_dims(f, j);
+      d.x += a.rope_offset;
+      d.y += a.rope_offset;
+    }
+    float x0 = 0.f, x1 = 0.f;
+    if (2 * p < a.D_qk && r0 + i < n_rows) {
+      const int b = (r0 + i) / G, h = g * G + r0 + i - b * G;
+      const T* qr = static_cast<const T*>(a.q) + (static_cast<long long>(b) * a.n_h + h) * a.D_qk;
+      x0 = to_f32(qr[d.x]);
+      x1 = to_f32(qr[d.y]);
+      if (rot) {
+        float s, c;
+        rope_sincos(max(paged_len(a, b), 1) - 1, f.hi[j], f.lo[j], &s, &c);
+        rotate_pair(x0, x1, s, c);
+      }
+    }
+    q_t[d.x * kPad + i] = x0 * a.scale_log2;
+    q_t[d.y * kPad + i] = x1 * a.scale_log2;
+  }
+
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // keys 4 tx .. and dims VD tx .. of rows 4 ty ..
+  float2 o[4][VD / 2];
+  float m_run[4], l_part[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m_run[i] = -INFINITY;
+    l_part[i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < VD / 2; ++e) o[i][e] = make_float2(0.f, 0.f);
+  }
+  const long long k_tok = static_cast<long long>(a.n_kv) * a.D_qk;
+  const T* const kb = static_cast<const T*>(a.k_pages) + static_cast<long long>(g) * a.D_qk;
+  const T* const vb = static_cast<const T*>(a.v_pages) + static_cast<long long>(g) * a.D_v;
+  const int row_mask = (1 << a.page_shift) - 1;
+  auto slot_of = [&](int key) -> long long {  // -1: behind the chunk, or in a page outside the cache (zeros)
+    if (key >= end) return -1;
+    const int page = pages[(key >> a.page_shift) - page0];
+    return page >= 0 && page < a.n_pages ? (static_cast<long long>(page) << a.page_shift) + (key & row_mask) : -1;
+  };
+
+  for (int k0 = start; k0 < end; k0 += kTile) {
+    __syncthreads();  // the tile before has been read (and, the first time, the pages and queries are there)
+#pragma unroll 2
+    for (int idx = threadIdx.x; idx < kTile * (DM / 8); idx += kThreads) {
+      const int key = idx % kTile, c = idx / kTile;
+      const long long slot = slot_of(k0 + key);
+      Raw8<T> raw;
+      if (slot >= 0 && c * 8 < a.D_qk) raw.load(kb + slot * k_tok + c * 8);
+      else raw.zero();
+      float x[8];
+      raw.unpack(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) kv[(c * 8 + e) * kPad + key] = x[e];
+    }
+    __syncthreads();
+    float2 s2[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s2[i][0] = s2[i][1] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int d = 0; d < DM; ++d) {
+      const float4 q4 = *reinterpret_cast<const float4*>(q_t + d * kPad + 4 * ty);
+      const float4 k4 = *reinterpret_cast<const float4*>(kv + d * kPad + 4 * tx);
+      const float2 ka = make_float2(k4.x, k4.y), kc = make_float2(k4.z, k4.w);
+      const float q[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 qq = make_float2(q[i], q[i]);
+        s2[i][0] = __ffma2_rn(qq, ka, s2[i][0]);
+        s2[i][1] = __ffma2_rn(qq, kc, s2[i][1]);
+      }
+    }
+    float p[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i][0] = s2[i][0].x;
+      p[i][1] = s2[i][0].y;
+      p[i][2] = s2[i][1].x;
+      p[i][3] = s2[i][1].y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k0 + 4 * tx + e >= end) p[i][e] = -INFINITY;
+      float mx = fmaxf(fmaxf(p[i][0], p[i][1]), fmaxf(p[i][2], p[i][3]));
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float m_new = fmaxf(m_run[i], mx);
+      const float m_ref = m_new == -INFINITY ? 0.f : m_new;  // every score so far is -inf: weights 0
+      const float alpha = fast_exp2(m_run[i] - m_ref);
+      m_run[i] = m_new;
+      l_part[i] *= alpha;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p[i][e] = fast_exp2(p[i][e] - m_ref);
+        l_part[i] += p[i][e];
+      }
+#pragma unroll
+      for (int e = 0; e < VD / 2; ++e) o[i][e] = make_float2(o[i][e].x * alpha, o[i][e].y * alpha);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float4*>(p_t + (4 * tx + e) * kPad + 4 * ty) = make_float4(p[0][e], p[1][e], p[2][e], p[3][e]);
+    __syncthreads();  // K^T has been read, P^T is whole
+#pragma unroll 2
+    for (int idx = threadIdx.x; idx < kTile * (DM / 8); idx += kThreads) {
+      const int key = idx / (DM / 8), c = idx % (DM / 8);
+      const long long slot = slot_of(k0 + key);
+      Raw8<T> raw;
+      if (slot >= 0 && c * 8 < a.D_v) raw.load(vb + slot * a.v_token_stride + c * 8);
+      else raw.zero();
+      float x[8];
+      raw.unpack(x);
+      float4* const dst = reinterpret_cast<float4*>(kv + key * (DM + 4) + c * 8);
+      dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+      dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int j = 0; j < kTile; ++j) {
+      const float4 p4 = *reinterpret_cast<const float4*>(p_t + j * kPad + 4 * ty);
+      const float pj[4] = {p4.x, p4.y, p4.z, p4.w};
+      float2 v[VD / 2];
+#pragma unroll
+      for (int e = 0; e < VD / 4; ++e) {
+        const float4 x = *reinterpret_cast<const float4*>(kv + j * (DM + 4) + VD * tx + 4 * e);
+        v[2 * e] = make_float2(x.x, x.y);
+        v[2 * e + 1] = make_float2(x.z, x.w);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 pp = make_float2(pj[i], pj[i]);
+#pragma unroll
+        for (int e = 0; e < VD / 2; ++e) o[i][e] = __ffma2_rn(pp, v[e], o[i][e]);
+      }
+    }
+  }
+
+  const int ns = plan.slots();
+  float* const ws_o = static_cast<float*>(a.workspace);
+  float* const ws_lse = ws_o + static_cast<long long>(a.B) * a.n_h * ns * a.D_v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float l = l_part[i];
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    const int r = r0 + 4 * ty + i;
+    if (r >= n_rows) continue;
+    const int b = r / G, h = g * G + r - b * G;
+    const long long slot = (static_cast<long long>(b) * a.n_h + h) * ns + split;
+    const float inv = l > 0.f ? 1.f / l : l;  // 0: every score is -inf, the weight is 0; NaN stays
+#pragma unroll
+    for (int e = 0; e < VD / 2; ++e) {
+      const int d = VD * tx + 2 * e;
+      if (d < a.D_v) *reinterpret_cast<float2*>(ws_o + slot * a.D_v + d) = make_float2(o[i][e].x * inv, o[i][e].y * inv);
+    }
+    if (tx == 0) ws_lse[slot] = m_run[i] + log2f(l);
+  }
+}
+
 // Four consecutive fp32 values stored as T.
 template <typename T>
 __device__ __forceinline__ void store4(T* p, float4 v) {
@@ -276,57 +476,98 @@ __device__ __forceinline__ void store4(T* p, float4 v) {
   }
 }
 
-// One warp per (request b, head h): the written partials are the prefix's n_pre chunks and the
-// first ceil((L - P) / chunk) of its own.  D_v <= 512, a multiple of 8: dims 4 lane + 128 c.
+// The written partials of a (request b, head h) are the prefix's n_pre chunks and the first
+// ceil((L - P) / own_chunk) of its own.  A warp per row takes them kBatch at a time, its lanes four dims
+// at 4 lane + 128 c (D_v <= 512, a multiple of 8); SPLIT: the eight warps of a block take every eighth
+// partial of one row each and merge in shared memory, for rows in many partials.
 constexpr int kCombineWarps = 8;
+constexpr int kBatch = 4;
 
-template <typename T>
+template <typename T, bool SPLIT>
 __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(PagedDecodeArgs a, Plan plan) {
-  const int lane = threadIdx.x & 31;
-  const long long bh = static_cast<long long>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
+  __shared__ float red_o[SPLIT ? kCombineWarps * 512 : 1];
+  __shared__ float red_m[kCombineWarps], red_l[kCombineWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long bh = SPLIT ? blockIdx.x : static_cast<long long>(blockIdx.x) * kCombineWarps + warp;
   if (bh >= static_cast<long long>(a.B) * a.n_h) return;  // whole warps only
   const int L = paged_len(a, static_cast<int>(bh / a.n_h));
   T* const out = static_cast<T*>(a.out) + bh * a.D_v;
   if (L <= a.prefix_len) {  // an empty place of the batch
+    if (SPLIT && warp > 0) return;
     for (int d0 = 4 * lane; d0 < a.D_v; d0 += 128) store4<T>(out + d0, make_float4(0.f, 0.f, 0.f, 0.f));
     if (a.lse != nullptr && lane == 0) a.lse[bh] = -INFINITY;
     return;
   }
   const int ns = plan.slots();
-  const int n = plan.n_pre + static_cast<int>((static_cast<long long>(L) - a.prefix_len + plan.chunk - 1) / plan.chunk);
+  const int n = plan.n_pre + static_cast<int>((static_cast<long long>(L) - a.prefix_len + plan.own_chunk - 1) / plan.own_chunk);
   const float* const po = static_cast<const float*>(a.workspace) + bh * ns * a.D_v;
   const float* const lse = static_cast<const float*>(a.workspace) + static_cast<long long>(a.B) * a.n_h * ns * a.D_v +
                            bh * ns;
-  float M = -INFINITY;
-  for (int j = lane; j < n; j += 32) M = fmaxf(M, lse[j]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float den = 0.f;
+  constexpr int kStep = SPLIT ? kCombineWarps : 1;
+  float M = -INFINITY, den = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const float wl = j0 + lane < n ? exp2f(lse[j0 + lane] - M) : 0.f;
-    den += wl;
-    const int nj = min(32, n - j0);
-    for (int jj = 0; jj < nj; ++jj) {
-      const float w = __shfl_sync(0xffffffffu, wl, jj);
-      const float* pj = po + static_cast<long long>(j0 + jj) * a.D_v;
+#pragma unroll 1
+  for (int j0 = SPLIT ? warp : 0; j0 < n; j0 += kBatch * kStep) {
+    float l[kBatch];
+    float4 v[kBatch][4];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int j = j0 + k * kStep;
+      l[k] = j < n ? lse[j] : -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int d0 = 4 * lane + 128 * c;
-        if (d0 < a.D_v) {
-          const float4 v = *reinterpret_cast<const float4*>(pj + d0);
-          acc[c].x = fmaf(w, v.x, acc[c].x);
-          acc[c].y = fmaf(w, v.y, acc[c].y);
-          acc[c].z = fmaf(w, v.z, acc[c].z);
-          acc[c].w = fmaf(w, v.w, acc[c].w);
-        }
+        v[k][c] = j < n && d0 < a.D_v ? *reinterpret_cast<const float4*>(po + static_cast<long long>(j) * a.D_v + d0)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) m = fmaxf(m, l[k]);
+    const float m_ref = m == -INFINITY ? 0.f : m;  // every score so far is -inf: weights 0
+    const float alpha = exp2f(M - m_ref);
+    M = m;
+    den *= alpha;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(acc[c].x * alpha, acc[c].y * alpha, acc[c].z * alpha, acc[c].w * alpha);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float w = exp2f(l[k] - m_ref);
+      den += w;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[c] = make_float4(fmaf(w, v[k][c].x, acc[c].x), fmaf(w, v[k][c].y, acc[c].y), fmaf(w, v[k][c].z, acc[c].z),
+                             fmaf(w, v[k][c].w, acc[c].w));
+    }
+  }
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<float4*>(red_o + warp * 512 + 4 * lane + 128 * c) = acc[c];
+    if (lane == 0) {
+      red_m[warp] = M;
+      red_l[warp] = den;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    M = -INFINITY;
+    den = 0.f;
+    for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, red_m[w]);
+    const float m_ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < kCombineWarps; ++w) {
+      const float x = exp2f(red_m[w] - m_ref);
+      den = fmaf(red_l[w], x, den);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 v = *reinterpret_cast<const float4*>(red_o + w * 512 + 4 * lane + 128 * c);
+        acc[c] = make_float4(fmaf(x, v.x, acc[c].x), fmaf(x, v.y, acc[c].y), fmaf(x, v.z, acc[c].z), fmaf(x, v.w, acc[c].w));
       }
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   const float inv = 1.f / den;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -345,18 +586,30 @@ int pick_hg(int rows, int D_qk, int D_v) {
   return rows >= 2 ? 2 : 1;
 }
 
-// Keys per block: the smallest power of two from 256 that keeps the grid near 8192 blocks, at
-// most kMaxChunk (the staged page indices).
+// Whether the shared part runs as 64 x 64 tiles.
+bool prefix_tiles(const PagedDecodeArgs& a) {
+  return a.D_qk <= 128 && a.D_v <= 128 && static_cast<long long>(a.B) * (a.n_h / a.n_kv) >= kTileMinRows;
+}
+
+// Keys per block for `units` blocks per chunk: a power of two from 64, at most kMaxChunk (the staged page
+// indices).  Chunks below 256 keys only while the grid stays under `fill` blocks, from 256 on under 8192.
+int pick_chunk(long long units, long long keys, int fill) {
+  int c = 64;
+  while (c < kMaxChunk && c < keys && units * ((keys + c - 1) / c) > (c < 256 ? fill : 8192)) c *= 2;
+  return c;
+}
+
 Plan make_plan(const PagedDecodeArgs& a) {
   const int G = a.n_h / a.n_kv;
   const int hg = pick_hg(G, a.D_qk, a.D_v);
   const long long own = (static_cast<long long>(a.max_blocks) << a.page_shift) - a.prefix_len;  // keys at most
-  const long long units = static_cast<long long>(a.B) * a.n_kv * ((G + hg - 1) / hg);
+  const long long rows = static_cast<long long>(a.B) * G;
   Plan p;
-  p.chunk = 256;
-  while (p.chunk < kMaxChunk && p.chunk < own && units * ((own + p.chunk - 1) / p.chunk) > 8192) p.chunk *= 2;
-  p.n_pre = (a.prefix_len + p.chunk - 1) / p.chunk;
-  p.n_own = static_cast<int>((own + p.chunk - 1) / p.chunk);
+  p.own_chunk = pick_chunk(static_cast<long long>(a.B) * a.n_kv * ((G + hg - 1) / hg), own, 608);
+  p.pre_chunk = prefix_tiles(a) ? pick_chunk((rows + kTile - 1) / kTile * a.n_kv, a.prefix_len, 152)
+                                : pick_chunk((rows + hg - 1) / hg * a.n_kv, a.prefix_len, 608);
+  p.n_pre = (a.prefix_len + p.pre_chunk - 1) / p.pre_chunk;
+  p.n_own = static_cast<int>((own + p.own_chunk - 1) / p.own_chunk);
   return p;
 }
 
@@ -390,9 +643,28 @@ cudaError_t launch_hg(const PagedDecodeArgs& a, const RopeFreq& f, const Plan& p
   return launch_split<T, NQC, NVC, 1, PREFIX>(a, f, plan, st, launches);
 }
 
+template <typename T, int DM>
+cudaError_t launch_prefix_tile(const PagedDecodeArgs& a, const RopeFreq& f, const Plan& plan, cudaStream_t st,
+                               int* launches) {
+  auto kern = paged_prefix_tile_kernel<T, DM>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, prefix_tile_smem<DM>());
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(a.B) * (a.n_h / a.n_kv);
+  const long long grid = (rows + kTile - 1) / kTile * a.n_kv * plan.n_pre;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kern<<<static_cast<unsigned>(grid), kThreads, prefix_tile_smem<DM>(), st>>>(a, f, plan);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
 template <typename T, bool PREFIX>
 cudaError_t launch_part(const PagedDecodeArgs& a, const RopeFreq& f, const Plan& plan, cudaStream_t st,
                         int* launches) {
+  if constexpr (PREFIX) {
+    if (prefix_tiles(a))
+      return a.D_qk <= 64 && a.D_v <= 64 ? launch_prefix_tile<T, 64>(a, f, plan, st, launches)
+                                         : launch_prefix_tile<T, 128>(a, f, plan, st, launches);
+  }
   const int nq = (a.D_qk + 127) / 128, nv = (a.D_v + 127) / 128;
   if (nq == 1 && nv == 1) return launch_hg<T, 1, 1, PREFIX>(a, f, plan, st, launches);
   if (nq <= 2 && nv <= 2) return launch_hg<T, 2, 2, PREFIX>(a, f, plan, st, launches);
@@ -410,9 +682,15 @@ cudaError_t launch_all(const PagedDecodeArgs& a, const RopeFreq& f, cudaStream_t
     const cudaError_t e = launch_part<T, false>(a, f, plan, st, launches);
     if (e != cudaSuccess) return e;
   }
-  const long long grid = (static_cast<long long>(a.B) * a.n_h + kCombineWarps - 1) / kCombineWarps;
+  // eight warps per row where rows are few and may have many partials
+  const long long rows = static_cast<long long>(a.B) * a.n_h;
+  const bool split = rows <= 2432 && plan.slots() > 8;
+  const long long grid = split ? rows : (rows + kCombineWarps - 1) / kCombineWarps;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  paged_combine_kernel<T><<<static_cast<unsigned>(grid), kCombineWarps * 32, 0, st>>>(a, plan);
+  if (split)
+    paged_combine_kernel<T, true><<<static_cast<unsigned>(grid), kCombineWarps * 32, 0, st>>>(a, plan);
+  else
+    paged_combine_kernel<T, false><<<static_cast<unsigned>(grid), kCombineWarps * 32, 0, st>>>(a, plan);
   *launches += 1;
   return cudaGetLastError();
 }

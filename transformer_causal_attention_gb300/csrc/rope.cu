@@ -270,7 +270,7 @@ template <typename T, bool HALF>
 __global__ void __launch_bounds__(256) kv_append_rows_kernel(const __grid_constant__ KvAppendArgs a,
                                                              const __grid_constant__ RopeFreq rf) {
   constexpr int CH = 16 / sizeof(T);  // elements per chunk
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 4, kPairs = HALF ? 2 : 4;  // value chunks and key items in flight (a pair of chunks each)
   constexpr int kAngles = HALF ? CH : CH / 2;
   __shared__ float freq[2 * kMaxRopePairs];
   const SmemFreq f = stage_freq(rf, freq);
@@ -291,18 +291,20 @@ __global__ void __launch_bounds__(256) kv_append_rows_kernel(const __grid_consta
   T* const vd = static_cast<T*>(a.vcache) + slot * a.v_token_stride;
   float sn[kAngles], cs[kAngles];
   bool have = false;
-  for (int i0 = lane; i0 < n_k || i0 < n_v; i0 += L * kBatch) {
-    uint4 k0[kBatch], k1[kBatch], v[kBatch];
+  for (int i0 = lane, j0 = lane; i0 < n_k || j0 < n_v; i0 += L * kPairs, j0 += L * kBatch) {
+    uint4 k0[kPairs], k1[kPairs], v[kBatch];
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
+    for (int e = 0; e < kPairs; ++e) {
       const int i = i0 + L * e;
       if (i < n_k) {
         const int at = HALF ? (i / hc) * a.D_qk + (i % hc) * CH : i * CH;
         k0[e] = __ldg(reinterpret_cast<const uint4*>(ks + at));
         if (HALF) k1[e] = __ldg(reinterpret_cast<const uint4*>(ks + at + a.D_qk / 2));
       }
-      if (i < n_v) v[e] = __ldg(reinterpret_cast<const uint4*>(vs + i * CH));
     }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (j0 + L * e < n_v) v[e] = __ldg(reinterpret_cast<const uint4*>(vs + (j0 + L * e) * CH));
     if (!have && f.n_pairs) {
       have = true;
       const int c = lane % hc;  // of every item of this lane (hc divides the lanes)
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(256) kv_append_rows_kernel(const __grid_consta
       }
     }
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
+    for (int e = 0; e < kPairs; ++e) {
       const int i = i0 + L * e;
       if (i < n_k) {
         const int at = HALF ? (i / hc) * a.D_qk + (i % hc) * CH : i * CH;
@@ -336,8 +338,10 @@ __global__ void __launch_bounds__(256) kv_append_rows_kernel(const __grid_consta
         *reinterpret_cast<uint4*>(kd + at) = k0[e];
         if (HALF) *reinterpret_cast<uint4*>(kd + at + a.D_qk / 2) = k1[e];
       }
-      if (i < n_v) *reinterpret_cast<uint4*>(vd + i * CH) = v[e];
     }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (j0 + L * e < n_v) *reinterpret_cast<uint4*>(vd + (j0 + L * e) * CH) = v[e];
   }
 }
 
