@@ -221,6 +221,13 @@ DECODE = [
     ([1, 2, 100, 0, 1024], 0, 32, 12, 12, 64, 64, dict(dtype="f32")),
     ([700, 33], 0, 16, 10, 2, 128, 128, dict(dtype="f32", rope=5e5, pairing="half")),
     ([5000], 0, 16, 3, 1, 40, 24, dict(dtype="f32")),
+    # 128 heads over one latent head (the MLA-absorbed shape, on CTA pairs), values in front of the keys
+    ([300, 129, 1, 0, 1030, 256], 0, 16, 128, 1, 576, 512, dict(rope=1e4, roff=512, rdims=64, alias=True)),
+    ([513, 40], 0, 64, 128, 1, 576, 512, dict(scale=0.0722, alias=True)),
+    ([2000, 100, 257], 0, 256, 128, 1, 576, 512, dict(rope=1e4, roff=512, rdims=64, pairing="half", alias=True)),
+    ([900, 600, 513, 3, 512, 1300], 512, 32, 128, 1, 576, 512, dict(rope=1e4, roff=512, rdims=64, alias=True)),
+    ([4000 + 300 * i for i in range(5)], 3968, 128, 128, 1, 576, 512, dict(alias=True)),
+    ([300, 40], 0, 64, 128, 1, 576, 512, {}),                   # values apart from the keys: CUDA cores
     # behind a shared prefix
     ([17], 16, 16, 1, 1, 64, 64, {}),
     ([65, 128, 100, 64, 0], 64, 64, 32, 8, 128, 128, dict(rope=5e5)),
@@ -261,12 +268,14 @@ def test_lengths_above_the_table_are_clamped(lib, D, dtype):
         check_result(to_np(out), to_np(lse), want, want_lse, err, v_of, dtype)
 
 
-@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "bf16"), (96, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "bf16"), (96, "bf16"), (64, "f32"), (576, "bf16")])
 def test_pages_outside_the_cache_read_as_zero(lib, D, dtype):
     dt = TYPES[dtype]
     lens, prefix, page = [200, 150, 90], 64, 16
-    k, v, table, pre, k_of, v_of = ref.make_cache(lens, prefix, page, 2, D, D, dt)
-    q = torch.randn(3, 8, D, generator=torch.Generator().manual_seed(9)).to(dt)
+    mla = D == 576
+    n_kv, n_h, Dv = (1, 128, 512) if mla else (2, 8, D)
+    k, v, table, pre, k_of, v_of = ref.make_cache(lens, prefix, page, n_kv, D, Dv, dt, alias=mla)
+    q = torch.randn(3, n_h, D, generator=torch.Generator().manual_seed(9)).to(dt)
     n_pages = k.shape[0]
     for (b, j), bad in (((0, 5), -1), ((0, 12), n_pages), ((1, 4), 2**31 - 1), ((1, 9), -2**31), ((2, 5), 1 << 27)):
         table[b, j] = bad
@@ -277,11 +286,13 @@ def test_pages_outside_the_cache_read_as_zero(lib, D, dtype):
         k_of[b][2 * page:3 * page] = 0
         v_of[b][2 * page:3 * page] = 0
     want, want_lse, err = ref.attend(q, k_of, v_of)
-    out, lse = lib.decode_shared(q.to(DEV), k.to(DEV), v.to(DEV), pre.to(DEV), table.to(DEV), ints(lens), lse=True)
+    kd = k.to(DEV)
+    vd = kd[..., :Dv] if mla else v.to(DEV)
+    out, lse = lib.decode_shared(q.to(DEV), kd, vd, pre.to(DEV), table.to(DEV), ints(lens), lse=True)
     check_result(to_np(out), to_np(lse), want, want_lse, err, v_of, dtype)
     # the same cache read as one without a prefix
     whole = torch.cat([pre.repeat(3, 1), table[:, 4:]], 1).contiguous()
-    out, lse = lib.decode_paged(q.to(DEV), k.to(DEV), v.to(DEV), whole.to(DEV), ints(lens), lse=True)
+    out, lse = lib.decode_paged(q.to(DEV), kd, vd, whole.to(DEV), ints(lens), lse=True)
     check_result(to_np(out), to_np(lse), want, want_lse, err, v_of, dtype)
 
 

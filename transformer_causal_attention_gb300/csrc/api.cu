@@ -88,7 +88,7 @@ bool make_map4(CUtensorMap* map, const void* base, int D, int heads, int rows, i
 
 // 3-D tensor map over a bf16 tensor indexed (d, row, batch): boxes of 64 dims x
 // box_rows rows x 1 batch, 128-byte swizzle, zero fill outside.
-static bool make_map3(CUtensorMap* map, const void* base, int D, int rows, int B, unsigned long long row_stride,
+bool make_map3(CUtensorMap* map, const void* base, int D, int rows, int B, unsigned long long row_stride,
                unsigned long long batch_stride, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (!enc) return false;

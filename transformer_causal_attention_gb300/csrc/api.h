@@ -28,6 +28,10 @@ bool make_map4(CUtensorMap* map, const void* base, int D, int heads, int rows, i
 bool make_map_box(CUtensorMap* map, const void* base, int D, int n1, int n2, int n3, unsigned long long s1,
                   unsigned long long s2, unsigned long long s3, int box1, int box2, int box3, bool promote_256);
 
+// 3-D tensor map over a bf16 tensor indexed (d, row, batch); see api.cu.
+bool make_map3(CUtensorMap* map, const void* base, int D, int rows, int B, unsigned long long row_stride,
+               unsigned long long batch_stride, int box_rows);
+
 // The dtype argument: element type in the low byte, ATTN_ROPE_HALF optionally OR'd in.
 bool parse_dtype(attn_dtype_t dtype, bool* bf16, bool* half);
 

@@ -50,9 +50,20 @@ int check_sizes(int B, int n_h, int n_kv, int D_qk, int D_v, int n_pages, int pa
   return ATTN_OK;
 }
 
-// Scratch of either path (which one a call takes also depends on its RoPE span).
+// The MLA-absorbed shape on the tensor cores (decode_mla.cu), its partials: outputs, then log-sum-exps.
+bool mla_shape(const PagedDecodeArgs& a, bool bf16) {
+  const long long keys = static_cast<long long>(a.max_blocks) << a.page_shift;
+  return decode_mla_supported(a.B, a.n_h, a.n_kv, a.D_qk, a.D_v, a.D_qk, true, bf16) && keys * a.B <= INT_MAX;
+}
+size_t mla_slots(const PagedDecodeArgs& a) { return static_cast<size_t>(kMlaMaxPairs + a.B) * a.n_h; }
+
+// Scratch of every path (which one a call takes also depends on its RoPE span and where its values lie).
 size_t workspace_of(const PagedDecodeArgs& a, bool bf16) {
-  const size_t n = decode_paged_workspace(a);
+  size_t n = decode_paged_workspace(a);
+  if (mla_shape(a, bf16)) {
+    const size_t mla = mla_slots(a) * (a.D_v + 1) * sizeof(float);
+    if (mla > n) n = mla;
+  }
   if (!decode_paged_tc_supported(a, bf16, 0, 0, false)) return n;
   const size_t tc = decode_paged_tc_workspace(a);
   return tc > n ? tc : n;
@@ -103,6 +114,20 @@ int decode_impl(const void* q, const void* k_pages, const void* v_pages, int v_t
   const RopeFreq rf = make_rope(rope_base, rope ? rope_dims : 0, half);
   int launches = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (mla_shape(a, bf16) && v_pages == k_pages && ldv == D_qk &&
+      (!rope || decode_mla_rope_ok(rope_offset, rope_dims, half))) {
+    float* const ws_o = static_cast<float*>(workspace);
+    const DecodeArgs da{q, k_pages, v_pages, ldv, seqlens, out, lse, B, n_h, n_kv, D_qk, D_v, max_blocks << a.page_shift,
+                        a.rope_offset, a.scale_log2, ws_o, ws_o + mla_slots(a) * D_v, decode_mla_pairs(dev.sms), 0,
+                        dev.status, a.wait_limit_ns, 0, 0, nullptr};
+    const MlaPages pages{block_table, prefix_pages, a.page_shift, max_blocks, prefix_len};
+    CUtensorMap maps[2];
+    const unsigned long long row = static_cast<unsigned long long>(D_qk) * 2;
+    if (!make_map3(&maps[0], q, D_qk, n_h, B, row, row * n_h, 64) ||
+        !make_map3(&maps[1], k_pages, D_qk, page_size, n_pages, row, row * page_size, page_size < 128 ? page_size : 128))
+      return finish(cudaErrorInvalidValue, launches);
+    return finish(launch_decode_mla_paged(da, rf, pages, maps, st, &launches), launches);
+  }
   if (!decode_paged_tc_supported(a, bf16, rope_offset, rope_dims, rope))
     return finish(launch_decode_paged(a, rf, bf16, st, &launches), launches);
   return finish(launch_decode_paged_tc(a, rf, dev.sms, st, &launches), launches);

@@ -52,6 +52,11 @@
 // for the new query, its rotation and a pipeline refill); each (pair, sequence) piece writes
 // one normalised partial, merged per sequence by mla_combine_kernel with the
 // log-sum-exp rule of the online softmax ("Transformer架构完全深度解析" §13).
+// PAGED (decode_paged.cu's callers): the latent rows live in pages.  The producer warp then loads a box of
+// 128 rows as one TMA per page, its lanes one page each, with the page indices of the next round's keys
+// fetched a round ahead; everything else is the same.  Requests behind a shared prefix are read through
+// the prefix's pages for their first keys: at 242 FLOP per byte the kernel is bound by its MMAs, which a
+// shared prefix leaves as they are, and its repeated reads come from L2.
 // Roles (384 threads): warp 0 TMA producer, warp 1 TMEM owner + MMA issuer (even
 // CTA), warp 2 key prefix sums, then the value-row fixer, warp 3 query RoPE and
 // hand-offs to the even CTA, warps 4-11 softmax (four lane quarters x two halves
@@ -261,9 +266,19 @@ __device__ __forceinline__ void scale_cols64(uint32_t taddr, const float* f) {
   }
 }
 
+// Keys of sequence i.  An empty place of a paged batch counts one key (of zeros): the combine clears it.
+template <bool PAGED>
+__device__ __forceinline__ int mla_len(const DecodeArgs& a, const MlaPages& pg, int i) {
+  const int L = a.seqlens[i];
+  if (PAGED && L <= pg.prefix_len) return 1;
+  return min(max(L, 1), a.max_len);
+}
+
+template <bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_decode_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ RopeFreq f,
-                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c) {
+                      const __grid_constant__ MlaPages pg, const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_c) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // aligned by pointer arithmetic on the shared array, so that the compiler keeps shared-memory addressing
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -318,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) prefix[0] = 0;
     for (int base = 0; base < a.B; base += 32) {
       const int i = base + lane;
-      int v = i < a.B ? min(max(a.seqlens[i], 1), a.max_len) : 0;
+      int v = i < a.B ? mla_len<PAGED>(a, pg, i) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int t = __shfl_up_sync(0xffffffffu, v, o);
@@ -343,7 +358,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   setmaxnreg_dec<kRegsCtl>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && run) {
+    if (PAGED && run) {
+      // the whole warp: lane l loads the rows of page l mod n_pg into box l / n_pg of a unit
+      const int box_shift = min(pg.shift, 7), n_pg = RK >> box_shift;
+      const int my_pg = lane & (n_pg - 1), my_box = lane / n_pg;
+      PieceIter it;
+      it.init(prefix, a.B, k_begin, k_end);
+      uint32_t st = 0, ph = 0, rph = 0, any_issued = 0;
+      int sb, lo, hi;
+      for (uint32_t n = 0; it.next(&sb, &lo, &hi); ++n) {
+        const int L = prefix[sb + 1] - prefix[sb];
+        const int nr = (hi - lo + kRoundKeys - 1) / kRoundKeys;
+        const int* const table = pg.table + static_cast<long long>(sb) * pg.max_blocks;
+        const bool empty = a.seqlens[sb] <= pg.prefix_len;
+        auto page_of = [&](int key0) -> int {  // this lane's page of the tile at key0; -1 (zeros) behind the end
+          const int key = key0 + (my_pg << box_shift);
+          if (key >= L || empty) return -1;
+          return key < pg.prefix_len ? pg.prefix_pages[key >> pg.shift] : table[key >> pg.shift];
+        };
+        // pages of the two halves of the round whose values are next, of the scores' round, of the one after
+        int v0 = -1, v1 = -1, s0 = page_of(lo), s1 = page_of(lo + RK), x0 = -1, x1 = -1;
+        if (!warp_wait_cl(&bars->q_empty, (n & 1) ^ 1, wc)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full, kQBytes);
+          for (int blk = 0; blk < kQBlocks; ++blk)
+            tma_load_3d_pair(smem + kQOff + blk * kQBlockBytes, &tm_q, smem_u32(&bars->q_full), blk * 64, HH * r, sb);
+        }
+        any_issued = 1;
+        const bool done = for_units(lo, nr, r, [&](const Unit& u) -> bool {
+          // a round's scores begin: its pages become the scores', the round before's the values'
+          if (!u.pv && u.d0 == 0) {
+            if (u.key0 != lo + r * RK) {
+              v0 = s0;
+              v1 = s1;
+              s0 = x0;
+              s1 = x1;
+            }
+            x0 = page_of(u.key0 - r * RK + kRoundKeys);
+            x1 = page_of(u.key0 - r * RK + kRoundKeys + RK);
+          }
+          const bool last = u.pv && u.key0 >= lo + (nr - 1) * kRoundKeys;  // behind the last scores
+          const bool second = u.pv ? ((u.key0 - lo) & RK) != 0 : r != 0;
+          const int page = u.pv && !last ? (second ? v1 : v0) : (second ? s1 : s0);
+          const int row = u.key0 & ((1 << pg.shift) - 1);
+          uint8_t* dst;
+          uint32_t bar;
+          if (u.rope_slot) {
+            if (!warp_wait_cl(&bars->rope_empty, rph ^ 1, wc)) return false;
+            if (r == 0 && lane == 0) mbar_arrive_expect_tx(&bars->rope_full, 2 * kBoxBytes);
+            dst = smem + kRopeOff;
+            bar = cluster_addr(&bars->rope_full, 0);
+            rph ^= 1;
+          } else {
+            if (!warp_wait_cl(&bars->kv_empty[st], ph ^ 1, wc)) return false;
+            dst = smem + kRingOff + st * kUnitBytes;
+            if (needs_fix(u, L)) {
+              if (lane == 0) mbar_arrive_expect_tx(&bars->kv_tofix[st], u.nbox * kBoxBytes);
+              bar = cluster_addr(&bars->kv_tofix[st], static_cast<uint32_t>(r));
+            } else {
+              if (r == 0 && lane == 0) mbar_arrive_expect_tx(&bars->kv_full[st], 2 * u.nbox * kBoxBytes);
+              bar = cluster_addr(&bars->kv_full[st], 0);
+            }
+            if (++st == kStages) { st = 0; ph ^= 1; }
+          }
+          __syncwarp();
+          if (my_box < u.nbox)
+            tma_load_3d_pair(dst + my_box * kBoxBytes + (my_pg << (box_shift + 7)), &tm_c, bar, u.d0 + 64 * my_box, row,
+                             page);
+          return true;
+        });
+        if (!done) break;
+      }
+      if (bars->abort_flag && any_issued) {  // as below: time for copies in flight
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    } else if (lane == 0 && run) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_c);
       PieceIter it;
@@ -864,15 +955,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the 512 dims with 16-byte loads of the partials.
 constexpr int kCombineWarps = 8;
 
-__global__ void __launch_bounds__(kCombineWarps * 32) mla_combine_kernel(DecodeArgs a) {
+template <bool PAGED>
+__global__ void __launch_bounds__(kCombineWarps * 32) mla_combine_kernel(DecodeArgs a, MlaPages pg) {
   const int lane = threadIdx.x & 31;
   const int bh = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
   if (bh >= a.B * a.n_h) return;  // whole warps only
   const int b = bh / a.n_h, h = bh % a.n_h;
+  if (PAGED && a.seqlens[b] <= pg.prefix_len) {  // an empty place of the batch
+    uint2* const o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(bh) * DV);
+    for (int c = lane; c < DV / 4; c += 32) o[c] = make_uint2(0, 0);
+    if (a.lse != nullptr && lane == 0) a.lse[bh] = -INFINITY;
+    return;
+  }
   const int P = a.n_split;  // pairs
   long long before = 0, total = 0;
   for (int i = lane; i < a.B; i += 32) {
-    const long long L = min(max(a.seqlens[i], 1), a.max_len);
+    const long long L = mla_len<PAGED>(a, pg, i);
     total += L;
     if (i < b) before += L;
   }
@@ -882,7 +980,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) mla_combine_kernel(DecodeA
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
   const long long Teff = total + kPieceGap * (a.B - 1);
-  const long long Lb = min(max(a.seqlens[b], 1), a.max_len);
+  const long long Lb = mla_len<PAGED>(a, pg, b);
   const long long e0 = before + kPieceGap * b;  // effective position of
   const long long e1 = e0 + Lb - 1;              // sequence b's first, last key
   // pair holding effective position e: the largest p with floor(p Teff / P) <= e.  Rounding the
@@ -958,20 +1056,21 @@ bool decode_mla_rope_ok(int rope_offset, int rope_dims, bool half) {
 }
 
 namespace {
-std::atomic<unsigned> g_mla_ready{0};  // one bit per device whose shared-memory opt-in is done
 std::atomic<int> g_mla_pairs[32];      // per device: clusters of two CTAs that fit at once (0: not known)
 
+template <bool PAGED>
 cudaError_t mla_prepare(int dev) {
+  static std::atomic<unsigned> ready{0};  // one bit per device whose shared-memory opt-in is done
   const unsigned bit = 1u << (dev & 31);
-  if (g_mla_ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if (ready.load(std::memory_order_acquire) & bit) return cudaSuccess;
   // the register split must fit the registers the compiled kernel launches with
   cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, mla_decode_kernel);
+  cudaError_t e = cudaFuncGetAttributes(&fa, mla_decode_kernel<PAGED>);
   if (e != cudaSuccess) return e;
   if (static_cast<long long>(fa.numRegs) * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  e = cudaFuncSetAttribute(mla_decode_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  g_mla_ready.fetch_or(bit, std::memory_order_acq_rel);
+  ready.fetch_or(bit, std::memory_order_acq_rel);
   return cudaSuccess;
 }
 
@@ -994,13 +1093,13 @@ int decode_mla_pairs(int num_sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess && dev < 32) {
     int known = g_mla_pairs[dev].load(std::memory_order_acquire);
-    if (known == 0 && mla_prepare(dev) == cudaSuccess) {
+    if (known == 0 && mla_prepare<false>(dev) == cudaSuccess) {
       // every pair must be resident at once (the pairs of a GPC pair up its SMs)
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr;
       mla_config(&cfg, &attr, p < 1 ? 1 : p, nullptr);
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, mla_decode_kernel, &cfg) == cudaSuccess && n > 0) known = n;
+      if (cudaOccupancyMaxActiveClusters(&n, mla_decode_kernel<false>, &cfg) == cudaSuccess && n > 0) known = n;
       else (void)cudaGetLastError();
       if (known > 0) g_mla_pairs[dev].store(known, std::memory_order_release);
     }
@@ -1009,21 +1108,34 @@ int decode_mla_pairs(int num_sms) {
   return p < 1 ? 1 : (p > kMlaMaxPairs ? kMlaMaxPairs : p);
 }
 
-cudaError_t launch_decode_mla(const DecodeArgs& a, const RopeFreq& rope, const CUtensorMap* maps, cudaStream_t st,
-                              int* launches) {
+namespace {
+template <bool PAGED>
+cudaError_t launch_mla(const DecodeArgs& a, const RopeFreq& rope, const MlaPages& pg, const CUtensorMap* maps,
+                       cudaStream_t st, int* launches) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if ((e = mla_prepare(dev)) != cudaSuccess) return e;
+  if ((e = mla_prepare<PAGED>(dev)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   mla_config(&cfg, &attr, a.n_split, st);
-  e = cudaLaunchKernelEx(&cfg, mla_decode_kernel, a, rope, maps[0], maps[1]);
+  e = cudaLaunchKernelEx(&cfg, mla_decode_kernel<PAGED>, a, rope, pg, maps[0], maps[1]);
   *launches += 1;
   if (e != cudaSuccess) return e;
-  mla_combine_kernel<<<(a.B * a.n_h + kCombineWarps - 1) / kCombineWarps, kCombineWarps * 32, 0, st>>>(a);
+  mla_combine_kernel<PAGED><<<(a.B * a.n_h + kCombineWarps - 1) / kCombineWarps, kCombineWarps * 32, 0, st>>>(a, pg);
   *launches += 1;
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_decode_mla(const DecodeArgs& a, const RopeFreq& rope, const CUtensorMap* maps, cudaStream_t st,
+                              int* launches) {
+  return launch_mla<false>(a, rope, MlaPages{}, maps, st, launches);
+}
+
+cudaError_t launch_decode_mla_paged(const DecodeArgs& a, const RopeFreq& rope, const MlaPages& pg,
+                                    const CUtensorMap* maps, cudaStream_t st, int* launches) {
+  return launch_mla<true>(a, rope, pg, maps, st, launches);
 }
 
 }  // namespace attn

@@ -177,6 +177,15 @@ int decode_mla_pairs(int num_sms);
 bool decode_mla_rope_ok(int rope_offset, int rope_dims, bool half);
 cudaError_t launch_decode_mla(const DecodeArgs& a, const RopeFreq& rope, const CUtensorMap* maps, cudaStream_t st,
                               int* launches);
+// The same over pages: maps[1] indexes (d, row in page, page) with boxes of min(page_size, 128) rows; a.max_len is
+// max_blocks pages, and the batch's lengths are at most 2^31 - 1 together.
+struct MlaPages {
+  const int* table;         // [B, max_blocks]
+  const int* prefix_pages;  // [prefix_len >> shift], for the first prefix_len keys of every sequence
+  int shift, max_blocks, prefix_len;
+};
+cudaError_t launch_decode_mla_paged(const DecodeArgs& a, const RopeFreq& rope, const MlaPages& pages,
+                                    const CUtensorMap* maps, cudaStream_t st, int* launches);
 constexpr int kStreamTileKeys = 64;  // keys per TMA box of the streaming GQA decode
 constexpr int kDecodeTcMinChunk = 4096;  // keys per work unit of the tensor-core GQA decode, at least
 bool decode_tc_supported(int n_h, int n_kv, int D_qk, int D_v, bool bf16, int rope_offset, int rope_dims, bool rope);
