@@ -313,6 +313,53 @@ def test_large_scores(lib, dtype, D):
     assert np.max(np.abs(to_np(lse) - want_lse)) <= e + 1e-5 * np.max(np.abs(want_lse))
 
 
+# The rows of a piece on the tensor cores: in groups of eight with the rests of their queries (own keys of up to
+# 64 heads per KV head; a prefix's of up to eight groups), or one after the other.
+ROWS = [
+    # lens, prefix, heads per KV head
+    ([70, 300, 129, 128, 1] * 3, 0, 1),
+    ([70, 300], 0, 8), ([70, 300], 0, 9), ([140, 33, 600], 0, 31), ([140, 33], 0, 32), ([300, 140, 33], 0, 33),
+    ([300, 140, 33], 0, 64), ([300, 140], 0, 65), ([300, 140], 0, 96),
+    ([70 + i for i in range(64)], 64, 1), ([70 + i for i in range(65)], 64, 1),     # 8 groups of 8 requests, 9
+    ([400 + i for i in range(16)], 256, 3), ([400 + i for i in range(17)], 256, 3),  # 8 groups of 2 requests, 9
+    ([400 + i for i in range(8)], 256, 5), ([400 + i for i in range(9)], 256, 5),
+    ([200, 129, 0, 400], 128, 16), ([200, 129, 130, 0, 400], 128, 16),              # 8 groups, 10
+    ([200, 129, 400], 128, 12), ([200, 400], 128, 32), ([200, 0, 400], 128, 32), ([400], 128, 64), ([129], 128, 128),
+]
+
+
+@pytest.mark.parametrize("lens,prefix,G", ROWS)
+@pytest.mark.parametrize("D,rope", [(128, 1e4), (64, 1e4), (128, 0.0)])
+def test_rows_of_a_piece(lib, lens, prefix, G, D, rope):
+    check_decode(lib, lens, prefix, 16, 2 * G, 2, D, D, rope=rope, pairing="half" if G & 1 else "adjacent")
+
+
+@pytest.mark.parametrize("lens,prefix,G", [([1000, 30, 300], 0, 4), ([1000, 300], 0, 64), ([1000, 30, 300], 16, 20),
+                                           ([1000, 30], 16, 20),
+                                           ([500 + i for i in range(16)], 480, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_grouped_rows_keep_their_rests(lib, lens, prefix, G, D):
+    """Rows in groups are as good as fp32 but for the stored result: queries and weights to 17 bits, so that a score
+    is off by at most e = 2^-16 |q| |k| / sqrt(D) and a weight by 2 e + 2^-16, fp32 sums and the rotation's angles
+    (positions below 2^10, fp32 sine and cosine) by some 2^-16 more.  Three requests' 20 heads are 3 x 3 = 9 groups,
+    one too many for the prefix: there e has the 2^-8 of a bf16 query, and a weight another 2^-8."""
+    k, v, table, pre, k_of, v_of = ref.make_cache(lens, prefix, 16, 2, D, D, torch.bfloat16, seed=6)
+    q = torch.randn(len(lens), 2 * G, D, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    want, want_lse, _ = ref.attend(q, k_of, v_of, rope_base=1e4)
+    out, lse = lib.decode_shared(q.to(DEV), k.to(DEV), v.to(DEV), pre.to(DEV), table.to(DEV), ints(lens), rope_base=1e4,
+                                 lse=True) if prefix else \
+        lib.decode_paged(q.to(DEV), k.to(DEV), v.to(DEV), table.to(DEV), ints(lens), rope_base=1e4, lse=True)
+    norm = max(np.linalg.norm(x, axis=-1).max() for x in k_of if x.size)
+    groups = -(-len(lens) // (8 // G)) if G <= 8 else len(lens) * -(-G // 8)
+    bits = 2.0 ** -8 if prefix and groups > 8 else 2.0 ** -16
+    e = bits * q.double().norm(dim=-1).max().item() * norm / D ** 0.5
+    vmax = max(np.abs(x).max() for x in v_of if x.size)
+    got = to_np(out)
+    assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + (2 * e + bits + 2.0 ** -16) * vmax)
+    live = np.isfinite(want_lse)
+    assert np.max(np.abs(to_np(lse) - want_lse)[live]) <= e + 2.0 ** -16 * np.max(np.abs(want_lse[live])) + 2.0 ** -16
+
+
 def test_shared_equals_paged(lib):
     """The same batch with and without the prefix computed once: equal up to rounding."""
     lens, prefix, page = [3000 + 37 * i for i in range(24)], 2944, 64
@@ -323,7 +370,11 @@ def test_shared_equals_paged(lib):
     whole = torch.cat([pre.repeat(24, 1), table[:, prefix // page:]], 1).contiguous().to(DEV)
     b, lb = lib.decode_paged(q, k, v, whole, ints(lens), rope_base=5e5, lse=True)
     assert (a.float() - b.float()).norm() / b.float().norm() <= BF16_REL_L2
-    assert (la - lb).abs().max() <= 1e-4
+    # Only the prefix's 96 rows a KV head have their queries rounded (a request's own 4 rows, and all of b's, keep
+    # the rest): components off by at most 2^-8 of themselves move a score by at most 2^-8 |q| |k| / sqrt(128),
+    # and a log-sum-exp by no more than its scores.  fp32 sums: 1e-4.
+    moved = 2.0 ** -8 * q.float().norm(dim=-1).max() * k[~k.isnan().any(-1)].float().norm(dim=-1).max() / 128 ** 0.5
+    assert (la - lb).abs().max() <= moved + 1e-4
 
 
 def test_repeated_calls_give_the_same_bits(lib):

@@ -3,8 +3,7 @@
 //
 // Every piece of the work is one product of up to 128 query rows with the keys of
 // one KV head in tiles of 128: S = Q K^T, an online softmax over the rows, O += P V
-// ("Transformer架构完全深度解析" §13).  Rows are TMEM lanes (one thread per row, no
-// exchange between threads), so the same code serves
+// ("Transformer架构完全深度解析" §13).  The same code serves
 //   own     the G = n_h / n_kv rows of one request against its own keys
 //           [P, L) (P = prefix_len, 0 without a prefix), and
 //   prefix  up to 128 of the B * G rows of a KV head against the P shared keys,
@@ -15,6 +14,11 @@
 // tensor pipe.  An MMA of 128 rows costs the same however few of them are real, and
 // with 1024 pipe cycles per 64 KB tile (D = 128) against ~2800 cycles for which an SM
 // waits for those bytes at HBM speed, padding a request's rows to 128 costs nothing.
+// Pieces of at most 64 rows use the padding: each row comes with a second one, for what
+// rounding to bf16 left of its rotated query and then of its weights, so that only the
+// result is rounded (in 64 bits: error 0.0017 of the largest output, 0.0029 with both
+// rounded; at 59 requests of 4096 to 16384 keys the same time).  Rows of larger pieces are
+// a TMEM lane each, and rounded.
 //
 // Work split.  The pair tiles lie on one line, KV head by KV head, and the single ones on
 // another: prefix tiles of an odd last row tile, then request after request, KV head
@@ -64,9 +68,16 @@ struct PagedTcPlan {
   int n_pairs;       // pairs of row tiles of a KV head's prefix rows
   int odd;           // 1: one more row tile
   int prefix_tiles;  // key tiles of the prefix
+  // pieces of few rows have them in groups of up to 8 (kGroups):
+  int own_groups;     // groups of an own piece, 0: its rows lie one after the other
+  int prefix_groups;  // of a prefix piece
+  int own_group, prefix_group;  // rows per group
+  int group_reqs;     // requests per group of prefix rows: 8 / G, at least 1
+  int req_groups;     // groups per request: G / 8 rounded up
+  int lo_reqs;        // B with RoPE: the rest of request b's rotated queries is request b + B of the maps; 0 without
   // float offsets into the workspace: partial outputs and log-sum-exps of pair pieces [2 * rows],
   // single prefix pieces [rows] and own pieces [G]; then (int) B + 1 sums of points and the rotated
-  // queries (bf16 [B, n_h, D])
+  // queries (bf16 [2, B, n_h, D]: the rounded values and what the rounding left)
   long long o2, o1, o0, l2, l1, l0, sums, q, end;
 };
 
@@ -92,7 +103,7 @@ struct Piece {
   int b;         // own: the request; pair: the pair of row tiles
   int t, t_end;
   int keys;      // keys of the whole segment: tile t holds min(128, keys - 128 t) of them
-  int q_alt;     // 1: the query rows lie in the second half of the worker's Q tile
+  int q_alt;     // 1: the query rows lie kAltRows further on
   int q_back;    // they may be loaded when the Q K of this many pieces before are done
 };
 
@@ -180,12 +191,16 @@ struct Lines {
         singles(prefix_end + own * n_kv, 2 * p.ctas) {}
 };
 
-// Where a piece's query rows lie in its worker's Q tile: own pieces of at most 64 rows alternate
-// between the tile's halves, so that the next piece's rows load while this one's are read (an MMA
-// reads 128 rows from either; what lies behind a piece's rows reaches only lanes that nobody reads).
-// A piece whose rows alternate waits for the Q K of the piece two before it, any other for those of
-// the piece before.
-constexpr int kHalfRows = 64;
+// Where a piece's query rows lie in its worker's Q tile.  Up to kGroups groups of eight rows (an own piece's,
+// or the prefix's for a small batch): group j in rows 32 (j mod 4) + 16 (j / 4), so that a softmax warp has
+// one before any has two, followed by the rests of the same rows.  More rows than that: one after the other.
+// Own pieces of at most 4 groups alternate between the tile and the tile 16 rows on, so that the next piece's
+// rows load while this one's are read (an MMA reads 128 rows from either; what lies between a piece's rows
+// reaches only lanes that nobody reads).  A piece whose rows alternate waits for the Q K of the piece two
+// before it, any other for those of the piece before.
+constexpr int kGroups = 8;
+__host__ __device__ __forceinline__ int group_row(int j) { return 32 * (j & 3) + 16 * (j >> 2); }
+constexpr int kAltRows = 16;
 
 // A walk along one worker's parts of the lines: the next segment, its first point, its next tile, and
 // where the part ends.  Pair pieces come first (in both workers' walks), then single prefix pieces,
@@ -193,7 +208,7 @@ constexpr int kHalfRows = 64;
 struct Walk {
   int kind, g, b, t, s0, end;                                   // of the pairs, then of the rest
   int rest_kind, rest_g, rest_b, rest_t, rest_s0, rest_end;  // where the single tiles begin
-  int q_alt;  // Piece::q_alt of the last piece; -1: that piece's rows fill more than half a Q tile
+  int q_alt;  // Piece::q_alt of the last piece; -1: that piece's rows do not alternate
 };
 
 // The next piece of a walk; kind kNone at its end.
@@ -238,11 +253,10 @@ __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const Page
     if (w.t >= t_end) {
       if (w.t < nt) return u;  // the part ends here
     } else {
-      // own pieces of at most kHalfRows rows alternate between the halves of their Q tile
-      const bool half = w.kind == kOwn && a.n_h / a.n_kv <= kHalfRows;
-      const bool turn = half && w.q_alt >= 0;
+      const bool alternates = w.kind == kOwn && pl.own_groups > 0 && pl.own_groups <= 4;
+      const bool turn = alternates && w.q_alt >= 0;
       const int alt = turn ? w.q_alt ^ 1 : 0;
-      w.q_alt = half ? alt : -1;
+      w.q_alt = alternates ? alt : -1;
       u = Piece{w.kind, w.g, w.b, w.t, t_end, keys, alt, turn ? 2 : 1};
       w.t = t_end;
     }
@@ -324,12 +338,58 @@ struct Cursor {
 };
 
 // ------------------------------------------------------------------------------------- softmax of a tile
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+// 16 TMEM lanes as MMA fragments.  32-bit columns, 128 or 64 of them: thread t has, for j = 0, 1, .., columns
+// 8 j + 2 (t & 3) + {0, 1} of lane t / 4 in r[4 j], r[4 j + 1] and of lane t / 4 + 8 in r[4 j + 2], r[4 j + 3].
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// 128 columns of bf16 in 64 of 32 bits: the pair 8 j + 2 (t & 3) + {0, 1} of lane t / 4 in r[2 j], of lane
+// t / 4 + 8 in r[2 j + 1].
+__device__ __forceinline__ void tmem_st_frag_bf16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -348,6 +408,12 @@ __device__ __forceinline__ void rescale_o(uint32_t o_addr, float alpha) {
   }
 }
 
+__device__ __forceinline__ void swap(float& x, float& y) {
+  const float z = x;
+  x = y;
+  y = z;
+}
+
 // Among four lanes (lj = lane & 3): piece e of lane k becomes piece k of lane e.
 __device__ __forceinline__ void transpose_pieces(uint4* pc, int lj) {
   const bool b1 = (lj & 2) != 0, b0 = (lj & 1) != 0;
@@ -363,38 +429,45 @@ __device__ __forceinline__ void transpose_pieces(uint4* pc, int lj) {
   pc[3] = b0 ? pc[3] : q1;
 }
 
-// The scores of one tile (n real keys) in this thread's TMEM row become the weights P, written over
-// them as bf16: p = 2^(s * scale*log2e - m).  m moves only when the row maximum grew by more than the
-// threshold; O and l are then scaled by 2^(m_old - m_new), exactly (l and O share their reference).
-// This form takes 32 scores at a time, reading them twice: a quarter of the code of the form below,
-// which counts where pieces are short and every role's code has to stay cached.
+// A tile's scores (n real keys) of one group of eight rows become its weights P: p = 2^(s * scale*log2e - m).
+// m moves only when the row maximum grew by more than the threshold; O and l are then scaled by
+// 2^(m_old - m_new), exactly (l and O share their reference).
+// TMEM lane i of the group's 16 holds row i's product with the rounded queries, lane i + 8 (with RoPE) the one
+// with what that rounding left; their sum is the score.  The weights go back in the same way: lane i their
+// value as bf16, lane i + 8 what is left, so that O's two lanes add up to P V with P to 17 bits.  The MMA's
+// 128 rows cost the same, filled or not, so neither costs tensor time.  Four threads hold a row (32 keys each,
+// both lanes in the same thread): a quarter of a row per thread is a quarter of the latency and of the code.
+// l_run is this thread's keys' share.
 template <int D>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, int n, bool rescale, float scale_log2,
-                                             float& m_run, float& l_run) {
-  float m8[8];
+__device__ __forceinline__ void softmax_group(uint32_t s_addr, uint32_t o_addr, int n, bool rescale, bool lo, int col,
+                                              float scale_log2, float& m_run, float& l_run) {
+  uint32_t v[64];
+  tmem_ld_frag16(s_addr, v);
+  tmem_wait_ld();
+  float s[32];  // keys 8 j + col + {0, 1}, j = 0 .. 15
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
-    uint32_t v[32];
-    tmem_ld32(s_addr + c * 32, v);
-    tmem_wait_ld();
-    if (n < c * 32 + 32) {  // keys behind the segment's end
-      const uint32_t keep = n > c * 32 ? (1u << (n - c * 32)) - 1u : 0u;
+  for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(v[4 * (e >> 1) + (e & 1)]);
+  if (lo) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!(keep & (1u << e))) v[e] = __float_as_uint(-INFINITY);
-      tmem_st32(s_addr + c * 32, v);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      m8[e] = fmax3(m8[e], __uint_as_float(v[e]), __uint_as_float(v[8 + e]));
-      m8[e] = fmax3(m8[e], __uint_as_float(v[16 + e]), __uint_as_float(v[24 + e]));
-    }
+    for (int e = 0; e < 32; ++e) s[e] += __uint_as_float(v[4 * (e >> 1) + 2 + (e & 1)]);
   }
-  if (n < BN) tmem_wait_st();
-  const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7])) *
-                   scale_log2;
+  if (n < BN) {  // keys behind the segment's end
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (8 * (e >> 1) + (e & 1) >= n - col) s[e] = -INFINITY;
+  }
+  float m4[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m4[e] = fmax3(s[e], s[4 + e], s[8 + e]);
+#pragma unroll
+  for (int c = 12; c < 28; c += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m4[e] = fmax3(m4[e], s[c + e], s[c + 4 + e]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[28 + e]);
+  float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scale_log2;
   const bool need = mx > m_run + kRescaleThreshold;
   float alpha = 1.f;
   if (need) {
@@ -402,33 +475,41 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, i
     l_run *= alpha;
     m_run = mx;
   }
-  if (__any_sync(0xffffffffu, need && rescale)) rescale_o<D>(o_addr, alpha);
+  if (__any_sync(0xffffffffu, need && rescale)) {  // the P V before has completed
+#pragma unroll 1
+    for (int c = 0; c < D / 64; ++c) {
+      uint32_t o[32];
+      tmem_ld_frag8(o_addr + c * 64, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+      tmem_st_frag8(o_addr + c * 64, o);
+    }
+  }
   const float2 sl2 = make_float2(scale_log2, scale_log2);
   const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
   const float2 nm2 = make_float2(-m_ref, -m_ref);
   float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
-    uint32_t v[32], p[16];
-    tmem_ld32(s_addr + c * 32, v);
-    tmem_wait_ld();
+  uint32_t p[32];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sl2, nm2);
-      const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-      acc[e & 1] = __fadd2_rn(acc[e & 1], pp);
-      p[e] = pack_bf16x2(pp.x, pp.y);
-    }
-    tmem_st16(s_addr + c * 16, p);  // over scores already taken
+  for (int j = 0; j < 16; ++j) {
+    const float2 x = __ffma2_rn(make_float2(s[2 * j], s[2 * j + 1]), sl2, nm2);
+    const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+    acc[j & 1] = __fadd2_rn(acc[j & 1], pp);
+    p[2 * j] = pack_bf16x2(pp.x, pp.y);
+    p[2 * j + 1] = pack_bf16x2(pp.x - __uint_as_float(p[2 * j] << 16), pp.y - __uint_as_float(p[2 * j] & 0xffff0000u));
   }
+  tmem_st_frag_bf16(s_addr, p);  // over the scores
   acc[0] = __fadd2_rn(acc[0], acc[1]);
   l_run += acc[0].x + acc[0].y;
 }
 
-// The same with the whole row in registers, each score read once and the chains independent: for pair
-// tiles, which both workers' rows fill and the tensor pipe waits for.
+// The same for a row per thread (TMEM lane), P rounded to bf16: up to 128 rows fill the MMA, and a second
+// product for what the roundings of Q and P leave would cost half as much again.  (Each of the two moves an
+// output by about as much as its own rounding to bf16 does.)  The whole row is in registers, each score read
+// once and the chains independent, as on pair tiles the tensor pipe waits for the softmax.
 template <int D>
-__device__ __forceinline__ void softmax_tile_wide(uint32_t s_addr, uint32_t o_addr, int n, bool rescale,
+__device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, int n, bool rescale,
                                                   float scale_log2, float& m_run, float& l_run) {
   uint32_t sr[BN];
 #pragma unroll
@@ -488,8 +569,17 @@ __device__ __forceinline__ void softmax_tile_wide(uint32_t s_addr, uint32_t o_ad
   tmem_st32(s_addr + 32, pr + 32);
 }
 
-// The new tokens' queries rotated at their positions, bf16 [B, n_h, D]: one thread per (row, chunks
-// of 8 dims c and c + D / 16).  The decode kernel may start as soon as this one has.
+// What the rounding of x to bf16 left, as bf16; 0 behind an infinity.
+__device__ __forceinline__ uint4 bf16_rest(const float* x, uint4 rounded) {
+  float y[8];
+  bf16x8_to_f32(rounded, y);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = fabsf(y[e]) < INFINITY ? x[e] - y[e] : 0.f;
+  return f32_to_bf16x8(y);
+}
+
+// The new tokens' queries rotated at their positions, bf16 [2, B, n_h, D] (the values and the rests): one
+// thread per (row, chunks of 8 dims c and c + D / 16).  The decode kernel may start as soon as this one has.
 template <int D>
 __global__ void __launch_bounds__(256) paged_rope_q_kernel(const __grid_constant__ PagedDecodeArgs a,
                                                            const __grid_constant__ RopeFreq f, __nv_bfloat16* out) {
@@ -530,6 +620,9 @@ __global__ void __launch_bounds__(256) paged_rope_q_kernel(const __grid_constant
   }
   o[0] = f32_to_bf16x8(x0);
   o[kCP] = f32_to_bf16x8(x1);
+  uint4* const rest = o + static_cast<long long>(a.B) * a.n_h * (D / 8);
+  rest[0] = bf16_rest(x0, o[0]);
+  rest[kCP] = bf16_rest(x1, o[kCP]);
 }
 
 // tm_q: the query rows of one request and KV head per box; tm_qn: of row_reqs requests.
@@ -631,14 +724,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t m = n - back;
               if (!warp_wait(&bars->q_free[cur.w][m & 1u], (m >> 1) & 1u, wc)) break;
             }
+            const int tile = cur.u.kind == kPair ? 2 * cur.u.b + cur.w : 2 * pl.n_pairs;  // row tile of the prefix
+            const int groups = own ? pl.own_groups : pl.prefix_groups;
+            uint64_t* const bar = &bars->q_full[cur.w][n & 1u];
             if (lane == 0) {
-              const int tile = cur.u.kind == kPair ? 2 * cur.u.b + cur.w : 2 * pl.n_pairs;  // row tile of the prefix
-              uint8_t* const dst = smem + C::kQOff + cur.w * C::kTileBytes + cur.u.q_alt * (kHalfRows * 128);
-              uint64_t* const bar = &bars->q_full[cur.w][n & 1u];
-              mbar_arrive_expect_tx(bar, (own ? G : pl.rows) * 128 * C::kBlocks);
-              for (int i = 0; i < C::kBlocks; ++i)
-                tma_load_4d(dst + i * C::kBlockBytes, own ? &tm_q : &tm_qn, bar, i * 64, 0, cur.u.g,
-                            own ? cur.u.b : tile * pl.row_reqs);
+              const int rows = groups == 0 ? (own ? G : pl.rows) : groups * (own ? pl.own_group : pl.prefix_group);
+              mbar_arrive_expect_tx(bar, rows * (groups > 0 && pl.lo_reqs > 0 ? 2 : 1) * 128 * C::kBlocks);
+            }
+            __syncwarp();
+            // a lane per box: 64 dims i of group j's rows, or of what their rounding left
+            const int i = lane & (C::kBlocks - 1), lo = (lane / C::kBlocks) & 1, j = lane / (2 * C::kBlocks);
+            if (groups > 0 ? j < groups && (!lo || pl.lo_reqs > 0) : j == 0 && !lo) {
+              int req = cur.u.b, head = 8 * j;
+              if (!own) {
+                const int before = j / pl.req_groups;  // requests (groups of G <= 8 rows) before the group's
+                req = groups > 0 ? before * pl.group_reqs : tile * pl.row_reqs;
+                head = 8 * (j - before * pl.req_groups);
+              }
+              uint8_t* const dst = smem + C::kQOff + cur.w * C::kTileBytes +
+                                   (group_row(j) + lo * 8 + cur.u.q_alt * kAltRows) * 128;
+              tma_load_4d(dst + i * C::kBlockBytes, own ? &tm_q : &tm_qn, bar, i * 64, head, cur.u.g,
+                          req + lo * pl.lo_reqs);
             }
             __syncwarp();
           }
@@ -689,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pending = 0;                   // bit w: worker w's Q K is out, its P V not yet
         bool ok = cur.template take<Cursor<D>::kLane>(bars, wc) && oth.template take<Cursor<D>::kLane>(bars, wc);
         auto issue_qk = [&](uint32_t w, uint32_t alt, int from, int to) {
-          const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + alt * (kHalfRows * 128)) >> 4);
+          const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + alt * (kAltRows * 128)) >> 4);
           const uint64_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
 #pragma unroll
           for (int kk = from; kk < to; ++kk) {
@@ -966,6 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_addr = tmem + lane_off + (w ? 128u : 0u);
     const uint32_t o_addr = tmem + lane_off + C::kOCol + (w ? D : 0);
+    constexpr uint32_t kSecond = 16u << 16;  // to a warp's second group
     const int G = a.n_h / a.n_kv;
     uint32_t sph = 0, n_done = 0;
     bool ok = true;
@@ -973,23 +1080,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece& u = cur.u;
       const int tile = u.kind == kPair ? 2 * u.b + w : 2 * pl.n_pairs;  // row tile of the prefix
       const int n_rows = u.kind == kOwn ? G : min(pl.row_reqs, a.B - tile * pl.row_reqs) * G;
-      const bool active = quad * 32 < n_rows;  // this warp holds rows of the piece
-      float m_run = -INFINITY, l_run = 0.f;
-      for (int t = u.t; t < u.t_end; ++t) {
-        if (!row_wait(&bars->s_full[w], sph, wc)) { ok = false; break; }
-        sph ^= 1;
-        if (!active) {  // padding rows: whatever their P is, it reaches only their own O
+      const int groups = u.kind == kOwn ? pl.own_groups : pl.prefix_groups;
+      const bool active = groups > 0 ? quad < groups : quad * 32 < n_rows;  // this warp holds rows of the piece
+      const int per_group = u.kind == kOwn ? pl.own_group : pl.prefix_group;
+      const bool two = quad + 4 < groups;                                  // and two groups of them
+      float m_run = -INFINITY, l_run = 0.f, m_2nd = -INFINITY, l_2nd = 0.f;
+      if (groups == 0 && active) {  // a loop of its own (both in one: 256 requests behind 16384 tokens 98 us, so 95)
+        for (int t = u.t; t < u.t_end; ++t) {
+          if (!row_wait(&bars->s_full[w], sph, wc)) { ok = false; break; }
+          sph ^= 1;
+          tc_fence_after();
+          softmax_row<D>(s_addr, o_addr, tile_keys(u, t), t > u.t, a.scale_log2, m_run, l_run);
+          tmem_wait_st();
+          tc_fence_before();
           mbar_arrive(&bars->p_full[w]);
-          continue;
         }
-        tc_fence_after();
-        if (u.kind == kPair)
-          softmax_tile_wide<D>(s_addr, o_addr, tile_keys(u, t), t > u.t, a.scale_log2, m_run, l_run);
-        else
-          softmax_tile<D>(s_addr, o_addr, tile_keys(u, t), t > u.t, a.scale_log2, m_run, l_run);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[w]);
+      } else {
+        for (int t = u.t; t < u.t_end; ++t) {
+          if (!row_wait(&bars->s_full[w], sph, wc)) { ok = false; break; }
+          sph ^= 1;
+          if (!active) {  // padding rows: whatever their P is, it reaches only their own O
+            mbar_arrive(&bars->p_full[w]);
+            continue;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (uint32_t k = 0;; k = kSecond) {
+            softmax_group<D>(s_addr + k, o_addr + k, tile_keys(u, t), t > u.t, pl.lo_reqs > 0, 2 * (lane & 3),
+                             a.scale_log2, m_run, l_run);
+            if (!two) break;
+            swap(m_run, m_2nd);
+            swap(l_run, l_2nd);
+            if (k) break;
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[w]);
+        }
       }
       if (!__all_sync(0xffffffffu, ok)) break;
       // epilogue: the piece's normalised partial and its log-sum-exp
@@ -1011,51 +1138,70 @@ __global__ void __launch_bounds__(kThreads, 1)
           o_at = pl.o2;
           l_at = pl.l2;
         }
-        row += r;
-        float* const po = ws + o_at + row * D;
-        const float inv_l = l_run > 0.f ? 1.f / l_run : l_run;  // 0: every score is -inf; NaN stays
-        if (u.kind == kOwn) {  // mostly few rows: written row by row
+        if (groups > 0) {
+#pragma unroll 1
+          for (int k = 0; k < (two ? 2 : 1); ++k) {
+            const int i = lane >> 2;                  // this thread's row of the group
+            int rr = (quad + 4 * k) * per_group + i;  // and of the piece
+            bool real = i < per_group && rr < n_rows;
+            if (u.kind == kPrefix && G > 8) {  // a request's last group may be a part of one
+              const int req = (quad + 4 * k) / pl.req_groups, head = rr - 8 * req * pl.req_groups;
+              rr = req * G + head;
+              real = head < G && rr < n_rows;
+            }
+            float l = l_run + __shfl_xor_sync(0xffffffffu, l_run, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const float inv_l = l > 0.f ? 1.f / l : l;  // 0: every score is -inf; NaN stays
+            float* const po = ws + o_at + (row + rr) * D + 2 * (lane & 3);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t o[32];
+              tmem_ld_frag8(o_addr + k * kSecond + c * 64, o);
+              tmem_wait_ld();
+              if (real) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  *reinterpret_cast<float2*>(po + c * 64 + e * 8) =
+                      make_float2((__uint_as_float(o[4 * e]) + __uint_as_float(o[4 * e + 2])) * inv_l,
+                                  (__uint_as_float(o[4 * e + 1]) + __uint_as_float(o[4 * e + 3])) * inv_l);
+              }
+            }
+            if (real && (lane & 3) == 0) ws[l_at + row + rr] = m_run + log2f(l);
+            m_run = m_2nd;
+            l_run = l_2nd;
+          }
+        } else {
+          row += r;
+          const float inv_l = l_run > 0.f ? 1.f / l_run : l_run;
+          // four lanes exchange their rows' 16-byte pieces, so that a store writes 64 contiguous bytes of each
+          // of eight rows
+          const int lj = lane & 3;
+          float* const pg = ws + o_at + (row - lj) * D + lj * 4;  // the four lanes' first row, this lane's piece
+          const int left = n_rows - (r - lj);                     // rows of the four that exist
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t orow[32];
             tmem_ld32(o_addr + c * 32, orow);
             tmem_wait_ld();
-            if (r < n_rows) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(po + c * 32 + e) =
-                    make_float4(__uint_as_float(orow[e]) * inv_l, __uint_as_float(orow[e + 1]) * inv_l,
-                                __uint_as_float(orow[e + 2]) * inv_l, __uint_as_float(orow[e + 3]) * inv_l);
+            for (int h = 0; h < 2; ++h) {
+              uint4 pc[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t* o4 = orow + 16 * h + 4 * e;
+                pc[e] = make_uint4(__float_as_uint(__uint_as_float(o4[0]) * inv_l),
+                                   __float_as_uint(__uint_as_float(o4[1]) * inv_l),
+                                   __float_as_uint(__uint_as_float(o4[2]) * inv_l),
+                                   __float_as_uint(__uint_as_float(o4[3]) * inv_l));
+              }
+              transpose_pieces(pc, lj);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < left) *reinterpret_cast<uint4*>(pg + k * D + c * 32 + h * 16) = pc[k];
             }
           }
-        } else {
-        // four lanes exchange their rows' 16-byte pieces, so that a store writes 64 contiguous bytes of each
-        // of eight rows
-        const int lj = lane & 3;
-        float* const pg = po - static_cast<long long>(lj) * D + lj * 4;  // the group's first row, this lane's piece
-        const int left = n_rows - (r - lj);                             // rows of the group that exist
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t orow[32];
-          tmem_ld32(o_addr + c * 32, orow);
-          tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint4 pc[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t* o4 = orow + 16 * h + 4 * e;
-              pc[e] = make_uint4(__float_as_uint(__uint_as_float(o4[0]) * inv_l), __float_as_uint(__uint_as_float(o4[1]) * inv_l),
-                                 __float_as_uint(__uint_as_float(o4[2]) * inv_l), __float_as_uint(__uint_as_float(o4[3]) * inv_l));
-            }
-            transpose_pieces(pc, lj);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < left) *reinterpret_cast<uint4*>(pg + k * D + c * 32 + h * 16) = pc[k];
-          }
+          if (r < n_rows) ws[l_at + row] = m_run + log2f(l_run);
         }
-        }
-        if (r < n_rows) ws[l_at + row] = m_run + log2f(l_run);
         tc_fence_before();
       }
       mbar_arrive(&bars->o_empty[w]);
@@ -1231,12 +1377,20 @@ __global__ void __launch_bounds__(WARPS * 32)
 // CTAs at most: the workspace is sized for this many (a GB300 has 152 SMs).
 constexpr int kMaxCtas = 160;
 
-PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
+PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas, bool rotate) {
   PagedTcPlan p{};
   const int G = a.n_h / a.n_kv;
   p.ctas = ctas;
-  p.row_reqs = BM / G;
+  p.group_reqs = G <= 8 ? 8 / G : 1;
+  p.req_groups = (G + 7) / 8;
+  p.own_groups = p.req_groups <= kGroups ? p.req_groups : 0;
+  const long long groups = G <= 8 ? (a.B + p.group_reqs - 1) / p.group_reqs : static_cast<long long>(a.B) * p.req_groups;
+  p.prefix_groups = groups <= kGroups ? static_cast<int>(groups) : 0;
+  p.own_group = G < 8 ? G : 8;
+  p.prefix_group = G < 8 ? G * p.group_reqs : 8;
+  p.row_reqs = p.prefix_groups ? a.B : BM / G;
   p.rows = p.row_reqs * G;
+  p.lo_reqs = rotate ? a.B : 0;
   const int row_tiles = a.prefix_len > 0 ? (a.B + p.row_reqs - 1) / p.row_reqs : 0;
   p.n_pairs = row_tiles / 2;
   p.odd = row_tiles & 1;
@@ -1252,7 +1406,7 @@ PagedTcPlan make_plan(const PagedDecodeArgs& a, int ctas) {
   p.l0 = p.l1 + pieces1 * p.rows;
   p.sums = p.l0 + pieces0 * G;
   p.q = (p.sums + a.B + 1 + 31) & ~31LL;  // 128-byte aligned
-  p.end = p.q + static_cast<long long>(a.B) * a.n_h * (a.D_qk / 2);
+  p.end = p.q + static_cast<long long>(a.B) * a.n_h * a.D_qk;
   return p;
 }
 
@@ -1333,7 +1487,7 @@ bool decode_paged_tc_supported(const PagedDecodeArgs& a, bool bf16, int rope_off
         (!rope || (rope_offset == 0 && rope_dims == a.D_qk))))
     return false;
   // the line of tiles in 32-bit points: B * n_kv * keys up to some 3e10 (a table far wider than a cache's pages)
-  const PagedTcPlan p = make_plan(a, 1);
+  const PagedTcPlan p = make_plan(a, 1, rope);
   const long long own = ((static_cast<long long>(a.max_blocks) << a.page_shift) - a.prefix_len + BN - 1) / BN;
   const double points = static_cast<double>(a.n_kv) *
                         ((static_cast<double>(p.n_pairs) + p.odd) * (static_cast<double>(p.prefix_tiles) * kTileCost + kPieceCost) +
@@ -1342,31 +1496,35 @@ bool decode_paged_tc_supported(const PagedDecodeArgs& a, bool bf16, int rope_off
 }
 
 size_t decode_paged_tc_workspace(const PagedDecodeArgs& a) {
-  return static_cast<size_t>(make_plan(a, kMaxCtas).end) * sizeof(float);
+  return static_cast<size_t>(make_plan(a, kMaxCtas, true).end) * sizeof(float);
 }
 
 cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st,
                                    int* launches) {
   // no more CTAs than the call can have tiles
   const long long own = ((static_cast<long long>(a.max_blocks) << a.page_shift) - a.prefix_len + BN - 1) / BN;
-  const PagedTcPlan p = make_plan(a, 1);
+  const bool rotate = rope.n_pairs > 0;
+  const PagedTcPlan p = make_plan(a, 1, rotate);
   const long long most = static_cast<long long>(a.n_kv) *
                          (static_cast<long long>(p.n_pairs + p.odd) * p.prefix_tiles + own * a.B);
   long long ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   if (most < ctas) ctas = most > 0 ? most : 1;
-  const PagedTcPlan pl = make_plan(a, static_cast<int>(ctas));
+  const PagedTcPlan pl = make_plan(a, static_cast<int>(ctas), rotate);
   // query rows by (dim, head of the group, KV head, request); K and V by (dim, KV head, row in page, page),
   // a page per box (half of a 256-token page)
-  const void* q = rope.n_pairs > 0 ? static_cast<const float*>(a.workspace) + pl.q : a.q;
+  const void* q = rotate ? static_cast<const float*>(a.workspace) + pl.q : a.q;
   const unsigned long long hs = static_cast<unsigned long long>(a.D_qk) * 2, page = 1ull << a.page_shift;
   const unsigned long long ks = hs * a.n_kv, vs = static_cast<unsigned long long>(a.v_token_stride) * 2;
   const int G = a.n_h / a.n_kv, box_rows = page < 128 ? static_cast<int>(page) : 128;
+  const int g8 = G < 8 ? G : 8;  // heads per group of rows
+  const int reqs = a.B + pl.lo_reqs;
   CUtensorMap maps[4];
   // (a head's row of 64 dims is 128 bytes: fetched with its neighbour's, half of the traffic would be wasted)
   const bool wide = a.D_qk == 128;
   const int rows = static_cast<int>(page);
-  if (!make_map_box(&maps[0], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, 1, 1, wide) ||
-      !make_map_box(&maps[1], q, a.D_qk, G, a.n_kv, a.B, hs, hs * G, hs * a.n_h, G, 1, pl.row_reqs, wide) ||
+  if (!make_map_box(&maps[0], q, a.D_qk, G, a.n_kv, reqs, hs, hs * G, hs * a.n_h, pl.own_groups ? g8 : G, 1, 1, wide) ||
+      !make_map_box(&maps[1], q, a.D_qk, G, a.n_kv, reqs, hs, hs * G, hs * a.n_h, pl.prefix_groups ? g8 : G, 1,
+                    pl.prefix_groups ? pl.group_reqs : pl.row_reqs, wide) ||
       !make_map_box(&maps[2], a.k_pages, a.D_qk, a.n_kv, rows, a.n_pages, hs, ks, ks * page, 1, box_rows, 1, wide) ||
       !make_map_box(&maps[3], a.v_pages, a.D_v, a.n_kv, rows, a.n_pages, hs, vs, vs * page, 1, box_rows, 1, wide))
     return cudaErrorInvalidValue;
