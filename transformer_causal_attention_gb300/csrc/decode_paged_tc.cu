@@ -338,58 +338,40 @@ struct Cursor {
 };
 
 // ------------------------------------------------------------------------------------- softmax of a tile
-// 16 TMEM lanes as MMA fragments.  32-bit columns, 128 or 64 of them: thread t has, for j = 0, 1, .., columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// 16 TMEM lanes as MMA fragments, 32 columns of 32 bits: thread t has, for j = 0 .. 3, columns
 // 8 j + 2 (t & 3) + {0, 1} of lane t / 4 in r[4 j], r[4 j + 1] and of lane t / 4 + 8 in r[4 j + 2], r[4 j + 3].
-__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 128 columns of bf16 in 64 of 32 bits: the pair 8 j + 2 (t & 3) + {0, 1} of lane t / 4 in r[2 j], of lane
-// t / 4 + 8 in r[2 j + 1].
+// 32 columns of bf16 in 16 of 32 bits: the pair 8 j + 2 (t & 3) + {0, 1} of lane t / 4 in r[2 j], of lane t / 4 + 8
+// in r[2 j + 1].
 __device__ __forceinline__ void tmem_st_frag_bf16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 
@@ -435,37 +417,42 @@ __device__ __forceinline__ void transpose_pieces(uint4* pc, int lj) {
 // TMEM lane i of the group's 16 holds row i's product with the rounded queries, lane i + 8 (with RoPE) the one
 // with what that rounding left; their sum is the score.  The weights go back in the same way: lane i their
 // value as bf16, lane i + 8 what is left, so that O's two lanes add up to P V with P to 17 bits.  The MMA's
-// 128 rows cost the same, filled or not, so neither costs tensor time.  Four threads hold a row (32 keys each,
-// both lanes in the same thread): a quarter of a row per thread is a quarter of the latency and of the code.
-// l_run is this thread's keys' share.
+// 128 rows cost the same, filled or not, so neither costs tensor time.  Four threads hold a row, both lanes of
+// a key in the same thread; l_run is this thread's keys' share.
+// 32 keys at a time and every score read twice, for the sake of a short loop: many pieces are a tile or two,
+// and the roles' code is fetched again for each (1024 requests of 100 keys: 117 us; 64 keys at a time 126,
+// all 128 at once 136).
 template <int D>
 __device__ __forceinline__ void softmax_group(uint32_t s_addr, uint32_t o_addr, int n, bool rescale, bool lo, int col,
                                               float scale_log2, float& m_run, float& l_run) {
-  uint32_t v[64];
-  tmem_ld_frag16(s_addr, v);
-  tmem_wait_ld();
-  float s[32];  // keys 8 j + col + {0, 1}, j = 0 .. 15
+  const auto scores = [&](float* s, int c) {
+    uint32_t v[16];
+    tmem_ld_frag(s_addr + c, v);
+    tmem_wait_ld();
 #pragma unroll
-  for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(v[4 * (e >> 1) + (e & 1)]);
-  if (lo) {
+    for (int e = 0; e < 8; ++e) s[e] = __uint_as_float(v[4 * (e >> 1) + (e & 1)]);
+    if (lo) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) s[e] += __uint_as_float(v[4 * (e >> 1) + 2 + (e & 1)]);
+      for (int e = 0; e < 8; ++e) s[e] += __uint_as_float(v[4 * (e >> 1) + 2 + (e & 1)]);
+    }
+    if (n < c + 32) {  // keys behind the segment's end
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * (e >> 1) + (e & 1) >= n - col - c) s[e] = -INFINITY;
+    }
+  };
+  float mx = -INFINITY, m2 = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < BN; c += 32) {
+    float s[8];
+    scores(s, c);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      mx = fmax3(mx, s[e], s[e + 1]);
+      m2 = fmax3(m2, s[e + 2], s[e + 3]);
+    }
   }
-  if (n < BN) {  // keys behind the segment's end
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (8 * (e >> 1) + (e & 1) >= n - col) s[e] = -INFINITY;
-  }
-  float m4[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) m4[e] = fmax3(s[e], s[4 + e], s[8 + e]);
-#pragma unroll
-  for (int c = 12; c < 28; c += 8)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m4[e] = fmax3(m4[e], s[c + e], s[c + 4 + e]);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[28 + e]);
-  float mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+  mx = fmaxf(mx, m2);
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scale_log2;
   const bool need = mx > m_run + kRescaleThreshold;
@@ -477,37 +464,45 @@ __device__ __forceinline__ void softmax_group(uint32_t s_addr, uint32_t o_addr, 
   }
   if (__any_sync(0xffffffffu, need && rescale)) {  // the P V before has completed
 #pragma unroll 1
-    for (int c = 0; c < D / 64; ++c) {
-      uint32_t o[32];
-      tmem_ld_frag8(o_addr + c * 64, o);
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[16];
+      tmem_ld_frag(o_addr + c, o);
       tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-      tmem_st_frag8(o_addr + c * 64, o);
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+      tmem_st_frag(o_addr + c, o);
     }
   }
   const float2 sl2 = make_float2(scale_log2, scale_log2);
   const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
   const float2 nm2 = make_float2(-m_ref, -m_ref);
   float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  uint32_t p[32];
+#pragma unroll 1
+  for (int c = 0; c < BN; c += 32) {
+    float s[8];
+    scores(s, c);
+    uint32_t p[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float2 x = __ffma2_rn(make_float2(s[2 * j], s[2 * j + 1]), sl2, nm2);
-    const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-    acc[j & 1] = __fadd2_rn(acc[j & 1], pp);
-    p[2 * j] = pack_bf16x2(pp.x, pp.y);
-    p[2 * j + 1] = pack_bf16x2(pp.x - __uint_as_float(p[2 * j] << 16), pp.y - __uint_as_float(p[2 * j] & 0xffff0000u));
+    for (int j = 0; j < 8 / 2; ++j) {
+      const float2 x = __ffma2_rn(make_float2(s[2 * j], s[2 * j + 1]), sl2, nm2);
+      const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      acc[j & 1] = __fadd2_rn(acc[j & 1], pp);
+      p[2 * j] = pack_bf16x2(pp.x, pp.y);
+      p[2 * j + 1] = pack_bf16x2(pp.x - __uint_as_float(p[2 * j] << 16), pp.y - __uint_as_float(p[2 * j] & 0xffff0000u));
+    }
+    tmem_st_frag_bf16(s_addr + c / 2, p);  // over scores already taken
   }
-  tmem_st_frag_bf16(s_addr, p);  // over the scores
   acc[0] = __fadd2_rn(acc[0], acc[1]);
   l_run += acc[0].x + acc[0].y;
 }
 
-// The same for a row per thread (TMEM lane), P rounded to bf16: up to 128 rows fill the MMA, and a second
-// product for what the roundings of Q and P leave would cost half as much again.  (Each of the two moves an
-// output by about as much as its own rounding to bf16 does.)  The whole row is in registers, each score read
-// once and the chains independent, as on pair tiles the tensor pipe waits for the softmax.
+// The same for a row per thread (TMEM lane), with Q and P rounded to bf16: each of the two moves an output by
+// about as much as its own rounding to bf16 does (0.0029 of the largest output against 64 bits, instead of
+// 0.0017).  The rows fill the MMA here, and the products for what the roundings leave would be more MMAs: for P's,
+// 256 requests behind 16384 tokens took 138 us, so 92; for Q's there is no shared memory.
+// The whole row is in registers, each score read once and the chains independent: on pair tiles the tensor pipe
+// waits for the softmax (0.6 us of a worker's 1.6 us per tile; handing P over in two halves, for the first half's
+// P V to run beside the second's exponentials, made it 1.7).
 template <int D>
 __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, int n, bool rescale,
                                                   float scale_log2, float& m_run, float& l_run) {
@@ -1154,14 +1149,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv_l = l > 0.f ? 1.f / l : l;  // 0: every score is -inf; NaN stays
             float* const po = ws + o_at + (row + rr) * D + 2 * (lane & 3);
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-              uint32_t o[32];
-              tmem_ld_frag8(o_addr + k * kSecond + c * 64, o);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[16];
+              tmem_ld_frag(o_addr + k * kSecond + c * 32, o);
               tmem_wait_ld();
               if (real) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  *reinterpret_cast<float2*>(po + c * 64 + e * 8) =
+                for (int e = 0; e < 4; ++e)
+                  *reinterpret_cast<float2*>(po + c * 32 + e * 8) =
                       make_float2((__uint_as_float(o[4 * e]) + __uint_as_float(o[4 * e + 2])) * inv_l,
                                   (__uint_as_float(o[4 * e + 1]) + __uint_as_float(o[4 * e + 3])) * inv_l);
               }
@@ -1179,26 +1174,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* const pg = ws + o_at + (row - lj) * D + lj * 4;  // the four lanes' first row, this lane's piece
           const int left = n_rows - (r - lj);                     // rows of the four that exist
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t orow[32];
-            tmem_ld32(o_addr + c * 32, orow);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t orow[16];
+            tmem_ld16(o_addr + c * 16, orow);
             tmem_wait_ld();
+            uint4 pc[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint4 pc[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t* o4 = orow + 16 * h + 4 * e;
-                pc[e] = make_uint4(__float_as_uint(__uint_as_float(o4[0]) * inv_l),
-                                   __float_as_uint(__uint_as_float(o4[1]) * inv_l),
-                                   __float_as_uint(__uint_as_float(o4[2]) * inv_l),
-                                   __float_as_uint(__uint_as_float(o4[3]) * inv_l));
-              }
-              transpose_pieces(pc, lj);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (k < left) *reinterpret_cast<uint4*>(pg + k * D + c * 32 + h * 16) = pc[k];
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* o4 = orow + 4 * e;
+              pc[e] = make_uint4(__float_as_uint(__uint_as_float(o4[0]) * inv_l),
+                                 __float_as_uint(__uint_as_float(o4[1]) * inv_l),
+                                 __float_as_uint(__uint_as_float(o4[2]) * inv_l),
+                                 __float_as_uint(__uint_as_float(o4[3]) * inv_l));
             }
+            transpose_pieces(pc, lj);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < left) *reinterpret_cast<uint4*>(pg + k * D + c * 16) = pc[k];
           }
           if (r < n_rows) ws[l_at + row] = m_run + log2f(l_run);
         }
