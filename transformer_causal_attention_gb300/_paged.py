@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -171,11 +172,16 @@ def kv_append_paged(k_new, v_new, k_pages, v_pages, slots, positions=None, *, ro
     _b._check(rc, "attn_kv_append_paged")
 
 
+@functools.lru_cache(maxsize=256)  # a serving loop asks with the same sizes step after step
+def _workspace_size(*sizes) -> int:
+    return _lib().attn_decode_paged_workspace_size(*sizes)
+
+
 def decode_paged_workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len=0,
                                 dtype=torch.bfloat16) -> int:
     """Bytes of scratch of decode_paged (prefix_len = 0) or decode_shared."""
-    n = _lib().attn_decode_paged_workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len,
-                                                _b.ATTN_BF16 if dtype == torch.bfloat16 else _b.ATTN_F32)
+    n = _workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len,
+                        _b.ATTN_BF16 if dtype == torch.bfloat16 else _b.ATTN_F32)
     if n == _NO_SIZE:
         raise ValueError("invalid paged decode sizes")
     return n
@@ -217,8 +223,7 @@ def _decode(q, k_pages, v_pages, prefix_pages, block_table, seqlens, rope_base, 
         else:
             lse_t = torch.empty((B, n_h), dtype=torch.float32, device=device) if lse else None
         if workspace is None:
-            need = lib.attn_decode_paged_workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len,
-                                                        code & 0xff)
+            need = _workspace_size(B, n_h, n_kv, D_qk, D_v, page_size, max_blocks, prefix_len, code & 0xff)
             # invalid sizes: the call itself says what is wrong with them
             workspace = torch.empty(16 if need == _NO_SIZE else need, dtype=torch.uint8, device=device)
         else:
