@@ -15,7 +15,7 @@
  *    ATTN_ERR_UNSUPPORTED) and n_pages * page_size < 2^31 (else ATTN_ERR_ARG).
  *  - block_table is DEVICE int32 [B, max_blocks]: entry (b, j) is the page that
  *    holds tokens j * page_size .. of request b.  Entries behind a request's
- *    last token are never read.
+ *    last token are never read.  max_blocks * page_size < 2^31 (ATTN_ERR_ARG).
  *  - A page index outside [0, n_pages) in front of a request's last token reads
  *    as keys and values of zero; nothing outside the cache is read or written.
  *  - int32 pointers are 4-byte aligned, all others 16-byte (ATTN_ERR_ALIGN).
@@ -58,7 +58,8 @@ extern "C" {
  *   block_table  [B, max_blocks]: the entries of newly taken pages are written,
  *                the entry of each request's partly filled last page is read.
  *   free_pages   DEVICE int32 [free_cap]; n_free DEVICE int32 [1]: pages on the
- *                stack (clamped to 0 .. free_cap).
+ *                stack (clamped to 0 .. free_cap).  free_cap <= n_pages (else
+ *                ATTN_ERR_ARG).
  *   seqlens [B], cu_new [B + 1], slots and positions [max_tokens], n_left [1]:
  *                outputs, int32.  Rows behind the last new token get -1.
  *                n_left is the stack's height after the step; a released page is
@@ -109,9 +110,14 @@ ATTN_API size_t attn_decode_paged_workspace_size(int B, int n_h, int n_kv, int D
  *            -inf.  Values above max_blocks * page_size are clamped to it.
  *   v_token_stride  elements between consecutive slots of v_pages (0: n_kv * D_v);
  *            MLA passes v_pages = k_pages and v_token_stride = D_qk.
- * Other arguments, sizes and errors as attn_decode.  bf16 with D_qk = D_v = 64 or
- * 128, and RoPE over the whole head or none, runs on the tensor cores; other
- * shapes on CUDA cores.
+ * Outputs must not overlap inputs, the workspace or each other.
+ * Other arguments, sizes and errors as attn_decode.  On the tensor cores run bf16 with
+ * D_qk = D_v = 64 or 128, at most 128 query heads per KV head and RoPE over the whole
+ * head or none, and the MLA-absorbed shape (128 heads over one of 576 dims, v_pages =
+ * k_pages); other shapes on CUDA cores.  Sums are fp32; queries after RoPE and softmax
+ * weights are rounded to bf16 on the way into the tensor cores, but for pieces of at
+ * most 64 rows (a request's own keys under up to 64 heads per KV head, the shared
+ * prefix of a small batch), which keep what that rounding leaves.
  */
 ATTN_API int attn_decode_paged(const void* q, const void* k_pages, const void* v_pages, int v_token_stride,
                                const int* block_table, const int* seqlens, void* out, float* lse, int B, int n_h,

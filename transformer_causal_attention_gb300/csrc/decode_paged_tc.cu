@@ -51,6 +51,9 @@
 // one-tile piece took 10 us, the instruction fetches of the SMs saturating their shared
 // caches.  For the same reason the queries are rotated before, by a kernel of their own
 // that this one overlaps with its start (programmatic launch).
+// Measured (32 query heads over 8 KV heads, D = 128): 59 requests of 4096 to 8192 keys, 1.49 GB in 225 to 232 us
+// (0.95 to 0.98 of the card's copy rate), whether pages hold 16 tokens or 128; 64 requests behind 32768
+// shared tokens 57 us (0.53 of the copy rate), 256 behind 16384 103 us (670 TFLOP/s).
 // TMEM: S/P of the workers in columns [0, 128) and [128, 256), O behind them.
 #include <math.h>
 
@@ -620,7 +623,8 @@ __global__ void __launch_bounds__(256) paged_rope_q_kernel(const __grid_constant
   rest[kCP] = bf16_rest(x1, o[kCP]);
 }
 
-// tm_q: the query rows of one request and KV head per box; tm_qn: of row_reqs requests.
+// tm_q: boxes of the query rows of one request and KV head (own pieces: all G of them, or a group's); tm_qn: of
+// the requests of a prefix piece (a row tile's, or a group's).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedDecodeArgs a, const __grid_constant__ PagedTcPlan pl,
