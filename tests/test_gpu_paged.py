@@ -256,6 +256,14 @@ def test_decode_of_empty_batch_places_only(lib, prefix):
     check_decode(lib, [prefix, 0, -1, -2**31], prefix, 16, 6, 2, 96, 96)
 
 
+@pytest.mark.parametrize("prefix,D,dtype", [(0, 128, "bf16"), (64, 128, "bf16"), (64, 64, "bf16"), (64, 96, "bf16"),
+                                            (64, 64, "f32")])
+def test_lowest_lengths_are_empty_places(lib, prefix, D, dtype):
+    """Between live requests: the lowest lengths less a prefix do not fit 32 bits."""
+    low = -2**31
+    check_decode(lib, [400, low, 700, low + 1, low + prefix, 0, 300], prefix, 16, 8, 2, D, D, dtype=dtype)
+
+
 @pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "bf16"), (96, "bf16"), (64, "f32")])
 def test_lengths_above_the_table_are_clamped(lib, D, dtype):
     dt = TYPES[dtype]

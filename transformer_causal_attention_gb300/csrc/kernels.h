@@ -132,9 +132,9 @@ struct PagedDecodeArgs {
   unsigned long long wait_limit_ns;
 };
 
-// Keys of request b; at most prefix_len (0 without a prefix) for an empty place of the batch.
+// Keys of request b, 0 or more; at most prefix_len (0 without a prefix) for an empty place of the batch.
 __device__ __forceinline__ int paged_len(const PagedDecodeArgs& a, int b) {
-  return min(a.seqlens[b], a.max_blocks << a.page_shift);  // the table's tokens fit 32 bits (checked by the caller)
+  return min(max(a.seqlens[b], 0), a.max_blocks << a.page_shift);  // the table's tokens fit 32 bits (checked by the caller)
 }
 
 // Each launcher returns the launch error (cudaSuccess when enqueued) and adds
