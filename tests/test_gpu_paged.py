@@ -321,6 +321,33 @@ def test_large_scores(lib, dtype, D):
     assert np.max(np.abs(to_np(lse) - want_lse)) <= e + 1e-5 * np.max(np.abs(want_lse))
 
 
+@pytest.mark.parametrize("B,G,D,dtype", [(4, 4, 128, "bf16"), (40, 4, 128, "bf16"), (80, 4, 64, "bf16"), (4, 4, 96, "bf16"),
+                                         (3, 2, 96, "bf16"), (3, 2, 64, "f32"), (20, 2, 64, "f32"), (3, 1, 256, "f32")])
+@pytest.mark.parametrize("prefix", [0, 128])
+def test_nan_of_a_live_token_shows(lib, B, G, D, dtype, prefix):
+    """A NaN in a query, a key or a value reaches the rows that see it, and no other."""
+    dt = TYPES[dtype]
+    lens = [prefix + 40 + 150 * (b % 3) for b in range(B)]
+    k, v, table, pre, k_of, v_of = ref.make_cache(lens, prefix, 16, 2, D, D, dt, seed=8)
+    q = torch.randn(B, 2 * G, D, generator=torch.Generator().manual_seed(5)).to(dt)
+    want, want_lse, err = ref.attend(q, k_of, v_of)
+    own = table[:, prefix // 16:]
+    q[1, 0] = float("nan")                         # head 0 of request 1
+    k[own[0, 1], 3, 1, 7] = float("nan")           # a key of request 0, KV head 1
+    v[own[2, 2], 15, 0, 9] = float("nan")          # a value of request 2, KV head 0, dim 9
+    if prefix:
+        out, lse = lib.decode_shared(q.to(DEV), k.to(DEV), v.to(DEV), pre.to(DEV), table.to(DEV), ints(lens), lse=True)
+    else:
+        out, lse = lib.decode_paged(q.to(DEV), k.to(DEV), v.to(DEV), table.to(DEV), ints(lens), lse=True)
+    out, lse = to_np(out), to_np(lse)
+    bad = np.zeros(out.shape, bool)
+    bad[1, 0] = bad[0, G:] = bad[2, :G, 9] = True
+    np.testing.assert_array_equal(np.isnan(out), bad)
+    np.testing.assert_array_equal(np.isnan(lse), bad.all(-1))
+    out[bad], lse[bad.all(-1)] = want[bad], want_lse[bad.all(-1)]
+    check_result(out, lse, want, want_lse, err, v_of, dtype)
+
+
 # The rows of a piece on the tensor cores: in groups of eight with the rests of their queries (own keys of up to
 # 64 heads per KV head; a prefix's of up to eight groups), or one after the other.
 ROWS = [

@@ -257,17 +257,16 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a
     if (r0 + i >= n_rows) continue;
     float M = -INFINITY;
     for (int w = 0; w < kHalfWarps; ++w) M = fmaxf(M, red_m[w * HG + i]);
+    const float m_ref = M == -INFINITY ? 0.f : M;
     float num = 0.f, den = 0.f;
     for (int w = 0; w < kHalfWarps; ++w) {
-      const float mw = red_m[w * HG + i];
-      if (mw == -INFINITY) continue;  // this half-warp saw no key
-      const float sc = fast_exp2(mw - M);
+      const float sc = fast_exp2(red_m[w * HG + i] - m_ref);  // 0 for a half-warp that saw no key; NaN in its sums stays
       num = fmaf(red_o[(w * HG + i) * NVC * 128 + d], sc, num);
       den = fmaf(red_l[w * HG + i], sc, den);
     }
     const long long slot = (static_cast<long long>(row_b(i)) * a.n_h + row_h(i)) * ns +
                            (PREFIX ? split : plan.n_pre + split);
-    ws_o[slot * a.D_v + d] = den > 0.f ? num / den : 0.f;  // den = 0: every score is -inf, the weight is 0
+    ws_o[slot * a.D_v + d] = den > 0.f ? num / den : den;  // 0: every score is -inf, the weight is 0; NaN stays
     if (d == 0) ws_lse[slot] = M + log2f(den);
   }
 }
