@@ -15,7 +15,8 @@
  *    ATTN_ERR_UNSUPPORTED) and n_pages * page_size < 2^31 (else ATTN_ERR_ARG).
  *  - block_table is DEVICE int32 [B, max_blocks]: entry (b, j) is the page that
  *    holds tokens j * page_size .. of request b.  Entries behind a request's
- *    last token are never read.  max_blocks * page_size < 2^31 (ATTN_ERR_ARG).
+ *    last token are never read.  max_blocks * page_size <= 2^31 - 2^16
+ *    (else ATTN_ERR_ARG).
  *  - A page index outside [0, n_pages) in front of a request's last token reads
  *    as keys and values of zero; nothing outside the cache is read or written.
  *  - int32 pointers are 4-byte aligned, all others 16-byte (ATTN_ERR_ALIGN).

@@ -123,6 +123,7 @@ def test_decode_refusals(lib):
     assert decode(lib, ws_bytes=16) == -6
     assert decode(lib, n_pages=1 << 27) == -1
     assert decode(lib, max_blocks=1 << 27) == -1
+    assert decode(lib, max_blocks=(1 << 27) - 4095) == -1  # past 2^31 - 2^16 tokens
     assert decode(lib, B=1 << 20, n_h=1 << 12, n_kv=1 << 11) == -1
 
 
@@ -130,7 +131,9 @@ def test_workspace_size(lib):
     f = lib.attn_decode_paged_workspace_size
     assert 0 < f(59, 32, 8, 128, 128, 64, 128, 0, 1) < 256 << 20
     assert 0 < f(59, 32, 8, 128, 128, 64, 128, 4096, 1) < 256 << 20
-    for bad in ((0, 32, 8, 128, 128, 64, 128, 0, 1), (4, 32, 5, 128, 128, 64, 128, 0, 1),
+    assert 0 < f(1, 1, 1, 8, 8, 16, (1 << 27) - 4096, 0, 1) < NO_SIZE
+    assert 0 < f(1, 1, 1, 8, 8, 16, (1 << 27) - 4096, (1 << 31) - (1 << 16), 1) < NO_SIZE
+    for bad in ((1, 1, 1, 8, 8, 16, (1 << 27) - 4095, 0, 1), (0, 32, 8, 128, 128, 64, 128, 0, 1), (4, 32, 5, 128, 128, 64, 128, 0, 1),
                 (4, 32, 8, 128, 128, 60, 128, 0, 1), (4, 32, 8, 128, 128, 64, 128, 100, 1),
                 (4, 32, 8, 128, 128, 64, 128, 64 * 129, 1), (4, 32, 8, 128, 128, 64, 128, 0, 9)):
         assert f(*bad) == NO_SIZE

@@ -18,12 +18,16 @@ int page_shift_of(int page_size) {
   return -1;
 }
 
+// Tokens of a table row: 32-bit positions with room for a few tiles or chunks more, which loops over keys step past.
+constexpr long long kMaxRequestTokens = (1LL << 31) - (1 << 16);
+
 // The sizes of a paged cache and of a table over it.
 int check_pages(int n_pages, int page_size, int max_blocks, int* shift) {
   if (n_pages <= 0 || page_size <= 0 || max_blocks <= 0) return ATTN_ERR_ARG;
   *shift = page_shift_of(page_size);
   if (*shift < 0) return ATTN_ERR_UNSUPPORTED;
-  if ((static_cast<long long>(n_pages) << *shift) > INT_MAX || (static_cast<long long>(max_blocks) << *shift) > INT_MAX)
+  if ((static_cast<long long>(n_pages) << *shift) > INT_MAX ||
+      (static_cast<long long>(max_blocks) << *shift) > kMaxRequestTokens)
     return ATTN_ERR_ARG;
   return ATTN_OK;
 }
