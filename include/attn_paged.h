@@ -81,7 +81,8 @@ ATTN_API int attn_page_plan(const int* lens, const int* n_new, int* block_table,
  * outside [0, n_pages * page_size) are skipped.
  *
  *   k_new   [T, n_kv, D_qk]; v_new [T, n_kv, D_v], or NULL when values alias the
- *           keys (MLA); v_token_stride as in attn_decode (0 = n_kv * D_v).
+ *           keys (MLA), which v_pages must not overlap otherwise (ATTN_ERR_ARG);
+ *           v_token_stride as in attn_decode (0 = n_kv * D_v).
  *   slots   DEVICE int32 [T]; slots of one call must differ (of two rows with the
  *           same slot either may be stored, mixed in pieces of 8 dims).
  *   positions DEVICE int32 [T]; may be NULL when rope_base <= 0.

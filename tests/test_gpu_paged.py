@@ -569,6 +569,10 @@ def test_calls_refuse_what_does_not_fit(lib):
         rest = {x: y for x, y in bad.items() if x not in a}
         with pytest.raises((ValueError, TypeError)):
             lib.decode_paged(a["q"], a["k"], a["v"], a["t"], a["sl"], **rest)
+    with pytest.raises(ValueError, match="slice"):     # the slice's heads are not D_v apart
+        lib.decode_paged(q, k, k[..., :32], t, sl)
+    with pytest.raises(lib.AttnError):                 # values over the keys
+        lib.kv_append_paged(k[0, :2], k[0, :2], k, k, ints([0, 1]))
     with pytest.raises(lib.AttnError):
         lib.decode_shared(q, k, k.clone(), ints([0, 1, 2]), t, sl)   # a prefix longer than the table
     with pytest.raises(lib.AttnError):

@@ -86,6 +86,9 @@ def test_kv_append_paged_refusals(lib):
     assert append(lib, k=P[0] + 8) == -3
     assert append(lib, slots=P[4] + 2) == -3
     assert append(lib, n_pages=1 << 27) == -1
+    for vp in (P[2], P[2] + 16, P[2] + 2 * 64 * 2 * 127):  # values over the keys
+        assert append(lib, vp=vp) == -1
+    assert append(lib, vp=P[2] - 2 * 64 * 2 * 16) == -1
 
 
 def decode(lib, q=P[0], kp=P[1], vp=P[2], ldv=0, pages=P[3], prefix=64, table=P[4], sl=P[5], out=P[6], lse=None, B=2,

@@ -84,8 +84,8 @@ def _on(device, stream):
 
 
 def _page_dims(k_pages, v_pages, device):
-    """(n_pages, page_size, n_kv, D_qk, D_v, v_token_stride) of a cache; v_pages contiguous, or a leading slice of
-    k_pages' last dim (MLA: the values are the first D_v latent dims)."""
+    """(n_pages, page_size, n_kv, D_qk, D_v, v_token_stride) of a cache; v_pages contiguous, or a leading slice of the
+    last dim of k_pages with its one head (MLA: the values are the first D_v latent dims)."""
     ks, vs = k_pages.shape, v_pages.shape
     if len(ks) != 4 or len(vs) != 4 or vs[:3] != ks[:3]:
         raise ValueError("k_pages and v_pages must be [n_pages, page_size, n_kv, D] with the same first three sizes")
@@ -93,10 +93,11 @@ def _page_dims(k_pages, v_pages, device):
         raise TypeError("k_pages and v_pages must share a dtype and a device")
     if v_pages.is_contiguous():
         ldv = 0
-    elif v_pages.data_ptr() == k_pages.data_ptr() and v_pages.stride() == k_pages.stride() and vs[3] <= ks[3]:
+    elif (v_pages.data_ptr() == k_pages.data_ptr() and v_pages.stride() == k_pages.stride() and vs[3] <= ks[3]
+          and ks[2] == 1):
         ldv = v_pages.stride(1)
     else:
-        raise ValueError("v_pages must be contiguous or a leading slice of k_pages' last dim")
+        raise ValueError("v_pages must be contiguous or a leading slice of the last dim of k_pages (of one head)")
     return ks[0], ks[1], ks[2], ks[3], vs[3], ldv
 
 

@@ -201,6 +201,8 @@ int attn_kv_append_paged(const void* k_new, const void* v_new, void* k_pages, vo
   const long long ldv = v_token_stride ? v_token_stride : static_cast<long long>(n_kv) * D_v;
   if (v_new && ldv < static_cast<long long>(n_kv) * D_v) return ATTN_ERR_ARG;  // slots would overlap
   if (v_new && ldv % 8) return ATTN_ERR_UNSUPPORTED;
+  const size_t slots_all = static_cast<size_t>(n_pages) << shift, e = bf16 ? 2 : 4;
+  if (v_new && overlap(k_pages, slots_all * n_kv * D_qk * e, v_pages, slots_all * ldv * e)) return ATTN_ERR_ARG;
   if (!aligned16(k_new) || !aligned16(k_pages) || (v_new && (!aligned16(v_new) || !aligned16(v_pages))) ||
       !aligned4(slots) || !aligned4(positions))
     return ATTN_ERR_ALIGN;
@@ -220,9 +222,9 @@ int attn_kv_append_paged(const void* k_new, const void* v_new, void* k_pages, vo
   a.positions = positions;
   a.n_slots = n_pages << shift;
   int launches = 0;
-  const cudaError_t e = launch_kv_append_paged(a, make_rope(rope_base, rope ? rope_dims : 0, half), bf16,
-                                               static_cast<cudaStream_t>(stream), &launches);
-  return finish(e, launches);
+  const cudaError_t err = launch_kv_append_paged(a, make_rope(rope_base, rope ? rope_dims : 0, half), bf16,
+                                                 static_cast<cudaStream_t>(stream), &launches);
+  return finish(err, launches);
 }
 
 size_t attn_decode_paged_workspace_size(int B, int n_h, int n_kv, int D_qk, int D_v, int page_size, int max_blocks,
