@@ -395,6 +395,42 @@ def test_grouped_rows_keep_their_rests(lib, lens, prefix, G, D):
     assert np.max(np.abs(to_np(lse) - want_lse)[live]) <= e + 2.0 ** -16 * np.max(np.abs(want_lse[live])) + 2.0 ** -16
 
 
+@pytest.mark.parametrize("n_h,n_kv,D,Dv,dtype,slots", [
+    (32, 8, 128, 128, "bf16", 2_300_032), (12, 6, 96, 96, "bf16", 3_900_032), (8, 8, 128, 128, "f32", 2_300_032),
+    (128, 1, 576, 512, "bf16", 3_900_032)])
+def test_offsets_past_32_bits(lib, n_h, n_kv, D, Dv, dtype, slots):
+    """A cache of more than 2^31 elements: pages at its far end, written and read, give what a small cache gives."""
+    dt, page, mla = TYPES[dtype], 64, D == 576
+    lens, prefix = [200, 130, 64 + 1], 64
+    assert slots * n_kv * D > 2**31
+    k, v, table, pre, _, _ = ref.make_cache(lens, prefix, page, n_kv, D, Dv, dt, alias=mla)
+    n = k.shape[0]
+    shift = slots // page - n
+    rope = dict(rope_base=1e4, rope_offset=512, rope_dims=64) if mla else dict(rope_base=1e4)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(3, n_h, D, generator=g).to(dt).to(DEV)
+    k_new = torch.randn(3, n_kv, D, generator=g).to(dt).to(DEV)
+    v_new = None if mla else torch.randn(3, n_kv, Dv, generator=g).to(dt).to(DEV)
+
+    def run(k, v, first):
+        last = [int(table[b, (L - 1) // page]) * page + (L - 1) % page for b, L in enumerate(lens)]
+        lib.kv_append_paged(k_new, v_new, k, v, ints([first * page + x for x in last]), ints([L - 1 for L in lens]), **rope)
+        t, p = (table + first).to(DEV), (pre + first).to(DEV)
+        whole = torch.cat([p.repeat(3, 1), t[:, 1:]], 1).contiguous()
+        return (lib.decode_shared(q, k, v, p, t, ints(lens), **rope, lse=True) +
+                lib.decode_paged(q, k, v, whole, ints(lens), **rope, lse=True))
+
+    ks, big_k = k.to(DEV), torch.empty(slots // page, page, n_kv, D, dtype=dt, device=DEV)
+    big_k[-n:] = ks
+    if mla:
+        vs, big_v = ks[..., :Dv], big_k[..., :Dv]
+    else:
+        vs, big_v = v.to(DEV), torch.empty(slots // page, page, n_kv, Dv, dtype=dt, device=DEV)
+        big_v[-n:] = vs
+    for a, b in zip(run(ks, vs, 0), run(big_k, big_v, shift)):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
 def test_shared_equals_paged(lib):
     """The same batch with and without the prefix computed once: equal up to rounding."""
     lens, prefix, page = [3000 + 37 * i for i in range(24)], 2944, 64
