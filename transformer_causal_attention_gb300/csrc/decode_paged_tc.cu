@@ -212,67 +212,85 @@ struct Walk {
   int kind, g, b, t, s0, end;                                   // of the pairs, then of the rest
   int rest_kind, rest_g, rest_b, rest_t, rest_s0, rest_end;  // where the single tiles begin
   int q_alt;  // Piece::q_alt of the last piece; -1: that piece's rows do not alternate
+  int keys, nt;  // own keys and tiles of request b, once the walk is there
 };
 
-// The next piece of a walk; kind kNone at its end.
+// To the first request from w.b on that has keys of its own.
+__device__ __forceinline__ void seek_request(const PagedDecodeArgs& a, Walk& w) {
+  for (; w.b < a.B; ++w.b) {
+    w.keys = paged_len(a, w.b) - a.prefix_len;
+    if (w.keys > 0) break;
+  }
+  w.nt = static_cast<int>((static_cast<unsigned>(w.keys) + BN - 1) / BN);
+}
+
+// The next piece of a walk; kind kNone at its end.  Own pieces, of which there may be thousands, take few
+// instructions: one warp hands out all pieces of a CTA, and its code is fetched again for each.
 __device__ __forceinline__ Piece next_piece(const PagedDecodeArgs& a, const PagedTcPlan& pl, Walk& w) {
   Piece u;
-  if (w.kind == kPair) {
-    const int t_end = tile_at(w.end, w.s0 + kPieceCost, pl.prefix_tiles);
-    if (w.g < a.n_kv && w.t < t_end) {
-      u = Piece{kPair, w.g, w.b, w.t, t_end, a.prefix_len, 0, 1};
-      w.t = t_end;
-      if (t_end == pl.prefix_tiles) {
-        w.t = 0;
-        w.s0 += seg_points(pl.prefix_tiles);
-        if (++w.b == pl.n_pairs) {
-          w.b = 0;
-          ++w.g;
-        }
-      }
-      return u;
-    }
-    w.kind = w.rest_kind;
-    w.g = w.rest_g;
-    w.b = w.rest_b;
-    w.t = w.rest_t;
-    w.s0 = w.rest_s0;
-    w.end = w.rest_end;
-  }
   u.kind = kNone;
-  for (;;) {
-    if (w.kind == kPrefix && w.g == a.n_kv) {  // on to the requests
-      w.kind = kOwn;
-      w.g = 0;
+  if (w.kind != kOwn) {
+    if (w.kind == kPair) {
+      const int t_end = tile_at(w.end, w.s0 + kPieceCost, pl.prefix_tiles);
+      if (w.g < a.n_kv && w.t < t_end) {
+        u = Piece{kPair, w.g, w.b, w.t, t_end, a.prefix_len, 0, 1};
+        w.t = t_end;
+        if (t_end == pl.prefix_tiles) {
+          w.t = 0;
+          w.s0 += seg_points(pl.prefix_tiles);
+          if (++w.b == pl.n_pairs) {
+            w.b = 0;
+            ++w.g;
+          }
+        }
+        return u;
+      }
+      w.kind = w.rest_kind;
+      w.g = w.rest_g;
+      w.b = w.rest_b;
+      w.t = w.rest_t;
+      w.s0 = w.rest_s0;
+      w.end = w.rest_end;
     }
-    if (w.kind == kOwn && w.b >= a.B) return u;
-    const int keys = w.kind == kOwn ? paged_len(a, w.b) - a.prefix_len : a.prefix_len;
-    if (keys <= 0) {  // an empty place of the batch
-      ++w.b;
-      continue;
-    }
-    const int nt = static_cast<int>((static_cast<unsigned>(keys) + BN - 1) / BN);
-    const int t_end = tile_at(w.end, w.s0 + kPieceCost, nt);
-    if (w.t >= t_end) {
-      if (w.t < nt) return u;  // the part ends here
-    } else {
-      const bool alternates = w.kind == kOwn && pl.own_groups > 0 && pl.own_groups <= 4;
-      const bool turn = alternates && w.q_alt >= 0;
-      const int alt = turn ? w.q_alt ^ 1 : 0;
-      w.q_alt = alternates ? alt : -1;
-      u = Piece{w.kind, w.g, w.b, w.t, t_end, keys, alt, turn ? 2 : 1};
+    for (; w.kind == kPrefix && w.g < a.n_kv; ++w.g) {
+      const int t_end = tile_at(w.end, w.s0 + kPieceCost, pl.prefix_tiles), t = w.t;
+      if (t >= t_end && t < pl.prefix_tiles) return u;  // the part ends here
+      if (t < t_end) u = Piece{kPrefix, w.g, 0, t, t_end, a.prefix_len, 0, 1};
       w.t = t_end;
-    }
-    if (w.t == nt) {
+      if (t_end < pl.prefix_tiles) return u;
       w.t = 0;
-      w.s0 += seg_points(nt);
-      if (++w.g == a.n_kv && w.kind == kOwn) {
+      w.s0 += seg_points(pl.prefix_tiles);
+      if (t < t_end) {
+        ++w.g;
+        return u;
+      }
+    }
+    if (w.kind == kPrefix) w.g = 0;
+    w.kind = kOwn;
+    seek_request(a, w);
+  }
+  while (w.b < a.B) {
+    const int t_end = tile_at(w.end, w.s0 + kPieceCost, w.nt), t = w.t;
+    if (t >= t_end && t < w.nt) break;  // the part ends here
+    if (t < t_end) {
+      const bool turn = w.q_alt >= 0;
+      const int alt = turn ? w.q_alt ^ 1 : 0;
+      if (pl.own_groups > 0 && pl.own_groups <= 4) w.q_alt = alt;
+      u = Piece{kOwn, w.g, w.b, t, t_end, w.keys, alt, turn ? 2 : 1};
+    }
+    w.t = t_end;
+    if (t_end == w.nt) {
+      w.t = 0;
+      w.s0 += seg_points(w.nt);
+      if (++w.g == a.n_kv) {
         w.g = 0;
         ++w.b;
+        seek_request(a, w);
       }
     }
-    if (u.kind != kNone) return u;
+    if (t < t_end) break;
   }
+  return u;
 }
 
 // Keys of tile t.
@@ -308,6 +326,29 @@ __device__ __noinline__ void drain_wait(uint64_t* bar, uint32_t parity, unsigned
   }
 }
 
+// The MMAs with shared-memory descriptors by their low words (address and leading offset): the high words of all
+// tiles here are the same, and a burst's descriptors differ by constants that never carry.  Half the instructions
+// per MMA of 64-bit descriptors.
+constexpr uint32_t kDescHigh = static_cast<uint32_t>(sdesc_sw128(0, 16, 1024) >> 32);
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+      : "memory");
+}
+
 struct Ring {
   uint32_t st = 0, ph = 0;
   __device__ __forceinline__ void next(uint32_t n) {
@@ -338,6 +379,22 @@ struct Cursor {
     return ok;
   }
   __device__ __forceinline__ bool live() const { return u.kind != kNone; }
+};
+
+// What the MMA issuer keeps of a piece: its tiles left (0: no piece), whether none has its P V yet, whether its last
+// tile is not whole.  (With whole pieces kept, a visit took long enough to bound short pieces and 64-dim heads.)
+struct Slim {
+  int left;
+  uint32_t n, w;  // pieces taken, the worker
+  bool first, part, alt, pair;
+  __device__ __forceinline__ Slim(const Piece& u, uint32_t taken, uint32_t worker)
+      : left(u.kind == kNone ? 0 : u.t_end - u.t),
+        n(taken),
+        w(worker),
+        first(true),
+        part(u.keys < u.t_end * BN),
+        alt(u.q_alt != 0),
+        pair(u.kind == kPair) {}
 };
 
 // ------------------------------------------------------------------------------------- softmax of a tile
@@ -694,7 +751,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box_shift = min(a.page_shift, 7);  // rows per box: a page, or half of a 256-token page
       const int boxes = BN >> box_shift;            // per column block of a tile
       const int box = lane & (boxes - 1), blk = lane / boxes;  // lane l loads block l / boxes of page l mod boxes
-      const int G = a.n_h / a.n_kv;
+      // query rows, a lane per box: 64 dims of group q_j's rows, or (q_lo) of what their rounding left
+      const int q_lo = (lane / C::kBlocks) & 1, q_j = lane / (2 * C::kBlocks), q_dim = (lane & (C::kBlocks - 1)) * 64;
+      const int q_dst = (group_row(q_j) + q_lo * 8) * 128 + q_dim / 64 * C::kBlockBytes;
+      const int q_head = 8 * q_j, q_rest = q_lo * pl.lo_reqs;  // of an own piece
+      const bool q_box = pl.own_groups > 0 ? q_j < pl.own_groups && (!q_lo || pl.lo_reqs > 0) : q_j == 0 && !q_lo;
+      const int q_bytes = (pl.own_groups > 0 ? pl.own_groups * pl.own_group * (pl.lo_reqs > 0 ? 2 : 1) : a.n_h / a.n_kv) *
+                          128 * C::kBlocks;
       Ring r;
       uint32_t issued = 0, last_ph = 0;
       int id_cur = -1, id_oth = -1;  // the lane's page of each worker's next tile
@@ -723,27 +786,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t m = n - back;
               if (!warp_wait(&bars->q_free[cur.w][m & 1u], (m >> 1) & 1u, wc)) break;
             }
-            const int tile = cur.u.kind == kPair ? 2 * cur.u.b + cur.w : 2 * pl.n_pairs;  // row tile of the prefix
-            const int groups = own ? pl.own_groups : pl.prefix_groups;
             uint64_t* const bar = &bars->q_full[cur.w][n & 1u];
-            if (lane == 0) {
-              const int rows = groups == 0 ? (own ? G : pl.rows) : groups * (own ? pl.own_group : pl.prefix_group);
-              mbar_arrive_expect_tx(bar, rows * (groups > 0 && pl.lo_reqs > 0 ? 2 : 1) * 128 * C::kBlocks);
-            }
-            __syncwarp();
-            // a lane per box: 64 dims i of group j's rows, or of what their rounding left
-            const int i = lane & (C::kBlocks - 1), lo = (lane / C::kBlocks) & 1, j = lane / (2 * C::kBlocks);
-            if (groups > 0 ? j < groups && (!lo || pl.lo_reqs > 0) : j == 0 && !lo) {
-              int req = cur.u.b, head = 8 * j;
-              if (!own) {
-                const int before = j / pl.req_groups;  // requests (groups of G <= 8 rows) before the group's
-                req = groups > 0 ? before * pl.group_reqs : tile * pl.row_reqs;
-                head = 8 * (j - before * pl.req_groups);
+            uint8_t* const dst = smem + C::kQOff + cur.w * C::kTileBytes + q_dst + cur.u.q_alt * (kAltRows * 128);
+            if (own) {
+              if (lane == 0) mbar_arrive_expect_tx(bar, q_bytes);
+              __syncwarp();
+              if (q_box) tma_load_4d(dst, &tm_q, bar, q_dim, q_head, cur.u.g, cur.u.b + q_rest);
+            } else {
+              const int groups = pl.prefix_groups;
+              if (lane == 0)
+                mbar_arrive_expect_tx(bar, (groups > 0 ? groups * pl.prefix_group * (pl.lo_reqs > 0 ? 2 : 1) : pl.rows) *
+                                               128 * C::kBlocks);
+              __syncwarp();
+              if (groups > 0 ? q_j < groups && (!q_lo || pl.lo_reqs > 0) : q_j == 0 && !q_lo) {
+                const int before = q_j / pl.req_groups;  // requests (groups of G <= 8 rows) before the group's
+                const int tile = cur.u.kind == kPair ? 2 * cur.u.b + cur.w : 2 * pl.n_pairs;  // row tile of the prefix
+                tma_load_4d(dst, &tm_qn, bar, q_dim, 8 * (q_j - before * pl.req_groups), cur.u.g,
+                            (groups > 0 ? before * pl.group_reqs : tile * pl.row_reqs) + q_rest);
               }
-              uint8_t* const dst = smem + C::kQOff + cur.w * C::kTileBytes +
-                                   (group_row(j) + lo * 8 + cur.u.q_alt * kAltRows) * 128;
-              tma_load_4d(dst + i * C::kBlockBytes, own ? &tm_q : &tm_qn, bar, i * 64, head, cur.u.g,
-                          req + lo * pl.lo_reqs);
             }
             __syncwarp();
           }
@@ -786,37 +846,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       if (lane == 0) {
-        const uint64_t q_desc0 = sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024);
-        const uint64_t k_desc0 = sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024);
-        const uint64_t v_desc0 = sdesc_sw128(smem_u32(smem + C::kVOff), C::kBlockBytes, 1024);
+        const uint32_t q_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024));
+        const uint32_t k_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024));
+        const uint32_t v_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kVOff), C::kBlockBytes, 1024));
         Ring kr, vr;
         uint32_t pph = 0, oph = 0, fix_ph = 0;  // parities, one bit per worker (fix_ph: per stage)
         uint32_t pending = 0;                   // bit w: worker w's Q K is out, its P V not yet
         bool ok = cur.template take<Cursor<D>::kLane>(bars, wc) && oth.template take<Cursor<D>::kLane>(bars, wc);
         auto issue_qk = [&](uint32_t w, uint32_t alt, int from, int to) {
-          const uint64_t a0 = q_desc0 + ((w * C::kTileBytes + alt * (kAltRows * 128)) >> 4);
-          const uint64_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+          const uint32_t a0 = q_desc0 + ((w * C::kTileBytes + alt * (kAltRows * 128)) >> 4);
+          const uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
 #pragma unroll
           for (int kk = from; kk < to; ++kk) {
             const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-            mma_ss(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+            mma_ss_lo(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
           }
         };
         auto issue_pv = [&](uint32_t w, bool first) {
-          const uint64_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
+          const uint32_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
+            mma_ts_lo(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
                    (!first || kk > 0) ? 1u : 0u);
         };
+        Slim me(cur.u, cur.n, 0), you(oth.u, oth.n, 1);
         // one visit: P V of the worker's tile, then Q K of its next one
-        while (ok && (cur.live() || oth.live())) {
-          if (cur.u.kind == kPair && cur.w == 0 && pending == 3u && cur.t > cur.u.t && cur.t + 2 < cur.u.t_end) {
-            // inside a pair piece, both workers at tile t: no piece begins or ends before t_end - 2, and the tiles
-            // are whole (only a segment's last one may not be).  What the next turn needs is waited for in front
+        while (ok && (me.left || you.left)) {
+          if (me.pair && me.w == 0 && pending == 3u && !me.first && me.left > 2) {
+            // inside a pair piece, both workers at the same tile: no piece begins or ends before its last two, and the
+            // tiles are whole (only a segment's last one may not be).  What the next turn needs is waited for in front
             // of this turn's last MMAs, so that the tensor pipe does not run dry.
-            if (!lane_wait(&bars->v_full[vr.st], vr.ph, wc) || !lane_wait(&bars->k_full[kr.st], kr.ph, wc)) break;
-            for (; cur.t + 2 < cur.u.t_end; ++cur.t) {
+            if (!(ok = lane_wait(&bars->v_full[vr.st], vr.ph, wc) && lane_wait(&bars->k_full[kr.st], kr.ph, wc))) break;
+            for (; me.left > 2; --me.left) {
               if (!(ok = lane_wait(&bars->p_full[0], pph & 1u, wc))) break;
               pph ^= 1u;
               tc_fence_after();
@@ -839,59 +900,60 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_commit(&bars->k_empty[kr.st]);
               kr = kn;
             }
-            oth.t = cur.t;
+            you.left = me.left;
             if (!ok) break;
           }
-          if (cur.live()) {
-            const uint32_t w = cur.w, bit = 1u << w;
+          if (me.left) {
+            const uint32_t w = me.w, bit = 1u << w;
             if (pending & bit) {
-              const bool pair = cur.u.kind == kPair, first = cur.t == cur.u.t, last = cur.t + 1 == cur.u.t_end;
-              if (!pair || w == 0) {
-                if (!lane_wait(&bars->v_full[vr.st], vr.ph, wc)) break;
-                if (tile_keys(cur.u, cur.t) < BN) {  // the rows behind the last key are cleared first
-                  if (!lane_wait(&bars->v_fixed[vr.st], (fix_ph >> vr.st) & 1u, wc)) break;
+              if (!me.pair || w == 0) {
+                if (!(ok = lane_wait(&bars->v_full[vr.st], vr.ph, wc))) break;
+                if (me.left == 1 && me.part) {  // the rows behind the last key are cleared first
+                  if (!(ok = lane_wait(&bars->v_fixed[vr.st], (fix_ph >> vr.st) & 1u, wc))) break;
                   fix_ph ^= 1u << vr.st;
                 }
               }
-              if (!lane_wait(&bars->p_full[w], (pph >> w) & 1u, wc)) break;
+              if (!(ok = lane_wait(&bars->p_full[w], (pph >> w) & 1u, wc))) break;
               pph ^= bit;
-              if (first) {  // O has been read
-                if (!lane_wait(&bars->o_empty[w], ((oph >> w) & 1u) ^ 1u, wc)) break;
+              if (me.first) {  // O has been read
+                if (!(ok = lane_wait(&bars->o_empty[w], ((oph >> w) & 1u) ^ 1u, wc))) break;
                 oph ^= bit;
               }
               tc_fence_after();
-              issue_pv(w, first);
-              if (last) mma_commit(&bars->o_done[w]);
-              if (!pair || w == 1) {
+              issue_pv(w, me.first);
+              if (!me.pair || w == 1) {
                 mma_commit(&bars->v_empty[vr.st]);
                 vr.next(C::kVStages);
               }
-              ++cur.t;
-              if (last && !cur.template take<Cursor<D>::kLane>(bars, wc)) break;
+              me.first = false;
               pending &= ~bit;
-            }
-            if (cur.live()) {
-              const bool pair = cur.u.kind == kPair;
-              if (!pair || w == 0) {
-                if (!lane_wait(&bars->k_full[kr.st], kr.ph, wc)) break;
+              if (--me.left == 0) {
+                mma_commit(&bars->o_done[w]);
+                if (!(ok = lane_wait(&bars->piece_full[w][me.n % C::kQueue], (me.n / C::kQueue) & 1u, wc))) break;
+                me = Slim(bars->piece[w][me.n % C::kQueue], me.n + 1, w);
               }
-              const uint32_t n = cur.n - 1;
-              if (cur.t == cur.u.t && !lane_wait(&bars->q_full[w][n & 1u], (n >> 1) & 1u, wc)) break;
+            }
+            if (me.left) {
+              if (!me.pair || w == 0) {
+                if (!(ok = lane_wait(&bars->k_full[kr.st], kr.ph, wc))) break;
+              }
+              const uint32_t n = me.n - 1;
+              if (me.first && !(ok = lane_wait(&bars->q_full[w][n & 1u], (n >> 1) & 1u, wc))) break;
               tc_fence_after();
-              issue_qk(w, cur.u.q_alt, 0, D / 16);
+              issue_qk(w, me.alt, 0, D / 16);
               mma_commit(&bars->s_full[w]);
-              if (cur.t + 1 == cur.u.t_end) mma_commit(&bars->q_free[w][n & 1u]);
-              if (!pair || w == 1) {
+              if (!me.pair || w == 1) {
                 mma_commit(&bars->k_empty[kr.st]);
                 kr.next(C::kKStages);
               }
+              if (me.left == 1) mma_commit(&bars->q_free[w][n & 1u]);
               pending |= bit;
             }
           }
-          if (oth.live()) {
-            const Cursor<D> x = cur;
-            cur = oth;
-            oth = x;
+          if (you.left) {
+            const Slim x = me;
+            me = you;
+            you = x;
           }
         }
         // every MMA issued so far completes before TMEM is released
@@ -910,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int strip = (a.B + 31) / 32;
         const int b_lo = min(a.B, lane * strip), b_hi = min(a.B, b_lo + strip);
         int mine = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int b = b_lo; b < b_hi; ++b) mine += seg_points(own_tiles(a, b));
         int before = mine;
 #pragma unroll
