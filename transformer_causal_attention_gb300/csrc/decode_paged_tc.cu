@@ -903,6 +903,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             you.left = me.left;
             if (!ok) break;
           }
+          if constexpr (D == 64) {
+            // likewise inside two single pieces: a tile of 64-dim heads comes every 0.75 us from HBM, less than a
+            // visit with all its questions takes
+            int turns = min(me.left, you.left) - 2;
+            if (turns > 0 && !me.pair && !you.pair && pending == 3u && !me.first && !you.first) {
+              me.left -= turns;
+              you.left -= turns;
+              uint32_t w = me.w;
+              for (turns *= 2; turns > 0; --turns) {
+                if (!(ok = lane_wait(&bars->v_full[vr.st], vr.ph, wc) && lane_wait(&bars->p_full[w], (pph >> w) & 1u, wc) &&
+                           lane_wait(&bars->k_full[kr.st], kr.ph, wc)))
+                  break;
+                tc_fence_after();
+                issue_pv(w, false);
+                mma_commit(&bars->v_empty[vr.st]);
+                issue_qk(w, me.w == w ? me.alt : you.alt, 0, D / 16);
+                mma_commit(&bars->s_full[w]);
+                mma_commit(&bars->k_empty[kr.st]);
+                vr.next(C::kVStages);
+                kr.next(C::kKStages);
+                pph ^= 1u << w;
+                w ^= 1u;
+              }
+              if (!ok) break;
+            }
+          }
           if (me.left) {
             const uint32_t w = me.w, bit = 1u << w;
             if (pending & bit) {
