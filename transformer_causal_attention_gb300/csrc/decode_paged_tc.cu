@@ -51,9 +51,9 @@
 // one-tile piece took 10 us, the instruction fetches of the SMs saturating their shared
 // caches.  For the same reason the queries are rotated before, by a kernel of their own
 // that this one overlaps with its start (programmatic launch).
-// Measured (32 query heads over 8 KV heads, D = 128): 59 requests of 4096 to 8192 keys, 1.49 GB in 225 to 232 us
-// (0.95 to 0.98 of the card's copy rate), whether pages hold 16 tokens or 128; 64 requests behind 32768
-// shared tokens 57 us (0.53 of the copy rate), 256 behind 16384 103 us (670 TFLOP/s).
+// Measured (32 query heads over 8 KV heads, D = 128): 59 requests of 4096 to 8192 keys, 1.49 GB in 224 to 232 us
+// (0.95 to 0.99 of the card's copy rate), whether pages hold 16 tokens or 128, with 64-dim heads 137 us (0.81);
+// 64 requests behind 32768 shared tokens 56.5 us (0.54 of the copy rate), 256 behind 16384 100 us (690 TFLOP/s).
 // TMEM: S/P of the workers in columns [0, 128) and [128, 256), O behind them.
 #include <math.h>
 
@@ -559,7 +559,7 @@ __device__ __forceinline__ void softmax_group(uint32_t s_addr, uint32_t o_addr, 
 // The same for a row per thread (TMEM lane), with Q and P rounded to bf16: each of the two moves an output by
 // about as much as its own rounding to bf16 does (0.0029 of the largest output against 64 bits, instead of
 // 0.0017).  The rows fill the MMA here, and the products for what the roundings leave would be more MMAs: for P's,
-// 256 requests behind 16384 tokens took 138 us, so 92; for Q's there is no shared memory.
+// 256 requests behind 16384 tokens took 138 us, without 92; for Q's there is no shared memory.
 // The whole row is in registers, each score read once and the chains independent: on pair tiles the tensor pipe
 // waits for the softmax (0.6 us of a worker's 1.6 us per tile; handing P over in two halves, for the first half's
 // P V to run beside the second's exponentials, made it 1.7).
@@ -1172,7 +1172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int per_group = u.kind == kOwn ? pl.own_group : pl.prefix_group;
       const bool two = quad + 4 < groups;                                  // and two groups of them
       float m_run = -INFINITY, l_run = 0.f, m_2nd = -INFINITY, l_2nd = 0.f;
-      if (groups == 0 && active) {  // a loop of its own (both in one: 256 requests behind 16384 tokens 98 us, so 95)
+      if (groups == 0 && active) {  // a loop of its own (both kinds in one: 256 requests behind 16384 tokens 98 us, so 95)
         for (int t = u.t; t < u.t_end; ++t) {
           if (!row_wait(&bars->s_full[w], sph, wc)) { ok = false; break; }
           sph ^= 1;
