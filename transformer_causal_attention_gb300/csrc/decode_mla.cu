@@ -266,12 +266,17 @@ __device__ __forceinline__ void scale_cols64(uint32_t taddr, const float* f) {
   }
 }
 
-// Keys of sequence i.  An empty place of a paged batch counts one key (of zeros): the combine clears it.
+// An empty place of a paged batch: no key behind the prefix, once the length is clamped to the table (which may end
+// with the prefix).
+__device__ __forceinline__ bool mla_empty(const DecodeArgs& a, const MlaPages& pg, int i) {
+  return min(a.seqlens[i], a.max_len) <= pg.prefix_len;
+}
+
+// Keys of sequence i.  An empty place counts one key (of zeros): the combine clears it.
 template <bool PAGED>
 __device__ __forceinline__ int mla_len(const DecodeArgs& a, const MlaPages& pg, int i) {
-  const int L = a.seqlens[i];
-  if (PAGED && L <= pg.prefix_len) return 1;
-  return min(max(L, 1), a.max_len);
+  if (PAGED && mla_empty(a, pg, i)) return 1;
+  return min(max(a.seqlens[i], 1), a.max_len);
 }
 
 template <bool PAGED>
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int L = prefix[sb + 1] - prefix[sb];
         const int nr = (hi - lo + kRoundKeys - 1) / kRoundKeys;
         const int* const table = pg.table + static_cast<long long>(sb) * pg.max_blocks;
-        const bool empty = a.seqlens[sb] <= pg.prefix_len;
+        const bool empty = mla_empty(a, pg, sb);
         auto page_of = [&](int key0) -> int {  // this lane's page of the tile at key0; -1 (zeros) behind the end
           const int key = key0 + (my_pg << box_shift);
           if (key >= L || empty) return -1;
@@ -961,7 +966,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) mla_combine_kernel(DecodeA
   const int bh = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
   if (bh >= a.B * a.n_h) return;  // whole warps only
   const int b = bh / a.n_h, h = bh % a.n_h;
-  if (PAGED && a.seqlens[b] <= pg.prefix_len) {  // an empty place of the batch
+  if (PAGED && mla_empty(a, pg, b)) {
     uint2* const o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(bh) * DV);
     for (int c = lane; c < DV / 4; c += 32) o[c] = make_uint2(0, 0);
     if (a.lse != nullptr && lane == 0) a.lse[bh] = -INFINITY;
