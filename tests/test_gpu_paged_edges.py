@@ -53,3 +53,52 @@ def test_lengths_above_a_longer_table_are_clamped(lib, n_h, n_kv, D, Dv, dtype):
     out, lse = lib.decode_shared(q.to(DEV), kd, vd, pre.to(DEV), table.to(DEV), ints([81, 80, 2**31 - 1]), scale=0.1,
                                  lse=True)
     check_result(to_np(out), to_np(lse), want, want_lse, err, v_of, dtype)
+
+
+# --------------------------------------------------------------------------------------------- infinities
+# B, heads per KV head, D, dtype: rows in groups with the rests of their roundings, one after the other, CUDA cores
+NON_FINITE = [(4, 4, 128, "bf16"), (4, 4, 64, "bf16"), (40, 4, 128, "bf16"), (4, 4, 96, "bf16"), (3, 2, 64, "f32"),
+              (20, 2, 64, "f32")]
+
+
+@pytest.mark.parametrize("prefix", [0, 128])
+@pytest.mark.parametrize("rope", [0.0, 1e4])
+@pytest.mark.parametrize("B,G,D,dtype", NON_FINITE)
+def test_infinite_values_reach_their_rows(lib, B, G, D, dtype, rope, prefix):
+    """A weight above 0 times an infinite value is that infinity; both infinities in one dim give NaN.  (Scores of
+    these inputs lie within some 30 of each other, so that no weight is 0.)"""
+    dt = TYPES[dtype]
+    lens = [prefix + (1, 40, 190, 340)[b % 4] for b in range(B)]
+    k, v, table, pre, k_of, v_of = ref.make_cache(lens, prefix, 16, 2, D, D, dt, seed=8)
+    q = normal((B, 2 * G, D), dt, 5)
+    want, want_lse, err = ref.attend(q, k_of, v_of, rope_base=rope)
+    own = table[:, prefix // 16:]
+    inf = float("inf")
+    v[own[0, 0], 0, 0, 9] = inf        # request 0's first own token, without a prefix its only one: KV head 0, dim 9
+    v[own[1, 2], 3, 1, 0] = -inf       # request 1, KV head 1
+    v[own[2, 3], 15, 0, D - 1] = inf   # request 2: two of one sign, two of both
+    v[own[2, 9], 1, 0, D - 1] = inf
+    v[own[2, 0], 2, 1, 8] = inf
+    v[own[2, 11], 0, 1, 8] = -inf
+    for h, want_inf in ((slice(0, G), (0, 9, inf)), (slice(G, None), (1, 0, -inf)), (slice(0, G), (2, D - 1, inf)),
+                        (slice(G, None), (2, 8, float("nan")))):
+        b, d, x = want_inf
+        want[b, h, d] = x
+    if prefix:
+        v[pre[3], 5, 1, 3] = -inf      # a shared token: every request's rows of KV head 1
+        want[:, G:, 3] = -inf
+        call, first = lib.decode_shared, (pre.to(DEV), table.to(DEV))
+    else:
+        call, first = lib.decode_paged, (table.to(DEV),)
+    out, lse = call(q.to(DEV), k.to(DEV), v.to(DEV), *first, ints(lens), rope_base=rope, lse=True)
+    check_non_finite(to_np(out), to_np(lse), want, want_lse, err, v_of, dtype)
+
+
+def check_non_finite(out, lse, want, want_lse, err, v_of, dtype):
+    odd = ~np.isfinite(want)
+    np.testing.assert_array_equal(out[odd], want[odd])
+    odd_lse = ~np.isfinite(want_lse)
+    np.testing.assert_array_equal(lse[odd_lse], want_lse[odd_lse])
+    assert np.isfinite(out[~odd]).all() and np.isfinite(lse[~odd_lse]).all()
+    check_result(np.where(odd, 0, out), np.where(odd_lse, 0, lse), np.where(odd, 0, want),
+                 np.where(odd_lse, 0, want_lse), err, v_of, dtype)

@@ -471,6 +471,13 @@ __device__ __forceinline__ void transpose_pieces(uint4* pc, int lj) {
   pc[3] = b0 ? pc[3] : q1;
 }
 
+// A sum and the rest that belongs to it.  A sum that an infinity has made infinite is the result: the rests of the
+// factors it met may be 0 or of the other sign, and make NaN of it.
+__device__ __forceinline__ float with_rest(uint32_t sum, uint32_t rest) {
+  const float x = __uint_as_float(sum);
+  return fabsf(x) < INFINITY ? x + __uint_as_float(rest) : x;
+}
+
 // A tile's scores (n real keys) of one group of eight rows become its weights P: p = 2^(s * scale*log2e - m).
 // m moves only when the row maximum grew by more than the threshold; O and l are then scaled by
 // 2^(m_old - m_new), exactly (l and O share their reference).
@@ -1249,8 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   *reinterpret_cast<float2*>(po + c * 32 + e * 8) =
-                      make_float2((__uint_as_float(o[4 * e]) + __uint_as_float(o[4 * e + 2])) * inv_l,
-                                  (__uint_as_float(o[4 * e + 1]) + __uint_as_float(o[4 * e + 3])) * inv_l);
+                      make_float2(with_rest(o[4 * e], o[4 * e + 2]) * inv_l, with_rest(o[4 * e + 1], o[4 * e + 3]) * inv_l);
               }
             }
             if (real && (lane & 3) == 0) ws[l_at + row + rr] = m_run + log2f(l);
