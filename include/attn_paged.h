@@ -121,8 +121,8 @@ ATTN_API size_t attn_decode_paged_workspace_size(int B, int n_h, int n_kv, int D
  * most 64 rows (a request's own keys under up to 64 heads per KV head, the shared
  * prefix of a small batch), which keep what that rounding leaves.  NaN in a query, key or
  * value reaches the rows that see it and no other; an infinite value gives them that
- * infinity (both infinities in one dim, or a weight of 0: NaN); an infinite key may give
- * NaN where its score would be -inf.
+ * infinity (both infinities in one dim, or a weight of 0: NaN); a key with a score of -inf
+ * has no weight, one with a score of inf makes its rows NaN.
  */
 ATTN_API int attn_decode_paged(const void* q, const void* k_pages, const void* v_pages, int v_token_stride,
                                const int* block_table, const int* seqlens, void* out, float* lse, int B, int n_h,

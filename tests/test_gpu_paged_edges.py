@@ -102,3 +102,78 @@ def check_non_finite(out, lse, want, want_lse, err, v_of, dtype):
     assert np.isfinite(out[~odd]).all() and np.isfinite(lse[~odd_lse]).all()
     check_result(np.where(odd, 0, out), np.where(odd_lse, 0, lse), np.where(odd, 0, want),
                  np.where(odd_lse, 0, want_lse), err, v_of, dtype)
+
+
+@pytest.mark.parametrize("prefix", [0, 128])
+@pytest.mark.parametrize("rope", [0.0, 1e4])
+@pytest.mark.parametrize("B,G,D,dtype", NON_FINITE)
+def test_keys_with_a_score_of_minus_infinity_have_no_weight(lib, B, G, D, dtype, rope, prefix):
+    """An infinite component of a key makes its score -inf for the heads whose (rotated) query has the other sign
+    there - their rows are those without that key - and inf for the others, whose softmax is NaN."""
+    dt = TYPES[dtype]
+    lens = [prefix + (2, 40, 190, 340)[b % 4] for b in range(B)]
+    k, v, table, pre, k_of, v_of = ref.make_cache(lens, prefix, 16, 2, D, D, dt, seed=8)
+    q = normal((B, 2 * G, D), dt, 5)
+    own = table[:, prefix // 16:]
+    turned = to64(q) if rope <= 0 else np.stack([oracle.rope_rotate(to64(q[b]), np.full(2 * G, lens[b] - 1), rope)
+                                                 for b in range(B)])
+    hit = np.zeros((B, 2 * G), int)     # the sign of the infinite score that a row sees
+
+    def spoil(b, g, key, d, sign):      # key of request b's own, KV head g
+        n = prefix + key
+        k[own[b, key // 16], key % 16, g, d] = sign * float("inf")
+        rows = slice(g * G, (g + 1) * G)
+        assert np.abs(turned[b, rows, d]).min() > 1e-3  # the sign hangs on no rounding
+        hit[b, rows] = np.sign(sign * turned[b, rows, d])
+        k_of[b][n, g] = 0               # for the rows of score -inf: as if the key were not there
+        gone.append((b, g, n))
+    gone = []
+    spoil(0, 1, 0, 7, 1)
+    spoil(1, 0, 33, D // 2, -1)
+    spoil(2, 1, 128, 0, 1)
+    want, want_lse = np.zeros((B, 2 * G, D)), np.zeros((B, 2 * G))
+    err = np.zeros((B, 2 * G))
+    for g in range(2):                  # each KV head of each request with its own set of keys
+        rows = slice(g * G, (g + 1) * G)
+        keep = [np.setdiff1d(np.arange(lens[b]), [n for bb, gg, n in gone if (bb, gg) == (b, g)]) for b in range(B)]
+        for b in range(B):
+            s = turned[b, rows] @ k_of[b][keep[b], g].T / np.sqrt(D)
+            top = s.max(-1, keepdims=True)
+            p = np.exp(s - top)
+            want[b, rows] = p @ v_of[b][keep[b], g] / p.sum(-1, keepdims=True)
+            want_lse[b, rows] = top[:, 0] + np.log(p.sum(-1))
+            if rope > 0:
+                err[b, rows] = (np.abs(turned[b, rows]) @ np.abs(k_of[b][:, g]).T).max(-1) / np.sqrt(D) * 2.0 ** -8
+    if prefix:
+        call, first = lib.decode_shared, (pre.to(DEV), table.to(DEV))
+    else:
+        call, first = lib.decode_paged, (table.to(DEV),)
+    out, lse = call(q.to(DEV), k.to(DEV), v.to(DEV), *first, ints(lens), rope_base=rope, lse=True)
+    out, lse = to_np(out), to_np(lse)
+    assert (hit > 0).any() and (hit < 0).any()
+    assert np.isnan(out[hit > 0]).all() and not np.isfinite(lse[hit > 0]).any()
+    out[hit > 0], lse[hit > 0] = want[hit > 0], want_lse[hit > 0]
+    check_result(out, lse, want, want_lse, err, v_of, dtype)
+
+
+@pytest.mark.parametrize("prefix", [0, 128])
+def test_latent_rows_with_a_score_of_minus_infinity_have_no_weight(lib, prefix):
+    """The same in the MLA-absorbed shape, in the dims behind the values (0 times an infinite value would be NaN)."""
+    lens = [prefix + n for n in (2, 340, 700)]
+    k, _, table, pre, k_of, v_of = ref.make_cache(lens, prefix, 16, 1, 576, 512, torch.bfloat16, seed=8, alias=True)
+    q = normal((3, 128, 576), torch.bfloat16, 5)
+    own = table[:, prefix // 16:]
+    spoilt = [(0, 1, 570), (1, 300, 512), (2, 129, 575)]  # request, own key, dim
+    hit = np.zeros((3, 128), bool)
+    for b, key, d in spoilt:
+        k[own[b, key // 16], key % 16, 0, d] = float("inf")
+        hit[b] = to64(q)[b, :, d] > 0
+        k_of[b], v_of[b] = (np.delete(x, prefix + key, 0) for x in (k_of[b], v_of[b]))
+    want, want_lse, err = ref.attend(q, k_of, v_of, scale=0.0722)
+    kd = k.to(DEV)
+    call, first = (lib.decode_shared, (pre.to(DEV), table.to(DEV))) if prefix else (lib.decode_paged, (table.to(DEV),))
+    out, lse = call(q.to(DEV), kd, kd[..., :512], *first, ints(lens), scale=0.0722, lse=True)
+    out, lse = to_np(out), to_np(lse)
+    assert np.isnan(out[hit]).all() and not np.isfinite(lse[hit]).any()
+    out[hit], lse[hit] = want[hit], want_lse[hit]
+    check_result(out, lse, want, want_lse, err, v_of, "bf16")
