@@ -177,3 +177,36 @@ def test_latent_rows_with_a_score_of_minus_infinity_have_no_weight(lib, prefix):
     assert np.isnan(out[hit]).all() and not np.isfinite(lse[hit]).any()
     out[hit], lse[hit] = want[hit], want_lse[hit]
     check_result(out, lse, want, want_lse, err, v_of, "bf16")
+
+
+@pytest.mark.parametrize("prefix", [0, 128])
+@pytest.mark.parametrize("far", [False, True])
+def test_nan_of_a_live_latent_row_shows(lib, prefix, far):
+    """The MLA-absorbed shape, whose keys' first dims are the values: a NaN in a query reaches its head's row, a NaN in
+    a latent row (in its values, in its rotary part) all heads of the request, and neither any other row.  far: the
+    key's score lies so far below the others' that its piece's weight is 0, and 0 times NaN is NaN."""
+    lens = [prefix + n for n in (40, 4190, 340, 700, 90)]
+    k, _, table, pre, k_of, v_of = ref.make_cache(lens, prefix, 16, 1, 576, 512, torch.bfloat16, seed=8, alias=True)
+    q = normal((5, 128, 576), torch.bfloat16, 5)
+    own = table[:, prefix // 16:]
+    if far:  # request 1's first 2048 own keys score far below the others
+        rows = k[own[1, :128].long()]
+        k[own[1, :128].long()] = (-40 * q[1, 0] + rows * 0).to(torch.bfloat16)
+        k_of[1][prefix:prefix + 2048] = v_of[1][prefix:prefix + 2048] = 0
+    want, want_lse, err = ref.attend(q, k_of, v_of, scale=0.0722)
+    q[3, 77, 500] = float("nan")
+    k[own[1, 2], 3, 0, 7] = float("nan")
+    k[own[2, 5], 15, 0, 570] = float("nan")
+    kd = k.to(DEV)
+    if prefix:
+        call, first = lib.decode_shared, (pre.to(DEV), table.to(DEV))
+    else:
+        call, first = lib.decode_paged, (table.to(DEV),)
+    out, lse = call(q.to(DEV), kd, kd[..., :512], *first, ints(lens), scale=0.0722, lse=True)
+    out, lse = to_np(out), to_np(lse)
+    bad = np.zeros((5, 128), bool)
+    bad[3, 77] = bad[1] = bad[2] = True
+    np.testing.assert_array_equal(np.isnan(out), np.broadcast_to(bad[..., None], out.shape))
+    np.testing.assert_array_equal(np.isnan(lse), bad)
+    out[bad], lse[bad] = want[bad], want_lse[bad]
+    check_result(out, lse, want, want_lse, err, v_of, "bf16")
