@@ -19,6 +19,8 @@
  *    (else ATTN_ERR_ARG).
  *  - A page index outside [0, n_pages) in front of a request's last token reads
  *    as keys and values of zero; nothing outside the cache is read or written.
+ *  - Tokens are rotated at any 32-bit position, with angles to some 1e-6 rad and
+ *    |position| * 2^-48 more (1e-5 rad at 2^31).
  *  - int32 pointers are 4-byte aligned, all others 16-byte (ATTN_ERR_ALIGN).
  *  - Results do not depend on the order in which blocks of a kernel run: the
  *    same call on the same inputs gives the same bits.

@@ -210,3 +210,72 @@ def test_nan_of_a_live_latent_row_shows(lib, prefix, far):
     np.testing.assert_array_equal(np.isnan(lse), bad)
     out[bad], lse[bad] = want[bad], want_lse[bad]
     check_result(out, lse, want, want_lse, err, v_of, "bf16")
+
+
+# ------------------------------------------------------------------------- positions of more than 24 bits
+FAR = [2**24 - 1, 2**24, 2**24 + 1, 2**24 + 3, 2**25 + 1, 2**27 + 5, 2**30 + 63, 2**31 - 2**16 - 1, 2**31 - 1, -1,
+       -2**24 - 1, -2**31, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pairing", ["adjacent", "half"])
+@pytest.mark.parametrize("D,roff,rdims", [(128, 0, 128), (64, 0, 64), (128, 64, 64), (576, 512, 64)])
+def test_append_at_far_positions(lib, D, roff, rdims, pairing, dtype):
+    """Frequencies f (in turns, at most 0.16) are held to 2^-48 of themselves, so that an angle is off by |pos| 2^-48
+    from there - doubled for the power that f comes from -, by some 1e-6 from fp32 sums of turns below 2, and by 1e-6
+    from sine and cosine; the result is rounded once."""
+    dt, T = TYPES[dtype], len(FAR)
+    k = normal((T, 2, D), dt, 3)
+    kp = torch.zeros(2, 16, 2, D, dtype=dt, device=DEV)
+    lib.kv_append_paged(k.to(DEV), k[..., :8].contiguous().to(DEV), kp, torch.zeros(2, 16, 2, 8, dtype=dt, device=DEV),
+                        ints(range(T)), ints(FAR), rope_base=1e4, rope_offset=roff, rope_dims=rdims, pairing=pairing)
+    got = to_np(kp.flatten(0, 1)[:T])
+    pos = np.array(FAR, dtype=np.float64)[:, None]
+    want = oracle.rope_rotate(to64(k), np.broadcast_to(pos, (T, 2)), 1e4, roff, rdims, pairing=pairing)
+    half_step = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    angle = 2 * np.abs(pos[..., None]) * 2.0 ** -48 + 4e-6
+    longest = 2 ** 0.5 * k.double().abs().max().item()  # of a pair
+    assert np.all(np.abs(got - want) <= half_step * np.abs(want) + angle * longest)
+
+
+@pytest.mark.parametrize("n", [2**24 + 2, 2**25 + 4])
+@pytest.mark.parametrize("n_h,n_kv,D,Dv,roff,dtype,pairing,shared", [
+    (4, 1, 128, 128, 0, "bf16", "adjacent", False), (4, 1, 64, 64, 0, "bf16", "half", False),
+    (4, 1, 64, 64, 32, "bf16", "adjacent", False), (2, 1, 64, 64, 0, "f32", "adjacent", False),
+    (2, 1, 64, 64, 0, "f32", "half", True), (16, 1, 64, 64, 0, "f32", "adjacent", True),
+    (128, 1, 576, 512, 512, "bf16", "adjacent", False), (128, 1, 576, 512, 512, "bf16", "half", True)])
+def test_decode_at_far_positions(lib, n, n_h, n_kv, D, Dv, roff, dtype, pairing, shared):
+    """n keys in four pages that the table lists over and over: the softmax over 1024 distinct keys, each as often as
+    it occurs.  The query's fastest pair is long, and the
+    values repeat the keys', so that the angle decides where the output points."""
+    dt, page = TYPES[dtype], 256
+    kp = normal((4, page, 1, D), dt, 7)
+    q = normal((1, n_h, D), dt, 9) / 4
+    rope = dict(rope_base=1e4, rope_offset=roff, rope_dims=D - roff, pairing=pairing)
+    first = [roff, roff + 1] if pairing == "adjacent" else [roff, roff + (D - roff) // 2]
+    q[..., first] = q[..., first] * 64
+    if D == 576:
+        kp[..., :2] = kp[..., first]
+    vp = kp[..., :Dv].contiguous()
+    blocks = -(-n // page)
+    table = (torch.arange(blocks, dtype=torch.int32) % 4)[None].to(DEV)
+    times = np.bincount(np.arange(n) % (4 * page), minlength=4 * page)
+    turned = oracle.rope_rotate(to64(q[0]), np.full(n_h, n - 1), 1e4, roff, D - roff, pairing=pairing)
+    s = turned @ to64(kp).reshape(-1, D).T / np.sqrt(D) + np.log(times)
+    top = s.max(-1, keepdims=True)
+    p = np.exp(s - top)
+    want = (p @ to64(vp).reshape(-1, Dv) / p.sum(-1, keepdims=True))[None]
+    want_lse = (top[:, 0] + np.log(p.sum(-1)))[None]
+    err = ((np.abs(turned) @ np.abs(to64(kp).reshape(-1, D)).T).max(-1) / np.sqrt(D))[None]
+    kd, qd = kp.to(DEV), q.to(DEV)
+    vd = kd[..., :Dv] if D == 576 else vp.to(DEV)
+    if shared:
+        out, lse = lib.decode_shared(qd, kd, vd, table[0, :blocks - 1].contiguous(), table, ints([n]), lse=True, **rope)
+    else:
+        out, lse = lib.decode_paged(qd, kd, vd, table, ints([n]), lse=True, **rope)
+    # angles are off by some 4e-6 (see above), a score by as much of err's dot product of absolute values
+    moved = err * (4e-6 if dtype == "f32" else 2.0 ** -8 + 4e-6)
+    diff, vmax = np.abs(to_np(out) - want), np.abs(to64(vp)).max()
+    weights = 2 * moved[..., None] + (2.0 ** -8 if dtype == "bf16" else 1e-5)  # fp32 sums over 2^24 and more keys: 1e-5
+    assert np.all(diff <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(want) + weights * vmax)
+    assert np.all(np.abs(to_np(lse) - want_lse) <= moved + 1e-5 * np.abs(want_lse) + 1e-5)

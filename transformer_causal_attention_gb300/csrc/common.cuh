@@ -60,6 +60,31 @@ __device__ __forceinline__ void rope_sincos_fast(int pos, float f_hi, float f_lo
   __sincosf(6.28318530717958647692f * t, s, c);
 }
 
+// The paged calls take any 32-bit position.  Behind 2^24 it is split into a float and a rest of 7 bits, and the
+// products of both with both words of f_i are reduced one by one: the angle is off by the error of f_i, |pos| * 2^-48
+// rad at most, and by some 1e-6 from these sums.  Nearer positions give the bits of the two functions above.
+__device__ __forceinline__ bool rope_is_far(int pos) { return pos > (1 << 24) || pos < -(1 << 24); }
+__device__ __forceinline__ void rope_sincos_far(int pos, float f_hi, float f_lo, float* s, float* c) {
+  const float p = __int2float_rz(pos);                              // not beyond pos
+  const float r = static_cast<float>(pos - static_cast<int>(p));
+  const float a = __fmul_rn(p, f_hi), b = __fmul_rn(p, f_lo), d = __fmul_rn(r, f_hi);
+  const float ae = fmaf(p, f_hi, -a), be = fmaf(p, f_lo, -b), de = fmaf(r, f_hi, -d);
+  const float t = (a - rintf(a)) + (ae - rintf(ae)) + (b - rintf(b)) + (d - rintf(d)) + fmaf(r, f_lo, be + de);
+  sincospif(2.0f * t, s, c);
+}
+// f(angle), where angle(f_hi, f_lo, &s, &c) gives a pair's sine and cosine at pos: FAST by rope_sincos_fast, ANY at any
+// position.  f's code is there twice then, so that nearer positions do not ask pair by pair (which made 8 MLA queries
+// behind 1000 keys each 2.5 us slower).
+template <bool ANY, bool FAST, typename F>
+__device__ __forceinline__ void with_angles(int pos, const F& f) {
+  if (ANY && rope_is_far(pos))
+    f([=](float f_hi, float f_lo, float* s, float* c) { rope_sincos_far(pos, f_hi, f_lo, s, c); });
+  else if (FAST)
+    f([=](float f_hi, float f_lo, float* s, float* c) { rope_sincos_fast(pos, f_hi, f_lo, s, c); });
+  else
+    f([=](float f_hi, float f_lo, float* s, float* c) { rope_sincos(pos, f_hi, f_lo, s, c); });
+}
+
 // Rotate the pair (x0, x1) = (x_{2i}, x_{2i+1}) by the angle with sin s, cos c.
 __device__ __forceinline__ void rotate_pair(float& x0, float& x1, float s, float c) {
   const float r0 = x0 * c - x1 * s;

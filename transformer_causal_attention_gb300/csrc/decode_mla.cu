@@ -643,42 +643,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (f.n_pairs) {
           // rotate dims [rope_offset, rope_offset + 2 n_pairs) of this CTA's 64 heads at the new token's position
           const int c0 = a.rope_offset / 8;  // first 8-dim chunk of the span
-          for (int hl = lane; hl < HH; hl += 32) {
-            uint8_t* row = smem + kQOff + hl * 128;
-            auto chunk = [&](int c) {
-              return reinterpret_cast<uint4*>(row + (c >> 3) * kQBlockBytes + (((c & 7) ^ (hl & 7)) << 4));
-            };
-            if (f.half) {
-              for (int i = 0; i < f.n_pairs / 8; ++i) {
-                uint4* p0 = chunk(c0 + i);
-                uint4* p1 = chunk(c0 + i + f.n_pairs / 8);
-                float x0[8], x1[8];
-                bf16x8_to_f32(*p0, x0);
-                bf16x8_to_f32(*p1, x1);
+          with_angles<PAGED, false>(L - 1, [&](auto angle) {  // a page table may be longer than 2^24 tokens
+            for (int hl = lane; hl < HH; hl += 32) {
+              uint8_t* row = smem + kQOff + hl * 128;
+              auto chunk = [&](int c) {
+                return reinterpret_cast<uint4*>(row + (c >> 3) * kQBlockBytes + (((c & 7) ^ (hl & 7)) << 4));
+              };
+              if (f.half) {
+                for (int i = 0; i < f.n_pairs / 8; ++i) {
+                  uint4* p0 = chunk(c0 + i);
+                  uint4* p1 = chunk(c0 + i + f.n_pairs / 8);
+                  float x0[8], x1[8];
+                  bf16x8_to_f32(*p0, x0);
+                  bf16x8_to_f32(*p1, x1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  float sn, cs;
-                  rope_sincos(L - 1, f.hi[i * 8 + e], f.lo[i * 8 + e], &sn, &cs);
-                  rotate_pair(x0[e], x1[e], sn, cs);
+                  for (int e = 0; e < 8; ++e) {
+                    float sn, cs;
+                    angle(f.hi[i * 8 + e], f.lo[i * 8 + e], &sn, &cs);
+                    rotate_pair(x0[e], x1[e], sn, cs);
+                  }
+                  *p0 = f32_to_bf16x8(x0);
+                  *p1 = f32_to_bf16x8(x1);
                 }
-                *p0 = f32_to_bf16x8(x0);
-                *p1 = f32_to_bf16x8(x1);
-              }
-            } else {
-              for (int i = 0; i < f.n_pairs / 4; ++i) {
-                uint4* ptr = chunk(c0 + i);
-                float x[8];
-                bf16x8_to_f32(*ptr, x);
+              } else {
+                for (int i = 0; i < f.n_pairs / 4; ++i) {
+                  uint4* ptr = chunk(c0 + i);
+                  float x[8];
+                  bf16x8_to_f32(*ptr, x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float sn, cs;
-                  rope_sincos(L - 1, f.hi[i * 4 + e], f.lo[i * 4 + e], &sn, &cs);
-                  rotate_pair(x[2 * e], x[2 * e + 1], sn, cs);
+                  for (int e = 0; e < 4; ++e) {
+                    float sn, cs;
+                    angle(f.hi[i * 4 + e], f.lo[i * 4 + e], &sn, &cs);
+                    rotate_pair(x[2 * e], x[2 * e + 1], sn, cs);
+                  }
+                  *ptr = f32_to_bf16x8(x);
                 }
-                *ptr = f32_to_bf16x8(x);
               }
             }
-          }
+          });
           fence_proxy_async_smem();
         }
         __syncwarp();

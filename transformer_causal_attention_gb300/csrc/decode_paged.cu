@@ -117,8 +117,10 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a
       x0 = to_f32(qr[d.x]);
       x1 = to_f32(qr[d.y]);
       if (rot) {
+        const int pos = max(paged_len(a, b), 1) - 1;
         float s, c;
-        rope_sincos(max(paged_len(a, b), 1) - 1, f.hi[j], f.lo[j], &s, &c);
+        if (rope_is_far(pos)) rope_sincos_far(pos, f.hi[j], f.lo[j], &s, &c);
+        else rope_sincos(pos, f.hi[j], f.lo[j], &s, &c);
         rotate_pair(x0, x1, s, c);
       }
     }
@@ -322,8 +324,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       x0 = to_f32(qr[d.x]);
       x1 = to_f32(qr[d.y]);
       if (rot) {
+        const int pos = max(paged_len(a, b), 1) - 1;
         float s, c;
-        rope_sincos(max(paged_len(a, b), 1) - 1, f.hi[j], f.lo[j], &s, &c);
+        if (rope_is_far(pos)) rope_sincos_far(pos, f.hi[j], f.lo[j], &s, &c);
+        else rope_sincos(pos, f.hi[j], f.lo[j], &s, &c);
         rotate_pair(x0, x1, s, c);
       }
     }

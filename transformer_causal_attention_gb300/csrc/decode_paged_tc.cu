@@ -652,7 +652,8 @@ __device__ __forceinline__ uint4 bf16_rest(const float* x, uint4 rounded) {
 
 // The new tokens' queries rotated at their positions, bf16 [2, B, n_h, D] (the values and the rests): one
 // thread per (row, chunks of 8 dims c and c + D / 16).  The decode kernel may start as soon as this one has.
-template <int D>
+// ANY: for tables of more than 2^24 tokens, at any position.
+template <int D, bool ANY>
 __global__ void __launch_bounds__(256) paged_rope_q_kernel(const __grid_constant__ PagedDecodeArgs a,
                                                            const __grid_constant__ RopeFreq f, __nv_bfloat16* out) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -673,23 +674,25 @@ __global__ void __launch_bounds__(256) paged_rope_q_kernel(const __grid_constant
   float x0[8], x1[8];
   bf16x8_to_f32(q[0], x0);
   bf16x8_to_f32(q[kCP], x1);
-  if (f.half) {  // pair 8 c + e is (x0[e], x1[e])
+  with_angles<ANY, true>(pos, [&](auto angle) {
+    if (f.half) {  // pair 8 c + e is (x0[e], x1[e])
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float sn, cs;
-      rope_sincos_fast(pos, f_hi[c * 8 + e], f_lo[c * 8 + e], &sn, &cs);
-      rotate_pair(x0[e], x1[e], sn, cs);
-    }
-  } else {
+      for (int e = 0; e < 8; ++e) {
+        float sn, cs;
+        angle(f_hi[c * 8 + e], f_lo[c * 8 + e], &sn, &cs);
+        rotate_pair(x0[e], x1[e], sn, cs);
+      }
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float sn, cs;
-      rope_sincos_fast(pos, f_hi[c * 4 + e], f_lo[c * 4 + e], &sn, &cs);
-      rotate_pair(x0[2 * e], x0[2 * e + 1], sn, cs);
-      rope_sincos_fast(pos, f_hi[D / 4 + c * 4 + e], f_lo[D / 4 + c * 4 + e], &sn, &cs);
-      rotate_pair(x1[2 * e], x1[2 * e + 1], sn, cs);
+      for (int e = 0; e < 4; ++e) {
+        float sn, cs;
+        angle(f_hi[c * 4 + e], f_lo[c * 4 + e], &sn, &cs);
+        rotate_pair(x0[2 * e], x0[2 * e + 1], sn, cs);
+        angle(f_hi[D / 4 + c * 4 + e], f_lo[D / 4 + c * 4 + e], &sn, &cs);
+        rotate_pair(x1[2 * e], x1[2 * e + 1], sn, cs);
+      }
     }
-  }
+  });
   o[0] = f32_to_bf16x8(x0);
   o[kCP] = f32_to_bf16x8(x1);
   uint4* const rest = o + static_cast<long long>(a.B) * a.n_h * (D / 8);
@@ -1555,7 +1558,9 @@ cudaError_t launch(const PagedDecodeArgs& a, const RopeFreq& rope, const CUtenso
   if (rotate) {
     const long long items = static_cast<long long>(a.B) * a.n_h * (D / 16);
     __nv_bfloat16* const q = reinterpret_cast<__nv_bfloat16*>(static_cast<float*>(a.workspace) + pl.q);
-    paged_rope_q_kernel<D><<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(a, rope, q);
+    const bool any = (a.max_blocks << a.page_shift) > 1 << 24;
+    auto rope_q = any ? paged_rope_q_kernel<D, true> : paged_rope_q_kernel<D, false>;
+    rope_q<<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(a, rope, q);
     *launches += 1;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }

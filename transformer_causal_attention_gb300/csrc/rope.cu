@@ -63,13 +63,22 @@ __device__ __forceinline__ SmemFreq stage_freq(const RopeFreq& f, float* buf) {
   return SmemFreq{buf, buf + kMaxRopePairs, f.n_pairs, f.half != 0};
 }
 
-template <typename T, int CH>
+// sn and cs of N pairs at pos.
+template <int N, bool ANY, bool FAST>
+__device__ __forceinline__ void pair_angles(int pos, const float* hi, const float* lo, float* sn, float* cs) {
+  with_angles<ANY, FAST>(pos, [&](auto angle) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) angle(hi[e], lo[e], sn + e, cs + e);
+  });
+}
+
+// ANY: at any 32-bit position (the paged calls).
+template <typename T, int CH, bool ANY = false>
 __device__ __forceinline__ void rotate_chunk_rows(const T* src, T* dst, long long stride, int n_rows, int rel, int pos,
                                                   const SmemFreq& f) {
   if (f.half) {
     float sn[CH], cs[CH];
-#pragma unroll
-    for (int e = 0; e < CH; ++e) rope_sincos(pos, f.hi[rel + e], f.lo[rel + e], &sn[e], &cs[e]);
+    pair_angles<CH, ANY, false>(pos, f.hi + rel, f.lo + rel, sn, cs);
     for (int h = 0; h < n_rows; ++h) {
       float x0[CH], x1[CH];
       load_chunk<T, CH>(src + h * stride, x0);
@@ -81,8 +90,7 @@ __device__ __forceinline__ void rotate_chunk_rows(const T* src, T* dst, long lon
     }
   } else {
     float sn[CH / 2], cs[CH / 2];
-#pragma unroll
-    for (int p = 0; p < CH / 2; ++p) rope_sincos(pos, f.hi[rel / 2 + p], f.lo[rel / 2 + p], &sn[p], &cs[p]);
+    pair_angles<CH / 2, ANY, false>(pos, f.hi + rel / 2, f.lo + rel / 2, sn, cs);
     for (int h = 0; h < n_rows; ++h) {
       float x[CH];
       load_chunk<T, CH>(src + h * stride, x);
@@ -100,11 +108,11 @@ constexpr int kRowBatch = 8;
 // bf16, adjacent pairs: the 8-dim chunk at src of n_rows rows stride elements apart, rotated by
 // the angles of pairs rel / 2 .. rel / 2 + 3 at position pos, to dst.  In place (dst == src) is
 // fine: each row is stored after its own load.
+template <bool ANY = false>
 __device__ __forceinline__ void rotate_rows_bf16(const __nv_bfloat16* src, __nv_bfloat16* dst, long long stride,
                                                  int n_rows, int rel, int pos, const SmemFreq& f) {
   float sn[4], cs[4];
-#pragma unroll
-  for (int p = 0; p < 4; ++p) rope_sincos(pos, f.hi[rel / 2 + p], f.lo[rel / 2 + p], &sn[p], &cs[p]);
+  pair_angles<4, ANY, false>(pos, f.hi + rel / 2, f.lo + rel / 2, sn, cs);
   for (int hb = 0; hb < n_rows; hb += kRowBatch) {
     uint4 raw[kRowBatch];
 #pragma unroll
@@ -224,11 +232,11 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a, RopeFreq
         if (f.half && rel >= f.n_pairs) continue;  // written with its partner chunk
         if constexpr (sizeof(T) == 2) {
           if (!f.half) {
-            rotate_rows_bf16(src, dst, a.D_qk, hpt, rel, pos, f);
+            rotate_rows_bf16<PAGED>(src, dst, a.D_qk, hpt, rel, pos, f);
             continue;
           }
         }
-        rotate_chunk_rows<T, 8>(src, dst, a.D_qk, hpt, rel, pos, f);
+        rotate_chunk_rows<T, 8, PAGED>(src, dst, a.D_qk, hpt, rel, pos, f);
       } else {
         for (int h = 0; h < hpt; ++h) {
           float x[8];
@@ -256,6 +264,28 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a, RopeFreq
           for (int e = 0; e < 8; ++e) dst[h * a.D_v + e] = src[h * a.D_v + e];
       }
     }
+  }
+}
+
+// The keys of one token of the kernel below at a far position: lane's chunks (with HALF pairs of them), one by one.
+template <typename T, bool HALF>
+__device__ __noinline__ void append_far_row(const T* src, T* dst, int n_k, int hc, int D, int pos, const float* hi,
+                                            const float* lo, int lane, int lanes) {
+  constexpr int CH = 16 / sizeof(T);
+  for (int i = lane; i < n_k; i += lanes) {
+    const int at = HALF ? (i / hc) * D + (i % hc) * CH : i * CH;
+    const int pair = (i % hc) * (HALF ? CH : CH / 2);
+    float x0[CH], x1[CH];
+    load_chunk<T, CH>(src + at, x0);
+    if (HALF) load_chunk<T, CH>(src + at + D / 2, x1);
+#pragma unroll
+    for (int e = 0; e < (HALF ? CH : CH / 2); ++e) {
+      float sn, cs;
+      rope_sincos_far(pos, hi[pair + e], lo[pair + e], &sn, &cs);
+      rotate_pair(HALF ? x0[e] : x0[2 * e], HALF ? x1[e] : x0[2 * e + 1], sn, cs);
+    }
+    store_chunk<T, CH>(dst + at, x0);
+    if (HALF) store_chunk<T, CH>(dst + at + D / 2, x1);
   }
 }
 
@@ -289,6 +319,12 @@ __global__ void __launch_bounds__(256) kv_append_rows_kernel(const __grid_consta
   const T* const vs = static_cast<const T*>(a.v_new) + t * row_v;
   T* const kd = static_cast<T*>(a.kcache) + slot * row_k;
   T* const vd = static_cast<T*>(a.vcache) + slot * a.v_token_stride;
+  if (f.n_pairs && rope_is_far(pos)) {  // before any load is in flight, and out of line: beside the loops it cost 20%
+    append_far_row<T, HALF>(ks, kd, n_k, hc, a.D_qk, pos, f.hi, f.lo, lane, L);
+    for (int j = lane; j < n_v; j += L)
+      *reinterpret_cast<uint4*>(vd + j * CH) = __ldg(reinterpret_cast<const uint4*>(vs + j * CH));
+    return;
+  }
   float sn[kAngles], cs[kAngles];
   bool have = false;
   for (int i0 = lane, j0 = lane; i0 < n_k || j0 < n_v; i0 += L * kPairs, j0 += L * kBatch) {
@@ -308,13 +344,8 @@ __global__ void __launch_bounds__(256) kv_append_rows_kernel(const __grid_consta
     if (!have && f.n_pairs) {
       have = true;
       const int c = lane % hc;  // of every item of this lane (hc divides the lanes)
-#pragma unroll
-      for (int e = 0; e < kAngles; ++e) {
-        if constexpr (sizeof(T) == 2)  // rounded to bf16 right after: the hardware sin/cos cannot be told apart
-          rope_sincos_fast(pos, f.hi[c * kAngles + e], f.lo[c * kAngles + e], &sn[e], &cs[e]);
-        else
-          rope_sincos(pos, f.hi[c * kAngles + e], f.lo[c * kAngles + e], &sn[e], &cs[e]);
-      }
+      // bf16 rounds right after: the hardware sin/cos cannot be told apart
+      pair_angles<kAngles, false, sizeof(T) == 2>(pos, f.hi + c * kAngles, f.lo + c * kAngles, sn, cs);
     }
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) {
