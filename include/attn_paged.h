@@ -98,8 +98,9 @@ ATTN_API int attn_kv_append_paged(const void* k_new, const void* v_new, void* k_
 /*
  * attn_decode_paged_workspace_size - bytes of device scratch that
  * attn_decode_paged (prefix_len = 0) and attn_decode_shared need for these
- * sizes; -1 cast to size_t for invalid ones.  The caller owns it; calls that
- * may overlap on the GPU (other streams, captured graphs) need one each.
+ * sizes; -1 cast to size_t for invalid ones.  It grows with the rows B * n_h, not
+ * with max_blocks.  The caller owns it; calls that may overlap on the GPU (other
+ * streams, captured graphs) need one each.
  */
 ATTN_API size_t attn_decode_paged_workspace_size(int B, int n_h, int n_kv, int D_qk, int D_v, int page_size,
                                                  int max_blocks, int prefix_len, attn_dtype_t dtype);

@@ -279,3 +279,44 @@ def test_decode_at_far_positions(lib, n, n_h, n_kv, D, Dv, roff, dtype, pairing,
     weights = 2 * moved[..., None] + (2.0 ** -8 if dtype == "bf16" else 1e-5)  # fp32 sums over 2^24 and more keys: 1e-5
     assert np.all(diff <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) * np.abs(want) + weights * vmax)
     assert np.all(np.abs(to_np(lse) - want_lse) <= moved + 1e-5 * np.abs(want_lse) + 1e-5)
+
+
+# ---------------------------------------------------------------------- tables wider than their requests
+@pytest.mark.parametrize("prefix", [0, 64])
+@pytest.mark.parametrize("n_h,n_kv,D,Dv,dtype,opts", [
+    (12, 12, 64, 64, "f32", {}), (32, 8, 128, 128, "bf16", dict(rope_base=1e4, rope_offset=64)),
+    (6, 2, 96, 96, "bf16", {}), (16, 1, 576, 512, "bf16", {}), (32, 8, 128, 128, "bf16", {}), (10, 2, 256, 256, "f32", {}),
+    (128, 1, 576, 512, "bf16", {})])
+def test_a_wider_table_changes_nothing(lib, n_h, n_kv, D, Dv, dtype, opts, prefix):
+    """Work is cut by the requests' lengths: not a bit depends on how many blocks a table row has room for."""
+    dt = TYPES[dtype]
+    lens = [1000, 0, 700, 65, 1900]
+    alias = D == 576
+    k, v, table, pre, k_of, v_of = ref.make_cache(lens, prefix, 16, n_kv, D, Dv, dt, alias=alias)
+    q = normal((5, n_h, D), dt, 1).to(DEV)
+    kd = k.to(DEV)
+    vd = kd[..., :Dv] if alias else v.to(DEV)
+    wide = torch.full((5, 64 * table.shape[1]), -7, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    results = []
+    for t in (table, wide):
+        if prefix:
+            results.append(lib.decode_shared(q, kd, vd, pre.to(DEV), t.to(DEV), ints(lens), lse=True, **opts))
+        else:
+            results.append(lib.decode_paged(q, kd, vd, t.to(DEV), ints(lens), lse=True, **opts))
+    (a, la), (b, lb) = results
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    want, want_lse, err = ref.attend(q.cpu(), k_of, v_of, **opts)
+    check_result(to_np(a), to_np(la), want, want_lse, err, v_of, dtype)
+
+
+# requests, prefix, lengths of their own: from one key each to a single request among empty places
+MIXES = [(1, 0, [4097]), (1, 0, [70000]), (2, 0, [1, 30000]), (40, 0, [5000] + [1] * 39), (300, 0, [1 + i % 130 for i in range(300)]),
+         (33, 0, [0] * 32 + [9000]), (33, 0, [9000] + [0] * 32), (64, 256, [0, 1, 64, 65] * 16), (1, 1024, [3]),
+         (9, 2048, [300] * 9), (2500, 0, [1 + i % 3 for i in range(2500)])]
+
+
+@pytest.mark.parametrize("B,prefix,own", MIXES)
+@pytest.mark.parametrize("n_h,n_kv,D,Dv,dtype", [(6, 2, 96, 96, "bf16"), (4, 4, 64, 64, "f32"), (5, 1, 256, 192, "f32")])
+def test_mixes_of_lengths_on_cuda_cores(lib, B, prefix, own, n_h, n_kv, D, Dv, dtype):
+    check_decode(lib, [prefix + n for n in own], prefix, 32, n_h, n_kv, D, Dv, dtype=dtype)
