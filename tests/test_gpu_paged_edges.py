@@ -320,3 +320,33 @@ MIXES = [(1, 0, [4097]), (1, 0, [70000]), (2, 0, [1, 30000]), (40, 0, [5000] + [
 @pytest.mark.parametrize("n_h,n_kv,D,Dv,dtype", [(6, 2, 96, 96, "bf16"), (4, 4, 64, 64, "f32"), (5, 1, 256, 192, "f32")])
 def test_mixes_of_lengths_on_cuda_cores(lib, B, prefix, own, n_h, n_kv, D, Dv, dtype):
     check_decode(lib, [prefix + n for n in own], prefix, 32, n_h, n_kv, D, Dv, dtype=dtype)
+
+
+# ----------------------------------------------------------------------------------- single-token appends
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pairing", ["adjacent", "half"])
+@pytest.mark.parametrize("n_kv,D,Dv,rope,roff,rdims,alias", [
+    (1, 64, 64, 1e4, 0, 64, False), (8, 128, 128, 5e5, 0, 128, False), (3, 128, 64, 1e4, 64, 64, False),
+    (2, 72, 40, 0.0, 0, 72, False), (1, 576, 512, 1e4, 512, 64, True)])
+def test_append_of_one_token(lib, n_kv, D, Dv, rope, roff, rdims, alias, pairing, dtype):
+    """One token to one slot, and nothing else; to a slot outside the cache, nothing at all."""
+    dt, page, n_pages = TYPES[dtype], 16, 3
+    k, v = normal((1, n_kv, D), dt, 1), normal((1, n_kv, Dv), dt, 2)
+    kp = normal((n_pages, page, n_kv, D), dt, 3)
+    vp = kp[..., :Dv] if alias else normal((n_pages, page, n_kv, Dv), dt, 4)
+    want = oracle.rope_rotate(to64(k), np.full((1, n_kv), 777), rope, roff, rdims, pairing=pairing) if rope > 0 else to64(k)
+    for slot in (0, 17, n_pages * page - 1, -1, n_pages * page):
+        kd = kp.to(DEV)
+        vd = kd[..., :Dv] if alias else vp.to(DEV)
+        lib.kv_append_paged(k.to(DEV), None if alias else v.to(DEV), kd, vd, ints([slot]), ints([777]) if rope > 0 else None,
+                            rope_base=rope, rope_offset=roff, rope_dims=rdims, pairing=pairing)
+        got, others = kd.flatten(0, 1).cpu(), torch.arange(n_pages * page) != slot
+        assert torch.equal(got[others], kp.flatten(0, 1)[others])
+        if not alias:
+            assert torch.equal(vd.flatten(0, 1).cpu()[others], vp.flatten(0, 1)[others])
+        if 0 <= slot < n_pages * page:
+            # half a step of the stored type, and 1e-6 of the pair's norm for the fp32 rotation
+            eps = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+            assert np.all(np.abs(to_np(got[slot]) - want[0]) <= eps * np.abs(want[0]) + 1e-6 * np.sqrt(2) * 6)
+            if not alias:
+                assert torch.equal(vd.flatten(0, 1)[slot].cpu(), v[0])
