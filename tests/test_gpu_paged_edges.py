@@ -350,3 +350,49 @@ def test_append_of_one_token(lib, n_kv, D, Dv, rope, roff, rdims, alias, pairing
             assert np.all(np.abs(to_np(got[slot]) - want[0]) <= eps * np.abs(want[0]) + 1e-6 * np.sqrt(2) * 6)
             if not alias:
                 assert torch.equal(vd.flatten(0, 1)[slot].cpu(), v[0])
+
+
+# --------------------------------------------------------------------------------- captured and side by side
+@pytest.mark.parametrize("prefix", [0, 64])
+@pytest.mark.parametrize("n_h,n_kv,D,Dv,dtype", SHAPES)
+def test_a_captured_call_follows_the_lengths(lib, n_h, n_kv, D, Dv, dtype, prefix):
+    """A graph is captured once; what it computes is cut by the lengths that it finds when it runs."""
+    dt, most = TYPES[dtype], [2500, 1000, 300, 90, 1700]
+    k, v, table, pre, _, _ = ref.make_cache([prefix + n for n in most], prefix, 16, n_kv, D, Dv, dt, alias=D == 576,
+                                            fill=0.5)
+    kd, td, pd = k.to(DEV), table.to(DEV), pre.to(DEV)
+    vd = kd[..., :Dv] if D == 576 else v.to(DEV)
+    q, lens = normal((5, n_h, D), dt, 1).to(DEV), ints([prefix + n for n in most])
+
+    def call():
+        if prefix:
+            return lib.decode_shared(q, kd, vd, pd, td, lens, lse=True)
+        return lib.decode_paged(q, kd, vd, td, lens, lse=True)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = call()
+    for own in (most, [1, 1, 1, 1, 1], [0, 0, 300, 0, 0], [0] * 5, [2500, 0, 1, 64, 65]):
+        lens.copy_(ints([prefix + n for n in own]))
+        want, want_lse = call()
+        out.fill_(7)
+        lse.fill_(7)
+        graph.replay()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_two_fp32_calls_on_two_streams(lib):
+    """Calls on CUDA cores that overlap, each with the scratch that it allocates itself."""
+    lens, prefix = [2100 + 100 * i for i in range(8)], 2048
+    k, v, table, pre, _, _ = (x.to(DEV) if torch.is_tensor(x) else x for x in
+                              ref.make_cache(lens, prefix, 64, 4, 64, 64, torch.float32))
+    q = [normal((8, 16, 64), torch.float32, i).to(DEV) for i in range(2)]
+    sl = ints(lens)
+    want = [lib.decode_shared(x, k, v, pre, table, sl)[0].clone() for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [lib.decode_shared(x, k, v, pre, table, sl, stream=s)[0] for x, s in zip(q, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
