@@ -122,7 +122,9 @@ ATTN_API size_t attn_decode_paged_workspace_size(int B, int n_h, int n_kv, int D
  * k_pages); other shapes on CUDA cores.  Sums are fp32; queries after RoPE and softmax
  * weights are rounded to bf16 on the way into the tensor cores, but for pieces of at
  * most 64 rows (a request's own keys under up to 64 heads per KV head, the shared
- * prefix of a small batch), which keep what that rounding leaves.  NaN in a query, key or
+ * prefix of a small batch), which keep what that rounding leaves: an output's error is
+ * then that of its own rounding, else larger (1.3 times without RoPE, 1.7 with it, for
+ * normally distributed inputs).  NaN in a query, key or
  * value reaches the rows that see it and no other; an infinite value gives them that
  * infinity (both infinities in one dim, or a weight of 0: NaN); a key with a score of -inf
  * has no weight, one with a score of inf makes its rows NaN.
@@ -139,6 +141,9 @@ ATTN_API int attn_decode_paged(const void* q, const void* k_pages, const void* v
  * read and multiplied once for the whole batch - one product of the B * n_h / n_kv
  * query rows of each KV head with its prefix keys - and joined with each
  * request's own keys by the log-sum-exp rule ("Transformer架构完全深度解析" §13).
+ * The MLA-absorbed shape on the tensor cores is the exception: the prefix is kept
+ * once, but read (from L2) and multiplied for each request, so that a call costs
+ * as much as attn_decode_paged over the same lengths.
  *
  *   prefix_pages  DEVICE int32 [prefix_len / page_size]: the pages of the prefix
  *            (what every row of block_table starts with; those entries of

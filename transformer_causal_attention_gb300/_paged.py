@@ -264,8 +264,9 @@ def decode_shared(q, k_pages, v_pages, prefix_pages, block_table, seqlens, *, ro
     """decode_paged() for a batch whose requests all start with the tokens in prefix_pages (attn_decode_shared).
 
     prefix_pages int32 [n]: the n full pages that every row of block_table starts with;
-    they are read and computed once for the whole batch.  seqlens counts them: request b
-    has seqlens[b] - n * page_size >= 1 tokens of its own (fewer: an empty place).
+    they are read and computed once for the whole batch (in the MLA-absorbed shape, values
+    sliced from one 576-dim head under 128 heads, once per request).  seqlens counts them:
+    request b has seqlens[b] - n * page_size >= 1 tokens of its own (fewer: an empty place).
     """
     if prefix_pages is None:
         raise ValueError("prefix_pages must be an int32 CUDA tensor")

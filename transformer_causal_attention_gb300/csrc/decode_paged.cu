@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(kThreads) paged_split_kernel(PagedDecodeArgs a
 // through shared memory.  S = Q K^T and O += P V are register tiles of 4 x 4 and 4 x (DM / 16) per
 // thread, fed by 16-byte loads of transposed tiles (Q^T and K^T by dim, P^T by key), with packed fp32
 // FMAs; a row's 16 threads sit in one half-warp, so its maximum takes four shuffles.  K and V take turns
-// in one buffer, which lets two blocks share an SM and cover each other's loads.  Bound by the fp32 FMA
-// pipes and the loads that feed them (256 requests behind 16384 tokens, 32 heads over 8, D = 128: 2256 us,
-// 30 TFLOP/s); the split kernel above, with a shuffle per 8 FMAs and a load of every key per 4 rows, took 5275.
+// in one buffer, which lets two blocks share an SM and cover each other's loads.  Bound by the loads from
+// shared memory (two thirds of their rate; warps wait for them more than for anything else, the FMA pipes are
+// 39% busy): 256 requests behind 16384 tokens, 32 heads over 8, D = 128, take 2256 us, 30 TFLOP/s; the split
+// kernel above, with a shuffle per 8 FMAs and a load of every key per 4 rows, took 5275.
 constexpr int kTile = 64;           // rows and keys
 constexpr int kPad = kTile + 4;     // row stride of the transposed tiles, in floats
 constexpr int kTileMinRows = 16;    // below, the split kernel's 4 rows per block waste less
