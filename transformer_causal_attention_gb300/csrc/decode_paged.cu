@@ -24,7 +24,7 @@
 // the number of partials depends on the table's width.  (Cut by the width, fp32, 8
 // requests of up to 1024 keys took 11.1 us with a table of 1024 tokens and 19.6
 // with one of 65536, now 10.9 and 11.3; and 1024 requests with tables of 131072
-// tokens needed 541 MB for partials, now 34.)  A step to the next piece of a block's part raises the block's
+// tokens needed 541 MB for partials, now 18.)  A step to the next piece of a block's part raises the block's
 // index or the request's, so their sum numbers the partials.
 // Behind a prefix with 16 rows or more (and head dims up to 128) the shared part is a
 // matrix product for the fp32 pipes instead: see paged_prefix_tile_kernel.
