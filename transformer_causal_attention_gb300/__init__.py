@@ -1,6 +1,6 @@
 """Causal scaled dot-product attention (prefill and KV-cache decode) on one GB300.
 
-Python face of libattn.so (include/attn.h, include/attn_paged.h).  The functions take CUDA torch
+Python face of libattn.so (include/attn.h, include/attn_paged.h, include/attn_packed.h).  The functions take CUDA torch
 tensors and call the C ABI; all computation happens in the library's sm_103a
 kernels.  Build the library first with ``transformer_causal_attention_gb300.build.build()``.
 """
@@ -31,4 +31,11 @@ from ._paged import (  # noqa: F401
     decode_shared,
     kv_append_paged,
     page_plan,
+)
+from ._packed import (  # noqa: F401
+    decode_tree,
+    draft_commit,
+    draft_plan,
+    packed_workspace_size,
+    prefill_paged,
 )

@@ -50,6 +50,26 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// A buffer's extent; p null: none.
+struct Extent {
+  const void* p;
+  size_t bytes;
+};
+// Whether an output overlaps an input or another output.
+inline bool overlaps(const Extent* outs, int n_outs, const Extent* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    if (!outs[i].p) continue;
+    for (int j = 0; j < n_ins; ++j)
+      if (ins[j].p && overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (outs[j].p && overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+  }
+  return false;
+}
+
+// The sizes of a paged cache and of a table over it; *shift: log2 of the page size (api_paged.cu).
+int check_pages(int n_pages, int page_size, int max_blocks, int* shift);
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 }  // namespace attn

@@ -21,6 +21,8 @@ int page_shift_of(int page_size) {
 // Tokens of a table row: 32-bit positions with room for a few tiles or chunks more, which loops over keys step past.
 constexpr long long kMaxRequestTokens = (1LL << 31) - (1 << 16);
 
+}  // namespace
+
 // The sizes of a paged cache and of a table over it.
 int check_pages(int n_pages, int page_size, int max_blocks, int* shift) {
   if (n_pages <= 0 || page_size <= 0 || max_blocks <= 0) return ATTN_ERR_ARG;
@@ -31,6 +33,8 @@ int check_pages(int n_pages, int page_size, int max_blocks, int* shift) {
     return ATTN_ERR_ARG;
   return ATTN_OK;
 }
+
+namespace {
 
 // The sizes of a decode call, filled into *a (everything that the workspace depends on).
 int check_sizes(int B, int n_h, int n_kv, int D_qk, int D_v, int n_pages, int page_size, int max_blocks,

@@ -137,6 +137,46 @@ __device__ __forceinline__ int paged_len(const PagedDecodeArgs& a, int b) {
   return min(max(a.seqlens[b], 0), a.max_blocks << a.page_shift);  // the table's tokens fit 32 bits (checked by the caller)
 }
 
+// Attention of packed new tokens over a paged cache: causal, or (visible != nullptr) by visibility bits among the
+// drafts.  Request b's new tokens are rows cu_new[b] .. of q, and the last of its seqlens[b] keys.
+struct PackedArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  long long v_token_stride;  // elements
+  const int* block_table;    // [B, max_blocks]
+  const int* cu_new;         // [B + 1]
+  const int* seqlens;
+  const int* positions;  // nullable: places
+  const int* visible;    // nullable: causal
+  void* out;
+  float* lse;  // nullable
+  int T, B, n_h, n_kv, D_qk, D_v, n_pages, page_shift, max_blocks, words;
+  int rope_offset;
+  float scale_log2;
+  void* workspace;
+  unsigned int* status;
+  unsigned long long wait_limit_ns;
+};
+// A request of the packed calls: rows first .. first + rows - 1 exist, its n new tokens are at places base ..
+// base + n - 1 (base < 0: the first -base of them are at no place), of len keys.
+struct PackedRequest {
+  int first, rows, n, base, len;
+};
+__device__ __forceinline__ int packed_len(const PackedArgs& a, int b) {
+  return min(max(a.seqlens[b], 0), a.max_blocks << a.page_shift);  // 32 bits (checked by the caller)
+}
+__device__ __forceinline__ int packed_first(const PackedArgs& a, int b) { return min(max(a.cu_new[b], 0), a.T); }
+__device__ __forceinline__ PackedRequest packed_request(const PackedArgs& a, int b) {
+  PackedRequest r;
+  r.first = packed_first(a, b);
+  r.n = max(max(a.cu_new[b + 1], 0) - r.first, 0);
+  r.rows = min(r.n, a.T - r.first);
+  r.len = packed_len(a, b);
+  r.base = r.len - r.n;
+  return r;
+}
+
 // Each launcher returns the launch error (cudaSuccess when enqueued) and adds
 // the number of kernels it enqueued to *launches.
 cudaError_t launch_prefill_simt(const PrefillArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
@@ -164,6 +204,35 @@ bool decode_paged_tc_supported(const PagedDecodeArgs& a, bool bf16, int rope_off
 size_t decode_paged_tc_workspace(const PagedDecodeArgs& a);
 cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st,
                                    int* launches);
+// Packed new tokens over pages on CUDA cores (any supported shape) and the scratch it needs.
+size_t packed_workspace(const PackedArgs& a);
+cudaError_t launch_packed(const PackedArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches);
+struct DraftPlanArgs {
+  const int* places;
+  const int* cu_new;
+  const int* parents;
+  int* positions;
+  int* visible;
+  int T, B, words;
+};
+constexpr int kMaxDrafts = 128;  // per request: 4 words of bits, entries of an accepted path
+cudaError_t launch_draft_plan(const DraftPlanArgs& a, cudaStream_t st, int* launches);
+struct DraftCommitArgs {
+  void* k_pages;
+  void* v_pages;  // null: values alias the keys
+  long long k_row, v_row, v_stride;  // 16-byte pieces of a token's keys and values; bytes between tokens of v_pages
+  const int* block_table;
+  const int* lens;
+  const int* seqlens;
+  const int* path;
+  const int* n_path;
+  int* new_lens;
+  int* free_pages;  // nullable
+  const int* n_free;
+  int* n_left;
+  int B, max_path, n_pages, page_shift, max_blocks, free_cap;
+};
+cudaError_t launch_draft_commit(const DraftCommitArgs& a, cudaStream_t st, int* launches);
 int decode_plan_splits(int B, int n_h, int n_kv, int D_qk, int D_v, int max_len, int* chunk);
 cudaError_t launch_decode(const DecodeArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st,
                           int* launches);

@@ -1,0 +1,372 @@
+// packed.cu - attention of packed new tokens over a paged KV cache on CUDA cores: causal, or
+// by visibility bits among drafted tokens (any head dims up to 640 / 512, bf16 or fp32).
+//
+// The rows of a KV head in request b are its n_b * G (token, head of the group) pairs, token
+// after token; a block takes 64 of them against 64 keys at a time: S = Q K^T with 4 x 4 scores
+// per thread, an online softmax over the rows ("Transformer架构完全深度解析" §13), O += P V with
+// 4 rows x 4 dims per thread and 64 dims.  Everything is fp32; Q stays in shared memory
+// (dim-major), K passes through it 32 dims at a time, P once per tile, V 64 dims at a time.
+// Bound by the FMA pipe and the shared-memory reads that feed it (8 floats per 16 FMAs).
+//
+// Tiles are numbered without a table: request b's start at floor(cu_new[b] * G / 64) + b, which
+// leaves each request at least as many numbers as it has tiles, so a block finds its request by
+// bisection and a number that nobody uses ends at once.  With few tiles the keys of each are cut
+// into n_split equal parts and a second kernel joins the parts of a row by their log-sum-exps.
+#include <math.h>
+
+#include "kernels.h"
+
+namespace attn {
+namespace {
+
+constexpr int R = 64;         // rows per tile
+constexpr int KT = 64;        // keys per tile
+constexpr int DC = 32;        // dims of K in shared memory at a time
+constexpr int kPad = 4;       // floats behind a row of 64: float4 rows on other banks
+constexpr int LD = 64 + kPad;
+constexpr int kThreads = 256;
+constexpr float kMasked = -1.f;  // stands for the weight of a key that the row does not see (weights are >= 0)
+
+// 8 consecutive elements as floats.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), x);
+}
+__device__ __forceinline__ void load8(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ long long tile_start(const PackedArgs& a, int b, int G) {
+  return static_cast<long long>(packed_first(a, b)) * G / R + b;
+}
+
+// NV: blocks of 64 value dims.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads)
+    packed_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ RopeFreq f, int n_split) {
+  extern __shared__ float4 smem4[];
+  float* const Qs = reinterpret_cast<float*>(smem4);  // [D_qk][LD]
+  float* const Ks = Qs + a.D_qk * LD;                 // [DC][LD], then V: [KT][LD]
+  float* const Ps = Ks + KT * LD;                     // [KT keys][LD rows]
+  __shared__ long long slot[KT];                      // slots of the tile's keys, -1: none
+  __shared__ uint32_t vis[R][4];
+  __shared__ int row_place[R];                        // -1: the row is empty or not there
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int G = a.n_h / a.n_kv, g = blockIdx.y, split = blockIdx.z;
+
+  // rows behind the last request's
+  if (split == 0) {
+    const long long from = static_cast<long long>(packed_first(a, a.B)) * G * a.D_v, to = static_cast<long long>(a.T) * G * a.D_v;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    for (long long i = from + 4LL * (blockIdx.x * kThreads + tid); i < to; i += 4LL * gridDim.x * kThreads) {
+      const long long row = i / (G * a.D_v);
+      const int at = static_cast<int>(i - row * (G * a.D_v));
+      store4(static_cast<T*>(a.out) + (row * a.n_h + g * G) * a.D_v + at, zero);
+      if (a.lse != nullptr && at % a.D_v == 0) a.lse[row * a.n_h + g * G + at / a.D_v] = -INFINITY;
+    }
+  }
+  int lo = 0, hi = a.B - 1;  // the last request whose numbers start at or before this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tile_start(a, mid, G) <= static_cast<long long>(blockIdx.x)) lo = mid;
+    else hi = mid - 1;
+  }
+  const int b = lo;
+  const PackedRequest rq = packed_request(a, b);
+  const long long row0 = (static_cast<long long>(blockIdx.x) - tile_start(a, b, G)) * R;
+  const long long n_rows = static_cast<long long>(rq.rows) * G;
+  if (row0 < 0 || row0 >= n_rows) return;
+  const int here = static_cast<int>(n_rows - row0 < R ? n_rows - row0 : R);
+
+  // places, bits, queries
+  if (tid < R) {
+    int place = -1;
+    if (tid < here) {
+      const int i = static_cast<int>((row0 + tid) / G);
+      const int t = rq.first + i;
+      place = rq.base + i;
+      if (a.positions != nullptr && a.positions[t] < 0) place = -1;
+      for (int w = 0; w < 4; ++w)
+        vis[tid][w] = w < a.words ? static_cast<uint32_t>(a.visible[static_cast<long long>(t) * a.words + w]) : 0u;
+    }
+    row_place[tid] = place;
+  }
+  for (int i = tid; i < R * (a.D_qk / 8); i += kThreads) {
+    const int r = i & (R - 1), d = (i >> 6) * 8;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < here) {
+      const long long row = row0 + r;
+      load8(static_cast<const T*>(a.q) + ((rq.first + row / G) * a.n_h + g * G + row % G) * a.D_qk + d, x);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) Qs[(d + e) * LD + r] = x[e];
+  }
+  __syncthreads();
+  if (f.n_pairs) {
+    for (int i = tid; i < here * f.n_pairs; i += kThreads) {
+      const int r = i % here, p = i / here;
+      const int t = rq.first + static_cast<int>((row0 + r) / G);
+      const int pos = a.positions != nullptr ? a.positions[t] : rq.base + static_cast<int>((row0 + r) / G);
+      if (pos < 0) continue;
+      float sn, cs;
+      with_angles<true, false>(pos, [&](auto angle) { angle(f.hi[p], f.lo[p], &sn, &cs); });
+      const int2 d = rope_pair_dims(f, p);
+      rotate_pair(Qs[(a.rope_offset + d.x) * LD + r], Qs[(a.rope_offset + d.y) * LD + r], sn, cs);
+    }
+  }
+  // the keys that the tile's last row may see, and this split's part of them
+  const int last = rq.base + static_cast<int>((row0 + here - 1) / G);
+  const int keys = a.visible != nullptr ? rq.len : min(max(last, -1) + 1, rq.len);
+  int part = (keys + n_split - 1) / n_split;
+  part = (part + KT - 1) / KT * KT;
+  const long long k_lo = static_cast<long long>(split) * part;
+  const int k_hi = static_cast<int>(k_lo + part < keys ? k_lo + part : keys);
+
+  float m[4], l[4], acc[NV][4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[v][i][j] = 0.f;
+  }
+  const int* const table = a.block_table + static_cast<long long>(b) * a.max_blocks;
+  const int first_place = max(rq.base + static_cast<int>(row0 / G), -1);
+  for (long long k64 = k_lo; k64 < k_hi; k64 += KT) {
+    const int k0 = static_cast<int>(k64);
+    __syncthreads();
+    if (tid < KT) {
+      const int key = k0 + tid;
+      long long s = -1;
+      if (key < k_hi) {
+        const int page = table[key >> a.page_shift];
+        if (page >= 0 && page < a.n_pages)
+          s = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+      }
+      slot[tid] = s;
+    }
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int d0 = 0; d0 < a.D_qk; d0 += DC) {
+      __syncthreads();
+      {  // 64 keys x 32 dims, 8 dims of a key per thread
+        const int key = tid >> 2, d = d0 + (tid & 3) * 8;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (d < a.D_qk && slot[key] >= 0)
+          load8(static_cast<const T*>(a.k_pages) + (slot[key] * a.n_kv + g) * a.D_qk + d, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) Ks[(d - d0 + e) * LD + key] = x[e];
+      }
+      __syncthreads();
+      const int dn = min(DC, a.D_qk - d0);
+#pragma unroll 8
+      for (int d = 0; d < dn; ++d) {
+        const float4 qv = *reinterpret_cast<const float4*>(Qs + (d0 + d) * LD + ty * 4);
+        const float4 kv = *reinterpret_cast<const float4*>(Ks + d * LD + tx * 4);
+        const float q4[4] = {qv.x, qv.y, qv.z, qv.w}, k4[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] = fmaf(q4[i], k4[j], s[i][j]);
+      }
+    }
+    // some row does not see some key of the tile
+    const bool masked = a.visible != nullptr ? k0 + KT > rq.base : k0 + KT - 1 > first_place || k0 + KT > k_hi;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i, place = row_place[r];
+      bool seen[4];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = k0 + tx * 4 + j;
+        if (a.visible != nullptr) {
+          const int draft = key - rq.base;  // base may be below 0: key - base <= len - base = n
+          seen[j] = key < k_hi && place >= 0 &&
+                    (draft < 0 || (draft < 32 * a.words && ((vis[r][draft >> 5] >> (draft & 31)) & 1u)));
+        } else {
+          seen[j] = key < k_hi && key <= place;
+        }
+        s[i][j] *= a.scale_log2;
+        if (seen[j]) mx = fmaxf(mx, s[i][j]);
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float m_new = fmaxf(m[i], mx);
+      const float m_ref = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m[i] - m_ref);
+      m[i] = m_new;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - m_ref);
+        s[i][j] = seen[j] ? p : kMasked;
+        if (seen[j]) sum += p;
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l[i] = fmaf(l[i], alpha, sum);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[v][i][j] *= alpha;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(Ps + (tx * 4 + j) * LD + ty * 4) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      __syncthreads();
+      for (int i = tid; i < KT * 8; i += kThreads) {
+        const int key = i >> 3, d = v * 64 + (i & 7) * 8;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (d < a.D_v && slot[key] >= 0)
+          load8(static_cast<const T*>(a.v_pages) + slot[key] * a.v_token_stride + g * a.D_v + d, x);
+        *reinterpret_cast<float4*>(Ks + key * LD + (i & 7) * 8) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(Ks + key * LD + (i & 7) * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+      }
+      __syncthreads();
+      const auto add = [&](auto with_mask) {
+#pragma unroll 8
+        for (int k = 0; k < KT; ++k) {
+          const float4 pv = *reinterpret_cast<const float4*>(Ps + k * LD + ty * 4);
+          const float4 vv = *reinterpret_cast<const float4*>(Ks + k * LD + tx * 4);
+          const float p4[4] = {pv.x, pv.y, pv.z, pv.w}, v4[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // a value that the row does not see may be anything
+            if (with_mask() && p4[i] == kMasked) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[v][i][j] = fmaf(p4[i], v4[j], acc[v][i][j]);
+          }
+        }
+      };
+      if (masked) add([] { return true; });
+      else add([] { return false; });
+    }
+  }
+  // out, or this split's normalised part
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+    if (r >= here) continue;
+    const long long row = row0 + r;
+    const long long at = (rq.first + row / G) * a.n_h + g * G + row % G;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];  // 0: no key with a weight; NaN stays
+    const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int d = v * 64 + tx * 4;
+      if (d >= a.D_v) continue;
+      float o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = l[i] == 0.f ? 0.f : acc[v][i][j] * inv;
+      if (n_split == 1)
+        store4(static_cast<T*>(a.out) + at * a.D_v + d, o);
+      else
+        store4(static_cast<float*>(a.workspace) + (static_cast<long long>(split) * a.T * a.n_h + at) * a.D_v + d, o);
+    }
+    if (tx == 0) {
+      if (n_split == 1) {
+        if (a.lse != nullptr) a.lse[at] = lse2 * 0.69314718055994530942f;
+      } else {
+        static_cast<float*>(a.workspace)[static_cast<long long>(n_split) * a.T * a.n_h * a.D_v +
+                                         static_cast<long long>(split) * a.T * a.n_h + at] = lse2;
+      }
+    }
+  }
+}
+
+// A warp per row: out = sum_j 2^(lse_j - lse) out_j over the splits.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_constant__ PackedArgs a, int n_split) {
+  const int lane = threadIdx.x & 31;
+  const long long at = blockIdx.x * static_cast<long long>(kThreads / 32) + (threadIdx.x >> 5);
+  const long long rows = static_cast<long long>(a.T) * a.n_h;
+  if (at >= rows || at >= static_cast<long long>(packed_first(a, a.B)) * a.n_h) return;  // those behind are written
+  const float* const ws = static_cast<const float*>(a.workspace);
+  const float* const lses = ws + n_split * rows * a.D_v + at;
+  float m = -INFINITY, den = 0.f;
+  for (int j = 0; j < n_split; ++j) m = fmaxf(m, lses[j * rows]);
+  const float m_ref = m == -INFINITY ? 0.f : m;
+  for (int j = 0; j < n_split; ++j) den += exp2f(lses[j * rows] - m_ref);
+  const float inv = den > 0.f ? 1.f / den : den;
+  for (int d = lane * 4; d < a.D_v; d += 128) {
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < n_split; ++j) {
+      const float lj = lses[j * rows];
+      if (lj == -INFINITY) continue;
+      const float w = exp2f(lj - m_ref) * inv;
+      const float4 x = *reinterpret_cast<const float4*>(ws + (j * rows + at) * a.D_v + d);
+      o[0] = fmaf(w, x.x, o[0]);
+      o[1] = fmaf(w, x.y, o[1]);
+      o[2] = fmaf(w, x.z, o[2]);
+      o[3] = fmaf(w, x.w, o[3]);
+    }
+    store4(static_cast<T*>(a.out) + at * a.D_v + d, o);
+  }
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[at] = den == 0.f ? -INFINITY : (m + log2f(den)) * 0.69314718055994530942f;
+}
+
+// Numbers of tiles (an upper bound of the tiles), and parts of each tile's keys: enough blocks for three per SM.
+// (Not by the table's width: tables are as wide as a request may grow.)
+long long tile_numbers(const PackedArgs& a) {
+  return static_cast<long long>(a.T) * (a.n_h / a.n_kv) / R + a.B;
+}
+int splits(const PackedArgs& a) {
+  const long long blocks = tile_numbers(a) * a.n_kv;
+  const long long n = (3 * 152 + blocks - 1) / blocks;
+  return static_cast<int>(n > 64 ? 64 : n);
+}
+size_t smem_bytes(const PackedArgs& a) { return static_cast<size_t>(a.D_qk + 2 * KT) * LD * sizeof(float); }
+
+template <typename T, int NV>
+cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
+  const size_t smem = smem_bytes(a);
+  const cudaError_t e = cudaFuncSetAttribute(packed_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>((640 + 2 * KT) * LD * sizeof(float)));
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(tile_numbers(a)), a.n_kv, n_split);
+  packed_kernel<T, NV><<<grid, kThreads, smem, st>>>(a, rope, n_split);
+  *launches += 1;
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || n_split == 1) return err;
+  const long long rows = static_cast<long long>(a.T) * a.n_h;
+  packed_combine_kernel<T><<<static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(a, n_split);
+  *launches += 1;
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_dims(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
+  if (a.D_v <= 64) return launch<T, 1>(a, rope, n_split, st, launches);
+  if (a.D_v <= 128) return launch<T, 2>(a, rope, n_split, st, launches);
+  if (a.D_v <= 256) return launch<T, 4>(a, rope, n_split, st, launches);
+  return launch<T, 8>(a, rope, n_split, st, launches);
+}
+
+}  // namespace
+
+size_t packed_workspace(const PackedArgs& a) {
+  const int n = splits(a);
+  return n == 1 ? 0 : static_cast<size_t>(n) * a.T * a.n_h * (a.D_v + 1) * sizeof(float);
+}
+
+cudaError_t launch_packed(const PackedArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches) {
+  const int n = splits(a);
+  return bf16 ? launch_dims<__nv_bfloat16>(a, rope, n, st, launches) : launch_dims<float>(a, rope, n, st, launches);
+}
+
+}  // namespace attn
