@@ -56,9 +56,15 @@ ATTN_API size_t attn_packed_workspace_size(int T, int B, int n_h, int n_kv, int 
  * Rows that are empty, that see no key (a place below 0) or that lie behind
  * cu_new[B] come out as 0, their lse as -inf.
  *
- * All arithmetic is fp32.  NaN or an infinity in a query, key or value reaches the rows
- * that see it and no other: values at places that a row does not see, of other
- * requests or behind the last token may be anything.
+ * bf16 with D_qk = D_v = 64 or 128, at most 128 query heads per KV head and a RoPE
+ * span of whole 16-byte pieces (none, or rope_offset % 8 == 0 and rope_dims % 8 == 0,
+ * % 16 with ATTN_ROPE_HALF) runs on the tensor cores, anything else on CUDA cores.
+ * Sums are fp32.  On the tensor cores softmax weights are rounded to bf16 on the way
+ * in, rotated queries to bf16 with what that leaves kept for five eighths of the
+ * dims (three quarters of 64), so that an output's error is at most 1.46 times that of its own
+ * rounding (for normally distributed inputs).  NaN or an infinity in a query, key or
+ * value reaches the rows that see it and no other: values at places that a row does
+ * not see, of other requests or behind the last token may be anything.
  * Outputs must not overlap inputs, the workspace or each other.
  */
 ATTN_API int attn_prefill_paged(const void* q, const void* k_pages, const void* v_pages, int v_token_stride,

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn.so")
 
 SOURCES = ["prefill_tc.cu", "prefill_pair.cu", "decode_mla.cu", "decode_tc.cu", "decode_stream.cu", "decode.cu",
-           "prefill_simt.cu", "rope.cu", "decode_paged_tc.cu", "decode_paged.cu", "page_plan.cu", "packed.cu", "draft.cu",
+           "prefill_simt.cu", "rope.cu", "decode_paged_tc.cu", "decode_paged.cu", "page_plan.cu", "packed_tc.cu", "packed.cu", "draft.cu",
            "api_paged.cu", "api_packed.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

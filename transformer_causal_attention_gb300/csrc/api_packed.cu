@@ -34,8 +34,9 @@ int check_sizes(int T, int B, int n_h, int n_kv, int D_qk, int D_v, int n_pages,
 
 // Scratch of either path (which one a call takes also depends on its RoPE span); never 0, so that a
 // workspace is always a pointer.
-size_t workspace_of(const PackedArgs& a, bool) {
-  const size_t n = packed_workspace(a);
+size_t workspace_of(const PackedArgs& a, bool bf16) {
+  size_t n = packed_workspace(a);
+  if (packed_tc_supported(a, bf16, 0, 0, false, false) && packed_tc_workspace(a) > n) n = packed_tc_workspace(a);
   return n > 16 ? n : 16;
 }
 
@@ -98,8 +99,10 @@ int attend(const void* q, const void* k_pages, const void* v_pages, int v_token_
   a.wait_limit_ns = wait_limit_ns();
   const RopeFreq rf = make_rope(rope_base, rope ? rope_dims : 0, half);
   int launches = 0;
-  const cudaError_t err = launch_packed(a, rf, bf16, static_cast<cudaStream_t>(stream), &launches);
-  return finish(err, launches);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (packed_tc_supported(a, bf16, rope_offset, rope_dims, rope, half))
+    return finish(launch_packed_tc(a, rf, dev.sms, st, &launches), launches);
+  return finish(launch_packed(a, rf, bf16, st, &launches), launches);
 }
 
 }  // namespace

@@ -207,6 +207,11 @@ cudaError_t launch_decode_paged_tc(const PagedDecodeArgs& a, const RopeFreq& rop
 // Packed new tokens over pages on CUDA cores (any supported shape) and the scratch it needs.
 size_t packed_workspace(const PackedArgs& a);
 cudaError_t launch_packed(const PackedArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches);
+// The same on the tensor cores (bf16, D_qk = D_v = 64 or 128, at most 128 query heads per KV head, a RoPE span of
+// whole 16-byte pieces).
+bool packed_tc_supported(const PackedArgs& a, bool bf16, int rope_offset, int rope_dims, bool rope, bool half);
+size_t packed_tc_workspace(const PackedArgs& a);
+cudaError_t launch_packed_tc(const PackedArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st, int* launches);
 struct DraftPlanArgs {
   const int* places;
   const int* cu_new;
