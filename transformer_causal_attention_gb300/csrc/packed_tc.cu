@@ -47,15 +47,15 @@ struct PackedTcPlan {
   int tile_toks;  // tokens per row tile: 128 / G
   int slot_rows;  // rows of a partial
   int lo_first;   // first MMA step with a second part of Q
-  // float offsets into the workspace: partials [2 * ctas, slot_rows, D], their log-sum-exps, records
-  long long l, rec, end;
+  int n_pairs, half;  // of the rotation
+  // float offsets into the workspace: partials [2 * ctas, slot_rows, D], their log-sum-exps, records, angles
+  long long l, rec, angles, end;
 };
 
 namespace {
 
 constexpr int BM = 128;  // rows per tile
 constexpr int BN = 128;  // keys per tile
-constexpr int kQuarter = 32;  // keys per V stage
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kCare = 3;   // care tiles of a piece, at most: 256 tokens of a pair, or 128 drafts
@@ -110,18 +110,16 @@ struct Cfg {
   static constexpr int kBlockBytes = BM * 128;                // one column block (128 rows x 128 bytes, swizzled)
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
   static constexpr int kSteps = D / 16;
-  static constexpr int kLoSteps = LO ? (D == 128 ? 5 : 3) : 0;
+  static constexpr int kLoSteps = LO ? D / 32 : 0;             // MMA steps with a second part of Q
   static constexpr int kLoBytes = kLoSteps * 2 * BM * 16;     // of a row tile
+  static constexpr int kPLoSteps = LO ? 4 : 0;                // steps of 16 keys with a second part of P
   static constexpr int kKStages = D == 128 ? 2 : 4;
-  static constexpr int kVBytes = kBlocks * kQuarter * 128;    // a quarter
-  static constexpr int kVStages = D == 128 ? 7 : 16;
+  static constexpr int kVStages = D == 128 ? 2 : 4;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + 2 * kTileBytes;
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
-  static constexpr int kLoOff = kVOff + kVStages * kVBytes;
-  static constexpr int kFreqOff = kLoOff + 2 * (D == 128 ? 5 : 3) * 2 * BM * 16;  // RoPE frequencies, hi then lo words
-  static constexpr int kFreqs = D / 2;
-  static constexpr int kMlOff = kFreqOff + 2 * kFreqs * 4;     // worker 1's maximum and sum of each row
+  static constexpr int kLoOff = kVOff + kVStages * kTileBytes;
+  static constexpr int kMlOff = kLoOff + 2 * kLoBytes;         // worker 1's maximum and sum of each row
   static constexpr int kBarOff = kMlOff + BM * 8;
   static constexpr uint32_t kOCol = 256;                       // O of worker w at kOCol + w D
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(BM, BN, false);
@@ -280,11 +278,11 @@ __device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t 
 }
 
 // ------------------------------------------------------------------------------------- rows
-// Rotate row r of a query tile at position pos: the rounded values in place, what the rounding left of chunks
-// [2 lo_first, 2 lo_first + 2 kLoSteps) to the second part (0 for dims outside the span).
-template <int D, int LO_CHUNKS>
-__device__ __noinline__ void rotate_row(uint8_t* tile, uint8_t* lo, int r, int pos, int rope_offset, int n_pairs,
-                                      bool half, const float* f_hi, const float* f_lo, int lo_chunk0) {
+// Rotate row r of a query tile by the cosines and sines at cs (a pair each): the rounded values in place, what the
+// rounding left of chunks [lo_chunk0, lo_chunk0 + LO_CHUNKS) to the second part (0 for dims outside the span).
+template <int LO_CHUNKS>
+__device__ __noinline__ void rotate_row(uint8_t* tile, uint8_t* lo, int r, const float2* cs, int rope_offset, int n_pairs,
+                                      bool half, int lo_chunk0) {
   auto chunk = [&](int c) { return reinterpret_cast<uint4*>(tile + (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
   auto rest = [&](int c, const float* x, uint4 rounded) {
     if (static_cast<unsigned>(c - lo_chunk0) >= static_cast<unsigned>(LO_CHUNKS)) return;
@@ -299,46 +297,72 @@ __device__ __noinline__ void rotate_row(uint8_t* tile, uint8_t* lo, int r, int p
     for (int c = 0; c < LO_CHUNKS; ++c)
       *reinterpret_cast<uint4*>(lo + c * (BM * 16) + r * 16) = make_uint4(0, 0, 0, 0);
   }
-  with_angles<true, true>(pos, [&](auto angle) {
-    if (half) {
-      const int hc = n_pairs / 8;
-#pragma unroll 1
-      for (int i = 0; i < hc; ++i) {
-        uint4* const p0 = chunk(c0 + i);
-        uint4* const p1 = chunk(c0 + i + hc);
-        float x0[8], x1[8];
-        bf16x8_to_f32(*p0, x0);
-        bf16x8_to_f32(*p1, x1);
+  const float4* const angles = reinterpret_cast<const float4*>(cs);  // two pairs each
+  if (half) {
+    const int hc = n_pairs / 8;
+#pragma unroll 2
+    for (int i = 0; i < hc; ++i) {
+      float4 w[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float sn, cs;
-          angle(f_hi[i * 8 + e], f_lo[i * 8 + e], &sn, &cs);
-          rotate_pair(x0[e], x1[e], sn, cs);
-        }
-        const uint4 y0 = f32_to_bf16x8(x0), y1 = f32_to_bf16x8(x1);
-        *p0 = y0;
-        *p1 = y1;
-        rest(c0 + i, x0, y0);
-        rest(c0 + i + hc, x1, y1);
-      }
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < n_pairs / 4; ++i) {
-        uint4* const p = chunk(c0 + i);
-        float x[8];
-        bf16x8_to_f32(*p, x);
+      for (int e = 0; e < 4; ++e) w[e] = __ldg(angles + 4 * i + e);
+      uint4* const p0 = chunk(c0 + i);
+      uint4* const p1 = chunk(c0 + i + hc);
+      float x0[8], x1[8];
+      bf16x8_to_f32(*p0, x0);
+      bf16x8_to_f32(*p1, x1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float sn, cs;
-          angle(f_hi[i * 4 + e], f_lo[i * 4 + e], &sn, &cs);
-          rotate_pair(x[2 * e], x[2 * e + 1], sn, cs);
-        }
-        const uint4 y = f32_to_bf16x8(x);
-        *p = y;
-        rest(c0 + i, x, y);
+      for (int e = 0; e < 4; ++e) {
+        rotate_pair(x0[2 * e], x1[2 * e], w[e].y, w[e].x);
+        rotate_pair(x0[2 * e + 1], x1[2 * e + 1], w[e].w, w[e].z);
       }
+      const uint4 y0 = f32_to_bf16x8(x0), y1 = f32_to_bf16x8(x1);
+      *p0 = y0;
+      *p1 = y1;
+      rest(c0 + i, x0, y0);
+      rest(c0 + i + hc, x1, y1);
     }
-  });
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < n_pairs / 4; ++i) {
+      const float4 w0 = __ldg(angles + 2 * i), w1 = __ldg(angles + 2 * i + 1);
+      uint4* const p = chunk(c0 + i);
+      float x[8];
+      bf16x8_to_f32(*p, x);
+      rotate_pair(x[0], x[1], w0.y, w0.x);
+      rotate_pair(x[2], x[3], w0.w, w0.z);
+      rotate_pair(x[4], x[5], w1.y, w1.x);
+      rotate_pair(x[6], x[7], w1.w, w1.z);
+      const uint4 y = f32_to_bf16x8(x);
+      *p = y;
+      rest(c0 + i, x, y);
+    }
+  }
+}
+
+// Cosines and sines of the rows' rotations, float2 [T, n_pairs]: computed once for all heads (in the attention kernel,
+// where all rows of a tile meet them at once, they took 3 us per piece).  A thread per (row, pair).
+__global__ void __launch_bounds__(256) packed_angles_kernel(const __grid_constant__ PackedArgs a,
+                                                            const __grid_constant__ RopeFreq f, float2* out) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the attention kernel starts, and waits where it reads these
+  const long long i = blockIdx.x * 256LL + threadIdx.x;
+  const int t = static_cast<int>(i / f.n_pairs), p = static_cast<int>(i - static_cast<long long>(t) * f.n_pairs);
+  if (t >= a.T) return;
+  int pos;
+  if (a.positions != nullptr) {
+    pos = a.positions[t];
+  } else {
+    int lo = 0, hi = a.B - 1;  // the last request that starts at or before the row
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (packed_first(a, mid) <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    const PackedRequest r = packed_request(a, lo);
+    pos = r.base + t - r.first;
+  }
+  float sn, cs;
+  with_angles<true, false>(max(pos, 0), [&](auto angle) { angle(f.hi[p], f.lo[p], &sn, &cs); });
+  out[i] = make_float2(cs, sn);
 }
 
 // Bits of the 128 keys from key0 on that a row sees: those below lim, or (tree) those below base and the drafts
@@ -376,7 +400,8 @@ __device__ __forceinline__ void seen_tree(const uint32_t* w, int base, int klim,
 
 // This thread's row of a tile's scores become its weights P (see prefill_tc.cu): p = 2^(s * scale*log2e - m), m moves
 // when the row maximum grew by more than the threshold.
-template <int D>
+// The first kLoKeys weights come as the sum of two bf16 values, the second ones behind all first ones.
+template <int D, int kLoKeys>
 __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, const uint32_t* mask,
                                             bool rescale, float scale_log2, float& m_run, float& l_run) {
   uint32_t sr[BN];
@@ -413,14 +438,19 @@ __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bo
   const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
   const float2 nm2 = make_float2(-m_ref, -m_ref);
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t pl[kLoKeys > 0 ? BN / 4 : 1];
 #pragma unroll
   for (int c = 0; c < BN / 4; ++c) {
     const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sl2, nm2);
     const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
     acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
     pr[c] = pack_bf16x2(pp.x, pp.y);
+    if (2 * c < kLoKeys)
+      pl[c] = pack_bf16x2(pp.x - __uint_as_float(pr[c] << 16), pp.y - __uint_as_float(pr[c] & 0xffff0000u));
   }
   tmem_st32(s_addr, pr);
+  static_assert(kLoKeys == 0 || kLoKeys == BN / 2, "second parts fill 32 columns");
+  if constexpr (kLoKeys > 0) tmem_st32(s_addr + 64, pl);
   if (__any_sync(0xffffffffu, need && rescale)) rescale_o<D>(o_addr, alpha);
 #pragma unroll
   for (int c = BN / 4; c < BN / 2; ++c) {
@@ -462,8 +492,8 @@ __device__ __noinline__ void add_bad(const PackedArgs& a, const Piece& u, int li
 template <int D, bool LO>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_tc_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ PackedTcPlan pl,
-                     const __grid_constant__ RopeFreq f, const __grid_constant__ CUtensorMap tm_q,
-                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, LO>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // no room is left for aligning it here
@@ -471,17 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   Bars<C>* bars = reinterpret_cast<Bars<C>*>(smem + C::kBarOff);
-  float* const f_hi = reinterpret_cast<float*>(smem + C::kFreqOff);
-  float* const f_lo = f_hi + C::kFreqs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.n_h / a.n_kv;
   asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may start to wait
-  if constexpr (LO) {
-    for (int i = threadIdx.x; i < f.n_pairs; i += kThreads) {
-      f_hi[i] = f.hi[i];
-      f_lo[i] = f.lo[i];
-    }
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
@@ -489,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < C::kVStages; ++s) {
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], 2);  // the MMA issuer and warp 3, which passes every quarter
+      mbar_init(&bars->v_empty[s], 2);  // the MMA issuer and warp 3, which passes every tile
       mbar_init(&bars->v_fixed[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
@@ -573,9 +595,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ TMA producers
       const bool is_v = warp == 2;
       const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+      uint8_t* const ring = smem + (is_v ? C::kVOff : C::kKOff);
+      uint64_t* const full = is_v ? bars->v_full : bars->k_full;
+      uint64_t* const empty = is_v ? bars->v_empty : bars->k_empty;
+      const uint32_t n_stages = is_v ? C::kVStages : C::kKStages;
       if (lane == 0) tma_prefetch_desc(map);
-      // rows per box: a page, or a part of it; a lane per box of a tile: block blk, rows from box_row on
-      const int box_shift = min(a.page_shift, is_v ? 5 : 7);
+      // rows per box: a page, or half of a 256-token page; a lane per box of a tile: block blk, rows from box_row on
+      const int box_shift = min(a.page_shift, 7);
       const int boxes = BN >> box_shift;
       const int box = lane & (boxes - 1), blk = lane / boxes;
       const int box_row = box << box_shift;
@@ -615,37 +641,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         for (; t < t_end; ++t) {
-          if (!is_v) {
-            if (!(ok = warp_wait(&bars->k_empty[r.st], r.ph ^ 1u, wc))) break;
-            const int n_boxes = min((min(klim - t * BN, BN) + (1 << box_shift) - 1) >> box_shift, boxes);
-            if (lane == 0)
-              mbar_arrive_expect_tx(&bars->k_full[r.st], static_cast<uint32_t>(n_boxes * C::kBlocks) << (box_shift + 7));
-            __syncwarp();
-            if (loads && box < n_boxes)
-              tma_load_4d(smem + C::kKOff + r.st * C::kTileBytes + blk * C::kBlockBytes + box_row * 128, map,
-                          &bars->k_full[r.st], blk * 64, g, (t * BN + box_row) & page_mask, id);
-            issued |= 1u << r.st;
-            last_ph = (last_ph & ~(1u << r.st)) | (r.ph << r.st);
-            r.next(C::kKStages);
-          } else {
-#pragma unroll 1
-            for (int q = 0; q < BN / kQuarter; ++q) {
-              if (!(ok = warp_wait(&bars->v_empty[r.st], r.ph ^ 1u, wc))) break;
-              const int n_keys = min(max(klim - t * BN - q * kQuarter, 0), kQuarter);
-              const int n_boxes = (n_keys + (1 << box_shift) - 1) >> box_shift;
-              if (lane == 0)
-                mbar_arrive_expect_tx(&bars->v_full[r.st], static_cast<uint32_t>(n_boxes * C::kBlocks) << (box_shift + 7));
-              __syncwarp();
-              const int in_q = box_row - q * kQuarter;  // row of the quarter
-              if (loads && in_q >= 0 && in_q < n_keys)
-                tma_load_4d(smem + C::kVOff + r.st * C::kVBytes + blk * (kQuarter * 128) + in_q * 128, map,
-                            &bars->v_full[r.st], blk * 64, g, (t * BN + box_row) & page_mask, id);
-              issued |= 1u << r.st;
-              last_ph = (last_ph & ~(1u << r.st)) | (r.ph << r.st);
-              r.next(C::kVStages);
-            }
-            if (!ok) break;
-          }
+          if (!(ok = warp_wait(&empty[r.st], r.ph ^ 1u, wc))) break;
+          const int n_boxes = (min(klim - t * BN, BN) + (1 << box_shift) - 1) >> box_shift;  // others hold no key
+          if (lane == 0)
+            mbar_arrive_expect_tx(&full[r.st], static_cast<uint32_t>(n_boxes * C::kBlocks) << (box_shift + 7));
+          __syncwarp();
+          if (loads && box < n_boxes)
+            tma_load_4d(ring + r.st * C::kTileBytes + blk * C::kBlockBytes + box_row * 128, map, &full[r.st], blk * 64, g,
+                        (t * BN + box_row) & page_mask, id);
+          issued |= 1u << r.st;
+          last_ph = (last_ph & ~(1u << r.st)) | (r.ph << r.st);
+          r.next(n_stages);
           id = fetch(t + 1);
         }
         if (!ok) break;
@@ -653,8 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->piece_empty[n % kQueue]);
       }
       if (bars->abort_flag) {  // let every copy in flight land before shared memory goes away
-        uint64_t* const full = is_v ? bars->v_full : bars->k_full;
-        for (int s = 0; s < (is_v ? C::kVStages : C::kKStages); ++s)
+        for (uint32_t s = 0; s < n_stages; ++s)
           if (issued & (1u << s)) drain_wait(&full[s], (last_ph >> s) & 1u, a.wait_limit_ns);
         for (int w = 0; w < 2; ++w)
           if (is_v && (q_used & (1u << w))) drain_wait(&bars->q_full[w], ((q_ph >> w) & 1u) ^ 1u, a.wait_limit_ns);
@@ -665,12 +670,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         const uint32_t q_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024));
         const uint32_t k_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024));
-        const uint32_t v_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kVOff), kQuarter * 128, 1024));
+        const uint32_t v_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kVOff), C::kBlockBytes, 1024));
         const uint32_t lo_desc0 = ((smem_u32(smem + C::kLoOff) & 0x3FFFFu) >> 4) | ((BM * 16 >> 4) << 16);
         Ring kr, vr;
         uint32_t q_ph = 0, p_ph = 0, o_ph = 0, fix_ph = 0;  // parities, bits per worker (fix_ph: per V stage)
-        const int lo_first = pl.lo_first;
-        auto issue_qk = [&](uint32_t w) {
+        // the K tile's byte offsets (>> 4) of the steps that Q's second part has
+        uint32_t lo_off[LO ? C::kLoSteps : 1];
+        if constexpr (LO) {
+#pragma unroll
+          for (int s = 0; s < C::kLoSteps; ++s) {
+            const int kk = pl.lo_first + s;
+            lo_off[s] = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
+          }
+        }
+        // Q K^T: the steps of Q's first part, those of its second part
+        auto qk_hi = [&](uint32_t w) {
           const uint32_t a0 = q_desc0 + ((w * C::kTileBytes) >> 4);
           const uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
 #pragma unroll
@@ -678,64 +692,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
             mma_ss_lo(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
           }
+        };
+        auto qk_lo = [&](uint32_t w) {
+          const uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
 #pragma unroll
-          for (int s = 0; s < C::kLoSteps; ++s) {
-            const int kk = lo_first + s;
-            mma_lo(tmem + w * 128u, lo_desc0 + ((w * C::kLoBytes + s * (2 * BM * 16)) >> 4),
-                   b0 + (((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4), C::kIdescQK);
-          }
+          for (int s = 0; s < C::kLoSteps; ++s)
+            mma_lo(tmem + w * 128u, lo_desc0 + ((w * C::kLoBytes + s * (2 * BM * 16)) >> 4), b0 + lo_off[s], C::kIdescQK);
+        };
+        auto issue_qk = [&](uint32_t w) {
+          qk_hi(w);
+          qk_lo(w);
           mma_commit(&bars->s_full[w]);
         };
-        // P V over a tile, a quarter of its keys at a time; wait: its quarters have to be waited for (fixed: in warp 3's
-        // hands first), release: nobody reads them after
-        auto issue_pv = [&](uint32_t w, bool first, bool wait, bool fixed, bool release) -> bool {
-          Ring x = vr;
+        // P V: P in columns 8 kk of the worker's S, its second part in columns 64 on
+        auto issue_pv = [&](uint32_t w, bool first) {
+          const uint32_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
 #pragma unroll
-          for (int q = 0; q < BN / kQuarter; ++q) {
-            if (wait) {
-              if (fixed) {
-                if (!lane_wait(&bars->v_fixed[x.st], (fix_ph >> x.st) & 1u, wc)) return false;
-                fix_ph ^= 1u << x.st;
-              } else if (!lane_wait(&bars->v_full[x.st], x.ph, wc)) {
-                return false;
-              }
-              tc_fence_after();
-            }
-            const uint32_t b0 = v_desc0 + ((x.st * C::kVBytes) >> 4);
+          for (int kk = 0; kk < BN / 16; ++kk)
+            mma_ts_lo(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
+                      (!first || kk > 0) ? 1u : 0u);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-              mma_ts_lo(tmem + C::kOCol + w * D, tmem + w * 128u + (2 * q + kk) * 8, b0 + ((kk * 16 * 128) >> 4),
-                        C::kIdescPV, (!first || q > 0 || kk > 0) ? 1u : 0u);
-            if (release) mma_commit(&bars->v_empty[x.st]);
-            x.next(C::kVStages);
-          }
-          if (release) vr = x;
-          return true;
+          for (int kk = 0; kk < C::kPLoSteps; ++kk)
+            mma_ts_lo(tmem + C::kOCol + w * D, tmem + w * 128u + 64 + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV, 1u);
         };
-        auto take_p = [&](uint32_t w, bool first) -> bool {
-          if (!lane_wait(&bars->p_full[w], (p_ph >> w) & 1u, wc)) return false;
+        auto wait_p = [&](uint32_t w) -> bool {
+          const bool there = lane_wait(&bars->p_full[w], (p_ph >> w) & 1u, wc);
           p_ph ^= 1u << w;
-          if (first) {  // O has been read
-            if (!lane_wait(&bars->o_empty[w], ((o_ph >> w) & 1u) ^ 1u, wc)) return false;
-            o_ph ^= 1u << w;
-          }
-          tc_fence_after();
-          return true;
+          return there;
         };
-        auto take_q = [&](uint32_t w) -> bool {
-          if (!lane_wait(LO ? &bars->q_ready[w] : &bars->q_full[w], (q_ph >> w) & 1u, wc)) return false;
+        auto wait_o = [&](uint32_t w) -> bool {  // O has been read
+          const bool there = lane_wait(&bars->o_empty[w], ((o_ph >> w) & 1u) ^ 1u, wc);
+          o_ph ^= 1u << w;
+          return there;
+        };
+        auto wait_q = [&](uint32_t w) -> bool {
+          const bool there = lane_wait(LO ? &bars->q_ready[w] : &bars->q_full[w], (q_ph >> w) & 1u, wc);
           q_ph ^= 1u << w;
-          tc_fence_after();
-          return true;
+          return there;
         };
-        auto take_k = [&]() -> bool {
-          if (!lane_wait(&bars->k_full[kr.st], kr.ph, wc)) return false;
-          tc_fence_after();
-          return true;
+        auto wait_k = [&]() -> bool { return lane_wait(&bars->k_full[kr.st], kr.ph, wc); };
+        auto wait_v = [&](bool care) -> bool {  // care: treated by warp 3
+          if (!care) return lane_wait(&bars->v_full[vr.st], vr.ph, wc);
+          const bool there = lane_wait(&bars->v_fixed[vr.st], (fix_ph >> vr.st) & 1u, wc);
+          fix_ph ^= 1u << vr.st;
+          return there;
         };
         auto k_done = [&]() {
           mma_commit(&bars->k_empty[kr.st]);
           kr.next(C::kKStages);
+        };
+        auto v_done = [&]() {
+          mma_commit(&bars->v_empty[vr.st]);
+          vr.next(C::kVStages);
         };
         for (uint32_t n = 0;; ++n) {
           if (!lane_wait(&bars->piece_full[n % kQueue], (n / kQueue) & 1u, wc)) break;
@@ -746,35 +754,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bars->piece_empty[n % kQueue]);
           bool ok = true;
           if (kind == kPair) {
-            if (!take_k()) break;
+            if (!wait_k()) break;
             if (n0 > 0) {
-              if (!take_q(0)) break;
+              if (!wait_q(0)) break;
+              tc_fence_after();
               issue_qk(0);
               if (n0 == 1) mma_commit(&bars->q_empty[0]);
             }
-            if (!take_q(1)) break;
+            if (!wait_q(1)) break;
+            tc_fence_after();
             issue_qk(1);
             if (nv == 1) mma_commit(&bars->q_empty[1]);
             k_done();
+            const int ve = min(n0 - 2, care);
             for (int v = 0; v < nv; ++v) {
-              const bool fixed = v >= care, next = v + 1 < nv;
+              if (v > 0 && v < ve) {
+                // Both workers take this tile and two more, and no care is needed: a loop without decisions, in which
+                // the waits for the next turn's tiles stand before this turn's last MMAs, so that the tensor pipe
+                // does not run dry.
+                if (!(ok = wait_v(false) && wait_k())) break;
+                for (; v < ve; ++v) {
+                  if (!(ok = wait_p(0))) break;
+                  tc_fence_after();
+                  issue_pv(0, false);
+                  issue_qk(0);
+                  if (!(ok = wait_p(1))) break;
+                  tc_fence_after();
+                  issue_pv(1, false);
+                  v_done();
+                  qk_hi(1);
+                  Ring kn = kr;
+                  kn.next(C::kKStages);
+                  if (v + 1 < ve && !(ok = wait_v(false) && lane_wait(&bars->k_full[kn.st], kn.ph, wc))) break;
+                  qk_lo(1);
+                  mma_commit(&bars->s_full[1]);
+                  mma_commit(&bars->k_empty[kr.st]);
+                  kr = kn;
+                }
+                if (!ok) break;
+              }
+              const bool next = v + 1 < nv;
+              if (!(ok = wait_v(v >= care))) break;
               bool have_k = false;
               if (v < n0) {
-                if (!(ok = take_p(0, v == 0) && issue_pv(0, v == 0, true, fixed, false))) break;
+                if (!(ok = wait_p(0) && (v > 0 || wait_o(0)))) break;
+                tc_fence_after();
+                issue_pv(0, v == 0);
                 if (v == n0 - 1) {
                   mma_commit(&bars->o_done[0]);
                 } else {
-                  if (!(ok = take_k())) break;
+                  if (!(ok = wait_k())) break;
                   have_k = true;
                   issue_qk(0);
                   if (v + 2 == n0) mma_commit(&bars->q_empty[0]);
                 }
               }
-              if (!(ok = take_p(1, v == 0) && issue_pv(1, v == 0, v >= n0, fixed, true))) break;
+              if (!(ok = wait_p(1) && (v > 0 || wait_o(1)))) break;
+              tc_fence_after();
+              issue_pv(1, v == 0);
+              v_done();
               if (!next) {
                 mma_commit(&bars->o_done[1]);
               } else {
-                if (!have_k && !(ok = take_k())) break;
+                if (!have_k && !(ok = wait_k())) break;
                 issue_qk(1);
                 if (v + 2 == nv) mma_commit(&bars->q_empty[1]);
                 k_done();
@@ -782,18 +824,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
             for (int v = 0; v < 2 && v < nv; ++v) {
-              if (!(ok = take_k() && take_q(v))) break;
+              if (!(ok = wait_k() && wait_q(v))) break;
+              tc_fence_after();
               issue_qk(v);
               k_done();
               if (v + 2 >= nv) mma_commit(&bars->q_empty[v]);
             }
             for (int v = 0; ok && v < nv; ++v) {
               const uint32_t w = v & 1;
-              if (!(ok = take_p(w, v < 2) && issue_pv(w, v < 2, true, v >= care, true))) break;
+              if (!(ok = wait_v(v >= care) && wait_p(w) && (v >= 2 || wait_o(w)))) break;
+              tc_fence_after();
+              issue_pv(w, v < 2);
+              v_done();
               if (v + 2 >= nv) {
                 mma_commit(&bars->o_done[w]);
               } else {
-                if (!(ok = take_k())) break;
+                if (!(ok = wait_k())) break;
                 issue_qk(w);
                 k_done();
                 if (v + 4 >= nv) mma_commit(&bars->q_empty[w]);
@@ -857,48 +903,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u->kind == kNone) break;
         const int care = u->care_t, klim = u->klim;
         uint32_t any = 0;
-        for (int t = u->t; ok && t < u->t_end; ++t) {
+        for (int t = u->t; t < u->t_end; ++t) {
+          if (!(ok = warp_wait(&bars->v_full[r.st], r.ph, wc))) break;
+          if (t >= care) {
+            uint8_t* const v = smem + C::kVOff + r.st * C::kTileBytes;
 #pragma unroll 1
-          for (int q = 0; q < BN / kQuarter; ++q) {
-            if (!(ok = warp_wait(&bars->v_full[r.st], r.ph, wc))) break;
-            if (t >= care) {
-              uint8_t* const v = smem + C::kVOff + r.st * C::kVBytes;
-              const int n_keys = klim - t * BN - q * kQuarter;
-              // lane l: the 16-byte pieces of row l, from another piece on than its neighbours
-              uint32_t seen_bad = 0;
-#pragma unroll 1
-              for (int blk = 0; blk < C::kBlocks; ++blk) {
-#pragma unroll 4
-                for (int i = 0; i < 8; ++i) {
-                  uint4* const p = reinterpret_cast<uint4*>(v + blk * (kQuarter * 128) + lane * 128 + (((i + lane) & 7) << 4));
-                  uint4 x = make_uint4(0, 0, 0, 0);
-                  if (lane < n_keys) {
-                    x = *p;
-                    uint32_t* const y = reinterpret_cast<uint32_t*>(&x);
-                    bool fine = true;
+            for (int q = 0; q < BN / 32; ++q) {
+              // lane l: row 32 q + l, whose 16-byte pieces it takes from another one on than its neighbours
+              const int row = 32 * q + lane;
+              uint8_t* const p = v + row * 128;
+              bool bad = false;
+              if (t * BN + row >= klim) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      const uint32_t lo_keep = (y[e] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu;
-                      const uint32_t hi_keep = (y[e] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
-                      fine = fine && (lo_keep | hi_keep) == 0xffffffffu;
-                      y[e] &= lo_keep | hi_keep;
-                    }
-                    if (fine) continue;
-                    seen_bad = 1;
+                for (int i = 0; i < D / 8; ++i)
+                  *reinterpret_cast<uint4*>(p + (i >> 3) * C::kBlockBytes + (((i + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+              } else {
+                uint32_t ones = 0;  // bits 15 and 31: an exponent of all ones
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                  const uint4 x = *reinterpret_cast<const uint4*>(p + (i >> 3) * C::kBlockBytes + (((i + lane) & 7) << 4));
+                  ones |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                          ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+                }
+                bad = (ones & 0x80008000u) != 0;
+                if (bad) {
+#pragma unroll 1
+                  for (int i = 0; i < D / 2; ++i) {
+                    uint32_t* const y = reinterpret_cast<uint32_t*>(p + (i >> 5) * C::kBlockBytes + (i & 31) * 4);
+                    uint32_t x = *y;
+                    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+                    *y = x;
                   }
-                  *p = x;
                 }
               }
-              const uint32_t bits = __ballot_sync(0xffffffffu, seen_bad);
+              const uint32_t bits = __ballot_sync(0xffffffffu, bad);
               if (lane == 0 && t - care < kCare) u->bad[t - care][q] = bits;
               any |= bits;
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars->v_fixed[r.st]);
             }
-            if (lane == 0) mbar_arrive(&bars->v_empty[r.st]);
-            r.next(C::kVStages);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->v_fixed[r.st]);
           }
+          if (lane == 0) mbar_arrive(&bars->v_empty[r.st]);
+          r.next(C::kVStages);
         }
         if (!ok) break;
         if (lane == 0) {
@@ -922,6 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_tok = r / G;  // token of this row in its tile
     uint32_t s_ph = 0, q_ph = 0, o_ph = 0, x_ph = 0;
     bool ok = true;
+    const float2* const angles = reinterpret_cast<const float2*>(static_cast<const float*>(a.workspace) + pl.angles);
     // Query tile of piece e of the queue, if this worker has one: rotate this thread's row and hand it over.
     auto prepare = [&](const Piece* u) -> bool {
       if constexpr (LO) {
@@ -930,15 +979,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_ph ^= 1u;
         const int tok = (u->kind == kPair && w ? pl.tile_toks : 0) + my_tok;
         if (my_tok < pl.tile_toks && tok < u->ntok) {
-          const int pos = a.positions != nullptr ? a.positions[u->row0 + tok] : u->place0 + tok;
-          rotate_row<D, 2 * C::kLoSteps>(smem + C::kQOff + w * C::kTileBytes, smem + C::kLoOff + w * C::kLoBytes, r,
-                                         max(pos, 0), a.rope_offset, f.n_pairs, f.half != 0, f_hi, f_lo, 2 * pl.lo_first);
+          rotate_row<2 * C::kLoSteps>(smem + C::kQOff + w * C::kTileBytes, smem + C::kLoOff + w * C::kLoBytes, r,
+                                      angles + static_cast<long long>(u->row0 + tok) * pl.n_pairs, a.rope_offset, pl.n_pairs,
+                                      pl.half != 0, 2 * pl.lo_first);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars->q_ready[w]);
       }
       return true;
     };
+    if constexpr (LO) asm volatile("griddepcontrol.wait;" ::: "memory");  // the angles are there
     ok = row_wait(&bars->piece_full[0], 0, wc) && prepare(&bars->piece[0]);
     for (uint32_t n = 0; ok; ++n) {
       const Piece* const u = &bars->piece[n % kQueue];
@@ -974,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (a.visible != nullptr) seen_tree(bits, base, klim, t * BN, mask);
             else seen_below(lim, t * BN, mask);
           }
-          softmax_row<D>(s_addr, o_addr, masked, mask, i > 0, a.scale_log2, m_run, l_run);
+          softmax_row<D, 16 * C::kPLoSteps>(s_addr, o_addr, masked, mask, i > 0, a.scale_log2, m_run, l_run);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars->p_full[w]);
@@ -1121,10 +1171,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* const ws = static_cast<const float*>(a.workspace);
   const Record* const rec = reinterpret_cast<const Record*>(ws + pl.rec);
-  const int c = blockIdx.x;
+  const int parts = (pl.slot_rows + kJoinRows - 1) / kJoinRows;
+  const int c = blockIdx.x / parts, part = blockIdx.x - c * parts;
   const Record head = rec[2 * c + 1];
   const int G = a.n_h / a.n_kv;
-  if (head.kt == 0 || static_cast<int>(blockIdx.y) * kJoinRows >= (head.kind == kPair ? 2 * BM : min(BM, head.ntok * G))) return;
+  if (head.kt == 0 || part * kJoinRows >= (head.kind == kPair ? 2 * BM : min(BM, head.ntok * G))) return;
   // the pieces: this one, then first pieces up to the one that ends the segment (a CTA may hold none)
   if (threadIdx.x == 0) slots[0] = 2 * c + 1;
   int n = 1;
@@ -1141,7 +1192,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __syncthreads();
   float* const wt = weights[warp];
   for (int k = warp; k < kJoinRows; k += kJoinWarps) {
-    const int rr = blockIdx.y * kJoinRows + k, r = rr & (BM - 1), w = rr / BM;
+    const int rr = part * kJoinRows + k, r = rr & (BM - 1), w = rr / BM;
     const int tk = r / G, tok = (w ? pl.tile_toks : 0) + tk;
     if (tk >= pl.tile_toks || tok >= head.ntok || (w && head.kind != kPair)) continue;
     float m = -INFINITY;
@@ -1191,17 +1242,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
 }
 
-PackedTcPlan make_plan(const PackedArgs& a, int ctas, int max_ctas, bool rope) {
+PackedTcPlan make_plan(const PackedArgs& a, int ctas, int max_ctas, int n_pairs, int half) {
   PackedTcPlan p{};
   const int G = a.n_h / a.n_kv;
   p.ctas = ctas;
   p.tile_toks = BM / G;
   p.slot_rows = a.T <= p.tile_toks ? a.T * G : 2 * BM;
-  const int steps = a.D_qk / 16, lo_steps = a.D_qk == 128 ? 5 : 3;
-  p.lo_first = rope ? (a.rope_offset / 16 < steps - lo_steps ? a.rope_offset / 16 : steps - lo_steps) : 0;
+  const int steps = a.D_qk / 16, rest = steps - a.D_qk / 32;
+  p.lo_first = n_pairs ? (a.rope_offset / 16 < rest ? a.rope_offset / 16 : rest) : 0;
+  p.n_pairs = n_pairs;
+  p.half = half;
   p.l = 2LL * max_ctas * p.slot_rows * a.D_v;
   p.rec = (p.l + 2LL * max_ctas * p.slot_rows + 3) & ~3LL;
-  p.end = p.rec + 2LL * max_ctas * static_cast<long long>(sizeof(Record) / 4);
+  p.angles = p.rec + 2LL * max_ctas * static_cast<long long>(sizeof(Record) / 4);
+  p.end = p.angles + 2LL * a.T * n_pairs;
   return p;
 }
 
@@ -1229,19 +1283,19 @@ cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, const CUtensorMap*
                    cudaStream_t st, int* launches) {
   cudaError_t e = prepare<D, LO>();
   if (e != cudaSuccess) return e;
-  packed_tc_kernel<D, LO><<<pl.ctas, kThreads, smem_bytes<Cfg<D, LO>>(), st>>>(a, pl, rope, maps[0], maps[1], maps[2]);
+  if (LO) {
+    const long long items = static_cast<long long>(a.T) * rope.n_pairs;
+    packed_angles_kernel<<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(
+        a, rope, reinterpret_cast<float2*>(static_cast<float*>(a.workspace) + pl.angles));
+    *launches += 1;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  e = launch_early(packed_tc_kernel<D, LO>, pl.ctas, kThreads, smem_bytes<Cfg<D, LO>>(), st, LO, a, pl, maps[0], maps[1],
+                   maps[2]);
   *launches += 1;
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pl.ctas, (pl.slot_rows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, packed_tc_join_kernel<D>, a, pl);
+  if (e != cudaSuccess) return e;
+  const unsigned parts = (pl.slot_rows + kJoinRows - 1) / kJoinRows;
+  e = launch_early(packed_tc_join_kernel<D>, pl.ctas * parts, kJoinWarps * 32, 0, st, true, a, pl);
   *launches += 1;
   return e;
 }
@@ -1254,7 +1308,7 @@ bool packed_tc_supported(const PackedArgs& a, bool bf16, int rope_offset, int ro
 }
 
 size_t packed_tc_workspace(const PackedArgs& a) {
-  return static_cast<size_t>(make_plan(a, kMaxCtas, kMaxCtas, false).end) * sizeof(float);
+  return static_cast<size_t>(make_plan(a, kMaxCtas, kMaxCtas, a.D_qk / 2, 0).end) * sizeof(float);
 }
 
 cudaError_t launch_packed_tc(const PackedArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st, int* launches) {
@@ -1264,7 +1318,7 @@ cudaError_t launch_packed_tc(const PackedArgs& a, const RopeFreq& rope, int num_
   const long long segments = static_cast<long long>(a.T) * (a.n_h / a.n_kv) / (2 * BM - 2 * (a.n_h / a.n_kv) + 2) + a.B;
   const long long most = segments * a.n_kv * (((static_cast<long long>(a.max_blocks) << a.page_shift) + BN - 1) / BN);
   if (most < ctas) ctas = most > 0 ? static_cast<int>(most) : 1;
-  const PackedTcPlan pl = make_plan(a, ctas, kMaxCtas, rotate);
+  const PackedTcPlan pl = make_plan(a, ctas, kMaxCtas, rope.n_pairs, rope.half);
   // query rows by (dim, head of the group, KV head, row), a row tile per box; K and V by (dim, KV head, row in
   // page, page), a page or a part of it per box
   const unsigned long long hs = static_cast<unsigned long long>(a.D_qk) * 2, page = 1ull << a.page_shift;
@@ -1274,7 +1328,7 @@ cudaError_t launch_packed_tc(const PackedArgs& a, const RopeFreq& rope, int num_
   const bool wide = a.D_qk == 128;
   if (!make_map_box(&maps[0], a.q, a.D_qk, G, a.n_kv, a.T, hs, hs * G, hs * a.n_h, G, 1, pl.tile_toks, wide) ||
       !make_map_box(&maps[1], a.k_pages, a.D_qk, a.n_kv, rows, a.n_pages, hs, ks, ks * page, 1, rows < 128 ? rows : 128, 1, wide) ||
-      !make_map_box(&maps[2], a.v_pages, a.D_v, a.n_kv, rows, a.n_pages, hs, vs, vs * page, 1, rows < kQuarter ? rows : kQuarter, 1, wide))
+      !make_map_box(&maps[2], a.v_pages, a.D_v, a.n_kv, rows, a.n_pages, hs, vs, vs * page, 1, rows < 128 ? rows : 128, 1, wide))
     return cudaErrorInvalidValue;
   if (a.D_qk == 64)
     return rotate ? launch<64, true>(a, rope, maps, pl, st, launches) : launch<64, false>(a, rope, maps, pl, st, launches);
