@@ -47,9 +47,10 @@ struct PackedTcPlan {
   int tile_toks;  // tokens per row tile: 128 / G
   int slot_rows;  // rows of a partial
   int lo_first;   // first MMA step with a second part of Q
-  int n_pairs, half;  // of the rotation
-  // float offsets into the workspace: partials [2 * ctas, slot_rows, D], their log-sum-exps, records, angles
-  long long l, rec, angles, end;
+  int wide;       // 1: out and workspace start on 32 bytes
+  // float offsets into the workspace: partials [2 * ctas, slot_rows, D], their log-sum-exps, records, the rotated
+  // queries (bf16 [T, n_h, D]) and what that rounding left (bf16 [T, n_h, 64])
+  long long l, rec, q, lo, end;
 };
 
 namespace {
@@ -58,6 +59,7 @@ constexpr int BM = 128;  // rows per tile
 constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kLoDims = 64;  // dims with a second part of Q: a column block
 constexpr int kCare = 3;   // care tiles of a piece, at most: 256 tokens of a pair, or 128 drafts
 constexpr int kQueue = 6;  // pieces in the queue; kAhead are handed out before warp 3 treats the first of them
 constexpr int kAhead = 3;
@@ -110,11 +112,12 @@ struct Cfg {
   static constexpr int kBlockBytes = BM * 128;                // one column block (128 rows x 128 bytes, swizzled)
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
   static constexpr int kSteps = D / 16;
-  static constexpr int kLoSteps = LO ? D / 32 : 0;             // MMA steps with a second part of Q
-  static constexpr int kLoBytes = kLoSteps * 2 * BM * 16;     // of a row tile
-  static constexpr int kPLoSteps = LO ? 4 : 0;                // steps of 16 keys with a second part of P
-  static constexpr int kKStages = D == 128 ? 2 : 4;
-  static constexpr int kVStages = D == 128 ? 2 : 4;
+  static constexpr int kLoSteps = LO ? kLoDims / 16 : 0;       // MMA steps with a second part of Q
+  static constexpr int kLoBytes = LO ? kBlockBytes : 0;        // of a row tile
+  static constexpr int kPLoSteps = LO && D == 128 ? 4 : 0;    // steps of 16 keys with a second part of P
+  static constexpr int kKStages = 2;
+  static constexpr int kVStages = 2;
+  static_assert(kKStages == 2 && kVStages == 2, "the MMA issuer's turns are written for two stages");
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + 2 * kTileBytes;
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
@@ -130,7 +133,7 @@ template <typename C>
 struct Bars {
   uint64_t k_full[C::kKStages], k_empty[C::kKStages];
   uint64_t v_full[C::kVStages], v_empty[C::kVStages], v_fixed[C::kVStages];
-  uint64_t q_full[2], q_ready[2], q_empty[2];
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
   uint64_t x_full, x_done;  // single pieces: worker 1's sums are there, have been read
   uint64_t piece_full[kQueue], piece_empty[kQueue], care_done[kQueue];
@@ -264,105 +267,87 @@ __device__ __noinline__ void next_piece(const PackedArgs& a, const PackedTcPlan&
   w.live = false;
 }
 
-// ------------------------------------------------------------------------------------- MMAs
-// A unswizzled (the second part of Q: 16-byte chunks of 128 rows one after the other), B as all tiles.
-constexpr uint32_t kLoHigh = (128u >> 4) | (1u << 14);  // 8-row groups 128 bytes apart, descriptor version, no swizzle
-__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %5};\n\t"
-      "setp.eq.b32 p, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kLoHigh), "n"(kDescHigh)
-      : "memory");
-}
-
 // ------------------------------------------------------------------------------------- rows
-// Rotate row r of a query tile by the cosines and sines at cs (a pair each): the rounded values in place, what the
-// rounding left of chunks [lo_chunk0, lo_chunk0 + LO_CHUNKS) to the second part (0 for dims outside the span).
-template <int LO_CHUNKS>
-__device__ __noinline__ void rotate_row(uint8_t* tile, uint8_t* lo, int r, const float2* cs, int rope_offset, int n_pairs,
-                                      bool half, int lo_chunk0) {
-  auto chunk = [&](int c) { return reinterpret_cast<uint4*>(tile + (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
-  auto rest = [&](int c, const float* x, uint4 rounded) {
-    if (static_cast<unsigned>(c - lo_chunk0) >= static_cast<unsigned>(LO_CHUNKS)) return;
-    float y[8];
-    bf16x8_to_f32(rounded, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = fabsf(y[e]) < INFINITY ? x[e] - y[e] : 0.f;  // 0 behind an infinity
-    *reinterpret_cast<uint4*>(lo + (c - lo_chunk0) * (BM * 16) + r * 16) = f32_to_bf16x8(y);
-  };
-  const int c0 = rope_offset / 8, c1 = c0 + n_pairs / 4;
-  if (c0 > lo_chunk0 || c1 < lo_chunk0 + LO_CHUNKS) {
-    for (int c = 0; c < LO_CHUNKS; ++c)
-      *reinterpret_cast<uint4*>(lo + c * (BM * 16) + r * 16) = make_uint4(0, 0, 0, 0);
-  }
-  const float4* const angles = reinterpret_cast<const float4*>(cs);  // two pairs each
-  if (half) {
-    const int hc = n_pairs / 8;
-#pragma unroll 2
-    for (int i = 0; i < hc; ++i) {
-      float4 w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = __ldg(angles + 4 * i + e);
-      uint4* const p0 = chunk(c0 + i);
-      uint4* const p1 = chunk(c0 + i + hc);
-      float x0[8], x1[8];
-      bf16x8_to_f32(*p0, x0);
-      bf16x8_to_f32(*p1, x1);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        rotate_pair(x0[2 * e], x1[2 * e], w[e].y, w[e].x);
-        rotate_pair(x0[2 * e + 1], x1[2 * e + 1], w[e].w, w[e].z);
+// The new tokens' queries rotated at their positions, bf16 [T, n_h, D], and what that rounding left of dims
+// [lo_dim, lo_dim + 64), bf16 [T, n_h, 64].  A thread owns 8 dims (and with split halves their partners) of a token for
+// heads_per heads, so that an angle is computed once for all of them; bound by HBM.  (Rotated by the softmax warps
+// of the attention kernel, where a query tile arrives with nothing to hide behind, it took 4 to 7 us per piece.)
+template <int D>
+__global__ void __launch_bounds__(256) packed_rotate_kernel(const __grid_constant__ PackedArgs a,
+                                                            const __grid_constant__ RopeFreq f, __nv_bfloat16* hi,
+                                                            __nv_bfloat16* lo, int lo_dim, int heads_per) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the attention kernel starts, and waits where it reads these
+  constexpr int kChunks = D / 8;
+  const int groups = a.n_h / heads_per;
+  const long long i = blockIdx.x * 256LL + threadIdx.x;
+  const int c = static_cast<int>(i % kChunks);
+  const long long tg = i / kChunks;
+  const int t = static_cast<int>(tg / groups), h0 = static_cast<int>(tg - static_cast<long long>(t) * groups) * heads_per;
+  if (t >= a.T) return;
+  const int rel = c * 8 - a.rope_offset;
+  const bool in = rel >= 0 && rel < 2 * f.n_pairs;
+  if (in && f.half && rel >= f.n_pairs) return;  // with its partner
+  float sn[8], cs[8];
+  if (in) {
+    int pos;
+    if (a.positions != nullptr) {
+      pos = a.positions[t];
+    } else {
+      int b = 0, e = a.B - 1;  // the last request that starts at or before the row
+      while (b < e) {
+        const int mid = (b + e + 1) >> 1;
+        if (packed_first(a, mid) <= t) b = mid;
+        else e = mid - 1;
       }
-      const uint4 y0 = f32_to_bf16x8(x0), y1 = f32_to_bf16x8(x1);
-      *p0 = y0;
-      *p1 = y1;
-      rest(c0 + i, x0, y0);
-      rest(c0 + i + hc, x1, y1);
+      const PackedRequest r = packed_request(a, b);
+      pos = r.base + t - r.first;
+    }
+    const int p0 = f.half ? rel : rel / 2, n = f.half ? 8 : 4;
+    with_angles<true, false>(max(pos, 0), [&](auto angle) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) angle(f.hi[p0 + e], f.lo[p0 + e], &sn[e], &cs[e]);
+    });
+  }
+  const long long row = static_cast<long long>(t) * a.n_h + h0;
+  const uint4* const q = static_cast<const uint4*>(a.q) + row * kChunks + c;
+  uint4* const o = reinterpret_cast<uint4*>(hi) + row * kChunks + c;
+  uint4* const s = reinterpret_cast<uint4*>(lo) + row * (kLoDims / 8);
+  const int lc = c - lo_dim / 8, partner = f.n_pairs / 8;
+  const auto put = [&](int h, int at, const float* x) {  // chunk c + at
+    const uint4 y = f32_to_bf16x8(x);
+    o[h * kChunks + at] = y;
+    if (static_cast<unsigned>(lc + at) < static_cast<unsigned>(kLoDims / 8)) {
+      float z[8];
+      bf16x8_to_f32(y, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = fabsf(z[e]) < INFINITY ? x[e] - z[e] : 0.f;  // 0 behind an infinity
+      s[h * (kLoDims / 8) + lc + at] = f32_to_bf16x8(z);
+    }
+  };
+  if (in && f.half) {
+#pragma unroll 2
+    for (int h = 0; h < heads_per; ++h) {
+      float x[8], y[8];
+      bf16x8_to_f32(__ldg(q + h * kChunks), x);
+      bf16x8_to_f32(__ldg(q + h * kChunks + partner), y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], sn[e], cs[e]);
+      put(h, 0, x);
+      put(h, partner, y);
     }
   } else {
 #pragma unroll 4
-    for (int i = 0; i < n_pairs / 4; ++i) {
-      const float4 w0 = __ldg(angles + 2 * i), w1 = __ldg(angles + 2 * i + 1);
-      uint4* const p = chunk(c0 + i);
+    for (int h = 0; h < heads_per; ++h) {
       float x[8];
-      bf16x8_to_f32(*p, x);
-      rotate_pair(x[0], x[1], w0.y, w0.x);
-      rotate_pair(x[2], x[3], w0.w, w0.z);
-      rotate_pair(x[4], x[5], w1.y, w1.x);
-      rotate_pair(x[6], x[7], w1.w, w1.z);
-      const uint4 y = f32_to_bf16x8(x);
-      *p = y;
-      rest(c0 + i, x, y);
+      bf16x8_to_f32(__ldg(q + h * kChunks), x);
+      if (in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rotate_pair(x[2 * e], x[2 * e + 1], sn[e], cs[e]);
+      }
+      put(h, 0, x);
     }
   }
-}
-
-// Cosines and sines of the rows' rotations, float2 [T, n_pairs]: computed once for all heads (in the attention kernel,
-// where all rows of a tile meet them at once, they took 3 us per piece).  A thread per (row, pair).
-__global__ void __launch_bounds__(256) packed_angles_kernel(const __grid_constant__ PackedArgs a,
-                                                            const __grid_constant__ RopeFreq f, float2* out) {
-  asm volatile("griddepcontrol.launch_dependents;");  // the attention kernel starts, and waits where it reads these
-  const long long i = blockIdx.x * 256LL + threadIdx.x;
-  const int t = static_cast<int>(i / f.n_pairs), p = static_cast<int>(i - static_cast<long long>(t) * f.n_pairs);
-  if (t >= a.T) return;
-  int pos;
-  if (a.positions != nullptr) {
-    pos = a.positions[t];
-  } else {
-    int lo = 0, hi = a.B - 1;  // the last request that starts at or before the row
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (packed_first(a, mid) <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    const PackedRequest r = packed_request(a, lo);
-    pos = r.base + t - r.first;
-  }
-  float sn, cs;
-  with_angles<true, false>(max(pos, 0), [&](auto angle) { angle(f.hi[p], f.lo[p], &sn, &cs); });
-  out[i] = make_float2(cs, sn);
 }
 
 // Bits of the 128 keys from key0 on that a row sees: those below lim, or (tree) those below base and the drafts
@@ -398,34 +383,47 @@ __device__ __forceinline__ void seen_tree(const uint32_t* w, int base, int klim,
   }
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // This thread's row of a tile's scores become its weights P (see prefill_tc.cu): p = 2^(s * scale*log2e - m), m moves
-// when the row maximum grew by more than the threshold.
-// The first kLoKeys weights come as the sum of two bf16 values, the second ones behind all first ones.
-template <int D, int kLoKeys>
+// when the row maximum grew by more than the threshold.  LO: the weights of the last 64 keys come as the sum of two bf16
+// values, the second ones in columns 64 on.
+// The scores are read twice, for the maximum and then 32 keys at a time for the weights: with the row kept in
+// registers in between, 148 bytes of it were spilled per thread, more than the L1 beside 226 KB of shared memory
+// holds, and a tile took 2350 cycles instead of 1600.
+template <int D, bool LO>
 __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, const uint32_t* mask,
                                             bool rescale, float scale_log2, float& m_run, float& l_run) {
-  uint32_t sr[BN];
+  float mx;
+  {
+    uint32_t x[BN];
 #pragma unroll
-  for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_addr + c * 32, sr + c * 32);
-  tmem_wait_ld();
-  float s[BN];
+    for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_addr + c * 32, x + c * 32);
+    tmem_wait_ld();
+    if (masked) {
 #pragma unroll
-  for (int c = 0; c < BN; ++c) s[c] = __uint_as_float(sr[c]);
-  if (masked) {
+      for (int c = 0; c < BN; ++c)
+        if (!((mask[c >> 5] >> (c & 31)) & 1u)) x[c] = 0xff800000u;
+    }
+    float m8[8];
 #pragma unroll
-    for (int c = 0; c < BN; ++c)
-      if (!((mask[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
+    for (int e = 0; e < 8; ++e) m8[e] = __uint_as_float(x[e]);
+#pragma unroll
+    for (int c = 8; c + 16 <= BN; c += 16)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m8[e] = fmax3(m8[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 8 + e]));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], __uint_as_float(x[BN - 8 + e]));
+    mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7])) * scale_log2;
   }
-  float m8[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m8[e] = s[e];
-#pragma unroll
-  for (int c = 8; c + 16 <= BN; c += 16)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m8[e] = fmax3(m8[e], s[c + e], s[c + 8 + e]);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], s[BN - 8 + e]);
-  const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7])) * scale_log2;
+  uint32_t sr[2][32];
+  tmem_ld32(s_addr, sr[0]);
   const bool need = mx > m_run + kRescaleThreshold;
   float alpha = 1.f;
   if (need) {
@@ -433,54 +431,99 @@ __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bo
     l_run *= alpha;
     m_run = mx;
   }
-  uint32_t pr[BN / 2];
   const float2 sl2 = make_float2(scale_log2, scale_log2);
   const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
   const float2 nm2 = make_float2(-m_ref, -m_ref);
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  uint32_t pl[kLoKeys > 0 ? BN / 4 : 1];
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-  for (int c = 0; c < BN / 4; ++c) {
-    const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sl2, nm2);
-    const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-    acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
-    pr[c] = pack_bf16x2(pp.x, pp.y);
-    if (2 * c < kLoKeys)
-      pl[c] = pack_bf16x2(pp.x - __uint_as_float(pr[c] << 16), pp.y - __uint_as_float(pr[c] & 0xffff0000u));
+    for (int q = 0; q < 2; ++q) {
+      tmem_wait_ld();
+      if (q == 0) tmem_ld32(s_addr + 64 * h + 32, sr[1]);
+      else if (h == 0) tmem_ld32(s_addr + 64, sr[0]);
+      uint32_t* const s = sr[q];
+      if (masked) {
+        const uint32_t m = h ? mask[2 + q] : mask[q];
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!((m >> c) & 1u)) s[c] = 0xff800000u;
+      }
+      uint32_t pr[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, nm2);
+        const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+        acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
+        pr[c] = pack_bf16x2(pp.x, pp.y);
+        if (LO) {
+          s[2 * c] = __float_as_uint(pp.x);
+          s[2 * c + 1] = __float_as_uint(pp.y);
+        }
+      }
+      // over scores that have been read: P's columns are half as many, those of the second parts lie over tile columns 64 on
+      tmem_st16(s_addr + 32 * h + 16 * q, pr);
+      if (LO && h == 1) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(pr[c] << 16), __uint_as_float(pr[c] & 0xffff0000u)),
+                                      make_float2(-1.f, -1.f),
+                                      make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])));
+          pr[c] = pack_bf16x2(y.x, y.y);
+        }
+        tmem_st16(s_addr + 64 + 16 * q, pr);
+      }
+    }
   }
-  tmem_st32(s_addr, pr);
-  static_assert(kLoKeys == 0 || kLoKeys == BN / 2, "second parts fill 32 columns");
-  if constexpr (kLoKeys > 0) tmem_st32(s_addr + 64, pl);
   if (__any_sync(0xffffffffu, need && rescale)) rescale_o<D>(o_addr, alpha);
-#pragma unroll
-  for (int c = BN / 4; c < BN / 2; ++c) {
-    const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sl2, nm2);
-    const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-    acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
-    pr[c] = pack_bf16x2(pp.x, pp.y);
-  }
   acc[0] = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
   l_run += acc[0].x + acc[0].y;
-  tmem_st32(s_addr + 32, pr + 32);
 }
 
-// The values that are not finite in care tiles, of dims [d, d + 32), added to the outputs of a row that sees them
-// (tree: by the bits w, else below lim).
-__device__ __noinline__ void add_bad(const PackedArgs& a, const Piece& u, int lim, const uint32_t* w, int d, float* o) {
+// 32 bytes of a row, whole sectors where the row starts on one (wide): in two stores of 16 bytes they are two writes to L2.
+__device__ __forceinline__ void store32(uint4* p, const uint4& a, const uint4& b, int wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    p[0] = a;
+    p[1] = b;
+  }
+}
+
+// The bits of what a row of worker w sees in the tile from key0 on; a row that is no query sees nothing.
+__device__ __noinline__ void row_mask(const PackedArgs& a, const PackedTcPlan& pl, const Piece& u, int w, int my_tok, int key0,
+                                    uint32_t* m) {
+  const int tok = (u.kind == kPair && w ? pl.tile_toks : 0) + my_tok;
+  const bool real = my_tok < pl.tile_toks && tok < u.ntok && u.place0 + tok >= 0;
+  if (a.visible == nullptr || !real) {
+    seen_below(real ? u.place0 + tok + 1 : 0, key0, m);
+    return;
+  }
+  uint32_t bits[4];
+  const int* const row = a.visible + static_cast<long long>(u.row0 + tok) * a.words;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bits[i] = i < a.words ? static_cast<uint32_t>(row[i]) : 0u;
+  seen_tree(bits, u.base, u.klim, key0, m);
+}
+
+// The values that are not finite in care tiles, of dims [d, d + 16), added to the outputs of a row that sees them.
+__device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl, const Piece& u, int w, int my_tok, int d,
+                                   float* o) {
   for (int i = 0; i < kCare; ++i) {
     const int key0 = (u.care_t + i) * BN;
     if (u.care_t + i >= u.t_end) break;
     if (u.care_t + i < u.t) continue;
     uint32_t m[4];
-    if (a.visible != nullptr) seen_tree(w, u.base, u.klim, key0, m);
-    else seen_below(lim, key0, m);
+    row_mask(a, pl, u, w, my_tok, key0, m);
     for (int j = 0; j < 4; ++j) {
       for (uint32_t left = u.bad[i][j] & m[j]; left; left &= left - 1) {
         const int key = key0 + 32 * j + __ffs(left) - 1;
         const int page = a.block_table[static_cast<long long>(u.b) * a.max_blocks + (key >> a.page_shift)];
         const long long slot = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
         const __nv_bfloat16* const v = static_cast<const __nv_bfloat16*>(a.v_pages) + slot * a.v_token_stride + u.g * a.D_v + d;
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 16; ++e) {
           const float x = __bfloat162float(v[e]);
           if (!(fabsf(x) < INFINITY)) o[e] += x;
         }
@@ -492,7 +535,8 @@ __device__ __noinline__ void add_bad(const PackedArgs& a, const Piece& u, int li
 template <int D, bool LO>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_tc_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ PackedTcPlan pl,
-                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_lo,
+                     const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<D, LO>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -516,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars->q_full[w], 1);
-      mbar_init(&bars->q_ready[w], 128);
       mbar_init(&bars->q_empty[w], 1);
       mbar_init(&bars->s_full[w], 1);
       mbar_init(&bars->p_full[w], 128);
@@ -607,6 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box_row = box << box_shift;
       const bool loads = blk < C::kBlocks;
       const int page_mask = (1 << a.page_shift) - 1;
+      if (LO && is_v) {  // the rotated queries come from the kernel before
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+      }
       Ring r;
       uint32_t q_ph = 0, q_used = 0;  // bits per worker: parity of its next query tile, whether one was loaded
       uint32_t issued = 0, last_ph = 0;
@@ -630,9 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(&bars->q_empty[w], ((q_ph >> w) & 1u) ^ 1u, wc)) { ok = false; break; }
             if (lane == 0) {
               const int row = pc->row0 + (kind == kPair && w ? pl.tile_toks : 0);
-              mbar_arrive_expect_tx(&bars->q_full[w], static_cast<uint32_t>(pl.tile_toks * G) * 128u * C::kBlocks);
+              mbar_arrive_expect_tx(&bars->q_full[w], static_cast<uint32_t>(pl.tile_toks * G) * 128u * (C::kBlocks + LO));
               for (int d = 0; d < C::kBlocks; ++d)
                 tma_load_4d(smem + C::kQOff + w * C::kTileBytes + d * C::kBlockBytes, &tm_q, &bars->q_full[w], d * 64, 0, g, row);
+              if (LO) tma_load_4d(smem + C::kLoOff + w * C::kLoBytes, &tm_lo, &bars->q_full[w], 0, 0, g, row);
             }
             __syncwarp();
             q_ph ^= 1u << w;
@@ -671,33 +719,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024));
         const uint32_t k_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024));
         const uint32_t v_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kVOff), C::kBlockBytes, 1024));
-        const uint32_t lo_desc0 = ((smem_u32(smem + C::kLoOff) & 0x3FFFFu) >> 4) | ((BM * 16 >> 4) << 16);
+        const uint32_t lo_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kLoOff), 16, 1024));
         Ring kr, vr;
         uint32_t q_ph = 0, p_ph = 0, o_ph = 0, fix_ph = 0;  // parities, bits per worker (fix_ph: per V stage)
-        // the K tile's byte offsets (>> 4) of the steps that Q's second part has
-        uint32_t lo_off[LO ? C::kLoSteps : 1];
-        if constexpr (LO) {
-#pragma unroll
-          for (int s = 0; s < C::kLoSteps; ++s) {
-            const int kk = pl.lo_first + s;
-            lo_off[s] = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-          }
-        }
-        // Q K^T: the steps of Q's first part, those of its second part
+        // Q K^T: the steps of Q's first part, those of its second part.  Loops, a few at a time: all code that runs side by
+        // side in an SM has to fit its instruction cache (with the MMAs written out, 48 a turn, a tile's softmax took
+        // 2350 cycles in the mean and 1600 at best).
         auto qk_hi = [&](uint32_t w) {
-          const uint32_t a0 = q_desc0 + ((w * C::kTileBytes) >> 4);
-          const uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+          uint32_t a0 = q_desc0 + ((w * C::kTileBytes) >> 4), b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+#pragma unroll 1
+          for (int blk = 0; blk < C::kBlocks; ++blk) {
 #pragma unroll
-          for (int kk = 0; kk < C::kSteps; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-            mma_ss_lo(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss_lo(tmem + w * 128u, a0 + kk * 2, b0 + kk * 2, C::kIdescQK, kk > 0 || blk > 0 ? 1u : 0u);
+            a0 += C::kBlockBytes >> 4;
+            b0 += C::kBlockBytes >> 4;
           }
         };
         auto qk_lo = [&](uint32_t w) {
-          const uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
-#pragma unroll
-          for (int s = 0; s < C::kLoSteps; ++s)
-            mma_lo(tmem + w * 128u, lo_desc0 + ((w * C::kLoBytes + s * (2 * BM * 16)) >> 4), b0 + lo_off[s], C::kIdescQK);
+          if constexpr (LO) {
+            const uint32_t a0 = lo_desc0 + ((w * C::kLoBytes) >> 4);
+            uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+#pragma unroll 1
+            for (int s = 0; s < C::kLoSteps; ++s) {
+              const int kk = pl.lo_first + s;
+              mma_ss_lo(tmem + w * 128u, a0 + s * 2, b0 + (((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4), C::kIdescQK, 1u);
+            }
+          }
         };
         auto issue_qk = [&](uint32_t w) {
           qk_hi(w);
@@ -706,14 +754,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // P V: P in columns 8 kk of the worker's S, its second part in columns 64 on
         auto issue_pv = [&](uint32_t w, bool first) {
-          const uint32_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4);
+          const uint32_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4), p0 = tmem + w * 128u, o0 = tmem + C::kOCol + w * D;
+#pragma unroll 1
+          for (int i = 0; i < BN / 16 + C::kPLoSteps; i += 4) {
+            const uint32_t a0 = p0 + i * 8, v0 = b0 + ((i < BN / 16 ? i : i - 4) * 128);  // steps of 16 keys x 128 bytes
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_ts_lo(tmem + C::kOCol + w * D, tmem + w * 128u + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV,
-                      (!first || kk > 0) ? 1u : 0u);
-#pragma unroll
-          for (int kk = 0; kk < C::kPLoSteps; ++kk)
-            mma_ts_lo(tmem + C::kOCol + w * D, tmem + w * 128u + 64 + kk * 8, b0 + ((kk * 16 * 128) >> 4), C::kIdescPV, 1u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts_lo(o0, a0 + kk * 8, v0 + kk * 128, C::kIdescPV, (!first || i > 0 || kk > 0) ? 1u : 0u);
+          }
         };
         auto wait_p = [&](uint32_t w) -> bool {
           const bool there = lane_wait(&bars->p_full[w], (p_ph >> w) & 1u, wc);
@@ -726,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return there;
         };
         auto wait_q = [&](uint32_t w) -> bool {
-          const bool there = lane_wait(LO ? &bars->q_ready[w] : &bars->q_full[w], (q_ph >> w) & 1u, wc);
+          const bool there = lane_wait(&bars->q_full[w], (q_ph >> w) & 1u, wc);
           q_ph ^= 1u << w;
           return there;
         };
@@ -744,6 +792,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto v_done = [&]() {
           mma_commit(&bars->v_empty[vr.st]);
           vr.next(C::kVStages);
+        };
+        // The same written out, for the loop inside pair pieces (48 MMAs a turn at 70 cycles instead of 90).
+        auto qk_hi_all = [&](uint32_t w) {
+          const uint32_t a0 = q_desc0 + ((w * C::kTileBytes) >> 4), b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < C::kSteps; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
+            mma_ss_lo(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
+          }
+        };
+        const uint32_t lo_k = ((pl.lo_first >> 2) * C::kBlockBytes + (pl.lo_first & 3) * 32) >> 4;
+        auto qk_lo_all = [&](uint32_t w) {
+          if constexpr (LO) {
+            const uint32_t a0 = lo_desc0 + ((w * C::kLoBytes) >> 4);
+            const uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
+            if ((pl.lo_first & 3) == 0) {
+#pragma unroll
+              for (int s = 0; s < C::kLoSteps; ++s) mma_ss_lo(tmem + w * 128u, a0 + s * 2, b0 + lo_k + s * 2, C::kIdescQK, 1u);
+            } else {
+              qk_lo(w);
+            }
+          }
+        };
+        auto pv_all = [&](uint32_t w) {
+          const uint32_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4), p0 = tmem + w * 128u, o0 = tmem + C::kOCol + w * D;
+#pragma unroll
+          for (int i = 0; i < BN / 16 + C::kPLoSteps; ++i)
+            mma_ts_lo(o0, p0 + i * 8, b0 + (i < BN / 16 ? i : i - 4) * 128, C::kIdescPV, 1u);
+        };
+        // A turn inside a pair piece (see below); more: another one follows.
+        auto turn = [&](bool more) -> bool {
+          if (!wait_p(0)) return false;
+          tc_fence_after();
+          pv_all(0);
+          qk_hi_all(0);
+          qk_lo_all(0);
+          mma_commit(&bars->s_full[0]);
+          if (!wait_p(1)) return false;
+          tc_fence_after();
+          pv_all(1);
+          v_done();
+          qk_hi_all(1);
+          Ring kn = kr;
+          kn.next(C::kKStages);
+          if (more && !(wait_v(false) && lane_wait(&bars->k_full[kn.st], kn.ph, wc))) return false;
+          qk_lo_all(1);
+          mma_commit(&bars->s_full[1]);
+          mma_commit(&bars->k_empty[kr.st]);
+          kr = kn;
+          return true;
         };
         for (uint32_t n = 0;; ++n) {
           if (!lane_wait(&bars->piece_full[n % kQueue], (n / kQueue) & 1u, wc)) break;
@@ -773,24 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the waits for the next turn's tiles stand before this turn's last MMAs, so that the tensor pipe
                 // does not run dry.
                 if (!(ok = wait_v(false) && wait_k())) break;
-                for (; v < ve; ++v) {
-                  if (!(ok = wait_p(0))) break;
-                  tc_fence_after();
-                  issue_pv(0, false);
-                  issue_qk(0);
-                  if (!(ok = wait_p(1))) break;
-                  tc_fence_after();
-                  issue_pv(1, false);
-                  v_done();
-                  qk_hi(1);
-                  Ring kn = kr;
-                  kn.next(C::kKStages);
-                  if (v + 1 < ve && !(ok = wait_v(false) && lane_wait(&bars->k_full[kn.st], kn.ph, wc))) break;
-                  qk_lo(1);
-                  mma_commit(&bars->s_full[1]);
-                  mma_commit(&bars->k_empty[kr.st]);
-                  kr = kn;
-                }
+                for (; ok && v < ve; ++v) ok = turn(v + 1 < ve);
                 if (!ok) break;
               }
               const bool next = v + 1 < nv;
@@ -968,51 +1049,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + lane_off + (w ? 128u : 0u);
     const uint32_t o_addr = tmem + lane_off + C::kOCol + (w ? D : 0);
     const int my_tok = r / G;  // token of this row in its tile
-    uint32_t s_ph = 0, q_ph = 0, o_ph = 0, x_ph = 0;
+    uint32_t s_ph = 0, o_ph = 0, x_ph = 0;
     bool ok = true;
-    const float2* const angles = reinterpret_cast<const float2*>(static_cast<const float*>(a.workspace) + pl.angles);
-    // Query tile of piece e of the queue, if this worker has one: rotate this thread's row and hand it over.
-    auto prepare = [&](const Piece* u) -> bool {
-      if constexpr (LO) {
-        if (u->kind == kNone || Share(*u, w).n == 0) return true;
-        if (!row_wait(&bars->q_full[w], q_ph, wc)) return false;
-        q_ph ^= 1u;
-        const int tok = (u->kind == kPair && w ? pl.tile_toks : 0) + my_tok;
-        if (my_tok < pl.tile_toks && tok < u->ntok) {
-          rotate_row<2 * C::kLoSteps>(smem + C::kQOff + w * C::kTileBytes, smem + C::kLoOff + w * C::kLoBytes, r,
-                                      angles + static_cast<long long>(u->row0 + tok) * pl.n_pairs, a.rope_offset, pl.n_pairs,
-                                      pl.half != 0, 2 * pl.lo_first);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&bars->q_ready[w]);
-      }
-      return true;
-    };
-    if constexpr (LO) asm volatile("griddepcontrol.wait;" ::: "memory");  // the angles are there
-    ok = row_wait(&bars->piece_full[0], 0, wc) && prepare(&bars->piece[0]);
     for (uint32_t n = 0; ok; ++n) {
+      if (!row_wait(&bars->piece_full[n % kQueue], (n / kQueue) & 1u, wc)) break;
       const Piece* const u = &bars->piece[n % kQueue];
       const int kind = u->kind;
       if (kind == kNone) break;
       const Share sh(*u, w);
-      const int tok = (kind == kPair && w ? pl.tile_toks : 0) + my_tok;
-      const bool real = my_tok < pl.tile_toks && tok < u->ntok;  // this row is a query
-      const int place = u->place0 + tok;
-      bool dead = !real || place < 0;
-      uint32_t bits[4] = {0u, 0u, 0u, 0u};
-      if (real) {
-        const long long row = u->row0 + tok;
-        if (a.positions != nullptr && a.positions[row] < 0) dead = true;
-        if (a.visible != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < a.words) bits[i] = static_cast<uint32_t>(a.visible[row * a.words + i]);
-        }
-      }
-      const int lim = dead ? 0 : place + 1;
+      // (what a row sees is looked up again for each care tile, and a row's place in the output for the epilogue: kept in
+      // registers beside the scores, it is spilled)
       float m_run = -INFINITY, l_run = 0.f;
       {
-        const int care = u->care_t, base = u->base, klim = u->klim;
+        const int care = u->care_t;
         int t = sh.first;
         for (int i = 0; i < sh.n; ++i, t += sh.step) {
           if (!row_wait(&bars->s_full[w], s_ph, wc)) { ok = false; break; }
@@ -1020,20 +1069,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           uint32_t mask[4];
           const bool masked = t >= care;
-          if (masked) {
-            if (a.visible != nullptr) seen_tree(bits, base, klim, t * BN, mask);
-            else seen_below(lim, t * BN, mask);
-          }
-          softmax_row<D, 16 * C::kPLoSteps>(s_addr, o_addr, masked, mask, i > 0, a.scale_log2, m_run, l_run);
+          if (masked) row_mask(a, pl, *u, w, my_tok, t * BN, mask);
+          softmax_row<D, (C::kPLoSteps > 0)>(s_addr, o_addr, masked, mask, i > 0, a.scale_log2, m_run, l_run);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars->p_full[w]);
         }
       }
       if (!__all_sync(0xffffffffu, ok)) break;
-      if (!row_wait(&bars->piece_full[(n + 1) % kQueue], ((n + 1) / kQueue) & 1u, wc)) break;
-      if (!prepare(&bars->piece[(n + 1) % kQueue])) break;
-
       // epilogue: the rows of the output, or the piece's normalised partial and its log-sum-exp
       if (sh.n > 0) {
         if (!row_wait(&bars->o_done[w], o_ph, wc)) break;
@@ -1067,76 +1110,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kind == kPair || w == 0) {
         if (!row_wait(&bars->care_done[n % kQueue], (n / kQueue) & 1u, wc)) break;
         const bool whole = u->slot < 0;
+        const int tok = (kind == kPair && w ? pl.tile_toks : 0) + my_tok;
+        const bool real = my_tok < pl.tile_toks && tok < u->ntok;  // this row is a query
+        const bool dead = !real || u->place0 + tok < 0 || (a.positions != nullptr && a.positions[u->row0 + tok] < 0);
         const bool none = dead || l_run == 0.f;  // no key with a weight; NaN is one
         const bool bad = u->bad_any != 0;
-        const int lj = lane & 3, r4 = r - lj;  // rows r4 .. r4 + 3 are stored by four lanes together, 64 bytes of each
         float* const ws = static_cast<float*>(a.workspace);
-        const long long slot_row = (2 * static_cast<long long>(blockIdx.x) + (whole ? 0 : u->slot)) * pl.slot_rows + w * BM;
-        int at[4];  // their rows of the output, -1: not a query
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int tk = (r4 + k) / G, i = (r4 + k) - tk * G, tok_k = (kind == kPair && w ? pl.tile_toks : 0) + tk;
-          at[k] = tk < pl.tile_toks && tok_k < u->ntok ? (u->row0 + tok_k) * a.n_h + u->g * G + i : -1;
-        }
+        const long long slot_row = (2 * static_cast<long long>(blockIdx.x) + (whole ? 0 : u->slot)) * pl.slot_rows + w * BM + r;
+        const long long out_row = static_cast<long long>(u->row0 + tok) * a.n_h + u->g * G + (r - my_tok * G);
         const float lse2 = none ? -INFINITY : m_run + log2f(l_run);
         if (real) {
-          if (!whole) ws[pl.l + slot_row + r] = lse2;
-          else if (a.lse != nullptr)
-            a.lse[static_cast<long long>(u->row0 + tok) * a.n_h + u->g * G + (r - my_tok * G)] = lse2 * 0.69314718055994530942f;
+          if (!whole) ws[pl.l + slot_row] = lse2;
+          else if (a.lse != nullptr) a.lse[out_row] = lse2 * 0.69314718055994530942f;
         }
         if (sh.n > 0) {
           tc_fence_after();
+          // (16 columns at a time and no exchange of pieces between lanes: short code, see rotate_row)
+          uint4* to = whole ? reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D)
+                            : reinterpret_cast<uint4*>(ws + slot_row * D);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            {
-              uint32_t x[32];
-              tmem_ld32(o_addr + c, x);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(o_addr + c, x);
+            tmem_wait_ld();
+            alignas(16) float o[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(x[e]) * f0;
+            if (both) {
+              tmem_ld16(o_addr + D + c, x);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * f0;
-              if (both) {
-                tmem_ld32(o_addr + D + c, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), f1, o[e]);
-              }
+              for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), f1, o[e]);
             }
-            if (bad && real) {
-              float y[32];
+            if (bad && !none) {
+              float y[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = o[e];
-              add_bad(a, *u, lim, bits, c, y);
+              for (int e = 0; e < 16; ++e) y[e] = o[e];
+              add_bad(a, pl, *u, w, my_tok, c, y);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = y[e];
+              for (int e = 0; e < 16; ++e) o[e] = y[e];
             }
             if (none) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+              for (int e = 0; e < 16; ++e) o[e] = 0.f;
             }
-            uint4 pc[4];
-            if (whole) {
+            if (real && whole) {
+              store32(to, f32_to_bf16x8(o), f32_to_bf16x8(o + 8), pl.wide);
+            } else if (real) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) pc[e] = f32_to_bf16x8(o + 8 * e);
-              transpose_pieces(pc, lj);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (at[k] >= 0)
-                  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(at[k]) * D + c + lj * 8) = pc[k];
-            } else {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  pc[e] = make_uint4(__float_as_uint(o[16 * h + 4 * e]), __float_as_uint(o[16 * h + 4 * e + 1]),
-                                     __float_as_uint(o[16 * h + 4 * e + 2]), __float_as_uint(o[16 * h + 4 * e + 3]));
-                transpose_pieces(pc, lj);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (at[k] >= 0)
-                    *reinterpret_cast<uint4*>(ws + (slot_row + r4 + k) * D + c + 16 * h + lj * 4) = pc[k];
+              for (int e = 0; e < 2; ++e) {
+                const uint4* const v = reinterpret_cast<const uint4*>(o + 8 * e);
+                store32(to + 2 * e, v[0], v[1], pl.wide);
               }
             }
+            to += whole ? 2 : 4;
           }
           tc_fence_before();
           mbar_arrive(&bars->o_empty[w]);
@@ -1158,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Blocks (CTA c of the kernel before, rows): if c's last piece is the head of a segment that goes on in the next
 // CTAs' first pieces, its rows are joined, a warp per row: the weights of the pieces by lanes, then D dims.
-constexpr int kJoinWarps = 8, kJoinRows = 16;
+constexpr int kJoinWarps = 8, kJoinPer = 4, kJoinRows = kJoinWarps * kJoinPer;
 constexpr int kMaxCtas = 160;  // the workspace is sized for this many (a GB300 has 152 SMs)
 
 template <int D>
@@ -1166,7 +1193,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     packed_tc_join_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ PackedTcPlan pl) {
   constexpr int kPer = D / 32;  // dims per lane
   __shared__ int slots[kMaxCtas];
-  __shared__ float weights[kJoinWarps][kMaxCtas];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* const ws = static_cast<const float*>(a.workspace);
@@ -1174,14 +1200,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int parts = (pl.slot_rows + kJoinRows - 1) / kJoinRows;
   const int c = blockIdx.x / parts, part = blockIdx.x - c * parts;
   const Record head = rec[2 * c + 1];
+  // the pieces: this one, then first pieces up to the one that ends the segment (a CTA may hold none)
+  int kt = 0, t_end = 0;
+  if (c + 1 + lane < pl.ctas) {
+    kt = rec[2 * (c + 1 + lane)].kt;
+    t_end = rec[2 * (c + 1 + lane)].t_end;
+  }
   const int G = a.n_h / a.n_kv;
   if (head.kt == 0 || part * kJoinRows >= (head.kind == kPair ? 2 * BM : min(BM, head.ntok * G))) return;
-  // the pieces: this one, then first pieces up to the one that ends the segment (a CTA may hold none)
   if (threadIdx.x == 0) slots[0] = 2 * c + 1;
   int n = 1;
   for (int c0 = c + 1; c0 < pl.ctas; c0 += 32) {
     const int cc = c0 + lane;
-    const int kt = cc < pl.ctas ? rec[2 * cc].kt : 0, t_end = kt ? rec[2 * cc].t_end : 0;
+    if (c0 > c + 1) {
+      kt = cc < pl.ctas ? rec[2 * cc].kt : 0;
+      t_end = cc < pl.ctas ? rec[2 * cc].t_end : 0;
+    }
     const uint32_t end = __ballot_sync(0xffffffffu, kt > 0 && t_end == kt);
     const uint32_t upto = end ? (end & (0u - end)) * 2u - 1u : 0xffffffffu;  // lanes up to the first that ends it
     const uint32_t some = __ballot_sync(0xffffffffu, kt > 0) & upto;
@@ -1190,72 +1224,90 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (end) break;
   }
   __syncthreads();
-  float* const wt = weights[warp];
-  for (int k = warp; k < kJoinRows; k += kJoinWarps) {
-    const int rr = part * kJoinRows + k, r = rr & (BM - 1), w = rr / BM;
-    const int tk = r / G, tok = (w ? pl.tile_toks : 0) + tk;
-    if (tk >= pl.tile_toks || tok >= head.ntok || (w && head.kind != kPair)) continue;
-    float m = -INFINITY;
-    for (int j = lane; j < n; j += 32) {
-      const float x = ws[pl.l + static_cast<long long>(slots[j]) * pl.slot_rows + rr];
-      wt[j] = x;
-      m = fmaxf(m, x);
-    }
+  // kJoinPer rows per warp, all loads of two pieces in flight, with a running maximum of their log-sum-exps
+  int rr[kJoinPer], at[kJoinPer];
+  float M[kJoinPer], den[kJoinPer], acc[kJoinPer][kPer];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float m_ref = m == -INFINITY ? 0.f : m;
-    float den = 0.f;
-    for (int j = lane; j < n; j += 32) {
-      const float x = exp2f(wt[j] - m_ref);
-      wt[j] = wt[j] == -INFINITY ? -1.f : x;  // nothing there
-      den += x;
-    }
+  for (int k = 0; k < kJoinPer; ++k) {
+    rr[k] = part * kJoinRows + warp * kJoinPer + k;
+    const int r = rr[k] & (BM - 1), w = rr[k] / BM, tk = r / G, tok = (w ? pl.tile_toks : 0) + tk;
+    at[k] = tk < pl.tile_toks && tok < head.ntok && (!w || head.kind == kPair)
+                ? (head.row0 + tok) * a.n_h + head.g * G + (r - tk * G) : -1;
+    M[k] = -INFINITY;
+    den[k] = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    __syncwarp();
-    float acc[kPer];
+    for (int e = 0; e < kPer; ++e) acc[k][e] = 0.f;
+  }
+#pragma unroll 1
+  for (int j = 0; j < n; j += 2) {
+    float l[2][kJoinPer], v[2][kJoinPer][kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const float x = wt[j];
-      if (x == -1.f) continue;
-      const float* const p = ws + (static_cast<long long>(slots[j]) * pl.slot_rows + rr) * D + lane * kPer;
-      float v[kPer];
-      if constexpr (kPer == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(p);
-        v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(p);
-        v[0] = y.x; v[1] = y.y;
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int k = 0; k < kJoinPer; ++k) {
+        l[q][k] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[q][k][e] = 0.f;
+        if (j + q < n && at[k] >= 0) {
+          const long long row = static_cast<long long>(slots[j + q]) * pl.slot_rows + rr[k];
+          l[q][k] = ws[pl.l + row];
+          const float* const p = ws + row * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            v[q][k][0] = y.x; v[q][k][1] = y.y; v[q][k][2] = y.z; v[q][k][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            v[q][k][0] = y.x; v[q][k][1] = y.y;
+          }
+        }
       }
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(x, v[e], acc[e]);
+    for (int k = 0; k < kJoinPer; ++k) {
+      const float m = fmax3(M[k], l[0][k], l[1][k]), m_ref = m == -INFINITY ? 0.f : m;
+      const float x = exp2f(M[k] - m_ref);
+      M[k] = m;
+      den[k] *= x;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[k][e] *= x;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (l[q][k] == -INFINITY) continue;  // a part without a weight holds nothing
+        const float y = exp2f(l[q][k] - m_ref);
+        den[k] += y;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[k][e] = fmaf(y, v[q][k][e], acc[k][e]);
+      }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    const long long at = (static_cast<long long>(head.row0) + tok) * a.n_h + head.g * G + (r - tk * G);
-    uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + at * D + lane * kPer);
-    out[0] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if constexpr (kPer == 4) out[1] = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-    if (lane == 0 && a.lse != nullptr) a.lse[at] = den == 0.f ? -INFINITY : (m + log2f(den)) * 0.69314718055994530942f;
-    __syncwarp();
+  }
+#pragma unroll
+  for (int k = 0; k < kJoinPer; ++k) {
+    if (at[k] < 0) continue;
+    const float inv = den[k] == 0.f ? 0.f : 1.f / den[k];
+    uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(at[k]) * D + lane * kPer);
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv), pack_bf16x2(acc[k][2] * inv, acc[k][3] * inv));
+    else
+      out[0] = pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv);
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[at[k]] = den[k] == 0.f ? -INFINITY : (M[k] + log2f(den[k])) * 0.69314718055994530942f;
   }
 }
 
-PackedTcPlan make_plan(const PackedArgs& a, int ctas, int max_ctas, int n_pairs, int half) {
+PackedTcPlan make_plan(const PackedArgs& a, int ctas, int max_ctas, bool rotate) {
   PackedTcPlan p{};
   const int G = a.n_h / a.n_kv;
   p.ctas = ctas;
   p.tile_toks = BM / G;
   p.slot_rows = a.T <= p.tile_toks ? a.T * G : 2 * BM;
-  const int steps = a.D_qk / 16, rest = steps - a.D_qk / 32;
-  p.lo_first = n_pairs ? (a.rope_offset / 16 < rest ? a.rope_offset / 16 : rest) : 0;
-  p.n_pairs = n_pairs;
-  p.half = half;
+  const int rest = (a.D_qk - kLoDims) / 16;
+  p.lo_first = a.rope_offset / 16 < rest ? a.rope_offset / 16 : rest;
+  p.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.workspace)) & 31u) == 0;
   p.l = 2LL * max_ctas * p.slot_rows * a.D_v;
   p.rec = (p.l + 2LL * max_ctas * p.slot_rows + 3) & ~3LL;
-  p.angles = p.rec + 2LL * max_ctas * static_cast<long long>(sizeof(Record) / 4);
-  p.end = p.angles + 2LL * a.T * n_pairs;
+  p.q = (p.rec + 2LL * max_ctas * static_cast<long long>(sizeof(Record) / 4) + 31) & ~31LL;
+  const long long rows = rotate ? static_cast<long long>(a.T) * a.n_h : 0;
+  p.lo = p.q + rows * a.D_qk / 2;
+  p.end = p.lo + rows * kLoDims / 2;
   return p;
 }
 
@@ -1284,14 +1336,19 @@ cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, const CUtensorMap*
   cudaError_t e = prepare<D, LO>();
   if (e != cudaSuccess) return e;
   if (LO) {
-    const long long items = static_cast<long long>(a.T) * rope.n_pairs;
-    packed_angles_kernel<<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(
-        a, rope, reinterpret_cast<float2*>(static_cast<float*>(a.workspace) + pl.angles));
+    // few tokens: fewer heads per thread, for some eight warps per SM
+    int heads = a.n_h;
+    while (heads % 2 == 0 && static_cast<long long>(a.T) * (a.n_h / heads) * (D / 8) < 152LL * 1024) heads /= 2;
+    const long long items = static_cast<long long>(a.T) * (a.n_h / heads) * (D / 8);
+    float* const ws = static_cast<float*>(a.workspace);
+    packed_rotate_kernel<D><<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(
+        a, rope, reinterpret_cast<__nv_bfloat16*>(ws + pl.q), reinterpret_cast<__nv_bfloat16*>(ws + pl.lo),
+        pl.lo_first * 16, heads);
     *launches += 1;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   e = launch_early(packed_tc_kernel<D, LO>, pl.ctas, kThreads, smem_bytes<Cfg<D, LO>>(), st, LO, a, pl, maps[0], maps[1],
-                   maps[2]);
+                   maps[2], maps[3]);
   *launches += 1;
   if (e != cudaSuccess) return e;
   const unsigned parts = (pl.slot_rows + kJoinRows - 1) / kJoinRows;
@@ -1308,7 +1365,7 @@ bool packed_tc_supported(const PackedArgs& a, bool bf16, int rope_offset, int ro
 }
 
 size_t packed_tc_workspace(const PackedArgs& a) {
-  return static_cast<size_t>(make_plan(a, kMaxCtas, kMaxCtas, a.D_qk / 2, 0).end) * sizeof(float);
+  return static_cast<size_t>(make_plan(a, kMaxCtas, kMaxCtas, true).end) * sizeof(float);
 }
 
 cudaError_t launch_packed_tc(const PackedArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st, int* launches) {
@@ -1318,17 +1375,23 @@ cudaError_t launch_packed_tc(const PackedArgs& a, const RopeFreq& rope, int num_
   const long long segments = static_cast<long long>(a.T) * (a.n_h / a.n_kv) / (2 * BM - 2 * (a.n_h / a.n_kv) + 2) + a.B;
   const long long most = segments * a.n_kv * (((static_cast<long long>(a.max_blocks) << a.page_shift) + BN - 1) / BN);
   if (most < ctas) ctas = most > 0 ? static_cast<int>(most) : 1;
-  const PackedTcPlan pl = make_plan(a, ctas, kMaxCtas, rope.n_pairs, rope.half);
+  const PackedTcPlan pl = make_plan(a, ctas, kMaxCtas, rotate);
   // query rows by (dim, head of the group, KV head, row), a row tile per box; K and V by (dim, KV head, row in
   // page, page), a page or a part of it per box
   const unsigned long long hs = static_cast<unsigned long long>(a.D_qk) * 2, page = 1ull << a.page_shift;
   const unsigned long long ks = hs * a.n_kv, vs = static_cast<unsigned long long>(a.v_token_stride) * 2;
   const int G = a.n_h / a.n_kv, rows = static_cast<int>(page);
-  CUtensorMap maps[3];
+  CUtensorMap maps[4];
+  float* const ws = static_cast<float*>(a.workspace);
+  const void* q = rotate ? ws + pl.q : a.q;
   const bool wide = a.D_qk == 128;
-  if (!make_map_box(&maps[0], a.q, a.D_qk, G, a.n_kv, a.T, hs, hs * G, hs * a.n_h, G, 1, pl.tile_toks, wide) ||
-      !make_map_box(&maps[1], a.k_pages, a.D_qk, a.n_kv, rows, a.n_pages, hs, ks, ks * page, 1, rows < 128 ? rows : 128, 1, wide) ||
-      !make_map_box(&maps[2], a.v_pages, a.D_v, a.n_kv, rows, a.n_pages, hs, vs, vs * page, 1, rows < 128 ? rows : 128, 1, wide))
+  if (!make_map_box(&maps[0], q, a.D_qk, G, a.n_kv, a.T, hs, hs * G, hs * a.n_h, G, 1, pl.tile_toks, wide) ||
+      !make_map_box(&maps[2], a.k_pages, a.D_qk, a.n_kv, rows, a.n_pages, hs, ks, ks * page, 1, rows < 128 ? rows : 128, 1, wide) ||
+      !make_map_box(&maps[3], a.v_pages, a.D_v, a.n_kv, rows, a.n_pages, hs, vs, vs * page, 1, rows < 128 ? rows : 128, 1, wide))
+    return cudaErrorInvalidValue;
+  maps[1] = maps[0];
+  const unsigned long long ls = kLoDims * 2;
+  if (rotate && !make_map_box(&maps[1], ws + pl.lo, kLoDims, G, a.n_kv, a.T, ls, ls * G, ls * a.n_h, G, 1, pl.tile_toks, false))
     return cudaErrorInvalidValue;
   if (a.D_qk == 64)
     return rotate ? launch<64, true>(a, rope, maps, pl, st, launches) : launch<64, false>(a, rope, maps, pl, st, launches);
