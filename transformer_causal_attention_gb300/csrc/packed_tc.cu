@@ -47,6 +47,7 @@ struct PackedTcPlan {
   int tile_toks;  // tokens per row tile: 128 / G
   int slot_rows;  // rows of a partial
   int lo_first;   // first MMA step with a second part of Q
+  unsigned long long nth;  // 2^64 / ctas
   int wide;       // 1: out and workspace start on 32 bytes
   // float offsets into the workspace: partials [2 * ctas, slot_rows, D], their log-sum-exps, records, the rotated
   // queries (bf16 [T, n_h, D]) and what that rounding left (bf16 [T, n_h, 64])
@@ -64,9 +65,9 @@ constexpr int kCare = 3;   // care tiles of a piece, at most: 256 tokens of a pa
 constexpr int kQueue = 6;  // pieces in the queue; kAhead are handed out before warp 3 treats the first of them
 constexpr int kAhead = 3;
 
-// Points on the line per key of a segment, and the leads, in keys of the same weight.
-constexpr int kPairWeight = 8, kSingleWeight = 6;
-constexpr int kPairLead = 256, kSingleLead = 256;
+// Points on the line: 2^shift per key of a segment, and a lead in front of its first tile.
+constexpr int kPairShift = 3, kSingleShift = 2;
+constexpr int kPairLead = 2048, kSingleLead = 1024;
 
 // Register split as in prefill_tc.cu: a softmax thread holds a row of 128 scores.
 constexpr int kLaunchRegs = 168;
@@ -112,7 +113,7 @@ struct Cfg {
   static constexpr int kBlockBytes = BM * 128;                // one column block (128 rows x 128 bytes, swizzled)
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
   static constexpr int kSteps = D / 16;
-  static constexpr int kLoSteps = LO ? kLoDims / 16 : 0;       // MMA steps with a second part of Q
+  [[maybe_unused]] static constexpr int kLoSteps = LO ? kLoDims / 16 : 0;       // MMA steps with a second part of Q
   static constexpr int kLoBytes = LO ? kBlockBytes : 0;        // of a row tile
   static constexpr int kPLoSteps = LO && D == 128 ? 4 : 0;    // steps of 16 keys with a second part of P
   static constexpr int kKStages = 2;
@@ -175,19 +176,17 @@ struct Seg {
   }
   __device__ __forceinline__ bool last_is_pair() const { return rem > tt; }
   __device__ __forceinline__ bool is_pair(int p) const { return p < np || last_is_pair(); }
-  __device__ __forceinline__ int weight(int p) const { return is_pair(p) ? kPairWeight : kSingleWeight; }
-  __device__ __forceinline__ long long lead(int p) const {
-    return is_pair(p) ? kPairLead * kPairWeight : kSingleLead * kSingleWeight;
-  }
+  __device__ __forceinline__ int shift(int p) const { return is_pair(p) ? kPairShift : kSingleShift; }
+  __device__ __forceinline__ int lead(int p) const { return is_pair(p) ? kPairLead : kSingleLead; }
   __device__ __forceinline__ int count() const { return np + (rem > 0); }
   __device__ __forceinline__ long long keys_of(int p) const {  // for the length
     return tree ? keys : static_cast<long long>(keys) + min((p + 1) * 2 * tt, r.rows);
   }
-  __device__ __forceinline__ long long length(int p) const { return lead(p) + keys_of(p) * weight(p); }
+  __device__ __forceinline__ long long length(int p) const { return lead(p) + (keys_of(p) << shift(p)); }
   // points in front of pair p <= np
   __device__ __forceinline__ long long before(int p) const {
     const long long q = p;
-    return q * (kPairLead * kPairWeight) + kPairWeight * (q * keys + (tree ? 0 : tt * q * (q + 1)));
+    return q * kPairLead + ((q * keys + (tree ? 0 : tt * q * (q + 1))) << kPairShift);
   }
   __device__ __forceinline__ long long own() const { return before(np) + (rem > 0 ? length(np) : 0); }
   // real keys of the segment's first n tokens, at least 1
@@ -197,18 +196,13 @@ struct Seg {
 };
 __device__ __forceinline__ int tiles_of(int keys) { return static_cast<int>((static_cast<unsigned>(keys) + BN - 1) / BN); }
 // The first tile that starts at or behind point x of a segment of kt tiles.
-__device__ __forceinline__ int tile_at(long long x, long long lead, int weight, int kt) {
+__device__ __forceinline__ int tile_at(long long x, int lead, int shift, int kt) {
   const long long d = x - lead;
   if (d <= 0) return 0;
-  const long long t = (d + BN * weight - 1) / (BN * weight);
+  const long long t = (d + (BN << shift) - 1) >> (shift + 7);
   return t < kt ? static_cast<int>(t) : kt;
 }
-struct Cut {
-  long long part;
-  int extra;
-  __device__ __forceinline__ Cut(long long total, int n) : part(total / n), extra(static_cast<int>(total % n)) {}
-  __device__ __forceinline__ long long at(int k) const { return part * k + min(k, extra); }
-};
+static_assert(BN == 1 << 7, "tile_at");
 
 // A walk along one CTA's part: the segment (b, g, p), its next tile, and the part's end from its first point.
 struct Walk {
@@ -233,7 +227,7 @@ __device__ __noinline__ void next_piece(const PackedArgs& a, const PackedTcPlan&
     const bool pair = s.is_pair(p);
     const int tok0 = p * 2 * s.tt, ntok = min(2 * s.tt, s.r.rows - tok0);
     const int klim = s.seen(p, ntok), kt = tiles_of(klim);
-    const int t = w.t, t_end = tile_at(w.end, s.lead(p), s.weight(p), kt);
+    const int t = w.t, t_end = tile_at(w.end, s.lead(p), s.shift(p), kt);
     if (t < t_end) {
       out->kind = pair ? kPair : kSingle;
       out->g = w.g;
@@ -615,8 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w < warp) before += bars->warp_sum[w];
     total += bars->warp_sum[w];
   }
-  const Cut cut(total, gridDim.x);
-  const long long part_lo = cut.at(blockIdx.x), part_hi = cut.at(blockIdx.x + 1);
+  // part k of n starts at the k / n-th of the line (n parts of equal length up to rounding; no divisions here)
+  const auto cut = [&](uint32_t k) {
+    return k == gridDim.x ? total : static_cast<long long>(__umul64hi(static_cast<unsigned long long>(total), k * pl.nth));
+  };
+  const long long part_lo = cut(blockIdx.x), part_hi = cut(blockIdx.x + 1);
   if (part_lo < part_hi && part_lo >= before && part_lo < before + mine) {
     long long at = before;
     int b = b_lo;
@@ -942,8 +939,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long own = s.own();
         long long off = bars->start_off;
         walk.b = bars->start_b;
-        walk.g = static_cast<int>(off / own);
-        off -= walk.g * own;
+        // KV head off / own: the quotient of floats is off by one at most
+        int g = min(static_cast<int>(static_cast<float>(off) / static_cast<float>(own)), a.n_kv - 1);
+        while (g > 0 && g * own > off) --g;
+        while (g + 1 < a.n_kv && (g + 1) * own <= off) ++g;
+        walk.g = g;
+        off -= g * own;
         int lo = 0, hi = s.np;  // the last segment that starts at or before off
         if (s.rem == 0) --hi;
         while (lo < hi) {
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         off -= s.before(lo);
         walk.p = lo;
         walk.end += off;
-        walk.t = tile_at(off, s.lead(lo), s.weight(lo), tiles_of(s.seen(lo, min(2 * s.tt, s.r.rows - lo * 2 * s.tt))));
+        walk.t = tile_at(off, s.lead(lo), s.shift(lo), tiles_of(s.seen(lo, min(2 * s.tt, s.r.rows - lo * 2 * s.tt))));
       }
       Record* const rec = reinterpret_cast<Record*>(static_cast<float*>(a.workspace) + pl.rec) + 2 * blockIdx.x;
       uint32_t recs = 0;  // bits: slots with a record
@@ -1125,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (sh.n > 0) {
           tc_fence_after();
-          // (16 columns at a time and no exchange of pieces between lanes: short code, see rotate_row)
+          // (16 columns at a time and no exchange of pieces between lanes: short code)
           uint4* to = whole ? reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D)
                             : reinterpret_cast<uint4*>(ws + slot_row * D);
 #pragma unroll 1
@@ -1185,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Blocks (CTA c of the kernel before, rows): if c's last piece is the head of a segment that goes on in the next
 // CTAs' first pieces, its rows are joined, a warp per row: the weights of the pieces by lanes, then D dims.
-constexpr int kJoinWarps = 8, kJoinPer = 4, kJoinRows = kJoinWarps * kJoinPer;
+constexpr int kJoinWarps = 8, kJoinPer = 2, kJoinFlight = 4, kJoinRows = 2 * kJoinWarps * kJoinPer;
 constexpr int kMaxCtas = 160;  // the workspace is sized for this many (a GB300 has 152 SMs)
 
 template <int D>
@@ -1224,72 +1225,78 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (end) break;
   }
   __syncthreads();
-  // kJoinPer rows per warp, all loads of two pieces in flight, with a running maximum of their log-sum-exps
-  int rr[kJoinPer], at[kJoinPer];
-  float M[kJoinPer], den[kJoinPer], acc[kJoinPer][kPer];
-#pragma unroll
-  for (int k = 0; k < kJoinPer; ++k) {
-    rr[k] = part * kJoinRows + warp * kJoinPer + k;
-    const int r = rr[k] & (BM - 1), w = rr[k] / BM, tk = r / G, tok = (w ? pl.tile_toks : 0) + tk;
-    at[k] = tk < pl.tile_toks && tok < head.ntok && (!w || head.kind == kPair)
-                ? (head.row0 + tok) * a.n_h + head.g * G + (r - tk * G) : -1;
-    M[k] = -INFINITY;
-    den[k] = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[k][e] = 0.f;
-  }
+  // kJoinPer rows per warp, all loads of kJoinFlight pieces in flight, with a running maximum of their log-sum-exps
 #pragma unroll 1
-  for (int j = 0; j < n; j += 2) {
-    float l[2][kJoinPer], v[2][kJoinPer][kPer];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int k = 0; k < kJoinPer; ++k) {
-        l[q][k] = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) v[q][k][e] = 0.f;
-        if (j + q < n && at[k] >= 0) {
-          const long long row = static_cast<long long>(slots[j + q]) * pl.slot_rows + rr[k];
-          l[q][k] = ws[pl.l + row];
-          const float* const p = ws + row * D + lane * kPer;
-          if constexpr (kPer == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(p);
-            v[q][k][0] = y.x; v[q][k][1] = y.y; v[q][k][2] = y.z; v[q][k][3] = y.w;
-          } else {
-            const float2 y = *reinterpret_cast<const float2*>(p);
-            v[q][k][0] = y.x; v[q][k][1] = y.y;
-          }
-        }
-      }
+  for (int pass = 0; pass < kJoinRows; pass += kJoinWarps * kJoinPer) {
+    int rr[kJoinPer], at[kJoinPer];
+    float M[kJoinPer], den[kJoinPer], acc[kJoinPer][kPer];
 #pragma unroll
     for (int k = 0; k < kJoinPer; ++k) {
-      const float m = fmax3(M[k], l[0][k], l[1][k]), m_ref = m == -INFINITY ? 0.f : m;
-      const float x = exp2f(M[k] - m_ref);
-      M[k] = m;
-      den[k] *= x;
+      rr[k] = part * kJoinRows + pass + warp * kJoinPer + k;
+      const int r = rr[k] & (BM - 1), w = rr[k] / BM, tk = r / G, tok = (w ? pl.tile_toks : 0) + tk;
+      at[k] = tk < pl.tile_toks && tok < head.ntok && (!w || head.kind == kPair)
+                  ? (head.row0 + tok) * a.n_h + head.g * G + (r - tk * G) : -1;
+      M[k] = -INFINITY;
+      den[k] = 0.f;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[k][e] *= x;
+      for (int e = 0; e < kPer; ++e) acc[k][e] = 0.f;
+    }
+#pragma unroll 1
+    for (int j = 0; j < n; j += kJoinFlight) {
+      float l[kJoinFlight][kJoinPer], v[kJoinFlight][kJoinPer][kPer];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (l[q][k] == -INFINITY) continue;  // a part without a weight holds nothing
-        const float y = exp2f(l[q][k] - m_ref);
-        den[k] += y;
+      for (int q = 0; q < kJoinFlight; ++q)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[k][e] = fmaf(y, v[q][k][e], acc[k][e]);
+        for (int k = 0; k < kJoinPer; ++k) {
+          l[q][k] = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) v[q][k][e] = 0.f;
+          if (j + q < n && at[k] >= 0) {
+            const long long row = static_cast<long long>(slots[j + q]) * pl.slot_rows + rr[k];
+            l[q][k] = ws[pl.l + row];
+            const float* const p = ws + row * D + lane * kPer;
+            if constexpr (kPer == 4) {
+              const float4 y = *reinterpret_cast<const float4*>(p);
+              v[q][k][0] = y.x; v[q][k][1] = y.y; v[q][k][2] = y.z; v[q][k][3] = y.w;
+            } else {
+              const float2 y = *reinterpret_cast<const float2*>(p);
+              v[q][k][0] = y.x; v[q][k][1] = y.y;
+            }
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < kJoinPer; ++k) {
+        float m = M[k];
+#pragma unroll
+        for (int q = 0; q < kJoinFlight; ++q) m = fmaxf(m, l[q][k]);
+        const float m_ref = m == -INFINITY ? 0.f : m;
+        const float x = exp2f(M[k] - m_ref);
+        M[k] = m;
+        den[k] *= x;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[k][e] *= x;
+#pragma unroll
+        for (int q = 0; q < kJoinFlight; ++q) {
+          if (l[q][k] == -INFINITY) continue;  // a part without a weight holds nothing
+          const float y = exp2f(l[q][k] - m_ref);
+          den[k] += y;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[k][e] = fmaf(y, v[q][k][e], acc[k][e]);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int k = 0; k < kJoinPer; ++k) {
-    if (at[k] < 0) continue;
-    const float inv = den[k] == 0.f ? 0.f : 1.f / den[k];
-    uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(at[k]) * D + lane * kPer);
-    if constexpr (kPer == 4)
-      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv), pack_bf16x2(acc[k][2] * inv, acc[k][3] * inv));
-    else
-      out[0] = pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv);
-    if (lane == 0 && a.lse != nullptr)
-      a.lse[at[k]] = den[k] == 0.f ? -INFINITY : (M[k] + log2f(den[k])) * 0.69314718055994530942f;
+    for (int k = 0; k < kJoinPer; ++k) {
+      if (at[k] < 0) continue;
+      const float inv = den[k] == 0.f ? 0.f : 1.f / den[k];
+      uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(at[k]) * D + lane * kPer);
+      if constexpr (kPer == 4)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv), pack_bf16x2(acc[k][2] * inv, acc[k][3] * inv));
+      else
+        out[0] = pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv);
+      if (lane == 0 && a.lse != nullptr)
+        a.lse[at[k]] = den[k] == 0.f ? -INFINITY : (M[k] + log2f(den[k])) * 0.69314718055994530942f;
+    }
   }
 }
 
@@ -1297,6 +1304,7 @@ PackedTcPlan make_plan(const PackedArgs& a, int ctas, int max_ctas, bool rotate)
   PackedTcPlan p{};
   const int G = a.n_h / a.n_kv;
   p.ctas = ctas;
+  p.nth = ctas > 1 ? ~0ull / ctas : 0;
   p.tile_toks = BM / G;
   p.slot_rows = a.T <= p.tile_toks ? a.T * G : 2 * BM;
   const int rest = (a.D_qk - kLoDims) / 16;
@@ -1371,10 +1379,10 @@ size_t packed_tc_workspace(const PackedArgs& a) {
 cudaError_t launch_packed_tc(const PackedArgs& a, const RopeFreq& rope, int num_sms, cudaStream_t st, int* launches) {
   const bool rotate = rope.n_pairs > 0;
   int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-  // no more CTAs than the call can have tiles
+  // no more CTAs than twice the tiles that the call can have (fewer would have to share)
   const long long segments = static_cast<long long>(a.T) * (a.n_h / a.n_kv) / (2 * BM - 2 * (a.n_h / a.n_kv) + 2) + a.B;
-  const long long most = segments * a.n_kv * (((static_cast<long long>(a.max_blocks) << a.page_shift) + BN - 1) / BN);
-  if (most < ctas) ctas = most > 0 ? static_cast<int>(most) : 1;
+  const long long most = 2 * segments * a.n_kv * (((static_cast<long long>(a.max_blocks) << a.page_shift) + BN - 1) / BN);
+  if (most < ctas) ctas = static_cast<int>(most);
   const PackedTcPlan pl = make_plan(a, ctas, kMaxCtas, rotate);
   // query rows by (dim, head of the group, KV head, row), a row tile per box; K and V by (dim, KV head, row in
   // page, page), a page or a part of it per box
