@@ -261,6 +261,15 @@ __device__ __noinline__ void next_piece(const PackedArgs& a, const PackedTcPlan&
   w.live = false;
 }
 
+// One lane of a converged warp, which the compiler knows to be one: the MMA issuer's descriptors then stay in uniform
+// registers (behind a test of the lane's number, each MMA took the issuer 70 to 90 cycles, more than the tensor pipe's 64,
+// and a turn inside a pair piece 4680 cycles; 4 prompts of 8192 tokens 2388 -> 2017 us).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 // ------------------------------------------------------------------------------------- rows
 // The new tokens' queries rotated at their positions, bf16 [T, n_h, D], and what that rounding left of dims
 // [lo_dim, lo_dim + 64), bf16 [T, n_h, 64].  A thread owns 8 dims (and with split halves their partners) of a token for
@@ -385,39 +394,70 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// This thread's row of a tile's scores become its weights P (see prefill_tc.cu): p = 2^(s * scale*log2e - m), m moves
-// when the row maximum grew by more than the threshold.  LO: the weights of the last 64 keys come as the sum of two bf16
-// values, the second ones in columns 64 on.
-// The scores are read twice, for the maximum and then 32 keys at a time for the weights: with the row kept in
-// registers in between, 148 bytes of it were spilled per thread, more than the L1 beside 226 KB of shared memory
-// holds, and a tile took 2350 cycles instead of 1600.
-template <int D, bool LO>
-__device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, const uint32_t* mask,
-                                            bool rescale, float scale_log2, float& m_run, float& l_run) {
-  float mx;
-  {
-    uint32_t x[BN];
-#pragma unroll
-    for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_addr + c * 32, x + c * 32);
-    tmem_wait_ld();
-    if (masked) {
-#pragma unroll
-      for (int c = 0; c < BN; ++c)
-        if (!((mask[c >> 5] >> (c & 31)) & 1u)) x[c] = 0xff800000u;
-    }
-    float m8[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m8[e] = __uint_as_float(x[e]);
-#pragma unroll
-    for (int c = 8; c + 16 <= BN; c += 16)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m8[e] = fmax3(m8[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 8 + e]));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], __uint_as_float(x[BN - 8 + e]));
-    mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7])) * scale_log2;
-  }
-  uint32_t sr[2][32];
+// This thread's row of a tile's scores become its weights P (see prefill_tc.cu): p = 2^(s * scale*log2e - m), and m
+// moves only when the row maximum grew by more than the threshold.  So a tile that every row sees whole is taken with
+// the m that is there, in one pass that finds the maximum beside the weights; P is stored behind the pass, where no row
+// asks for another m, else (false) nothing is and softmax_row does the tile.
+// LO: the weights of the last 64 keys come as the sum of two bf16 values, the second ones in columns 64 on.
+// (Short as it can be: all code that runs side by side in an SM has to fit its instruction cache, see the MMA issuer;
+// and no more registers than there are: spilled ones are more than the L1 beside 226 KB of shared memory holds.)
+template <bool LO>
+__device__ __forceinline__ bool softmax_fast(uint32_t s_addr, float scale_log2, float m_run, float& l_run) {
+  uint32_t sr[2][32], pr[64], rest[LO ? 32 : 1];
   tmem_ld32(s_addr, sr[0]);
+  const float2 sl2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m_run, -m_run);
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int q = 0; q < BN / 32; ++q) {
+    tmem_wait_ld();
+    if (q + 1 < BN / 32) tmem_ld32(s_addr + 32 * (q + 1), sr[(q + 1) & 1]);
+    const uint32_t* const s = sr[q & 1];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float2 y = make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+      mx[c & 3] = fmax3(mx[c & 3], y.x, y.y);
+      const float2 x = __ffma2_rn(y, sl2, nm2);
+      const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      acc[c & 1] = __fadd2_rn(acc[c & 1], pp);
+      pr[16 * q + c] = pack_bf16x2(pp.x, pp.y);
+      if (LO && q >= 2) {
+        const float2 z = __ffma2_rn(make_float2(__uint_as_float(pr[16 * q + c] << 16), __uint_as_float(pr[16 * q + c] & 0xffff0000u)),
+                                    make_float2(-1.f, -1.f), pp);
+        rest[16 * (q - 2) + c] = pack_bf16x2(z.x, z.y);
+      }
+    }
+  }
+  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+  if (__any_sync(0xffffffffu, top > m_run + kRescaleThreshold)) return false;
+  tmem_st32(s_addr, pr);
+  tmem_st32(s_addr + 32, pr + 32);
+  if constexpr (LO) tmem_st32(s_addr + 64, rest);
+  acc[0] = __fadd2_rn(acc[0], acc[1]);
+  l_run += acc[0].x + acc[0].y;
+  return true;
+}
+
+// The same for any tile, masked or with a new m: halves of the row in loops, the scores read twice.
+template <int D, bool LO>
+__device__ __noinline__ float2 softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, uint4 mask4, bool rescale,
+                                         float scale_log2, float m_run, float l_run) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    uint32_t x[32];
+    tmem_ld32(s_addr + 32 * h, x);
+    tmem_wait_ld();
+    const uint32_t m = !masked ? 0xffffffffu : h == 0 ? mask4.x : h == 1 ? mask4.y : h == 2 ? mask4.z : mask4.w;
+    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      const float y = (m >> c) & 1u ? __uint_as_float(x[c]) : -INFINITY, z = (m >> c) & 2u ? __uint_as_float(x[c + 1]) : -INFINITY;
+      m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], y, z);
+    }
+    mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+  }
+  mx *= scale_log2;
   const bool need = mx > m_run + kRescaleThreshold;
   float alpha = 1.f;
   if (need) {
@@ -428,50 +468,40 @@ __device__ __forceinline__ void softmax_row(uint32_t s_addr, uint32_t o_addr, bo
   const float2 sl2 = make_float2(scale_log2, scale_log2);
   const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
   const float2 nm2 = make_float2(-m_ref, -m_ref);
-  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 acc = make_float2(0.f, 0.f);
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 4; ++h) {
+    uint32_t x[32], pr[16];
+    tmem_ld32(s_addr + 32 * h, x);
+    tmem_wait_ld();
+    const uint32_t m = !masked ? 0xffffffffu : h == 0 ? mask4.x : h == 1 ? mask4.y : h == 2 ? mask4.z : mask4.w;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      tmem_wait_ld();
-      if (q == 0) tmem_ld32(s_addr + 64 * h + 32, sr[1]);
-      else if (h == 0) tmem_ld32(s_addr + 64, sr[0]);
-      uint32_t* const s = sr[q];
-      if (masked) {
-        const uint32_t m = h ? mask[2 + q] : mask[q];
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (!((m >> c) & 1u)) s[c] = 0xff800000u;
+    for (int c = 0; c < 16; ++c) {
+      float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sl2, nm2);
+      y.x = (m >> (2 * c)) & 1u ? fast_exp2(y.x) : 0.f;
+      y.y = (m >> (2 * c)) & 2u ? fast_exp2(y.y) : 0.f;
+      acc = __fadd2_rn(acc, y);
+      pr[c] = pack_bf16x2(y.x, y.y);
+      if (LO) {
+        x[2 * c] = __float_as_uint(y.x);
+        x[2 * c + 1] = __float_as_uint(y.y);
       }
-      uint32_t pr[16];
+    }
+    // over scores that have been read: P's columns are half as many, those of the second parts lie over tile columns 64 on
+    tmem_st16(s_addr + 16 * h, pr);
+    if (LO && h >= 2) {
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2, nm2);
-        const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-        acc[c & 3] = __fadd2_rn(acc[c & 3], pp);
-        pr[c] = pack_bf16x2(pp.x, pp.y);
-        if (LO) {
-          s[2 * c] = __float_as_uint(pp.x);
-          s[2 * c + 1] = __float_as_uint(pp.y);
-        }
+        const float2 z = __ffma2_rn(make_float2(__uint_as_float(pr[c] << 16), __uint_as_float(pr[c] & 0xffff0000u)),
+                                    make_float2(-1.f, -1.f),
+                                    make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])));
+        pr[c] = pack_bf16x2(z.x, z.y);
       }
-      // over scores that have been read: P's columns are half as many, those of the second parts lie over tile columns 64 on
-      tmem_st16(s_addr + 32 * h + 16 * q, pr);
-      if (LO && h == 1) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float2 y = __ffma2_rn(make_float2(__uint_as_float(pr[c] << 16), __uint_as_float(pr[c] & 0xffff0000u)),
-                                      make_float2(-1.f, -1.f),
-                                      make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])));
-          pr[c] = pack_bf16x2(y.x, y.y);
-        }
-        tmem_st16(s_addr + 64 + 16 * q, pr);
-      }
+      tmem_st16(s_addr + 64 + 16 * (h - 2), pr);
     }
   }
   if (__any_sync(0xffffffffu, need && rescale)) rescale_o<D>(o_addr, alpha);
-  acc[0] = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-  l_run += acc[0].x + acc[0].y;
+  return make_float2(m_run, l_run + acc.x + acc.y);
 }
 
 // 32 bytes of a row, whole sectors where the row starts on one (wide): in two stores of 16 bytes they are two writes to L2.
@@ -539,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   Bars<C>* bars = reinterpret_cast<Bars<C>*>(smem + C::kBarOff);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = a.n_h / a.n_kv;
   asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may start to wait
   if (threadIdx.x == 0) {
@@ -712,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t q_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kQOff), 16, 1024));
         const uint32_t k_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kKOff), 16, 1024));
         const uint32_t v_desc0 = static_cast<uint32_t>(sdesc_sw128(smem_u32(smem + C::kVOff), C::kBlockBytes, 1024));
@@ -720,8 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring kr, vr;
         uint32_t q_ph = 0, p_ph = 0, o_ph = 0, fix_ph = 0;  // parities, bits per worker (fix_ph: per V stage)
         // Q K^T: the steps of Q's first part, those of its second part.  Loops, a few at a time: all code that runs side by
-        // side in an SM has to fit its instruction cache (with the MMAs written out, 48 a turn, a tile's softmax took
-        // 2350 cycles in the mean and 1600 at best).
+        // side in an SM has to fit its instruction cache (with 96 MMAs written out, a tile's softmax took 2350 cycles in
+        // the mean and 1600 at best).
         auto qk_hi = [&](uint32_t w) {
           uint32_t a0 = q_desc0 + ((w * C::kTileBytes) >> 4), b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
 #pragma unroll 1
@@ -790,51 +820,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&bars->v_empty[vr.st]);
           vr.next(C::kVStages);
         };
-        // The same written out, for the loop inside pair pieces (48 MMAs a turn at 70 cycles instead of 90).
-        auto qk_hi_all = [&](uint32_t w) {
-          const uint32_t a0 = q_desc0 + ((w * C::kTileBytes) >> 4), b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < C::kSteps; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::kBlockBytes + (kk & 3) * 32) >> 4;
-            mma_ss_lo(tmem + w * 128u, a0 + off, b0 + off, C::kIdescQK, kk > 0 ? 1u : 0u);
-          }
-        };
-        const uint32_t lo_k = ((pl.lo_first >> 2) * C::kBlockBytes + (pl.lo_first & 3) * 32) >> 4;
-        auto qk_lo_all = [&](uint32_t w) {
-          if constexpr (LO) {
-            const uint32_t a0 = lo_desc0 + ((w * C::kLoBytes) >> 4);
-            const uint32_t b0 = k_desc0 + ((kr.st * C::kTileBytes) >> 4);
-            if ((pl.lo_first & 3) == 0) {
-#pragma unroll
-              for (int s = 0; s < C::kLoSteps; ++s) mma_ss_lo(tmem + w * 128u, a0 + s * 2, b0 + lo_k + s * 2, C::kIdescQK, 1u);
-            } else {
-              qk_lo(w);
-            }
-          }
-        };
-        auto pv_all = [&](uint32_t w) {
-          const uint32_t b0 = v_desc0 + ((vr.st * C::kTileBytes) >> 4), p0 = tmem + w * 128u, o0 = tmem + C::kOCol + w * D;
-#pragma unroll
-          for (int i = 0; i < BN / 16 + C::kPLoSteps; ++i)
-            mma_ts_lo(o0, p0 + i * 8, b0 + (i < BN / 16 ? i : i - 4) * 128, C::kIdescPV, 1u);
-        };
         // A turn inside a pair piece (see below); more: another one follows.
         auto turn = [&](bool more) -> bool {
           if (!wait_p(0)) return false;
           tc_fence_after();
-          pv_all(0);
-          qk_hi_all(0);
-          qk_lo_all(0);
-          mma_commit(&bars->s_full[0]);
+          issue_pv(0, false);
+          issue_qk(0);
           if (!wait_p(1)) return false;
           tc_fence_after();
-          pv_all(1);
+          issue_pv(1, false);
           v_done();
-          qk_hi_all(1);
+          qk_hi(1);
           Ring kn = kr;
           kn.next(C::kKStages);
           if (more && !(wait_v(false) && lane_wait(&bars->k_full[kn.st], kn.ph, wc))) return false;
-          qk_lo_all(1);
+          qk_lo(1);
           mma_commit(&bars->s_full[1]);
           mma_commit(&bars->k_empty[kr.st]);
           kr = kn;
@@ -1068,10 +1068,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!row_wait(&bars->s_full[w], s_ph, wc)) { ok = false; break; }
           s_ph ^= 1u;
           tc_fence_after();
-          uint32_t mask[4];
+          constexpr bool kLo = C::kPLoSteps > 0;
           const bool masked = t >= care;
-          if (masked) row_mask(a, pl, *u, w, my_tok, t * BN, mask);
-          softmax_row<D, (C::kPLoSteps > 0)>(s_addr, o_addr, masked, mask, i > 0, a.scale_log2, m_run, l_run);
+          if (masked || !__all_sync(0xffffffffu, m_run > -INFINITY) || !softmax_fast<kLo>(s_addr, a.scale_log2, m_run, l_run)) {
+            uint32_t mask[4] = {0u, 0u, 0u, 0u};
+            if (masked) row_mask(a, pl, *u, w, my_tok, t * BN, mask);
+            const float2 ml_new = softmax_row<D, kLo>(s_addr, o_addr, masked, make_uint4(mask[0], mask[1], mask[2], mask[3]),
+                                                      i > 0, a.scale_log2, m_run, l_run);
+            m_run = ml_new.x;
+            l_run = ml_new.y;
+          }
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars->p_full[w]);
