@@ -48,7 +48,6 @@ struct PackedTcPlan {
   int slot_rows;  // rows of a partial
   int lo_first;   // first MMA step with a second part of Q
   unsigned long long nth;  // 2^64 / ctas
-  int wide;       // 1: out and workspace start on 32 bytes
   // float offsets into the workspace: partials [2 * ctas, slot_rows, D], their log-sum-exps, records, the rotated
   // queries (bf16 [T, n_h, D]) and what that rounding left (bf16 [T, n_h, 64])
   long long l, rec, q, lo, end;
@@ -136,7 +135,7 @@ struct Bars {
   uint64_t v_full[C::kVStages], v_empty[C::kVStages], v_fixed[C::kVStages];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2], o_empty[2];
-  uint64_t x_full, x_done;  // single pieces: worker 1's sums are there, have been read
+  uint64_t x_full, x_back, x_done;  // single pieces: worker 1's sums are there, the rows' factors, worker 1 has read O
   uint64_t piece_full[kQueue], piece_empty[kQueue], care_done[kQueue];
   uint64_t fin;
   Piece piece[kQueue];
@@ -306,7 +305,8 @@ __global__ void __launch_bounds__(256) packed_rotate_kernel(const __grid_constan
       pos = r.base + t - r.first;
     }
     const int p0 = f.half ? rel : rel / 2, n = f.half ? 8 : 4;
-    with_angles<true, false>(max(pos, 0), [&](auto angle) {
+    // (the hardware sines are off by 2^-21: less than the second part's own rounding)
+    with_angles<true, true>(max(pos, 0), [&](auto angle) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (e < n) angle(f.hi[p0 + e], f.lo[p0 + e], &sn[e], &cs[e]);
@@ -386,49 +386,43 @@ __device__ __forceinline__ void seen_tree(const uint32_t* w, int base, int klim,
   }
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 // This thread's row of a tile's scores become its weights P (see prefill_tc.cu): p = 2^(s * scale*log2e - m), and m
-// moves only when the row maximum grew by more than the threshold.  So a tile that every row sees whole is taken with
-// the m that is there, in one pass that finds the maximum beside the weights; P is stored behind the pass, where no row
-// asks for another m, else (false) nothing is and softmax_row does the tile.
+// moves only when the row maximum grew by more than the threshold.  So a tile is taken with the m that is there, in one
+// pass that finds the maximum beside the weights; P is stored behind the pass, where no row asks for another m, else
+// (false) nothing is: prepare_row then moves m, and the tile is taken again (a copy of the code out of line: it is rare).
+// Masked tiles and a piece's first go through prepare_row before.
 // LO: the weights of the last 64 keys come as the sum of two bf16 values, the second ones in columns 64 on.
 // (Short as it can be: all code that runs side by side in an SM has to fit its instruction cache, see the MMA issuer;
 // and no more registers than there are: spilled ones are more than the L1 beside 226 KB of shared memory holds.)
 template <bool LO>
-__device__ __forceinline__ bool softmax_fast(uint32_t s_addr, float scale_log2, float m_run, float& l_run) {
-  uint32_t sr[2][32], pr[64], rest[LO ? 32 : 1];
-  tmem_ld32(s_addr, sr[0]);
-  const float2 sl2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m_run, -m_run);
+__device__ __forceinline__ bool softmax_row(uint32_t s_addr, float scale_log2, float m_run, float& l_run) {
+  uint32_t sr[2][16], pr[64], rest[LO ? 32 : 1];
+  tmem_ld16(s_addr, sr[0]);
+  const float m_ref = m_run == -INFINITY ? 0.f : m_run;  // every score so far is -inf: weights 0
+  const float2 sl2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m_ref, -m_ref);
   float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-  for (int q = 0; q < BN / 32; ++q) {
+  for (int q = 0; q < BN / 16; ++q) {
     tmem_wait_ld();
-    if (q + 1 < BN / 32) tmem_ld32(s_addr + 32 * (q + 1), sr[(q + 1) & 1]);
+    if (q + 1 < BN / 16) tmem_ld16(s_addr + 16 * (q + 1), sr[(q + 1) & 1]);
     const uint32_t* const s = sr[q & 1];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
+    for (int c = 0; c < 8; ++c) {
       const float2 y = make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-      mx[c & 3] = fmax3(mx[c & 3], y.x, y.y);
+      mx[c & 1] = fmax3(mx[c & 1], y.x, y.y);
       const float2 x = __ffma2_rn(y, sl2, nm2);
       const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
       acc[c & 1] = __fadd2_rn(acc[c & 1], pp);
-      pr[16 * q + c] = pack_bf16x2(pp.x, pp.y);
-      if (LO && q >= 2) {
-        const float2 z = __ffma2_rn(make_float2(__uint_as_float(pr[16 * q + c] << 16), __uint_as_float(pr[16 * q + c] & 0xffff0000u)),
+      pr[8 * q + c] = pack_bf16x2(pp.x, pp.y);
+      if (LO && q >= 4) {
+        const float2 z = __ffma2_rn(make_float2(__uint_as_float(pr[8 * q + c] << 16), __uint_as_float(pr[8 * q + c] & 0xffff0000u)),
                                     make_float2(-1.f, -1.f), pp);
-        rest[16 * (q - 2) + c] = pack_bf16x2(z.x, z.y);
+        rest[8 * (q - 4) + c] = pack_bf16x2(z.x, z.y);
       }
     }
   }
-  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+  const float top = fmaxf(mx[0], mx[1]) * scale_log2;
   if (__any_sync(0xffffffffu, top > m_run + kRescaleThreshold)) return false;
   tmem_st32(s_addr, pr);
   tmem_st32(s_addr + 32, pr + 32);
@@ -438,9 +432,10 @@ __device__ __forceinline__ bool softmax_fast(uint32_t s_addr, float scale_log2, 
   return true;
 }
 
-// The same for any tile, masked or with a new m: halves of the row in loops, the scores read twice.
-template <int D, bool LO>
-__device__ __noinline__ float2 softmax_row(uint32_t s_addr, uint32_t o_addr, bool masked, uint4 mask4, bool rescale,
+// Scores that the row does not see become -inf where they are, and m moves to the tile's maximum if that is higher by more
+// than the threshold, with l and O.
+template <int D>
+__device__ __noinline__ float2 prepare_row(uint32_t s_addr, uint32_t o_addr, bool masked, uint4 mask, bool rescale,
                                          float scale_log2, float m_run, float l_run) {
   float mx = -INFINITY;
 #pragma unroll 1
@@ -448,13 +443,17 @@ __device__ __noinline__ float2 softmax_row(uint32_t s_addr, uint32_t o_addr, boo
     uint32_t x[32];
     tmem_ld32(s_addr + 32 * h, x);
     tmem_wait_ld();
-    const uint32_t m = !masked ? 0xffffffffu : h == 0 ? mask4.x : h == 1 ? mask4.y : h == 2 ? mask4.z : mask4.w;
+    if (masked) {
+      const uint32_t m = mask.x;
+      mask = make_uint4(mask.y, mask.z, mask.w, 0u);
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (!((m >> c) & 1u)) x[c] = 0xff800000u;
+      tmem_st32(s_addr + 32 * h, x);
+    }
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float y = (m >> c) & 1u ? __uint_as_float(x[c]) : -INFINITY, z = (m >> c) & 2u ? __uint_as_float(x[c + 1]) : -INFINITY;
-      m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], y, z);
-    }
+    for (int c = 0; c < 32; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
     mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
   }
   mx *= scale_log2;
@@ -465,55 +464,15 @@ __device__ __noinline__ float2 softmax_row(uint32_t s_addr, uint32_t o_addr, boo
     l_run *= alpha;
     m_run = mx;
   }
-  const float2 sl2 = make_float2(scale_log2, scale_log2);
-  const float m_ref = (m_run == -INFINITY) ? 0.f : m_run;  // every score so far is -inf: weights 0
-  const float2 nm2 = make_float2(-m_ref, -m_ref);
-  float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 1
-  for (int h = 0; h < 4; ++h) {
-    uint32_t x[32], pr[16];
-    tmem_ld32(s_addr + 32 * h, x);
-    tmem_wait_ld();
-    const uint32_t m = !masked ? 0xffffffffu : h == 0 ? mask4.x : h == 1 ? mask4.y : h == 2 ? mask4.z : mask4.w;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sl2, nm2);
-      y.x = (m >> (2 * c)) & 1u ? fast_exp2(y.x) : 0.f;
-      y.y = (m >> (2 * c)) & 2u ? fast_exp2(y.y) : 0.f;
-      acc = __fadd2_rn(acc, y);
-      pr[c] = pack_bf16x2(y.x, y.y);
-      if (LO) {
-        x[2 * c] = __float_as_uint(y.x);
-        x[2 * c + 1] = __float_as_uint(y.y);
-      }
-    }
-    // over scores that have been read: P's columns are half as many, those of the second parts lie over tile columns 64 on
-    tmem_st16(s_addr + 16 * h, pr);
-    if (LO && h >= 2) {
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float2 z = __ffma2_rn(make_float2(__uint_as_float(pr[c] << 16), __uint_as_float(pr[c] & 0xffff0000u)),
-                                    make_float2(-1.f, -1.f),
-                                    make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])));
-        pr[c] = pack_bf16x2(z.x, z.y);
-      }
-      tmem_st16(s_addr + 64 + 16 * (h - 2), pr);
-    }
-  }
   if (__any_sync(0xffffffffu, need && rescale)) rescale_o<D>(o_addr, alpha);
-  return make_float2(m_run, l_run + acc.x + acc.y);
+  tmem_wait_st();
+  return make_float2(m_run, l_run);
 }
 
-// 32 bytes of a row, whole sectors where the row starts on one (wide): in two stores of 16 bytes they are two writes to L2.
-__device__ __forceinline__ void store32(uint4* p, const uint4& a, const uint4& b, int wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
-                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
-  } else {
-    p[0] = a;
-    p[1] = b;
-  }
+template <bool LO>
+__device__ __noinline__ float softmax_row_again(uint32_t s_addr, float scale_log2, float m_run, float l_run) {
+  softmax_row<LO>(s_addr, scale_log2, m_run, l_run);
+  return l_run;
 }
 
 // The bits of what a row of worker w sees in the tile from key0 on; a row that is no query sees nothing.
@@ -532,9 +491,9 @@ __device__ __noinline__ void row_mask(const PackedArgs& a, const PackedTcPlan& p
   seen_tree(bits, u.base, u.klim, key0, m);
 }
 
-// The values that are not finite in care tiles, of dims [d, d + 16), added to the outputs of a row that sees them.
-__device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl, const Piece& u, int w, int my_tok, int d,
-                                   float* o) {
+// The values that are not finite in care tiles, of dims [c0, c1), added to what has been stored of a row that sees them.
+__device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl, const Piece& u, int w, int my_tok, int c0, int c1,
+                                   __nv_bfloat16* out, float* partial) {
   for (int i = 0; i < kCare; ++i) {
     const int key0 = (u.care_t + i) * BN;
     if (u.care_t + i >= u.t_end) break;
@@ -546,12 +505,73 @@ __device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl
         const int key = key0 + 32 * j + __ffs(left) - 1;
         const int page = a.block_table[static_cast<long long>(u.b) * a.max_blocks + (key >> a.page_shift)];
         const long long slot = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-        const __nv_bfloat16* const v = static_cast<const __nv_bfloat16*>(a.v_pages) + slot * a.v_token_stride + u.g * a.D_v + d;
-        for (int e = 0; e < 16; ++e) {
-          const float x = __bfloat162float(v[e]);
-          if (!(fabsf(x) < INFINITY)) o[e] += x;
+        const __nv_bfloat16* const v = static_cast<const __nv_bfloat16*>(a.v_pages) + slot * a.v_token_stride + u.g * a.D_v;
+        for (int d = c0; d < c1; ++d) {
+          const float x = __bfloat162float(v[d]);
+          if (fabsf(x) < INFINITY) continue;
+          if (partial != nullptr) partial[d] += x;
+          else out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
         }
       }
+    }
+  }
+}
+
+// Columns [c0, c1) of the rows' O times f0 (both: and the one D columns on times f1), as bf16 to the output (whole) or as
+// fp32 to a partial; `to`: where this lane's row begins, `row` its number there (-1: not a query), step bytes per row.
+// none: zeros.  Four lanes exchange 16-byte pieces of their rows, so that a store instruction writes 64 bytes of each of
+// eight rows: with a row per lane it made 32 lines, and the load/store unit took 550 cycles for 16 columns.  Out of line:
+// beside the softmax it had registers of that spilled.
+template <int D>
+__device__ __noinline__ void store_rows(uint32_t o_col, int c0, int c1, bool both, bool whole, bool none, float f0, float f1, char* to,
+                                      int row, int step) {
+  const int lane = threadIdx.x & 31, lj = lane & 3;
+  to += lj * 16;
+  const auto put = [&](uint4* pc, int offset) {
+    transpose_pieces(pc, lj);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int other = __shfl_sync(0xffffffffu, row, (lane & 28) + k);
+      if (other >= 0) *reinterpret_cast<uint4*>(to + static_cast<long long>(other - (row >= 0 ? row : 0)) * step + offset) = pc[k];
+    }
+  };
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    float o[32];
+    {
+      uint32_t x[32];
+      tmem_ld32(o_col + c, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * f0;
+      if (both) {
+        tmem_ld32(o_col + D + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), f1, o[e]);
+      }
+    }
+    if (none) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = 0.f;
+    }
+    uint4 pc[4];
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pc[e] = f32_to_bf16x8(o + 8 * e);
+      put(pc, 0);
+      to += 64;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float* const v = o + 16 * h + 4 * e;
+          pc[e] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        }
+        put(pc, 64 * h);
+      }
+      to += 128;
     }
   }
 }
@@ -591,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->o_empty[w], 128);
     }
     mbar_init(&bars->x_full, 128);
+    mbar_init(&bars->x_back, 128);
     mbar_init(&bars->x_done, 128);
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&bars->piece_full[i], 1);
@@ -1068,15 +1089,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!row_wait(&bars->s_full[w], s_ph, wc)) { ok = false; break; }
           s_ph ^= 1u;
           tc_fence_after();
-          constexpr bool kLo = C::kPLoSteps > 0;
           const bool masked = t >= care;
-          if (masked || !__all_sync(0xffffffffu, m_run > -INFINITY) || !softmax_fast<kLo>(s_addr, a.scale_log2, m_run, l_run)) {
+          if (masked || i == 0) {
             uint32_t mask[4] = {0u, 0u, 0u, 0u};
             if (masked) row_mask(a, pl, *u, w, my_tok, t * BN, mask);
-            const float2 ml_new = softmax_row<D, kLo>(s_addr, o_addr, masked, make_uint4(mask[0], mask[1], mask[2], mask[3]),
-                                                      i > 0, a.scale_log2, m_run, l_run);
-            m_run = ml_new.x;
-            l_run = ml_new.y;
+            const float2 ml = prepare_row<D>(s_addr, o_addr, masked, make_uint4(mask[0], mask[1], mask[2], mask[3]), i > 0,
+                                             a.scale_log2, m_run, l_run);
+            m_run = ml.x;
+            l_run = ml.y;
+          }
+          if (!softmax_row<C::kPLoSteps != 0>(s_addr, a.scale_log2, m_run, l_run)) {
+            const float2 ml = prepare_row<D>(s_addr, o_addr, false, make_uint4(0u, 0u, 0u, 0u), i > 0, a.scale_log2, m_run, l_run);
+            m_run = ml.x;
+            l_run = softmax_row_again<C::kPLoSteps != 0>(s_addr, a.scale_log2, ml.x, ml.y);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -1085,24 +1110,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!__all_sync(0xffffffffu, ok)) break;
       // epilogue: the rows of the output, or the piece's normalised partial and its log-sum-exp
+      const int tok = (kind == kPair && w ? pl.tile_toks : 0) + my_tok;
+      const bool real = my_tok < pl.tile_toks && tok < u->ntok;  // this row is a query
+      const int position = real && a.positions != nullptr ? a.positions[u->row0 + tok] : 0;  // there by the time O is
       if (sh.n > 0) {
         if (!row_wait(&bars->o_done[w], o_ph, wc)) break;
         o_ph ^= 1u;
       }
-      // a single piece of more than one tile has a part of each row in both workers: worker 0 joins them
+      // A single piece of more than one tile has a part of each row in both workers: worker 0 joins the sums, and each
+      // worker writes half of the dims.
       const bool both = kind == kSingle && Share(*u, 1).n > 0;
       float2* const ml = reinterpret_cast<float2*>(smem + C::kMlOff) + r;
-      float f0 = l_run > 0.f ? 1.f / l_run : l_run, f1 = 0.f;  // factors of O of this worker, and of worker 1
+      float f0 = l_run > 0.f ? 1.f / l_run : l_run, f1 = 0.f;  // factors of O of this worker (both: of worker 0), and of worker 1
       if (both) {
         if (w == 1) {
-          if (!row_wait(&bars->x_done, x_ph ^ 1u, wc)) break;
           *ml = make_float2(m_run, l_run);
           tc_fence_before();
           mbar_arrive(&bars->x_full);
+          if (!row_wait(&bars->x_back, x_ph, wc)) break;
+          f0 = ml->x;
+          f1 = ml->y;
         } else {
           if (!row_wait(&bars->x_full, x_ph, wc)) break;
           const float2 o = *ml;
-          mbar_arrive(&bars->x_done);
           const float m = fmaxf(m_run, o.x), m_ref = m == -INFINITY ? 0.f : m;
           f0 = fast_exp2(m_run - m_ref);
           f1 = fast_exp2(o.x - m_ref);
@@ -1111,71 +1141,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = l_run > 0.f ? 1.f / l_run : l_run;
           f0 *= inv;
           f1 *= inv;
+          *ml = make_float2(f0, f1);
+          tc_fence_before();
+          mbar_arrive(&bars->x_back);
         }
-        x_ph ^= 1u;
       }
-      if (kind == kPair || w == 0) {
+      if (kind == kPair || w == 0 || both) {
         if (!row_wait(&bars->care_done[n % kQueue], (n / kQueue) & 1u, wc)) break;
         const bool whole = u->slot < 0;
-        const int tok = (kind == kPair && w ? pl.tile_toks : 0) + my_tok;
-        const bool real = my_tok < pl.tile_toks && tok < u->ntok;  // this row is a query
-        const bool dead = !real || u->place0 + tok < 0 || (a.positions != nullptr && a.positions[u->row0 + tok] < 0);
-        const bool none = dead || l_run == 0.f;  // no key with a weight; NaN is one
-        const bool bad = u->bad_any != 0;
+        const bool lead = !both || w == 0;  // writes the log-sum-exp
+        const bool dead = !real || u->place0 + tok < 0 || position < 0;
+        const bool none = dead || (f0 == 0.f && f1 == 0.f && l_run == 0.f);  // no key with a weight; NaN is one
         float* const ws = static_cast<float*>(a.workspace);
-        const long long slot_row = (2 * static_cast<long long>(blockIdx.x) + (whole ? 0 : u->slot)) * pl.slot_rows + w * BM + r;
+        const long long slot_row = (2 * static_cast<long long>(blockIdx.x) + (whole ? 0 : u->slot)) * pl.slot_rows + (kind == kPair ? w * BM : 0) + r;
         const long long out_row = static_cast<long long>(u->row0 + tok) * a.n_h + u->g * G + (r - my_tok * G);
         const float lse2 = none ? -INFINITY : m_run + log2f(l_run);
-        if (real) {
+        if (real && lead) {
           if (!whole) ws[pl.l + slot_row] = lse2;
           else if (a.lse != nullptr) a.lse[out_row] = lse2 * 0.69314718055994530942f;
         }
         if (sh.n > 0) {
           tc_fence_after();
-          // (16 columns at a time and no exchange of pieces between lanes: short code)
-          uint4* to = whole ? reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * D)
-                            : reinterpret_cast<uint4*>(ws + slot_row * D);
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t x[16];
-            tmem_ld16(o_addr + c, x);
-            tmem_wait_ld();
-            alignas(16) float o[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(x[e]) * f0;
-            if (both) {
-              tmem_ld16(o_addr + D + c, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), f1, o[e]);
-            }
-            if (bad && !none) {
-              float y[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = o[e];
-              add_bad(a, pl, *u, w, my_tok, c, y);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = y[e];
-            }
-            if (none) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = 0.f;
-            }
-            if (real && whole) {
-              store32(to, f32_to_bf16x8(o), f32_to_bf16x8(o + 8), pl.wide);
-            } else if (real) {
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint4* const v = reinterpret_cast<const uint4*>(o + 8 * e);
-                store32(to + 2 * e, v[0], v[1], pl.wide);
-              }
-            }
-            to += whole ? 2 : 4;
+          const int c0 = both && w == 1 ? D / 2 : 0, c1 = both && w == 0 ? D / 2 : D;
+          // rows that are no queries take the place of row 0 (they store nothing of their own)
+          const long long at = whole ? (real ? out_row : 0) : slot_row;
+          char* const to = whole ? static_cast<char*>(a.out) + at * (D * 2) : reinterpret_cast<char*>(ws + (real ? at : at - r) * D);
+          store_rows<D>(tmem + lane_off + C::kOCol + (both || w == 0 ? 0 : D), c0, c1, both, whole, none, f0, f1,
+                        to + c0 * (whole ? 2 : 4), real ? (whole ? static_cast<int>(at) : r) : -1, whole ? D * 2 : D * 4);
+          if (u->bad_any) {
+            __syncwarp();  // the row has been stored by four lanes
+            if (!none)
+              add_bad(a, pl, *u, w, my_tok, c0, c1, whole ? static_cast<__nv_bfloat16*>(a.out) + at * D : nullptr,
+                      whole ? nullptr : ws + slot_row * D);
           }
           tc_fence_before();
-          mbar_arrive(&bars->o_empty[w]);
-          if (both) mbar_arrive(&bars->o_empty[1]);
+          if (!both) {
+            mbar_arrive(&bars->o_empty[w]);
+          } else if (w == 1) {
+            mbar_arrive(&bars->x_done);
+          } else {
+            if (!row_wait(&bars->x_done, x_ph, wc)) break;
+            mbar_arrive(&bars->o_empty[0]);
+            mbar_arrive(&bars->o_empty[1]);
+          }
         }
+        if (both) x_ph ^= 1u;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->piece_empty[n % kQueue]);
@@ -1192,11 +1202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Blocks (CTA c of the kernel before, rows): if c's last piece is the head of a segment that goes on in the next
 // CTAs' first pieces, its rows are joined, a warp per row: the weights of the pieces by lanes, then D dims.
-constexpr int kJoinWarps = 8, kJoinPer = 2, kJoinFlight = 4, kJoinRows = 2 * kJoinWarps * kJoinPer;
+constexpr int kJoinWarps = 8, kJoinPer = 1, kJoinFlight = 4, kJoinRows = 2 * kJoinWarps * kJoinPer;
 constexpr int kMaxCtas = 160;  // the workspace is sized for this many (a GB300 has 152 SMs)
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32, 6)
     packed_tc_join_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ PackedTcPlan pl) {
   constexpr int kPer = D / 32;  // dims per lane
   __shared__ int slots[kMaxCtas];
@@ -1315,7 +1325,6 @@ PackedTcPlan make_plan(const PackedArgs& a, int ctas, int max_ctas, bool rotate)
   p.slot_rows = a.T <= p.tile_toks ? a.T * G : 2 * BM;
   const int rest = (a.D_qk - kLoDims) / 16;
   p.lo_first = a.rope_offset / 16 < rest ? a.rope_offset / 16 : rest;
-  p.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.workspace)) & 31u) == 0;
   p.l = 2LL * max_ctas * p.slot_rows * a.D_v;
   p.rec = (p.l + 2LL * max_ctas * p.slot_rows + 3) & ~3LL;
   p.q = (p.rec + 2LL * max_ctas * static_cast<long long>(sizeof(Record) / 4) + 31) & ~31LL;
@@ -1350,9 +1359,10 @@ cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, const CUtensorMap*
   cudaError_t e = prepare<D, LO>();
   if (e != cudaSuccess) return e;
   if (LO) {
-    // few tokens: fewer heads per thread, for some eight warps per SM
+    // few tokens: fewer heads per thread, but for four or more the angles are worth sharing (one head each: 36 us for
+    // 1888 tokens of 32, instead of 12)
     int heads = a.n_h;
-    while (heads % 2 == 0 && static_cast<long long>(a.T) * (a.n_h / heads) * (D / 8) < 152LL * 1024) heads /= 2;
+    while (heads % 2 == 0 && heads > 4 && static_cast<long long>(a.T) * (a.n_h / heads) * (D / 8) < 152LL * 2048) heads /= 2;
     const long long items = static_cast<long long>(a.T) * (a.n_h / heads) * (D / 8);
     float* const ws = static_cast<float*>(a.workspace);
     packed_rotate_kernel<D><<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(
