@@ -12,6 +12,10 @@
 // leaves each request at least as many numbers as it has tiles, so a block finds its request by
 // bisection and a number that nobody uses ends at once.  With few tiles the keys of each are cut
 // into n_split equal parts and a second kernel joins the parts of a row by their log-sum-exps.
+//
+// fp32 with head dims up to 128 has a kernel of its own, packed_f32_kernel: the same tiles, but K and V in
+// shared memory as they lie in the cache, copied asynchronously (K of the next tile while this one's P V
+// runs, V while the next scores do), and packed pairs of FMAs.
 #include <math.h>
 
 #include "kernels.h"
@@ -47,6 +51,296 @@ __device__ __forceinline__ long long tile_start(const PackedArgs& a, int b, int 
   return static_cast<long long>(packed_first(a, b)) * G / R + b;
 }
 
+// A block's rows: the request, its rows row0 .. row0 + here - 1, and the keys [k_lo, k_hi) of this split.
+struct Tile {
+  int b, here;
+  PackedRequest rq;
+  long long row0;
+  int k_lo, k_hi;
+  int first_place;  // of its first row, -1 or more
+};
+// Finds a block's tile (here = 0: none), and clears its share of the rows behind the last request's.
+template <typename T>
+__device__ __forceinline__ Tile find_tile(const PackedArgs& a, long long number, int n_split) {
+  const int tid = threadIdx.x, G = a.n_h / a.n_kv, g = blockIdx.y, split = blockIdx.z;
+  if (split == 0) {
+    const long long from = static_cast<long long>(packed_first(a, a.B)) * G * a.D_v, to = static_cast<long long>(a.T) * G * a.D_v;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    for (long long i = from + 4LL * (number * kThreads + tid); i < to; i += 4LL * gridDim.x * kThreads) {
+      const long long row = i / (G * a.D_v);
+      const int at = static_cast<int>(i - row * (G * a.D_v));
+      store4(static_cast<T*>(a.out) + (row * a.n_h + g * G) * a.D_v + at, zero);
+      if (a.lse != nullptr && at % a.D_v == 0) a.lse[row * a.n_h + g * G + at / a.D_v] = -INFINITY;
+    }
+  }
+  Tile t;
+  int lo = 0, hi = a.B - 1;  // the last request whose numbers start at or before this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tile_start(a, mid, G) <= number) lo = mid;
+    else hi = mid - 1;
+  }
+  t.b = lo;
+  t.rq = packed_request(a, lo);
+  t.row0 = (number - tile_start(a, lo, G)) * R;
+  const long long n_rows = static_cast<long long>(t.rq.rows) * G;
+  t.here = t.row0 < 0 || t.row0 >= n_rows ? 0 : static_cast<int>(n_rows - t.row0 < R ? n_rows - t.row0 : R);
+  if (t.here == 0) return t;
+  // the keys that the tile's last row may see, and this split's part of them
+  const int last = t.rq.base + static_cast<int>((t.row0 + t.here - 1) / G);
+  const int keys = a.visible != nullptr ? t.rq.len : min(max(last, -1) + 1, t.rq.len);
+  int part = (keys + n_split - 1) / n_split;
+  part = (part + KT - 1) / KT * KT;
+  const long long k_lo = static_cast<long long>(split) * part;
+  t.k_hi = static_cast<int>(k_lo + part < keys ? k_lo + part : keys);
+  t.k_lo = static_cast<int>(k_lo < t.k_hi ? k_lo : t.k_hi);  // part of 0 keys: none
+  t.first_place = max(t.rq.base + static_cast<int>(t.row0 / G), -1);
+  return t;
+}
+// What a row sees of the tile: its place (-1: nothing) and bits.
+__device__ __forceinline__ void load_row(const PackedArgs& a, const Tile& t, int r, int* place, uint32_t* vis) {
+  *place = -1;
+  if (r >= t.here) return;
+  const int i = static_cast<int>((t.row0 + r) / (a.n_h / a.n_kv)), row = t.rq.first + i;
+  *place = t.rq.base + i;
+  if (a.positions != nullptr && a.positions[row] < 0) *place = -1;
+  for (int w = 0; w < 4; ++w) vis[w] = w < a.words ? static_cast<uint32_t>(a.visible[static_cast<long long>(row) * a.words + w]) : 0u;
+}
+__device__ __forceinline__ bool sees(const PackedArgs& a, const Tile& t, int place, const uint32_t* vis, int key) {
+  if (a.visible == nullptr) return key < t.k_hi && key <= place;
+  const int draft = key - t.rq.base;  // base may be below 0: key - base <= len - base = n
+  return key < t.k_hi && place >= 0 && (draft < 0 || (draft < 32 * a.words && ((vis[draft >> 5] >> (draft & 31)) & 1u)));
+}
+// Whether some row of the tile does not see some of the 64 keys from k0 on.
+__device__ __forceinline__ bool partly_seen(const PackedArgs& a, const Tile& t, int k0) {
+  return a.visible != nullptr ? k0 + KT > t.rq.base : k0 + KT - 1 > t.first_place || k0 + KT > t.k_hi;
+}
+// The slot of a key of the tile's request, -1: none.
+__device__ __forceinline__ long long slot_of(const PackedArgs& a, const int* table, int key, int k_hi) {
+  if (key >= k_hi) return -1;
+  const int page = table[key >> a.page_shift];
+  if (page < 0 || page >= a.n_pages) return -1;
+  return (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+}
+// Row r's output dims d .. d + 3 (normalised) and, for put_lse, its log-sum-exp: to the output, or to this split's part.
+template <typename T>
+__device__ __forceinline__ void put_row(const PackedArgs& a, const Tile& t, int r, int d, const float* o, int n_split) {
+  const int G = a.n_h / a.n_kv;
+  const long long row = t.row0 + r, at = (t.rq.first + row / G) * a.n_h + blockIdx.y * G + row % G;
+  if (n_split == 1) store4(static_cast<T*>(a.out) + at * a.D_v + d, o);
+  else store4(static_cast<float*>(a.workspace) + (static_cast<long long>(blockIdx.z) * a.T * a.n_h + at) * a.D_v + d, o);
+}
+__device__ __forceinline__ void put_lse(const PackedArgs& a, const Tile& t, int r, float lse2, int n_split) {
+  const int G = a.n_h / a.n_kv;
+  const long long row = t.row0 + r, at = (t.rq.first + row / G) * a.n_h + blockIdx.y * G + row % G;
+  if (n_split == 1) {
+    if (a.lse != nullptr) a.lse[at] = lse2 * 0.69314718055994530942f;
+  } else {
+    static_cast<float*>(a.workspace)[static_cast<long long>(n_split) * a.T * a.n_h * a.D_v +
+                                     static_cast<long long>(blockIdx.z) * a.T * a.n_h + at] = lse2;
+  }
+}
+
+// fp32, D_qk <= 128, NV blocks of 64 value dims.  Thread (tx, ty) has the scores of rows 4 ty + i with keys tx + 16 j, and
+// dims 4 tx + 64 v of the same rows' outputs.  Rows of K, V, Q and P end 4 floats behind a multiple of 32, so that the
+// 16-byte reads of eight lanes fall on different banks.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {  // zeros where there is nothing
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait_all_but_last() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+template <int NV>
+__global__ void __launch_bounds__(kThreads, 2)
+    packed_f32_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ RopeFreq f, int n_split) {
+  extern __shared__ float4 smem4[];
+  constexpr int VLD = NV * 64 + kPad;
+  const int QLD = a.D_qk + (a.D_qk % 32 ? 36 - a.D_qk % 32 : 4);  // 4 behind a multiple of 32
+  float* const Qs = reinterpret_cast<float*>(smem4);
+  float* const Ks = Qs + R * QLD;
+  float* const Vs = Ks + KT * QLD;
+  float* const Ps = Vs + KT * VLD;  // [R][LD]
+  __shared__ long long slot[2][KT];
+  __shared__ uint32_t vis[R][4];
+  __shared__ int row_place[R];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int G = a.n_h / a.n_kv, g = blockIdx.y;
+  // the last tiles, which see the most keys, first
+  const Tile t = find_tile<float>(a, static_cast<long long>(gridDim.x) - 1 - blockIdx.x, n_split);
+  if (t.here == 0) return;
+  const int* const table = a.block_table + static_cast<long long>(t.b) * a.max_blocks;
+  const float* const kp = static_cast<const float*>(a.k_pages) + g * a.D_qk;
+  const float* const vp = static_cast<const float*>(a.v_pages) + g * a.D_v;
+  const int kc = a.D_qk / 4, vc = a.D_v / 4;
+  const auto fetch_k = [&](int s) {
+    for (int i = tid; i < KT * kc; i += kThreads) {
+      const int key = i / kc, c = i - key * kc;
+      const long long at = slot[s][key];
+      copy16(Ks + key * QLD + c * 4, kp + (at < 0 ? 0 : at) * a.n_kv * a.D_qk + c * 4, at >= 0);
+    }
+    copy_commit();
+  };
+  const auto fetch_v = [&](int s) {
+    for (int i = tid; i < KT * vc; i += kThreads) {
+      const int key = i / vc, c = i - key * vc;
+      const long long at = slot[s][key];
+      copy16(Vs + key * VLD + c * 4, vp + (at < 0 ? 0 : at) * a.v_token_stride + c * 4, at >= 0);
+    }
+    copy_commit();
+  };
+  if (tid < 2 * KT) slot[tid >> 6][tid & 63] = slot_of(a, table, t.k_lo + tid, t.k_hi);
+  if (tid < R) load_row(a, t, tid, &row_place[tid], vis[tid]);
+  for (int i = tid; i < R * kc; i += kThreads) {
+    const int r = i / kc, c = i - r * kc;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < t.here) {
+      const long long row = t.row0 + r;
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + ((t.rq.first + row / G) * a.n_h + g * G + row % G) * a.D_qk + c * 4);
+    }
+    *reinterpret_cast<float4*>(Qs + r * QLD + c * 4) = x;
+  }
+  for (int i = tid; i < KT * (NV * 16 - vc); i += kThreads) {  // value dims behind the last stay 0
+    const int n = NV * 16 - vc, key = i / n;
+    *reinterpret_cast<float4*>(Vs + key * VLD + (vc + i - key * n) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  fetch_k(0);
+  fetch_v(0);
+  for (int i = tid; i < t.here * f.n_pairs; i += kThreads) {
+    const int r = i / f.n_pairs, p = i - r * f.n_pairs;
+    const int row = t.rq.first + static_cast<int>((t.row0 + r) / G);
+    const int pos = a.positions != nullptr ? a.positions[row] : t.rq.base + static_cast<int>((t.row0 + r) / G);
+    if (pos < 0) continue;
+    float sn, cs;
+    with_angles<true, false>(pos, [&](auto angle) { angle(f.hi[p], f.lo[p], &sn, &cs); });
+    const int2 d = rope_pair_dims(f, p);
+    rotate_pair(Qs[r * QLD + a.rope_offset + d.x], Qs[r * QLD + a.rope_offset + d.y], sn, cs);
+  }
+  float m[4], l[4];
+  float2 acc[NV][4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) acc[v][i][0] = acc[v][i][1] = make_float2(0.f, 0.f);
+  }
+  int cur = 0;
+  for (int k0 = t.k_lo; k0 < t.k_hi; k0 += KT, cur ^= 1) {  // k_hi <= 2^31 - 2^16: no overflow
+    copy_wait_all_but_last();
+    __syncthreads();  // K, and before the first tile Q, are there
+    float2 s2[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 2
+    for (int d = 0; d < a.D_qk; d += 4) {
+      float4 q4[4], k4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q4[i] = *reinterpret_cast<const float4*>(Qs + (ty * 4 + i) * QLD + d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * QLD + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s2[i][j] = __ffma2_rn(make_float2(q4[i].x, q4[i].y), make_float2(k4[j].x, k4[j].y), s2[i][j]);
+          s2[i][j] = __ffma2_rn(make_float2(q4[i].z, q4[i].w), make_float2(k4[j].z, k4[j].w), s2[i][j]);
+        }
+    }
+    __syncthreads();
+    fetch_k(cur ^ 1);
+    const bool masked = partly_seen(a, t, k0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      float s[4], mx = -INFINITY;
+      bool seen[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[j] = (s2[i][j].x + s2[i][j].y) * a.scale_log2;
+        seen[j] = !masked || sees(a, t, row_place[r], vis[r], k0 + tx + 16 * j);
+        if (seen[j]) mx = fmaxf(mx, s[j]);
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float m_new = fmaxf(m[i], mx), m_ref = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m[i] - m_ref);
+      m[i] = m_new;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[j] - m_ref);
+        if (seen[j]) sum += p;
+        Ps[r * LD + tx + 16 * j] = seen[j] ? p : kMasked;
+      }
+      l[i] = fmaf(l[i], alpha, sum);  // of this thread's keys
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[v][i][j].x *= alpha;
+          acc[v][i][j].y *= alpha;
+        }
+    }
+    // the slots of the tile behind the next one take this one's place
+    const long long next = static_cast<long long>(k0) + 2 * KT + tid;
+    const long long next_slot = tid < KT && next < t.k_hi ? slot_of(a, table, static_cast<int>(next), t.k_hi) : -1;
+    copy_wait_all_but_last();
+    __syncthreads();  // V and P are there
+    const auto add = [&](auto with_mask) {
+#pragma unroll 2
+      for (int k = 0; k < KT; k += 4) {
+        float p4[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(Ps + (ty * 4 + i) * LD + k);
+          p4[i][0] = x.x; p4[i][1] = x.y; p4[i][2] = x.z; p4[i][3] = x.w;
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const float4 x = *reinterpret_cast<const float4*>(Vs + (k + kk) * VLD + v * 64 + tx * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // a value that the row does not see may be anything
+              if (with_mask() && p4[i][kk] == kMasked) continue;
+              const float2 p = make_float2(p4[i][kk], p4[i][kk]);
+              acc[v][i][0] = __ffma2_rn(p, make_float2(x.x, x.y), acc[v][i][0]);
+              acc[v][i][1] = __ffma2_rn(p, make_float2(x.z, x.w), acc[v][i][1]);
+            }
+          }
+      }
+    };
+    if (masked) add([] { return true; });
+    else add([] { return false; });
+    __syncthreads();
+    fetch_v(cur ^ 1);
+    if (tid < KT) slot[cur][tid] = next_slot;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+    if (r >= t.here) continue;
+    if (row_place[r] < 0) l[i] = 0.f;  // an empty row: tiles that are seen whole do not ask
+    const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];  // 0: no key with a weight; NaN stays
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int d = v * 64 + tx * 4;
+      if (d >= a.D_v) continue;
+      float o[4] = {acc[v][i][0].x * inv, acc[v][i][0].y * inv, acc[v][i][1].x * inv, acc[v][i][1].y * inv};
+      if (l[i] == 0.f) o[0] = o[1] = o[2] = o[3] = 0.f;
+      put_row<float>(a, t, r, d, o, n_split);
+    }
+    if (tx == 0) put_lse(a, t, r, l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
+  }
+}
+
 // NV: blocks of 64 value dims.
 template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads)
@@ -59,61 +353,27 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ uint32_t vis[R][4];
   __shared__ int row_place[R];                        // -1: the row is empty or not there
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int G = a.n_h / a.n_kv, g = blockIdx.y, split = blockIdx.z;
-
-  // rows behind the last request's
-  if (split == 0) {
-    const long long from = static_cast<long long>(packed_first(a, a.B)) * G * a.D_v, to = static_cast<long long>(a.T) * G * a.D_v;
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    for (long long i = from + 4LL * (blockIdx.x * kThreads + tid); i < to; i += 4LL * gridDim.x * kThreads) {
-      const long long row = i / (G * a.D_v);
-      const int at = static_cast<int>(i - row * (G * a.D_v));
-      store4(static_cast<T*>(a.out) + (row * a.n_h + g * G) * a.D_v + at, zero);
-      if (a.lse != nullptr && at % a.D_v == 0) a.lse[row * a.n_h + g * G + at / a.D_v] = -INFINITY;
-    }
-  }
-  int lo = 0, hi = a.B - 1;  // the last request whose numbers start at or before this one
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tile_start(a, mid, G) <= static_cast<long long>(blockIdx.x)) lo = mid;
-    else hi = mid - 1;
-  }
-  const int b = lo;
-  const PackedRequest rq = packed_request(a, b);
-  const long long row0 = (static_cast<long long>(blockIdx.x) - tile_start(a, b, G)) * R;
-  const long long n_rows = static_cast<long long>(rq.rows) * G;
-  if (row0 < 0 || row0 >= n_rows) return;
-  const int here = static_cast<int>(n_rows - row0 < R ? n_rows - row0 : R);
-
-  // places, bits, queries
-  if (tid < R) {
-    int place = -1;
-    if (tid < here) {
-      const int i = static_cast<int>((row0 + tid) / G);
-      const int t = rq.first + i;
-      place = rq.base + i;
-      if (a.positions != nullptr && a.positions[t] < 0) place = -1;
-      for (int w = 0; w < 4; ++w)
-        vis[tid][w] = w < a.words ? static_cast<uint32_t>(a.visible[static_cast<long long>(t) * a.words + w]) : 0u;
-    }
-    row_place[tid] = place;
-  }
+  const int G = a.n_h / a.n_kv, g = blockIdx.y;
+  const Tile t = find_tile<T>(a, blockIdx.x, n_split);
+  if (t.here == 0) return;
+  const int* const table = a.block_table + static_cast<long long>(t.b) * a.max_blocks;
+  if (tid < R) load_row(a, t, tid, &row_place[tid], vis[tid]);
   for (int i = tid; i < R * (a.D_qk / 8); i += kThreads) {
     const int r = i & (R - 1), d = (i >> 6) * 8;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (r < here) {
-      const long long row = row0 + r;
-      load8(static_cast<const T*>(a.q) + ((rq.first + row / G) * a.n_h + g * G + row % G) * a.D_qk + d, x);
+    if (r < t.here) {
+      const long long row = t.row0 + r;
+      load8(static_cast<const T*>(a.q) + ((t.rq.first + row / G) * a.n_h + g * G + row % G) * a.D_qk + d, x);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) Qs[(d + e) * LD + r] = x[e];
   }
   __syncthreads();
   if (f.n_pairs) {
-    for (int i = tid; i < here * f.n_pairs; i += kThreads) {
-      const int r = i % here, p = i / here;
-      const int t = rq.first + static_cast<int>((row0 + r) / G);
-      const int pos = a.positions != nullptr ? a.positions[t] : rq.base + static_cast<int>((row0 + r) / G);
+    for (int i = tid; i < t.here * f.n_pairs; i += kThreads) {
+      const int r = i % t.here, p = i / t.here;
+      const int row = t.rq.first + static_cast<int>((t.row0 + r) / G);
+      const int pos = a.positions != nullptr ? a.positions[row] : t.rq.base + static_cast<int>((t.row0 + r) / G);
       if (pos < 0) continue;
       float sn, cs;
       with_angles<true, false>(pos, [&](auto angle) { angle(f.hi[p], f.lo[p], &sn, &cs); });
@@ -121,14 +381,6 @@ __global__ void __launch_bounds__(kThreads)
       rotate_pair(Qs[(a.rope_offset + d.x) * LD + r], Qs[(a.rope_offset + d.y) * LD + r], sn, cs);
     }
   }
-  // the keys that the tile's last row may see, and this split's part of them
-  const int last = rq.base + static_cast<int>((row0 + here - 1) / G);
-  const int keys = a.visible != nullptr ? rq.len : min(max(last, -1) + 1, rq.len);
-  int part = (keys + n_split - 1) / n_split;
-  part = (part + KT - 1) / KT * KT;
-  const long long k_lo = static_cast<long long>(split) * part;
-  const int k_hi = static_cast<int>(k_lo + part < keys ? k_lo + part : keys);
-
   float m[4], l[4], acc[NV][4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -139,21 +391,9 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[v][i][j] = 0.f;
   }
-  const int* const table = a.block_table + static_cast<long long>(b) * a.max_blocks;
-  const int first_place = max(rq.base + static_cast<int>(row0 / G), -1);
-  for (long long k64 = k_lo; k64 < k_hi; k64 += KT) {
-    const int k0 = static_cast<int>(k64);
+  for (int k0 = t.k_lo; k0 < t.k_hi; k0 += KT) {
     __syncthreads();
-    if (tid < KT) {
-      const int key = k0 + tid;
-      long long s = -1;
-      if (key < k_hi) {
-        const int page = table[key >> a.page_shift];
-        if (page >= 0 && page < a.n_pages)
-          s = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-      }
-      slot[tid] = s;
-    }
+    if (tid < KT) slot[tid] = slot_of(a, table, k0 + tid, t.k_hi);
     float s[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -182,8 +422,7 @@ __global__ void __launch_bounds__(kThreads)
           for (int j = 0; j < 4; ++j) s[i][j] = fmaf(q4[i], k4[j], s[i][j]);
       }
     }
-    // some row does not see some key of the tile
-    const bool masked = a.visible != nullptr ? k0 + KT > rq.base : k0 + KT - 1 > first_place || k0 + KT > k_hi;
+    const bool masked = partly_seen(a, t, k0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i, place = row_place[r];
@@ -191,14 +430,7 @@ __global__ void __launch_bounds__(kThreads)
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = k0 + tx * 4 + j;
-        if (a.visible != nullptr) {
-          const int draft = key - rq.base;  // base may be below 0: key - base <= len - base = n
-          seen[j] = key < k_hi && place >= 0 &&
-                    (draft < 0 || (draft < 32 * a.words && ((vis[r][draft >> 5] >> (draft & 31)) & 1u)));
-        } else {
-          seen[j] = key < k_hi && key <= place;
-        }
+        seen[j] = sees(a, t, place, vis[r], k0 + tx * 4 + j);
         s[i][j] *= a.scale_log2;
         if (seen[j]) mx = fmaxf(mx, s[i][j]);
       }
@@ -261,11 +493,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty * 4 + i;
-    if (r >= here) continue;
-    const long long row = row0 + r;
-    const long long at = (rq.first + row / G) * a.n_h + g * G + row % G;
+    if (r >= t.here) continue;
     const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];  // 0: no key with a weight; NaN stays
-    const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int d = v * 64 + tx * 4;
@@ -273,19 +502,9 @@ __global__ void __launch_bounds__(kThreads)
       float o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = l[i] == 0.f ? 0.f : acc[v][i][j] * inv;
-      if (n_split == 1)
-        store4(static_cast<T*>(a.out) + at * a.D_v + d, o);
-      else
-        store4(static_cast<float*>(a.workspace) + (static_cast<long long>(split) * a.T * a.n_h + at) * a.D_v + d, o);
+      put_row<T>(a, t, r, d, o, n_split);
     }
-    if (tx == 0) {
-      if (n_split == 1) {
-        if (a.lse != nullptr) a.lse[at] = lse2 * 0.69314718055994530942f;
-      } else {
-        static_cast<float*>(a.workspace)[static_cast<long long>(n_split) * a.T * a.n_h * a.D_v +
-                                         static_cast<long long>(split) * a.T * a.n_h + at] = lse2;
-      }
-    }
+    if (tx == 0) put_lse(a, t, r, l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
   }
 }
 
@@ -333,6 +552,16 @@ int splits(const PackedArgs& a) {
 }
 size_t smem_bytes(const PackedArgs& a) { return static_cast<size_t>(a.D_qk + 2 * KT) * LD * sizeof(float); }
 
+// Behind a kernel's launch: the one that joins its splits.
+template <typename T>
+cudaError_t join(const PackedArgs& a, int n_split, cudaStream_t st, int* launches) {
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || n_split == 1) return err;
+  const long long rows = static_cast<long long>(a.T) * a.n_h;
+  packed_combine_kernel<T><<<static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(a, n_split);
+  *launches += 1;
+  return cudaGetLastError();
+}
 template <typename T, int NV>
 cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
   const size_t smem = smem_bytes(a);
@@ -342,15 +571,26 @@ cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaS
   const dim3 grid(static_cast<unsigned>(tile_numbers(a)), a.n_kv, n_split);
   packed_kernel<T, NV><<<grid, kThreads, smem, st>>>(a, rope, n_split);
   *launches += 1;
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || n_split == 1) return err;
-  const long long rows = static_cast<long long>(a.T) * a.n_h;
-  packed_combine_kernel<T><<<static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, st>>>(a, n_split);
+  return join<T>(a, n_split, st, launches);
+}
+template <int NV>
+cudaError_t launch_f32(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
+  constexpr int kMost = (2 * 64 * (128 + kPad) + 64 * (NV * 64 + kPad) + 64 * LD) * static_cast<int>(sizeof(float));
+  const cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (e != cudaSuccess) return e;
+  const int qld = a.D_qk + (a.D_qk % 32 ? 36 - a.D_qk % 32 : 4);
+  const size_t smem = (2 * 64 * qld + 64 * (NV * 64 + kPad) + 64 * LD) * sizeof(float);
+  const dim3 grid(static_cast<unsigned>(tile_numbers(a)), a.n_kv, n_split);
+  packed_f32_kernel<NV><<<grid, kThreads, smem, st>>>(a, rope, n_split);
   *launches += 1;
-  return cudaGetLastError();
+  return join<float>(a, n_split, st, launches);
 }
 template <typename T>
 cudaError_t launch_dims(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
+  if constexpr (sizeof(T) == 4) {
+    if (a.D_qk <= 128 && a.D_v <= 128)
+      return a.D_v <= 64 ? launch_f32<1>(a, rope, n_split, st, launches) : launch_f32<2>(a, rope, n_split, st, launches);
+  }
   if (a.D_v <= 64) return launch<T, 1>(a, rope, n_split, st, launches);
   if (a.D_v <= 128) return launch<T, 2>(a, rope, n_split, st, launches);
   if (a.D_v <= 256) return launch<T, 4>(a, rope, n_split, st, launches);
