@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[v][i][0] = acc[v][i][1] = make_float2(0.f, 0.f);
   }
+  const bool active = (tid >> 5) * 8 < t.here;  // this warp has rows (eight of them)
   int cur = 0;
   for (int k0 = t.k_lo; k0 < t.k_hi; k0 += KT, cur ^= 1) {  // k_hi <= 2^31 - 2^16: no overflow
     copy_wait_all_but_last();
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 2
-    for (int d = 0; d < a.D_qk; d += 4) {
+    for (int d = 0; active && d < a.D_qk; d += 4) {
       float4 q4[4], k4[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) q4[i] = *reinterpret_cast<const float4*>(Qs + (ty * 4 + i) * QLD + d);
@@ -252,37 +253,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     fetch_k(cur ^ 1);
     const bool masked = partly_seen(a, t, k0);
+    if (active) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
-      float s[4], mx = -INFINITY;
-      bool seen[4];
+      for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        float s[4], mx = -INFINITY;
+        bool seen[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j] = (s2[i][j].x + s2[i][j].y) * a.scale_log2;
-        seen[j] = !masked || sees(a, t, row_place[r], vis[r], k0 + tx + 16 * j);
-        if (seen[j]) mx = fmaxf(mx, s[j]);
-      }
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float m_new = fmaxf(m[i], mx), m_ref = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = exp2f(m[i] - m_ref);
-      m[i] = m_new;
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(s[j] - m_ref);
-        if (seen[j]) sum += p;
-        Ps[r * LD + tx + 16 * j] = seen[j] ? p : kMasked;
-      }
-      l[i] = fmaf(l[i], alpha, sum);  // of this thread's keys
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          acc[v][i][j].x *= alpha;
-          acc[v][i][j].y *= alpha;
+        for (int j = 0; j < 4; ++j) {
+          s[j] = (s2[i][j].x + s2[i][j].y) * a.scale_log2;
+          seen[j] = !masked || sees(a, t, row_place[r], vis[r], k0 + tx + 16 * j);
+          if (seen[j]) mx = fmaxf(mx, s[j]);
         }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float m_new = fmaxf(m[i], mx), m_ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = exp2f(m[i] - m_ref);
+        m[i] = m_new;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(s[j] - m_ref);
+          if (seen[j]) sum += p;
+          Ps[r * LD + tx + 16 * j] = seen[j] ? p : kMasked;
+        }
+        l[i] = fmaf(l[i], alpha, sum);  // of this thread's keys
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            acc[v][i][j].x *= alpha;
+            acc[v][i][j].y *= alpha;
+          }
+      }
     }
     // the slots of the tile behind the next one take this one's place
     const long long next = static_cast<long long>(k0) + 2 * KT + tid;
@@ -314,8 +317,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
       }
     };
-    if (masked) add([] { return true; });
-    else add([] { return false; });
+    if (active) {
+      if (masked) add([] { return true; });
+      else add([] { return false; });
+    }
     __syncthreads();
     fetch_v(cur ^ 1);
     if (tid < KT) slot[cur][tid] = next_slot;
@@ -540,15 +545,15 @@ __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_c
     a.lse[at] = den == 0.f ? -INFINITY : (m + log2f(den)) * 0.69314718055994530942f;
 }
 
-// Numbers of tiles (an upper bound of the tiles), and parts of each tile's keys: enough blocks for three per SM.
-// (Not by the table's width: tables are as wide as a request may grow.)
+// Numbers of tiles (an upper bound of the tiles), and parts of each tile's keys: as many as leave all blocks running at
+// once, two per SM.  (A second wave costs as much as the first: with half as many parts again, 6 requests of up to 16
+// drafts took 47 us.  Not by the table's width: tables are as wide as a request may grow.)
 long long tile_numbers(const PackedArgs& a) {
   return static_cast<long long>(a.T) * (a.n_h / a.n_kv) / R + a.B;
 }
 int splits(const PackedArgs& a) {
-  const long long blocks = tile_numbers(a) * a.n_kv;
-  const long long n = (3 * 152 + blocks - 1) / blocks;
-  return static_cast<int>(n > 64 ? 64 : n);
+  const long long n = 2 * 152 / (tile_numbers(a) * a.n_kv);
+  return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
 }
 size_t smem_bytes(const PackedArgs& a) { return static_cast<size_t>(a.D_qk + 2 * KT) * LD * sizeof(float); }
 
