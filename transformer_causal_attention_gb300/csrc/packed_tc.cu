@@ -390,7 +390,7 @@ __device__ __forceinline__ void seen_tree(const uint32_t* w, int base, int klim,
 // moves only when the row maximum grew by more than the threshold.  So a tile is taken with the m that is there, in one
 // pass that finds the maximum beside the weights; P is stored behind the pass, where no row asks for another m, else
 // (false) nothing is: prepare_row then moves m, and the tile is taken again (a copy of the code out of line: it is rare).
-// Masked tiles and a piece's first go through prepare_row before.
+// Masked tiles go through prepare_row before.
 // LO: the weights of the last 64 keys come as the sum of two bf16 values, the second ones in columns 64 on.
 // (Short as it can be: all code that runs side by side in an SM has to fit its instruction cache, see the MMA issuer;
 // and no more registers than there are: spilled ones are more than the L1 beside 226 KB of shared memory holds.)
@@ -430,6 +430,17 @@ __device__ __forceinline__ bool softmax_row(uint32_t s_addr, float scale_log2, f
   acc[0] = __fadd2_rn(acc[0], acc[1]);
   l_run += acc[0].x + acc[0].y;
   return true;
+}
+
+// The maximum of a row's first 32 scores: a piece's first m, mostly within the threshold of the whole tile's maximum.
+__device__ __noinline__ float max_of_some(uint32_t s_addr) {
+  uint32_t x[32];
+  tmem_ld32(s_addr, x);
+  tmem_wait_ld();
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
 }
 
 // Scores that the row does not see become -inf where they are, and m moves to the tile's maximum if that is higher by more
@@ -1090,13 +1101,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_ph ^= 1u;
           tc_fence_after();
           const bool masked = t >= care;
-          if (masked || i == 0) {
-            uint32_t mask[4] = {0u, 0u, 0u, 0u};
-            if (masked) row_mask(a, pl, *u, w, my_tok, t * BN, mask);
-            const float2 ml = prepare_row<D>(s_addr, o_addr, masked, make_uint4(mask[0], mask[1], mask[2], mask[3]), i > 0,
+          if (masked) {
+            uint32_t mask[4];
+            row_mask(a, pl, *u, w, my_tok, t * BN, mask);
+            const float2 ml = prepare_row<D>(s_addr, o_addr, true, make_uint4(mask[0], mask[1], mask[2], mask[3]), i > 0,
                                              a.scale_log2, m_run, l_run);
             m_run = ml.x;
             l_run = ml.y;
+          } else if (i == 0) {
+            m_run = max_of_some(s_addr) * a.scale_log2;
           }
           if (!softmax_row<C::kPLoSteps != 0>(s_addr, a.scale_log2, m_run, l_run)) {
             const float2 ml = prepare_row<D>(s_addr, o_addr, false, make_uint4(0u, 0u, 0u, 0u), i > 0, a.scale_log2, m_run, l_run);
