@@ -125,7 +125,8 @@ def compare(got, lse, want, want_lse, spread, err, dtype):
 
 # ------------------------------------------------------------------------------------------- packed prefill
 RAGGED = [5, 0, 1, 64, 33, 129, 2, 31, 200]
-HEADS = [(8, 2, 128), (4, 4, 64), (32, 8, 128), (6, 2, 64), (14, 2, 128), (8, 1, 64), (3, 3, 128), (40, 8, 64)]
+HEADS = [(8, 2, 128), (4, 4, 64), (32, 8, 128), (6, 2, 64), (14, 2, 128), (8, 1, 64), (3, 3, 128), (40, 8, 64),
+         (24, 1, 128), (96, 1, 64), (128, 1, 128)]
 
 
 @pytest.mark.parametrize("n_h,n_kv,D", HEADS)
@@ -304,6 +305,41 @@ def test_nan_and_infinities_reach_their_rows_only(lib):
                         assert torch.isnan(got[hit]).all()
 
 
+@pytest.mark.parametrize("n_h,n_kv,D,dtype", [(8, 2, 128, "bf16"), (4, 4, 64, "bf16"), (4, 2, 64, "f32")])
+@pytest.mark.parametrize("tree", [False, True])
+def test_infinities_behind_a_rotation(lib, n_h, n_kv, D, dtype, tree):
+    """Values, keys and queries that are infinite, in tiles that rows see whole and in part, with rotated queries: the
+    results are the reference's infinities, and NaN where it has NaN.  (A key with a score of -inf has no weight, one
+    with inf makes its rows NaN.)"""
+    for place in (3, 70, 127, 130, 141, 210):  # of request 0: 200 tokens held, 70 new ones
+        for value in (float("inf"), float("-inf")):
+            s = Step([70, 20], [200, 10], n_h, n_kv, D, dtype=dtype, tree=tree, seed=5, base=1e4)
+            page, row = int(s.table[0, place // 16]), place % 16
+            for what in ("v", "k"):
+                x, of = (s.v, s.v_of) if what == "v" else (s.k, s.k_of)
+                kept, kept_of = x[page, row, 0, 7].clone(), of[0][place, 0, 7]
+                x[page, row, 0, 7], of[0][place, 0, 7] = value, value
+                got, lse = s.run(lib)
+                with np.errstate(all="ignore"):
+                    if what == "v":  # weights are what they were
+                        sees = ref.causal(70, 200) if not tree else ref.tree(70, 200, s.visible[:70])
+                        hit = np.zeros((s.T, n_h), bool)
+                        hit[:70, :n_h // n_kv] = sees[:, place][:, None]
+                        o = to_np(got)
+                        assert (o[hit][:, 7] == value).all()
+                        assert np.isfinite(o[~hit]).all() and np.isfinite(np.delete(o[hit], 7, 1)).all()
+                    else:  # a score of inf or -inf, by the sign of the rotated query's element
+                        q = s.q[:70].double().numpy()
+                        turned = np.stack([ref.oracle.rope_rotate(q[:, h], s.positions[:70], 1e4) for h in range(n_h)], 1)
+                        sees = ref.causal(70, 200) if not tree else ref.tree(70, 200, s.visible[:70])
+                        sees = np.broadcast_to(sees[:, place][:, None], (70, n_h)) & (np.arange(n_h) < n_h // n_kv)[None]
+                        up = sees & (turned[:, :, 7] * value > 0)
+                        o = to_np(got)
+                        assert np.isnan(o[:70][up]).all()
+                        assert np.isfinite(o[:70][~up]).all() and np.isfinite(o[70:]).all()
+                x[page, row, 0, 7], of[0][place, 0, 7] = kept, kept_of
+
+
 def test_values_in_rows_of_no_token(lib):
     """What lies behind the last token, or in pages of others, may be anything."""
     s = Step([70, 20], [31, 0], 8, 2, 128, seed=4)
@@ -328,6 +364,30 @@ def test_scores_far_apart(lib):
         s.check(lib, )
         s.q[:] = 0
         s.check(lib)
+
+
+def test_caches_of_more_than_two_to_the_31_elements(lib):
+    """Pages at the end of a cache whose offsets pass 32 bits, attended and committed to."""
+    n_pages, page, n_kv, D = 33000, 64, 8, 128
+    k, v = (torch.zeros(n_pages, page, n_kv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    assert k.numel() > 2 ** 31
+    s = Step([20, 9], [100, 0], 32, n_kv, D, page=page, base=1e4)
+    n = s.k.shape[0]
+    small = s.run(lib)
+    k[-n:], v[-n:] = s.k.to(DEV), s.v.to(DEV)
+    args = list(s.tensors())
+    far = args[3] + (n_pages - n) * (args[3] >= 0).int()
+    args[1], args[2], args[3] = k, v, far
+    big = s.run(lib, args)
+    assert torch.equal(small[0], big[0]) and torch.equal(small[1], big[1])
+    before = k[-n:].clone()
+    new, _ = lib.draft_commit(k, v, far, ints([100, 0]), ints([120, 9]), ints([[3, 19], [0, 2]]), ints([2, 2]))
+    assert new.tolist() == [102, 2]
+    rows = k[-n:].view(-1, n_kv, D)
+    table = s.table.long()
+    for b, src, dst in ((0, 103, 100), (0, 119, 101), (1, 2, 1)):
+        at = [int(table[b, p // page]) * page + p % page for p in (src, dst)]
+        assert torch.equal(rows[at[1]], before.view(-1, n_kv, D)[at[0]])
 
 
 # ------------------------------------------------------------------------------------------- trees

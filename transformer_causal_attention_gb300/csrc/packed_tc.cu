@@ -60,6 +60,7 @@ constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kLoDims = 64;  // dims with a second part of Q: a column block
+constexpr float kTiny = 7.888609e-31f;  // 2^-100, for a second part of nothing
 constexpr int kCare = 3;   // care tiles of a piece, at most: 256 tokens of a pair, or 128 drafts
 constexpr int kQueue = 6;  // pieces in the queue; kAhead are handed out before warp 3 treats the first of them
 constexpr int kAhead = 3;
@@ -275,7 +276,7 @@ __device__ __forceinline__ bool elect_one() {
 // heads_per heads, so that an angle is computed once for all of them; bound by HBM.  (Rotated by the softmax warps
 // of the attention kernel, where a query tile arrives with nothing to hide behind, it took 4 to 7 us per piece.)
 template <int D>
-__global__ void __launch_bounds__(256) packed_rotate_kernel(const __grid_constant__ PackedArgs a,
+__global__ void __launch_bounds__(256, 4) packed_rotate_kernel(const __grid_constant__ PackedArgs a,
                                                             const __grid_constant__ RopeFreq f, __nv_bfloat16* hi,
                                                             __nv_bfloat16* lo, int lo_dim, int heads_per) {
   asm volatile("griddepcontrol.launch_dependents;");  // the attention kernel starts, and waits where it reads these
@@ -318,37 +319,65 @@ __global__ void __launch_bounds__(256) packed_rotate_kernel(const __grid_constan
   uint4* const s = reinterpret_cast<uint4*>(lo) + row * (kLoDims / 8);
   const int lc = c - lo_dim / 8, partner = f.n_pairs / 8;
   const auto put = [&](int h, int at, const float* x) {  // chunk c + at
+    const bool two = static_cast<unsigned>(lc + at) < static_cast<unsigned>(kLoDims / 8);
+    // With a second part the first is cut off, not rounded, and the second never 0: both have the query's sign, so that an
+    // infinite key gives both products the same infinity.
     const uint4 y = f32_to_bf16x8(x);
-    o[h * kChunks + at] = y;
-    if (static_cast<unsigned>(lc + at) < static_cast<unsigned>(kLoDims / 8)) {
-      float z[8];
-      bf16x8_to_f32(y, z);
+    uint32_t cut[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = fabsf(z[e]) < INFINITY ? x[e] - z[e] : 0.f;  // 0 behind an infinity
+    for (int e = 0; e < 4; ++e) cut[e] = __byte_perm(__float_as_uint(x[2 * e]), __float_as_uint(x[2 * e + 1]), 0x7632);
+    o[h * kChunks + at] = two ? make_uint4(cut[0], cut[1], cut[2], cut[3]) : y;
+    if (two) {
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
+        // (behind an infinity or NaN the difference is NaN: not above 0 either)
+        z[e] = x[e] - v;
+        z[e] = fabsf(z[e]) > 0.f ? z[e] : copysignf(kTiny, x[e]);
+      }
       s[h * (kLoDims / 8) + lc + at] = f32_to_bf16x8(z);
     }
   };
+  constexpr int kFlight = 4;  // heads whose loads are in flight together
   if (in && f.half) {
-#pragma unroll 2
-    for (int h = 0; h < heads_per; ++h) {
-      float x[8], y[8];
-      bf16x8_to_f32(__ldg(q + h * kChunks), x);
-      bf16x8_to_f32(__ldg(q + h * kChunks + partner), y);
+    for (int h0 = 0; h0 < heads_per; h0 += kFlight) {
+      uint4 a0[kFlight], a1[kFlight];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], sn[e], cs[e]);
-      put(h, 0, x);
-      put(h, partner, y);
+      for (int k = 0; k < kFlight; ++k)
+        if (h0 + k < heads_per) {
+          a0[k] = __ldg(q + (h0 + k) * kChunks);
+          a1[k] = __ldg(q + (h0 + k) * kChunks + partner);
+        }
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k)
+        if (h0 + k < heads_per) {
+          float x[8], y[8];
+          bf16x8_to_f32(a0[k], x);
+          bf16x8_to_f32(a1[k], y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], sn[e], cs[e]);
+          put(h0 + k, 0, x);
+          put(h0 + k, partner, y);
+        }
     }
   } else {
-#pragma unroll 4
-    for (int h = 0; h < heads_per; ++h) {
-      float x[8];
-      bf16x8_to_f32(__ldg(q + h * kChunks), x);
-      if (in) {
+    for (int h0 = 0; h0 < heads_per; h0 += kFlight) {
+      uint4 a0[kFlight];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rotate_pair(x[2 * e], x[2 * e + 1], sn[e], cs[e]);
-      }
-      put(h, 0, x);
+      for (int k = 0; k < kFlight; ++k)
+        if (h0 + k < heads_per) a0[k] = __ldg(q + (h0 + k) * kChunks);
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k)
+        if (h0 + k < heads_per) {
+          float x[8];
+          bf16x8_to_f32(a0[k], x);
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rotate_pair(x[2 * e], x[2 * e + 1], sn[e], cs[e]);
+          }
+          put(h0 + k, 0, x);
+        }
     }
   }
 }
@@ -394,6 +423,19 @@ __device__ __forceinline__ void seen_tree(const uint32_t* w, int base, int klim,
 // LO: the weights of the last 64 keys come as the sum of two bf16 values, the second ones in columns 64 on.
 // (Short as it can be: all code that runs side by side in an SM has to fit its instruction cache, see the MMA issuer;
 // and no more registers than there are: spilled ones are more than the L1 beside 226 KB of shared memory holds.)
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16x2_down(float lo, float hi) {  // toward 0
+  uint32_t d;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 template <bool LO>
 __device__ __forceinline__ bool softmax_row(uint32_t s_addr, float scale_log2, float m_run, float& l_run) {
   uint32_t sr[2][16], pr[64], rest[LO ? 32 : 1];
@@ -414,19 +456,27 @@ __device__ __forceinline__ bool softmax_row(uint32_t s_addr, float scale_log2, f
       const float2 x = __ffma2_rn(y, sl2, nm2);
       const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
       acc[c & 1] = __fadd2_rn(acc[c & 1], pp);
-      pr[8 * q + c] = pack_bf16x2(pp.x, pp.y);
       if (LO && q >= 4) {
-        const float2 z = __ffma2_rn(make_float2(__uint_as_float(pr[8 * q + c] << 16), __uint_as_float(pr[8 * q + c] & 0xffff0000u)),
-                                    make_float2(-1.f, -1.f), pp);
+        // the first part cut off, and the second 2^-20 of the weight too large, never 0 or of the other sign: an infinite
+        // value then gives both products the same infinity
+        pr[8 * q + c] = pack_bf16x2_down(pp.x, pp.y);
+        const float2 z = __ffma2_rn(pp, make_float2(1.f + 0x1p-20f, 1.f + 0x1p-20f),
+                                    make_float2(__uint_as_float((pr[8 * q + c] << 16) | 0x80000000u),
+                                                __uint_as_float((pr[8 * q + c] & 0xffff0000u) | 0x80000000u)));
         rest[8 * (q - 4) + c] = pack_bf16x2(z.x, z.y);
+      } else {
+        pr[8 * q + c] = pack_bf16x2(pp.x, pp.y);
       }
     }
   }
   const float top = fmaxf(mx[0], mx[1]) * scale_log2;
   if (__any_sync(0xffffffffu, top > m_run + kRescaleThreshold)) return false;
-  tmem_st32(s_addr, pr);
-  tmem_st32(s_addr + 32, pr + 32);
-  if constexpr (LO) tmem_st32(s_addr + 64, rest);
+#pragma unroll
+  for (int c = 0; c < 64; c += 16) tmem_st16(s_addr + c, pr + c);
+  if constexpr (LO) {
+    tmem_st16(s_addr + 64, rest);
+    tmem_st16(s_addr + 80, rest + 16);
+  }
   acc[0] = __fadd2_rn(acc[0], acc[1]);
   l_run += acc[0].x + acc[0].y;
   return true;
@@ -1094,25 +1144,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // registers beside the scores, it is spilled)
       float m_run = -INFINITY, l_run = 0.f;
       {
-        const int care = u->care_t;
-        int t = sh.first;
-        for (int i = 0; i < sh.n; ++i, t += sh.step) {
+        // beside the scores and second parts there are no registers for these: they are read again where they are needed
+        constexpr bool kReload = C::kPLoSteps > 0;
+        const int care_t = u->care_t, first_t = sh.first;
+        const auto care = [&] { return kReload ? u->care_t : care_t; };
+        const auto first = [&] { return kReload ? Share(*u, w).first : first_t; };
+        int left = sh.n;
+        for (int t = sh.first; left > 0; --left, t += kReload ? (kind == kPair ? 1 : 2) : sh.step) {
           if (!row_wait(&bars->s_full[w], s_ph, wc)) { ok = false; break; }
           s_ph ^= 1u;
           tc_fence_after();
-          const bool masked = t >= care;
-          if (masked) {
+          if (t >= care()) {
             uint32_t mask[4];
             row_mask(a, pl, *u, w, my_tok, t * BN, mask);
-            const float2 ml = prepare_row<D>(s_addr, o_addr, true, make_uint4(mask[0], mask[1], mask[2], mask[3]), i > 0,
-                                             a.scale_log2, m_run, l_run);
+            const float2 ml = prepare_row<D>(s_addr, o_addr, true, make_uint4(mask[0], mask[1], mask[2], mask[3]),
+                                             t != first(), a.scale_log2, m_run, l_run);
             m_run = ml.x;
             l_run = ml.y;
-          } else if (i == 0) {
+          } else if (t == first()) {
             m_run = max_of_some(s_addr) * a.scale_log2;
           }
           if (!softmax_row<C::kPLoSteps != 0>(s_addr, a.scale_log2, m_run, l_run)) {
-            const float2 ml = prepare_row<D>(s_addr, o_addr, false, make_uint4(0u, 0u, 0u, 0u), i > 0, a.scale_log2, m_run, l_run);
+            const float2 ml = prepare_row<D>(s_addr, o_addr, false, make_uint4(0u, 0u, 0u, 0u), t != first(),
+                                             a.scale_log2, m_run, l_run);
             m_run = ml.x;
             l_run = softmax_row_again<C::kPLoSteps != 0>(s_addr, a.scale_log2, ml.x, ml.y);
           }
