@@ -191,6 +191,17 @@ def test_many_requests(lib):
     Step(news, ctxs, 4, 2, 64, base=1e4, dtype="f32").check(lib)
 
 
+def test_padded_batches(lib):
+    """Thousands of places without new tokens, with and without a cache, between a few that have some."""
+    news, ctxs = [0] * 2500, [0] * 2500
+    for b, n, c in ((0, 3, 0), (31, 40, 100), (32, 1, 5), (33, 70, 0), (1700, 129, 20), (2499, 2, 300)):
+        news[b], ctxs[b] = n, c
+    ctxs[40], ctxs[2000] = 500, 77
+    for n_h, n_kv, D, dtype in ((8, 2, 128, "bf16"), (4, 2, 64, "f32")):
+        for tree in (False, True):
+            Step(news, ctxs, n_h, n_kv, D, dtype=dtype, base=1e4, pad=4, tree=tree, words=4).check(lib)
+
+
 def test_decode_is_the_single_token_case(lib):
     s = Step([1] * 6, [0, 5, 127, 128, 400, 2000], 8, 2, 128, base=5e5)
     args = s.tensors()

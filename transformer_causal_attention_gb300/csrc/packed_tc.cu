@@ -211,16 +211,22 @@ struct Walk {
   bool live;
 };
 
-__device__ __forceinline__ void next_request(const PackedArgs& a, Walk& w) {
-  do ++w.b;
-  while (w.b < a.B && packed_request(a, w.b).rows == 0);
-  if (w.b >= a.B) w.live = false;
+// To the next request that has rows, 32 at a time: the warp's lanes all walk alike.
+__device__ __forceinline__ void next_request(const PackedArgs& a, Walk& w, int lane) {
   w.g = w.p = w.t = 0;
+  for (int b = w.b + 1; b < a.B; b += 32) {
+    const uint32_t some = __ballot_sync(0xffffffffu, b + lane < a.B && packed_request(a, b + lane).rows > 0);
+    if (some) {
+      w.b = b + __ffs(some) - 1;
+      return;
+    }
+  }
+  w.live = false;
 }
 
 // The next piece of a walk (kind kNone at its end).
-__device__ __noinline__ void next_piece(const PackedArgs& a, const PackedTcPlan& pl, Walk& w, Piece* out) {
-  out->kind = kNone;
+// All lanes have its kind, slot and place in the line; lane 0 writes it.
+__device__ __forceinline__ int next_piece(const PackedArgs& a, const PackedTcPlan& pl, Walk& w, Piece* out, int lane) {
   while (w.live && w.end > 0) {
     const Seg s(a, pl, w.b);
     const int p = w.p;
@@ -228,22 +234,24 @@ __device__ __noinline__ void next_piece(const PackedArgs& a, const PackedTcPlan&
     const int tok0 = p * 2 * s.tt, ntok = min(2 * s.tt, s.r.rows - tok0);
     const int klim = s.seen(p, ntok), kt = tiles_of(klim);
     const int t = w.t, t_end = tile_at(w.end, s.lead(p), s.shift(p), kt);
-    if (t < t_end) {
-      out->kind = pair ? kPair : kSingle;
-      out->g = w.g;
-      out->b = w.b;
-      out->row0 = s.r.first + tok0;
-      out->ntok = ntok;
-      out->t = t;
-      out->t_end = t_end;
-      out->kt = kt;
-      out->kt0 = pair ? tiles_of(s.seen(p, s.tt)) : kt;
-      out->place0 = s.r.base + tok0;
-      out->base = s.r.base;
-      out->klim = klim;
-      out->care_t = max(s.tree ? s.r.base : s.r.base + tok0 + 1, 0) / BN;
-      out->slot = t > 0 ? 0 : t_end < kt ? 1 : -1;
-      out->bad_any = 0;
+    if (t < t_end && lane == 0) {
+      Piece u;
+      u.kind = pair ? kPair : kSingle;
+      u.g = w.g;
+      u.b = w.b;
+      u.row0 = s.r.first + tok0;
+      u.ntok = ntok;
+      u.t = t;
+      u.t_end = t_end;
+      u.kt = kt;
+      u.kt0 = pair ? tiles_of(s.seen(p, s.tt)) : kt;
+      u.place0 = s.r.base + tok0;
+      u.base = s.r.base;
+      u.klim = klim;
+      u.care_t = max(s.tree ? s.r.base : s.r.base + tok0 + 1, 0) / BN;
+      u.slot = t > 0 ? 0 : t_end < kt ? 1 : -1;
+      u.bad_any = 0;
+      *out = u;
     }
     w.t = t_end;
     if (t_end < kt) {  // the part ends here
@@ -253,12 +261,14 @@ __device__ __noinline__ void next_piece(const PackedArgs& a, const PackedTcPlan&
       w.end -= s.length(p);
       if (++w.p == s.count()) {
         w.p = 0;
-        if (++w.g == a.n_kv) next_request(a, w);
+        if (++w.g == a.n_kv) next_request(a, w, lane);
       }
     }
-    if (t < t_end) return;
+    if (t < t_end) return pair ? kPair : kSingle;
   }
   w.live = false;
+  if (lane == 0) out->kind = kNone;
+  return kNone;
 }
 
 // One lane of a converged warp, which the compiler knows to be one: the MMA issuer's descriptors then stay in uniform
@@ -536,20 +546,22 @@ __device__ __noinline__ float softmax_row_again(uint32_t s_addr, float scale_log
   return l_run;
 }
 
-// The bits of what a row of worker w sees in the tile from key0 on; a row that is no query sees nothing.
-__device__ __noinline__ void row_mask(const PackedArgs& a, const PackedTcPlan& pl, const Piece& u, int w, int my_tok, int key0,
-                                    uint32_t* m) {
-  const int tok = (u.kind == kPair && w ? pl.tile_toks : 0) + my_tok;
-  const bool real = my_tok < pl.tile_toks && tok < u.ntok && u.place0 + tok >= 0;
-  if (a.visible == nullptr || !real) {
-    seen_below(real ? u.place0 + tok + 1 : 0, key0, m);
-    return;
-  }
-  uint32_t bits[4];
-  const int* const row = a.visible + static_cast<long long>(u.row0 + tok) * a.words;
+// The bits of what a row of worker w sees in the tile from key0 on; a row that is no query sees nothing.  (Out of line, and
+// so with the kernel's arguments by value: through a reference they are read like global memory.)
+__device__ __noinline__ uint4 row_mask(const int* visible, int words, int tile_toks, const Piece* u, int w, int my_tok, int key0) {
+  uint32_t m[4];
+  const int tok = (u->kind == kPair && w ? tile_toks : 0) + my_tok;
+  const bool real = my_tok < tile_toks && tok < u->ntok && u->place0 + tok >= 0;
+  if (visible == nullptr || !real) {
+    seen_below(real ? u->place0 + tok + 1 : 0, key0, m);
+  } else {
+    uint32_t bits[4];
+    const int* const row = visible + static_cast<long long>(u->row0 + tok) * words;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bits[i] = i < a.words ? static_cast<uint32_t>(row[i]) : 0u;
-  seen_tree(bits, u.base, u.klim, key0, m);
+    for (int i = 0; i < 4; ++i) bits[i] = i < words ? static_cast<uint32_t>(row[i]) : 0u;
+    seen_tree(bits, u->base, u->klim, key0, m);
+  }
+  return make_uint4(m[0], m[1], m[2], m[3]);
 }
 
 // The values that are not finite in care tiles, of dims [c0, c1), added to what has been stored of a row that sees them.
@@ -559,8 +571,8 @@ __device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl
     const int key0 = (u.care_t + i) * BN;
     if (u.care_t + i >= u.t_end) break;
     if (u.care_t + i < u.t) continue;
-    uint32_t m[4];
-    row_mask(a, pl, u, w, my_tok, key0, m);
+    const uint4 seen = row_mask(a.visible, a.words, pl.tile_toks, &u, w, my_tok, key0);
+    const uint32_t m[4] = {seen.x, seen.y, seen.z, seen.w};
     for (int j = 0; j < 4; ++j) {
       for (uint32_t left = u.bad[i][j] & m[j]; left; left &= left - 1) {
         const int key = key0 + 32 * j + __ffs(left) - 1;
@@ -1049,17 +1061,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; !last && n_pub < n + kAhead; ++n_pub) {
           const uint32_t e = n_pub % kQueue;
           if (n_pub >= kQueue && !(ok = warp_wait(&bars->piece_empty[e], (n_pub / kQueue - 1) & 1u, wc))) break;
+          Piece* const u = &bars->piece[e];
+          const int kind = next_piece(a, pl, walk, u, lane);
+          last = kind == kNone;
           if (lane == 0) {
-            Piece* const u = &bars->piece[e];
-            next_piece(a, pl, walk, u);
-            if (u->kind != kNone && u->slot >= 0) {
+            if (!last && u->slot >= 0) {
               rec[u->slot] = Record{u->kind, u->g, u->row0, u->ntok, u->t, u->t_end, u->kt, 0};
               recs |= 1u << u->slot;
             }
-            last = u->kind == kNone;
             mbar_arrive(&bars->piece_full[e]);
           }
-          last = __shfl_sync(0xffffffffu, last ? 1 : 0, 0) != 0;
+          __syncwarp();
         }
         if (!ok) break;
         __syncwarp();
@@ -1155,10 +1167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_ph ^= 1u;
           tc_fence_after();
           if (t >= care()) {
-            uint32_t mask[4];
-            row_mask(a, pl, *u, w, my_tok, t * BN, mask);
-            const float2 ml = prepare_row<D>(s_addr, o_addr, true, make_uint4(mask[0], mask[1], mask[2], mask[3]),
-                                             t != first(), a.scale_log2, m_run, l_run);
+            const uint4 mask = row_mask(a.visible, a.words, pl.tile_toks, u, w, my_tok, t * BN);
+            const float2 ml = prepare_row<D>(s_addr, o_addr, true, mask, t != first(), a.scale_log2, m_run, l_run);
             m_run = ml.x;
             l_run = ml.y;
           } else if (t == first()) {
