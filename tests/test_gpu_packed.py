@@ -377,6 +377,19 @@ def test_scores_far_apart(lib):
         s.check(lib)
 
 
+@pytest.mark.parametrize("n_h", [1 << 22, (1 << 22) + 3])
+def test_heads_of_more_than_two_to_the_31_elements(lib, n_h):
+    """One KV head whose query heads' outputs pass 32 bits in a row: a token, and a row behind the last."""
+    D_v = 512
+    q = torch.zeros(2, n_h, 8, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(1, 16, 1, 8, dtype=torch.bfloat16, device=DEV)
+    v = torch.randn(1, 16, 1, D_v, dtype=torch.bfloat16, device=DEV)
+    out = torch.full((2, n_h, D_v), float("nan"), dtype=torch.bfloat16, device=DEV)
+    _, lse = lib.prefill_paged(q, k, v, ints([[0]]), ints([0, 1]), ints([1]), out=out, lse=True)
+    assert (out[0] == v[0, 0, 0]).all() and not lse[0].any()  # the one key's value, score 0
+    assert not out[1].any() and torch.isneginf(lse[1]).all()
+
+
 def test_caches_of_more_than_two_to_the_31_elements(lib):
     """Pages at the end of a cache whose offsets pass 32 bits, attended and committed to."""
     n_pages, page, n_kv, D = 33000, 64, 8, 128

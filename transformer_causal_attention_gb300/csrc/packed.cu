@@ -64,13 +64,13 @@ template <typename T>
 __device__ __forceinline__ Tile find_tile(const PackedArgs& a, long long number, int n_split) {
   const int tid = threadIdx.x, G = a.n_h / a.n_kv, g = blockIdx.y, split = blockIdx.z;
   if (split == 0) {
-    const long long from = static_cast<long long>(packed_first(a, a.B)) * G * a.D_v, to = static_cast<long long>(a.T) * G * a.D_v;
+    const long long per = static_cast<long long>(G) * a.D_v;  // of a KV head and row
+    const long long from = packed_first(a, a.B) * per, to = a.T * per;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     for (long long i = from + 4LL * (number * kThreads + tid); i < to; i += 4LL * gridDim.x * kThreads) {
-      const long long row = i / (G * a.D_v);
-      const int at = static_cast<int>(i - row * (G * a.D_v));
-      store4(static_cast<T*>(a.out) + (row * a.n_h + g * G) * a.D_v + at, zero);
-      if (a.lse != nullptr && at % a.D_v == 0) a.lse[row * a.n_h + g * G + at / a.D_v] = -INFINITY;
+      const long long row = i / per, at = i - row * per, head = row * a.n_h + static_cast<long long>(g) * G;
+      store4(static_cast<T*>(a.out) + head * a.D_v + at, zero);
+      if (a.lse != nullptr && at % a.D_v == 0) a.lse[head + at / a.D_v] = -INFINITY;
     }
   }
   Tile t;

@@ -659,6 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // no room is left for aligning it here
     if (threadIdx.x == 0) atomicOr(a.status, STATUS_LAYOUT);
+    if (threadIdx.x < 2)  // nothing to join
+      (reinterpret_cast<Record*>(static_cast<float*>(a.workspace) + pl.rec) + 2 * blockIdx.x)[threadIdx.x] = Record{0, 0, 0, 0, 0, 0, 0, 0};
     return;
   }
   Bars<C>* bars = reinterpret_cast<Bars<C>*>(smem + C::kBarOff);
