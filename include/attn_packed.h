@@ -60,11 +60,16 @@ ATTN_API size_t attn_packed_workspace_size(int T, int B, int n_h, int n_kv, int 
  * span of whole 16-byte pieces (none, or rope_offset % 8 == 0 and rope_dims % 8 == 0,
  * % 16 with ATTN_ROPE_HALF) runs on the tensor cores, anything else on CUDA cores.
  * Sums are fp32.  On the tensor cores softmax weights are rounded to bf16 on the way
- * in, rotated queries to bf16 with what that leaves kept for five eighths of the
- * dims (three quarters of 64), so that an output's error is at most 1.46 times that of its own
- * rounding (for normally distributed inputs).  NaN or an infinity in a query, key or
- * value reaches the rows that see it and no other: values at places that a row does
- * not see, of other requests or behind the last token may be anything.
+ * in, and so are rotated queries, but for what that leaves of 64 of their dims and, with
+ * D = 128, of half of the weights, which is kept: an output's error is about 1.45 times
+ * that of its own rounding (for normally distributed inputs).
+ * NaN or an infinity in a query, key or value reaches the rows that see it and no
+ * other: values at places that a row does not see, of other requests or behind the last
+ * token may be anything.  A key with a score of -inf has no weight, a row whose scores
+ * all are comes out as one that sees no key, a score of +inf makes its row NaN, and so
+ * does an infinite value whose weight is 0.
+ * The workspace of shapes that the tensor cores take holds T * n_h * (D + 64) * 2 bytes
+ * for the rotated queries, beside the partials of the pieces that requests are cut into.
  * Outputs must not overlap inputs, the workspace or each other.
  */
 ATTN_API int attn_prefill_paged(const void* q, const void* k_pages, const void* v_pages, int v_token_stride,

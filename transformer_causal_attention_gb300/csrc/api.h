@@ -1,4 +1,4 @@
-// api.h - host helpers shared by the exported entry points (api.cu, api_paged.cu):
+// api.h - host helpers shared by the exported entry points (api.cu, api_paged.cu, api_packed.cu):
 // per-device facts, argument checks, the RoPE table, tensor maps and the launch
 // counter.  Defined in api.cu; nothing here is exported.
 #pragma once

@@ -17,22 +17,32 @@
 // a segment: these leave a normalised partial and its log-sum-exp, which a second kernel joins; all other
 // pieces write their rows of the output.
 //
-// Rounding.  Weights are rounded to bf16.  A rotated query is kept as the sum of two bf16 values, the
-// second for kLoSteps of the D / 16 MMA steps (from the start of the rotated span on): one bf16 alone made the
-// output's error 1.5 times that of its own rounding behind 2000 keys and 1.7 times behind 30000 (normally
-// distributed inputs, against 64 bits), with five of eight steps it is at most 1.46 times.  The second part's
-// MMAs use the K tile that is there anyway.  It is kept unswizzled, 16 bytes of a row after the other row's.
+// Rounding.  Sums and softmax statistics are fp32.  With RoPE a query is rotated by a kernel before and kept as the sum of
+// two bf16 values, the second for 64 dims (from the start of the rotated span on), and with D = 128 the weights of
+// each tile's last 64 keys are such sums too; the other weights are rounded to bf16 once.  One bf16 for both made the output's
+// error against 64 bits 1.7 times that of its own rounding behind 30000 keys (normally distributed inputs); so it is
+// 1.41 to 1.44 times.  That is half as many MMAs again with D = 128, and a quarter with D = 64, on the K and V
+// tiles that are there anyway (4 x 8192 tokens, 32 heads over 8: 2.0 ms; without RoPE, with weights rounded once, 1.44 ms).
 //
 // What a row does not see.  Scores are masked by index.  A value whose weight is 0 still meets the MMA, so in
 // the tiles that some row sees in part ("care" tiles: the last ones of a segment) warp 3 clears value rows
 // behind the last key and replaces infinities and NaN by 0, noting their keys; the epilogue adds such
 // values to the rows that do see them.  The rest of the tiles is seen whole by every row.
 //
-// A CTA (384 threads): warp 0 loads K tiles by TMA, warp 2 query rows and V (in quarters of 32 keys, so that
-// the shared memory left by both parts of Q holds 1.75 V tiles), a lane per box; warp 1 issues the MMAs; warp 3
+// A CTA (384 threads): warp 0 loads K tiles by TMA, warp 2 query rows and V tiles, a lane per box (two stages of
+// each fill what shared memory both parts of two query tiles leave); warp 1 issues the MMAs; warp 3
 // walks the line, hands the pieces out through a queue in shared memory and treats care tiles; warps
 // 4-7 and 8-11 are the softmax of row tiles 0 and 1 (or of alternate key tiles), a row per thread.
 // TMEM: S/P of the two in columns [0, 128) and [128, 256), O behind them.
+//
+// Bounds.  Long prompts: the tensor pipe (1 x 8192 tokens, 32 heads over 8, D = 128, RoPE: its counter is active 83% of
+// the time; a turn of a pair piece - two row tiles, 128 keys - is 3072 cycles of MMA and takes 3500 to 3600).  4 x 8192:
+// 2.0 ms, 1.1 PFLOP/s as the formula counts and 1.65 as issued.  Drafts behind long caches: HBM (59 requests of 32
+// drafts behind 4096 to 8192 tokens: 1.53 GB read in 250 us, 6.2 TB/s).  Few short requests: the chain launch, walk, TMA,
+// MMA, softmax, MMA, store, and a join (one prompt of 100 tokens 15 us).  What limits beside these is instruction fetch:
+// five programs run side by side on an SM, and their hot loops have to fit its instruction cache together, so loops stay
+// rolled, rare code is out of line, and a start or end of a piece (some 11000 to 14000 cycles beside its turns) costs more
+// in cold code than in work.
 #include <math.h>
 
 #include <atomic>
