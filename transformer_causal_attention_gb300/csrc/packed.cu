@@ -58,23 +58,35 @@ struct Tile {
   long long row0;
   int k_lo, k_hi;
   int first_place;  // of its first row, -1 or more
+  bool whole;       // one part: the rows go to the output
 };
-// Finds a block's tile (here = 0: none), and clears its share of the rows behind the last request's.
+// Keys that a tile's last row may see, and keys in each of its parts.
+__device__ __forceinline__ int keys_of(const PackedArgs& a, const PackedRequest& rq, long long last_row, int G) {
+  const int last = rq.base + static_cast<int>(last_row / G);
+  return a.visible != nullptr ? rq.len : min(max(last, -1) + 1, rq.len);
+}
+__device__ __forceinline__ int part_of(int keys, int n_split) {
+  const int part = static_cast<int>((static_cast<long long>(keys) + n_split - 1) / n_split);
+  return max((part + KT - 1) / KT, 1) * KT;
+}
+// Finds a block's tile and part (here = 0: none), and clears its share of the rows behind the last request's.  Blocks
+// count from the last tile, which sees the most keys of its request, the KV heads of a tile side by side.
 template <typename T>
-__device__ __forceinline__ Tile find_tile(const PackedArgs& a, long long number, int n_split) {
-  const int tid = threadIdx.x, G = a.n_h / a.n_kv, g = blockIdx.y, split = blockIdx.z;
+__device__ __forceinline__ Tile find_tile(const PackedArgs& a, int g, int n_split) {
+  const int tid = threadIdx.x, G = a.n_h / a.n_kv, split = blockIdx.y;
+  const long long numbers = gridDim.x / a.n_kv, number = numbers - 1 - blockIdx.x / a.n_kv;
   if (split == 0) {
     const long long per = static_cast<long long>(G) * a.D_v;  // of a KV head and row
     const long long from = packed_first(a, a.B) * per, to = a.T * per;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    for (long long i = from + 4LL * (number * kThreads + tid); i < to; i += 4LL * gridDim.x * kThreads) {
+    for (long long i = from + 4LL * (number * kThreads + tid); i < to; i += 4LL * numbers * kThreads) {
       const long long row = i / per, at = i - row * per, head = row * a.n_h + static_cast<long long>(g) * G;
       store4(static_cast<T*>(a.out) + head * a.D_v + at, zero);
       if (a.lse != nullptr && at % a.D_v == 0) a.lse[head + at / a.D_v] = -INFINITY;
     }
   }
   Tile t;
-  int lo = 0, hi = a.B - 1;  // the last request whose numbers start at or before this one
+  int lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (tile_start(a, mid, G) <= number) lo = mid;
@@ -86,25 +98,31 @@ __device__ __forceinline__ Tile find_tile(const PackedArgs& a, long long number,
   const long long n_rows = static_cast<long long>(t.rq.rows) * G;
   t.here = t.row0 < 0 || t.row0 >= n_rows ? 0 : static_cast<int>(n_rows - t.row0 < R ? n_rows - t.row0 : R);
   if (t.here == 0) return t;
-  // the keys that the tile's last row may see, and this split's part of them
-  const int last = t.rq.base + static_cast<int>((t.row0 + t.here - 1) / G);
-  const int keys = a.visible != nullptr ? t.rq.len : min(max(last, -1) + 1, t.rq.len);
-  int part = (keys + n_split - 1) / n_split;
-  part = (part + KT - 1) / KT * KT;
+  const int keys = keys_of(a, t.rq, t.row0 + t.here - 1, G), part = part_of(keys, n_split);
   const long long k_lo = static_cast<long long>(split) * part;
+  if (k_lo >= keys && split > 0) t.here = 0;
+  t.whole = keys <= part;
   t.k_hi = static_cast<int>(k_lo + part < keys ? k_lo + part : keys);
-  t.k_lo = static_cast<int>(k_lo < t.k_hi ? k_lo : t.k_hi);  // part of 0 keys: none
+  t.k_lo = static_cast<int>(k_lo < t.k_hi ? k_lo : t.k_hi);
   t.first_place = max(t.rq.base + static_cast<int>(t.row0 / G), -1);
   return t;
 }
-// What a row sees of the tile: its place (-1: nothing) and bits.
-__device__ __forceinline__ void load_row(const PackedArgs& a, const Tile& t, int r, int* place, uint32_t* vis) {
-  *place = -1;
+// A row of the tile: which (token, head) of q and out it is, the position at which it is rotated, and what it sees - its
+// place (-1: nothing, and no rotation) and bits.  (Once per row: divisions by G at each use were a third of a tile's time.)
+struct Rows {
+  int at[R], pos[R], place[R];
+  uint32_t vis[R][4];
+};
+__device__ __forceinline__ void load_row(const PackedArgs& a, const Tile& t, int g, int r, Rows* rows) {
+  rows->place[r] = -1;
   if (r >= t.here) return;
-  const int i = static_cast<int>((t.row0 + r) / (a.n_h / a.n_kv)), row = t.rq.first + i;
-  *place = t.rq.base + i;
-  if (a.positions != nullptr && a.positions[row] < 0) *place = -1;
-  for (int w = 0; w < 4; ++w) vis[w] = w < a.words ? static_cast<uint32_t>(a.visible[static_cast<long long>(row) * a.words + w]) : 0u;
+  const int G = a.n_h / a.n_kv;
+  const int i = static_cast<int>((t.row0 + r) / G), row = t.rq.first + i;
+  rows->at[r] = row * a.n_h + g * G + static_cast<int>(t.row0 + r - static_cast<long long>(i) * G);
+  const int place = t.rq.base + i, pos = a.positions != nullptr ? a.positions[row] : place;
+  rows->pos[r] = pos;
+  rows->place[r] = pos < 0 ? -1 : place;
+  for (int w = 0; w < 4; ++w) rows->vis[r][w] = w < a.words ? static_cast<uint32_t>(a.visible[static_cast<long long>(row) * a.words + w]) : 0u;
 }
 __device__ __forceinline__ bool sees(const PackedArgs& a, const Tile& t, int place, const uint32_t* vis, int key) {
   if (a.visible == nullptr) return key < t.k_hi && key <= place;
@@ -122,22 +140,19 @@ __device__ __forceinline__ long long slot_of(const PackedArgs& a, const int* tab
   if (page < 0 || page >= a.n_pages) return -1;
   return (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
 }
-// Row r's output dims d .. d + 3 (normalised) and, for put_lse, its log-sum-exp: to the output, or to this split's part.
+// Dims d .. d + 3 of the output row `at` (normalised) and, for put_lse, its log-sum-exp: to the output, or to this part's
+// scratch.
 template <typename T>
-__device__ __forceinline__ void put_row(const PackedArgs& a, const Tile& t, int r, int d, const float* o, int n_split) {
-  const int G = a.n_h / a.n_kv;
-  const long long row = t.row0 + r, at = (t.rq.first + row / G) * a.n_h + blockIdx.y * G + row % G;
-  if (n_split == 1) store4(static_cast<T*>(a.out) + at * a.D_v + d, o);
-  else store4(static_cast<float*>(a.workspace) + (static_cast<long long>(blockIdx.z) * a.T * a.n_h + at) * a.D_v + d, o);
+__device__ __forceinline__ void put_row(const PackedArgs& a, bool whole, long long at, int d, const float* o) {
+  if (whole) store4(static_cast<T*>(a.out) + at * a.D_v + d, o);
+  else store4(static_cast<float*>(a.workspace) + (static_cast<long long>(blockIdx.y) * a.T * a.n_h + at) * a.D_v + d, o);
 }
-__device__ __forceinline__ void put_lse(const PackedArgs& a, const Tile& t, int r, float lse2, int n_split) {
-  const int G = a.n_h / a.n_kv;
-  const long long row = t.row0 + r, at = (t.rq.first + row / G) * a.n_h + blockIdx.y * G + row % G;
-  if (n_split == 1) {
+__device__ __forceinline__ void put_lse(const PackedArgs& a, bool whole, long long at, float lse2, int n_split) {
+  if (whole) {
     if (a.lse != nullptr) a.lse[at] = lse2 * 0.69314718055994530942f;
   } else {
     static_cast<float*>(a.workspace)[static_cast<long long>(n_split) * a.T * a.n_h * a.D_v +
-                                     static_cast<long long>(blockIdx.z) * a.T * a.n_h + at] = lse2;
+                                     static_cast<long long>(blockIdx.y) * a.T * a.n_h + at] = lse2;
   }
 }
 
@@ -148,9 +163,10 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool there)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void copy_wait_all_but_last() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-template <int NV>
+template <int NV, int ST>
 __global__ void __launch_bounds__(kThreads, 2)
     packed_f32_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ RopeFreq f, int n_split) {
   extern __shared__ float4 smem4[];
@@ -158,58 +174,59 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int QLD = a.D_qk + (a.D_qk % 32 ? 36 - a.D_qk % 32 : 4);  // 4 behind a multiple of 32
   float* const Qs = reinterpret_cast<float*>(smem4);
   float* const Ks = Qs + R * QLD;
-  float* const Vs = Ks + KT * QLD;
-  float* const Ps = Vs + KT * VLD;  // [R][LD]
+  float* const Vs = Ks + ST * KT * QLD;
+  float* const Ps = Vs + ST * KT * VLD;  // [R][LD]; a warp reads what it wrote itself
   __shared__ long long slot[2][KT];
-  __shared__ uint32_t vis[R][4];
-  __shared__ int row_place[R];
+  __shared__ Rows rows;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int G = a.n_h / a.n_kv, g = blockIdx.y;
-  // the last tiles, which see the most keys, first
-  const Tile t = find_tile<float>(a, static_cast<long long>(gridDim.x) - 1 - blockIdx.x, n_split);
+  const int g = blockIdx.x % a.n_kv;
+  const Tile t = find_tile<float>(a, g, n_split);
   if (t.here == 0) return;
   const int* const table = a.block_table + static_cast<long long>(t.b) * a.max_blocks;
   const float* const kp = static_cast<const float*>(a.k_pages) + g * a.D_qk;
   const float* const vp = static_cast<const float*>(a.v_pages) + g * a.D_v;
   const int kc = a.D_qk / 4, vc = a.D_v / 4;
+  const long long k_row = static_cast<long long>(a.n_kv) * a.D_qk;
+  // 16-byte pieces of 64 keys, a thread's first one and the step to its next (no divisions in the loop over tiles)
+  const int k_key = tid / kc, k_c = tid - k_key * kc, k_step = kThreads / kc, k_rest = kThreads - k_step * kc;
+  const int v_key = tid / vc, v_c = tid - v_key * vc, v_step = kThreads / vc, v_rest = kThreads - v_step * vc;
   const auto fetch_k = [&](int s) {
-    for (int i = tid; i < KT * kc; i += kThreads) {
-      const int key = i / kc, c = i - key * kc;
+    for (int key = k_key, c = k_c; key < KT;) {
       const long long at = slot[s][key];
-      copy16(Ks + key * QLD + c * 4, kp + (at < 0 ? 0 : at) * a.n_kv * a.D_qk + c * 4, at >= 0);
+      copy16(Ks + ((ST - 1) * s * KT + key) * QLD + c * 4, kp + (at < 0 ? 0 : at) * k_row + c * 4, at >= 0);
+      key += k_step;
+      if ((c += k_rest) >= kc) c -= kc, ++key;
     }
     copy_commit();
   };
   const auto fetch_v = [&](int s) {
-    for (int i = tid; i < KT * vc; i += kThreads) {
-      const int key = i / vc, c = i - key * vc;
+    for (int key = v_key, c = v_c; key < KT;) {
       const long long at = slot[s][key];
-      copy16(Vs + key * VLD + c * 4, vp + (at < 0 ? 0 : at) * a.v_token_stride + c * 4, at >= 0);
+      copy16(Vs + ((ST - 1) * s * KT + key) * VLD + c * 4, vp + (at < 0 ? 0 : at) * a.v_token_stride + c * 4, at >= 0);
+      key += v_step;
+      if ((c += v_rest) >= vc) c -= vc, ++key;
     }
     copy_commit();
   };
   if (tid < 2 * KT) slot[tid >> 6][tid & 63] = slot_of(a, table, t.k_lo + tid, t.k_hi);
-  if (tid < R) load_row(a, t, tid, &row_place[tid], vis[tid]);
-  for (int i = tid; i < R * kc; i += kThreads) {
-    const int r = i / kc, c = i - r * kc;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < t.here) {
-      const long long row = t.row0 + r;
-      x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + ((t.rq.first + row / G) * a.n_h + g * G + row % G) * a.D_qk + c * 4);
-    }
-    *reinterpret_cast<float4*>(Qs + r * QLD + c * 4) = x;
-  }
-  for (int i = tid; i < KT * (NV * 16 - vc); i += kThreads) {  // value dims behind the last stay 0
+  if (tid < R) load_row(a, t, g, tid, &rows);
+  for (int i = tid; i < ST * KT * (NV * 16 - vc); i += kThreads) {  // value dims behind the last stay 0
     const int n = NV * 16 - vc, key = i / n;
     *reinterpret_cast<float4*>(Vs + key * VLD + (vc + i - key * n) * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
   fetch_k(0);
   fetch_v(0);
+  for (int r = k_key, c = k_c; r < R;) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < t.here) x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + static_cast<long long>(rows.at[r]) * a.D_qk + c * 4);
+    *reinterpret_cast<float4*>(Qs + r * QLD + c * 4) = x;
+    r += k_step;
+    if ((c += k_rest) >= kc) c -= kc, ++r;
+  }
+  if (f.n_pairs) __syncthreads();
   for (int i = tid; i < t.here * f.n_pairs; i += kThreads) {
-    const int r = i / f.n_pairs, p = i - r * f.n_pairs;
-    const int row = t.rq.first + static_cast<int>((t.row0 + r) / G);
-    const int pos = a.positions != nullptr ? a.positions[row] : t.rq.base + static_cast<int>((t.row0 + r) / G);
+    const int r = i / f.n_pairs, p = i - r * f.n_pairs, pos = rows.pos[r];
     if (pos < 0) continue;
     float sn, cs;
     with_angles<true, false>(pos, [&](auto angle) { angle(f.hi[p], f.lo[p], &sn, &cs); });
@@ -228,8 +245,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   const bool active = (tid >> 5) * 8 < t.here;  // this warp has rows (eight of them)
   int cur = 0;
   for (int k0 = t.k_lo; k0 < t.k_hi; k0 += KT, cur ^= 1) {  // k_hi <= 2^31 - 2^16: no overflow
-    copy_wait_all_but_last();
-    __syncthreads();  // K, and before the first tile Q, are there
+    if constexpr (ST == 2) copy_wait_all();
+    else copy_wait_all_but_last();
+    __syncthreads();  // K (two stages: and V), and before the first tile Q, are there; the stage before is free
+    long long next_slot = -1;  // of the tile behind the next one, which takes this one's place
+    const auto look = [&] {
+      const long long next = static_cast<long long>(k0) + 2 * KT + tid;
+      if (tid < KT && next < t.k_hi) next_slot = slot_of(a, table, static_cast<int>(next), t.k_hi);
+    };
+    if (ST == 2) look();
+    if (ST == 2 && k0 + KT < t.k_hi) {
+      fetch_k(cur ^ 1);
+      fetch_v(cur ^ 1);
+    }
+    const float* const Kt = Ks + (ST - 1) * cur * KT * QLD;
+    const float* const Vt = Vs + (ST - 1) * cur * KT * VLD;
     float2 s2[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -241,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) q4[i] = *reinterpret_cast<const float4*>(Qs + (ty * 4 + i) * QLD + d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * j) * QLD + d);
+      for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4*>(Kt + (tx + 16 * j) * QLD + d);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -250,8 +280,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           s2[i][j] = __ffma2_rn(make_float2(q4[i].z, q4[i].w), make_float2(k4[j].z, k4[j].w), s2[i][j]);
         }
     }
-    __syncthreads();
-    fetch_k(cur ^ 1);
+    if constexpr (ST == 1) {
+      __syncthreads();
+      fetch_k(cur ^ 1);
+    }
     const bool masked = partly_seen(a, t, k0);
     if (active) {
 #pragma unroll
@@ -262,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           s[j] = (s2[i][j].x + s2[i][j].y) * a.scale_log2;
-          seen[j] = !masked || sees(a, t, row_place[r], vis[r], k0 + tx + 16 * j);
+          seen[j] = !masked || sees(a, t, rows.place[r], rows.vis[r], k0 + tx + 16 * j);
           if (seen[j]) mx = fmaxf(mx, s[j]);
         }
 #pragma unroll
@@ -287,11 +319,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
       }
     }
-    // the slots of the tile behind the next one take this one's place
-    const long long next = static_cast<long long>(k0) + 2 * KT + tid;
-    const long long next_slot = tid < KT && next < t.k_hi ? slot_of(a, table, static_cast<int>(next), t.k_hi) : -1;
-    copy_wait_all_but_last();
-    __syncthreads();  // V and P are there
+    if constexpr (ST == 1) {
+      look();
+      copy_wait_all_but_last();
+      __syncthreads();  // V and P are there
+    } else {
+      __syncwarp();
+    }
     const auto add = [&](auto with_mask) {
 #pragma unroll 2
       for (int k = 0; k < KT; k += 4) {
@@ -305,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
-            const float4 x = *reinterpret_cast<const float4*>(Vs + (k + kk) * VLD + v * 64 + tx * 4);
+            const float4 x = *reinterpret_cast<const float4*>(Vt + (k + kk) * VLD + v * 64 + tx * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // a value that the row does not see may be anything
@@ -321,8 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (masked) add([] { return true; });
       else add([] { return false; });
     }
-    __syncthreads();
-    fetch_v(cur ^ 1);
+    if constexpr (ST == 1) {
+      __syncthreads();
+      fetch_v(cur ^ 1);
+    }
     if (tid < KT) slot[cur][tid] = next_slot;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -332,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
     if (r >= t.here) continue;
-    if (row_place[r] < 0) l[i] = 0.f;  // an empty row: tiles that are seen whole do not ask
+    if (rows.place[r] < 0) l[i] = 0.f;  // an empty row: tiles that are seen whole do not ask
     const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];  // 0: no key with a weight; NaN stays
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -340,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (d >= a.D_v) continue;
       float o[4] = {acc[v][i][0].x * inv, acc[v][i][0].y * inv, acc[v][i][1].x * inv, acc[v][i][1].y * inv};
       if (l[i] == 0.f) o[0] = o[1] = o[2] = o[3] = 0.f;
-      put_row<float>(a, t, r, d, o, n_split);
+      put_row<float>(a, t.whole, rows.at[r], d, o);
     }
-    if (tx == 0) put_lse(a, t, r, l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
+    if (tx == 0) put_lse(a, t.whole, rows.at[r], l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
   }
 }
 
@@ -355,30 +391,25 @@ __global__ void __launch_bounds__(kThreads)
   float* const Ks = Qs + a.D_qk * LD;                 // [DC][LD], then V: [KT][LD]
   float* const Ps = Ks + KT * LD;                     // [KT keys][LD rows]
   __shared__ long long slot[KT];                      // slots of the tile's keys, -1: none
-  __shared__ uint32_t vis[R][4];
-  __shared__ int row_place[R];                        // -1: the row is empty or not there
+  __shared__ Rows rows;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int G = a.n_h / a.n_kv, g = blockIdx.y;
-  const Tile t = find_tile<T>(a, blockIdx.x, n_split);
+  const int g = blockIdx.x % a.n_kv;
+  const Tile t = find_tile<T>(a, g, n_split);
   if (t.here == 0) return;
   const int* const table = a.block_table + static_cast<long long>(t.b) * a.max_blocks;
-  if (tid < R) load_row(a, t, tid, &row_place[tid], vis[tid]);
+  if (tid < R) load_row(a, t, g, tid, &rows);
+  __syncthreads();
   for (int i = tid; i < R * (a.D_qk / 8); i += kThreads) {
     const int r = i & (R - 1), d = (i >> 6) * 8;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (r < t.here) {
-      const long long row = t.row0 + r;
-      load8(static_cast<const T*>(a.q) + ((t.rq.first + row / G) * a.n_h + g * G + row % G) * a.D_qk + d, x);
-    }
+    if (r < t.here) load8(static_cast<const T*>(a.q) + static_cast<long long>(rows.at[r]) * a.D_qk + d, x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) Qs[(d + e) * LD + r] = x[e];
   }
   __syncthreads();
   if (f.n_pairs) {
     for (int i = tid; i < t.here * f.n_pairs; i += kThreads) {
-      const int r = i % t.here, p = i / t.here;
-      const int row = t.rq.first + static_cast<int>((t.row0 + r) / G);
-      const int pos = a.positions != nullptr ? a.positions[row] : t.rq.base + static_cast<int>((t.row0 + r) / G);
+      const int r = i % t.here, p = i / t.here, pos = rows.pos[r];
       if (pos < 0) continue;
       float sn, cs;
       with_angles<true, false>(pos, [&](auto angle) { angle(f.hi[p], f.lo[p], &sn, &cs); });
@@ -430,12 +461,12 @@ __global__ void __launch_bounds__(kThreads)
     const bool masked = partly_seen(a, t, k0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i, place = row_place[r];
+      const int r = ty * 4 + i, place = rows.place[r];
       bool seen[4];
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        seen[j] = sees(a, t, place, vis[r], k0 + tx * 4 + j);
+        seen[j] = sees(a, t, place, rows.vis[r], k0 + tx * 4 + j);
         s[i][j] *= a.scale_log2;
         if (seen[j]) mx = fmaxf(mx, s[i][j]);
       }
@@ -507,13 +538,13 @@ __global__ void __launch_bounds__(kThreads)
       float o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = l[i] == 0.f ? 0.f : acc[v][i][j] * inv;
-      put_row<T>(a, t, r, d, o, n_split);
+      put_row<T>(a, t.whole, rows.at[r], d, o);
     }
-    if (tx == 0) put_lse(a, t, r, l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
+    if (tx == 0) put_lse(a, t.whole, rows.at[r], l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
   }
 }
 
-// A warp per row: out = sum_j 2^(lse_j - lse) out_j over the splits.
+// A warp per row whose keys were cut: out = sum_j 2^(lse_j - lse) out_j over the parts.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_constant__ PackedArgs a, int n_split) {
   const int lane = threadIdx.x & 31;
@@ -522,14 +553,28 @@ __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_c
   if (at >= rows || at >= static_cast<long long>(packed_first(a, a.B)) * a.n_h) return;  // those behind are written
   const float* const ws = static_cast<const float*>(a.workspace);
   const float* const lses = ws + n_split * rows * a.D_v + at;
+  const int t = static_cast<int>(at / a.n_h), G = a.n_h / a.n_kv;
+  int lo = 0, hi = a.B - 1;  // the row's request: the last one that starts at or before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (packed_first(a, mid) <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const PackedRequest rq = packed_request(a, lo);
+  const long long n_rows = static_cast<long long>(rq.rows) * G;
+  long long end = (static_cast<long long>(t - rq.first) * G + (at - static_cast<long long>(t) * a.n_h) % G) / R * R + R;  // of its tile
+  end = end < n_rows ? end : n_rows;
+  const int keys = keys_of(a, rq, end - 1, G), part = part_of(keys, n_split);
+  if (keys <= part) return;
+  const int parts = static_cast<int>((static_cast<long long>(keys) + part - 1) / part);
   float m = -INFINITY, den = 0.f;
-  for (int j = 0; j < n_split; ++j) m = fmaxf(m, lses[j * rows]);
+  for (int j = 0; j < parts; ++j) m = fmaxf(m, lses[j * rows]);
   const float m_ref = m == -INFINITY ? 0.f : m;
-  for (int j = 0; j < n_split; ++j) den += exp2f(lses[j * rows] - m_ref);
+  for (int j = 0; j < parts; ++j) den += exp2f(lses[j * rows] - m_ref);
   const float inv = den > 0.f ? 1.f / den : den;
   for (int d = lane * 4; d < a.D_v; d += 128) {
     float o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < n_split; ++j) {
+    for (int j = 0; j < parts; ++j) {
       const float lj = lses[j * rows];
       if (lj == -INFINITY) continue;
       const float w = exp2f(lj - m_ref) * inv;
@@ -545,12 +590,15 @@ __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_c
     a.lse[at] = den == 0.f ? -INFINITY : (m + log2f(den)) * 0.69314718055994530942f;
 }
 
-// Numbers of tiles (an upper bound of the tiles), and parts of each tile's keys: as many as leave all blocks running at
-// once, two per SM.  (A second wave costs as much as the first: with half as many parts again, 6 requests of up to 16
-// drafts took 47 us.  Not by the table's width: tables are as wide as a request may grow.)
+// Numbers of tiles: an upper bound of the tiles.
 long long tile_numbers(const PackedArgs& a) {
   return static_cast<long long>(a.T) * (a.n_h / a.n_kv) / R + a.B;
 }
+// Parts of a tile's keys, at most: as many as leave all blocks running at once, two per SM.  (A second wave costs as much
+// as the first: with half as many parts again, 6 requests of up to 16 drafts took 47 us instead of 31; cut into two to four
+// parts of 256 keys or more where there are one to four waves, 8 prompts of up to 500 tokens of 12 heads took 94 to 106 us
+// instead of 93, and 4 x 128 tokens behind 2000 of 32 heads 705 to 727 instead of 657.  Not by the table's width: tables are
+// as wide as a request may grow.)
 int splits(const PackedArgs& a) {
   const long long n = 2 * 152 / (tile_numbers(a) * a.n_kv);
   return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
@@ -573,20 +621,20 @@ cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaS
   const cudaError_t e = cudaFuncSetAttribute(packed_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>((640 + 2 * KT) * LD * sizeof(float)));
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(tile_numbers(a)), a.n_kv, n_split);
+  const dim3 grid(static_cast<unsigned>(tile_numbers(a) * a.n_kv), n_split);
   packed_kernel<T, NV><<<grid, kThreads, smem, st>>>(a, rope, n_split);
   *launches += 1;
   return join<T>(a, n_split, st, launches);
 }
-template <int NV>
+template <int NV, int ST>
 cudaError_t launch_f32(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
-  constexpr int kMost = (2 * 64 * (128 + kPad) + 64 * (NV * 64 + kPad) + 64 * LD) * static_cast<int>(sizeof(float));
-  const cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  if (e != cudaSuccess) return e;
   const int qld = a.D_qk + (a.D_qk % 32 ? 36 - a.D_qk % 32 : 4);
-  const size_t smem = (2 * 64 * qld + 64 * (NV * 64 + kPad) + 64 * LD) * sizeof(float);
-  const dim3 grid(static_cast<unsigned>(tile_numbers(a)), a.n_kv, n_split);
-  packed_f32_kernel<NV><<<grid, kThreads, smem, st>>>(a, rope, n_split);
+  const size_t smem = ((1 + ST) * 64 * qld + ST * 64 * (NV * 64 + kPad) + 64 * LD) * sizeof(float);
+  constexpr int kMost = ((1 + ST) * 64 * ((ST == 2 ? 64 : 128) + kPad) + ST * 64 * (NV * 64 + kPad) + 64 * LD) * static_cast<int>(sizeof(float));
+  const cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<NV, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(tile_numbers(a) * a.n_kv), n_split);
+  packed_f32_kernel<NV, ST><<<grid, kThreads, smem, st>>>(a, rope, n_split);
   *launches += 1;
   return join<float>(a, n_split, st, launches);
 }
@@ -594,7 +642,9 @@ template <typename T>
 cudaError_t launch_dims(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
   if constexpr (sizeof(T) == 4) {
     if (a.D_qk <= 128 && a.D_v <= 128)
-      return a.D_v <= 64 ? launch_f32<1>(a, rope, n_split, st, launches) : launch_f32<2>(a, rope, n_split, st, launches);
+      return a.D_v > 64    ? launch_f32<2, 1>(a, rope, n_split, st, launches)
+             : a.D_qk > 64 ? launch_f32<1, 1>(a, rope, n_split, st, launches)
+                           : launch_f32<1, 2>(a, rope, n_split, st, launches);
   }
   if (a.D_v <= 64) return launch<T, 1>(a, rope, n_split, st, launches);
   if (a.D_v <= 128) return launch<T, 2>(a, rope, n_split, st, launches);
@@ -610,8 +660,8 @@ size_t packed_workspace(const PackedArgs& a) {
 }
 
 cudaError_t launch_packed(const PackedArgs& a, const RopeFreq& rope, bool bf16, cudaStream_t st, int* launches) {
-  const int n = splits(a);
-  return bf16 ? launch_dims<__nv_bfloat16>(a, rope, n, st, launches) : launch_dims<float>(a, rope, n, st, launches);
+  const int n_split = splits(a);
+  return bf16 ? launch_dims<__nv_bfloat16>(a, rope, n_split, st, launches) : launch_dims<float>(a, rope, n_split, st, launches);
 }
 
 }  // namespace attn
