@@ -6,16 +6,22 @@
 // per thread, an online softmax over the rows ("Transformer架构完全深度解析" §13), O += P V with
 // 4 rows x 4 dims per thread and 64 dims.  Everything is fp32; Q stays in shared memory
 // (dim-major), K passes through it 32 dims at a time, P once per tile, V 64 dims at a time.
-// Bound by the FMA pipe and the shared-memory reads that feed it (8 floats per 16 FMAs).
+// Bound by the FMA pipe and the shared-memory reads that feed it (8 floats per 16 FMAs): bf16, D = 96, 3 prompts of
+// 300 to 900 tokens, 32 heads over 8: 338 us, 23 TFLOP/s.
 //
 // Tiles are numbered without a table: request b's start at floor(cu_new[b] * G / 64) + b, which
 // leaves each request at least as many numbers as it has tiles, so a block finds its request by
-// bisection and a number that nobody uses ends at once.  With few tiles the keys of each are cut
-// into n_split equal parts and a second kernel joins the parts of a row by their log-sum-exps.
+// bisection and a number that nobody uses ends at once.  Blocks start with the last tiles, which see the most keys,
+// of all heads (head by head, one fp32 prompt of 2000 tokens of 8 heads took 293 us instead of 203).  With few tiles the keys
+// of each are cut into equal parts and a second kernel joins the parts of a row by their log-sum-exps.
 //
 // fp32 with head dims up to 128 has a kernel of its own, packed_f32_kernel: the same tiles, but K and V in
-// shared memory as they lie in the cache, copied asynchronously (K of the next tile while this one's P V
-// runs, V while the next scores do), and packed pairs of FMAs.
+// shared memory as they lie in the cache, copied asynchronously (with 64 dims in two stages; else K of the next tile while
+// this one's P V runs, V while the next scores do), and packed pairs of FMAs.  8 prompts of up to 500 tokens, 12 heads of 64
+// dims: 81 us, 16 TFLOP/s; 4 x 128 tokens behind 2000, 32 heads over 8 of 128 dims: 574 us, 30 TFLOP/s.  A tile of 64 keys
+// takes a block some 7 us, whether it has an SM for itself or shares it: its chain of shared-memory reads, FMAs and
+// shuffles has too few warps to hide behind.  (Three blocks per SM spill; 8 x 4 scores per thread of 128 threads, weights
+// twice in shared memory so that they are read as pairs, and unrolling the products by 4 were not faster.)
 #include <math.h>
 
 #include "kernels.h"
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       fetch_k(cur ^ 1);
     }
     const bool masked = partly_seen(a, t, k0);
-    if (active) {
+    const auto weights = [&](auto with_mask) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = ty * 4 + i;
@@ -293,19 +299,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         bool seen[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[j] = (s2[i][j].x + s2[i][j].y) * a.scale_log2;
-          seen[j] = !masked || sees(a, t, rows.place[r], rows.vis[r], k0 + tx + 16 * j);
+          s[j] = s2[i][j].x + s2[i][j].y;
+          seen[j] = !with_mask() || sees(a, t, rows.place[r], rows.vis[r], k0 + tx + 16 * j);
           if (seen[j]) mx = fmaxf(mx, s[j]);
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float m_new = fmaxf(m[i], mx), m_ref = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2f(m[i] - m_ref);
+        const float m_new = fmaxf(m[i], mx * a.scale_log2), m_ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = fast_exp2(m[i] - m_ref);
         m[i] = m_new;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float p = exp2f(s[j] - m_ref);
+          const float p = fast_exp2(fmaf(s[j], a.scale_log2, -m_ref));
           if (seen[j]) sum += p;
           Ps[r * LD + tx + 16 * j] = seen[j] ? p : kMasked;
         }
@@ -318,6 +324,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             acc[v][i][j].y *= alpha;
           }
       }
+    };
+    if (active) {
+      if (masked) weights([] { return true; });
+      else weights([] { return false; });
     }
     if constexpr (ST == 1) {
       look();
@@ -595,10 +605,9 @@ long long tile_numbers(const PackedArgs& a) {
   return static_cast<long long>(a.T) * (a.n_h / a.n_kv) / R + a.B;
 }
 // Parts of a tile's keys, at most: as many as leave all blocks running at once, two per SM.  (A second wave costs as much
-// as the first: with half as many parts again, 6 requests of up to 16 drafts took 47 us instead of 31; cut into two to four
-// parts of 256 keys or more where there are one to four waves, 8 prompts of up to 500 tokens of 12 heads took 94 to 106 us
-// instead of 93, and 4 x 128 tokens behind 2000 of 32 heads 705 to 727 instead of 657.  Not by the table's width: tables are
-// as wide as a request may grow.)
+// as the first: with half as many parts again, 6 requests of up to 16 drafts took half as long again.  Two to four parts of
+// 256 keys or more where there are one to four waves made 8 prompts of up to 500 tokens, 12 heads, up to 14% slower, and 4 x
+// 128 tokens behind 2000, 32 heads, 7% to 11%.  Not by the table's width: tables are as wide as a request may grow.)
 int splits(const PackedArgs& a) {
   const long long n = 2 * 152 / (tile_numbers(a) * a.n_kv);
   return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
