@@ -38,8 +38,8 @@
 // Bounds.  Long prompts: the tensor pipe (1 x 8192 tokens, 32 heads over 8, D = 128, RoPE: its counter is active 83% of
 // the time; a turn of a pair piece - two row tiles, 128 keys - is 3072 cycles of MMA and takes 3500 to 3600).  4 x 8192:
 // 2.0 ms, 1.1 PFLOP/s as the formula counts and 1.65 as issued.  Drafts behind long caches: HBM (59 requests of 32
-// drafts behind 4096 to 8192 tokens: 1.53 GB read in 250 us, 6.2 TB/s).  Few short requests: the chain launch, walk, TMA,
-// MMA, softmax, MMA, store, and a join (one prompt of 100 tokens 15 us).  What limits beside these is instruction fetch:
+// drafts behind 4096 to 8192 tokens: 1.53 GB read in 244 us, 6.3 TB/s).  Few short requests: the chain launch, walk, TMA,
+// MMA, softmax, MMA, store, and a join (one prompt of 77 tokens 15 us).  What limits beside these is instruction fetch:
 // five programs run side by side on an SM, and their hot loops have to fit its instruction cache together, so loops stay
 // rolled, rare code is out of line, and a start or end of a piece (some 11000 to 14000 cycles beside its turns) costs more
 // in cold code than in work.
