@@ -16,12 +16,13 @@
 // of each are cut into equal parts and a second kernel joins the parts of a row by their log-sum-exps.
 //
 // fp32 with head dims up to 128 has a kernel of its own, packed_f32_kernel: the same tiles, but K and V in
-// shared memory as they lie in the cache, copied asynchronously (with 64 dims in two stages; else K of the next tile while
-// this one's P V runs, V while the next scores do), and packed pairs of FMAs.  8 prompts of up to 500 tokens, 12 heads of 64
-// dims: 81 us, 16 TFLOP/s; 4 x 128 tokens behind 2000, 32 heads over 8 of 128 dims: 574 us, 30 TFLOP/s.  A tile of 64 keys
-// takes a block some 7 us, whether it has an SM for itself or shares it: its chain of shared-memory reads, FMAs and
-// shuffles has too few warps to hide behind.  (Three blocks per SM spill; 8 x 4 scores per thread of 128 threads, weights
-// twice in shared memory so that they are read as pairs, and unrolling the products by 4 were not faster.)
+// shared memory as they lie in the cache, copied asynchronously, and packed pairs of FMAs.  Where there is room, K and V have
+// two stages, and a tile one barrier: 64 dims in two blocks per SM, 128 in one (with values of 64 dims or fewer and keys of
+// more, one stage: K of the next tile comes while this one's P V runs, V while the next scores do).  8 prompts of up to 500
+// tokens, 12 heads of 64 dims: 80 us, 16 TFLOP/s; 4 x 128 tokens behind 2000, 32 heads over 8 of 128 dims: 553 us, 31 TFLOP/s
+// (one stage: 573).  A tile of 64 keys takes a block some 7 us, whether it has an SM for itself or shares it: its chain of
+// shared-memory reads, FMAs and shuffles has too few warps to hide behind.  (Three blocks per SM spill; 8 x 4 scores per
+// thread of 128 threads, and weights twice in shared memory so that they are read as pairs, were not faster.)
 #include <math.h>
 
 #include "kernels.h"
@@ -173,7 +174,7 @@ __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_al
 __device__ __forceinline__ void copy_wait_all_but_last() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 template <int NV, int ST>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, NV == 2 ? 1 : 2)
     packed_f32_kernel(const __grid_constant__ PackedArgs a, const __grid_constant__ RopeFreq f, int n_split) {
   extern __shared__ float4 smem4[];
   constexpr int VLD = NV * 64 + kPad;
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int d = 0; active && d < a.D_qk; d += 4) {
       float4 q4[4], k4[4];
 #pragma unroll
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
     }
     const auto add = [&](auto with_mask) {
-#pragma unroll 2
+#pragma unroll 4
       for (int k = 0; k < KT; k += 4) {
         float p4[4][4];
 #pragma unroll
@@ -639,7 +640,7 @@ template <int NV, int ST>
 cudaError_t launch_f32(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
   const int qld = a.D_qk + (a.D_qk % 32 ? 36 - a.D_qk % 32 : 4);
   const size_t smem = ((1 + ST) * 64 * qld + ST * 64 * (NV * 64 + kPad) + 64 * LD) * sizeof(float);
-  constexpr int kMost = ((1 + ST) * 64 * ((ST == 2 ? 64 : 128) + kPad) + ST * 64 * (NV * 64 + kPad) + 64 * LD) * static_cast<int>(sizeof(float));
+  constexpr int kMost = ((1 + ST) * 64 * ((NV == 1 && ST == 2 ? 64 : 128) + kPad) + ST * 64 * (NV * 64 + kPad) + 64 * LD) * static_cast<int>(sizeof(float));
   const cudaError_t e = cudaFuncSetAttribute(packed_f32_kernel<NV, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(tile_numbers(a) * a.n_kv), n_split);
@@ -651,7 +652,7 @@ template <typename T>
 cudaError_t launch_dims(const PackedArgs& a, const RopeFreq& rope, int n_split, cudaStream_t st, int* launches) {
   if constexpr (sizeof(T) == 4) {
     if (a.D_qk <= 128 && a.D_v <= 128)
-      return a.D_v > 64    ? launch_f32<2, 1>(a, rope, n_split, st, launches)
+      return a.D_v > 64    ? launch_f32<2, 2>(a, rope, n_split, st, launches)
              : a.D_qk > 64 ? launch_f32<1, 1>(a, rope, n_split, st, launches)
                            : launch_f32<1, 2>(a, rope, n_split, st, launches);
   }
