@@ -162,6 +162,18 @@ def test_other_shapes(lib, n_h, n_kv, D_qk, D_v, dtype, offset, dims, pairing):
     Step([5, 40, 9], [70, 0, 130], n_h, n_kv, D_qk, D_v, tree=True, **kw).check(lib)
 
 
+@pytest.mark.parametrize("n_h,n_kv,D_qk,D_v", [
+    (3, 1, 96, 40), (5, 1, 40, 24), (6, 2, 8, 8), (4, 4, 64, 72), (14, 2, 128, 128), (7, 7, 64, 64), (2, 1, 120, 64),
+    (100, 1, 32, 128), (4, 2, 136, 64), (4, 2, 64, 136)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_f32_shapes(lib, n_h, n_kv, D_qk, D_v, tree):
+    """Key parts of several tiles and of none, tiles that hold rows of several tokens or of part of one."""
+    kw = dict(page=16, dtype="f32", base=1e4, tree=tree)
+    Step([100, 1, 64, 0, 17], [0, 700, 5, 20, 333], n_h, n_kv, D_qk, D_v, pad=2, **kw).check(lib)
+    Step([3], [1500], n_h, n_kv, D_qk, D_v, **kw).check(lib)
+    Step([128] * 20, [64 * i for i in range(20)], n_h, n_kv, D_qk, D_v, **kw).check(lib)
+
+
 def test_mla_latent_rows(lib):
     """128 heads over one latent head whose first dims are the values."""
     for tree in (False, True):
