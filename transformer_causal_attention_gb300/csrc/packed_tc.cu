@@ -36,7 +36,7 @@
 // TMEM: S/P of the two in columns [0, 128) and [128, 256), O behind them.
 //
 // Bounds.  Long prompts: the tensor pipe (1 x 8192 tokens, 32 heads over 8, D = 128, RoPE: its counter is active 83% of
-// the time; a turn of a pair piece - two row tiles, 128 keys - is 3072 cycles of MMA and takes 3500 to 3600).  4 x 8192:
+// the time; a turn of a pair piece - two row tiles, 128 keys - is 48 MMAs of 64 cycles and takes 3500 to 3600).  4 x 8192:
 // 2.0 ms, 1.1 PFLOP/s as the formula counts and 1.65 as issued.  Drafts behind long caches: HBM (59 requests of 32
 // drafts behind 4096 to 8192 tokens: 1.53 GB read in 244 us, 6.3 TB/s).  Few short requests: the chain launch, walk, TMA,
 // MMA, softmax, MMA, store, and a join (one prompt of 77 tokens 15 us).  What limits beside these is instruction fetch:
@@ -75,9 +75,12 @@ constexpr int kCare = 3;   // care tiles of a piece, at most: 256 tokens of a pa
 constexpr int kQueue = 6;  // pieces in the queue; kAhead are handed out before warp 3 treats the first of them
 constexpr int kAhead = 3;
 
-// Points on the line: 2^shift per key of a segment, and a lead in front of its first tile.
+// Points on the line: 2^shift per key of a segment, and a lead in front of its first tile, three tiles of a pair: of the 11000
+// to 14000 cycles that starting and ending a piece takes, a single one saves little.  (With 2048 and 1024, 64 prompts of up to
+// 500 tokens, 32 heads over 8, took 240 us instead of 214, 30 trees of up to 64 drafts, 16 heads, 52 instead of 43, 128 single
+// tokens behind up to 3000 166 instead of 150; 4096 for either was no better.)
 constexpr int kPairShift = 3, kSingleShift = 2;
-constexpr int kPairLead = 2048, kSingleLead = 1024;
+constexpr int kPairLead = 3 * BN << kPairShift, kSingleLead = kPairLead;
 
 // Register split as in prefill_tc.cu: a softmax thread holds a row of 128 scores.
 constexpr int kLaunchRegs = 168;
