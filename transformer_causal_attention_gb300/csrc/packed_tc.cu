@@ -125,7 +125,6 @@ struct Cfg {
   static constexpr int kBlocks = D / 64;                      // 64-dim column blocks of a tile
   static constexpr int kBlockBytes = BM * 128;                // one column block (128 rows x 128 bytes, swizzled)
   static constexpr int kTileBytes = kBlocks * kBlockBytes;
-  static constexpr int kSteps = D / 16;
   [[maybe_unused]] static constexpr int kLoSteps = LO ? kLoDims / 16 : 0;       // MMA steps with a second part of Q
   static constexpr int kLoBytes = LO ? kBlockBytes : 0;        // of a row tile
   static constexpr int kPLoSteps = LO && D == 128 ? 4 : 0;    // steps of 16 keys with a second part of P
@@ -296,23 +295,27 @@ __device__ __forceinline__ bool elect_one() {
 // ------------------------------------------------------------------------------------- rows
 // The new tokens' queries rotated at their positions, bf16 [T, n_h, D], and what that rounding left of dims
 // [lo_dim, lo_dim + 64), bf16 [T, n_h, 64].  A thread owns 8 dims (and with split halves their partners) of a token for
-// heads_per heads, so that an angle is computed once for all of them; bound by HBM.  (Rotated by the softmax warps
+// heads_per heads, so that an angle is computed once for all of them; bound by HBM (32768 tokens of 32 heads of 128 dims
+// 104 us, 6.4 TB/s; 16384 of split halves 59).  (Rotated by the softmax warps
 // of the attention kernel, where a query tile arrives with nothing to hide behind, it took 4 to 7 us per piece.)
+template <int D>
+__host__ __device__ __forceinline__ int rotate_owners(const RopeFreq& f) {  // threads for a token's dims
+  return D / 8 - (f.half ? f.n_pairs / 8 : 0);
+}
 template <int D>
 __global__ void __launch_bounds__(256, 4) packed_rotate_kernel(const __grid_constant__ PackedArgs a,
                                                             const __grid_constant__ RopeFreq f, __nv_bfloat16* hi,
                                                             __nv_bfloat16* lo, int lo_dim, int heads_per) {
   asm volatile("griddepcontrol.launch_dependents;");  // the attention kernel starts, and waits where it reads these
   constexpr int kChunks = D / 8;
-  const int groups = a.n_h / heads_per;
-  const long long i = blockIdx.x * 256LL + threadIdx.x;
-  const int c = static_cast<int>(i % kChunks);
-  const long long tg = i / kChunks;
+  const int groups = a.n_h / heads_per, owners = rotate_owners<D>(f);
+  const long long i = blockIdx.x * 256LL + threadIdx.x, tg = i / owners;
   const int t = static_cast<int>(tg / groups), h0 = static_cast<int>(tg - static_cast<long long>(t) * groups) * heads_per;
   if (t >= a.T) return;
+  int c = static_cast<int>(i - tg * owners);
+  if (f.half && c * 8 >= a.rope_offset + f.n_pairs) c += f.n_pairs / 8;  // chunks with a partner before them are its thread's
   const int rel = c * 8 - a.rope_offset;
   const bool in = rel >= 0 && rel < 2 * f.n_pairs;
-  if (in && f.half && rel >= f.n_pairs) return;  // with its partner
   float sn[8], cs[8];
   if (in) {
     int pos;
@@ -364,25 +367,15 @@ __global__ void __launch_bounds__(256, 4) packed_rotate_kernel(const __grid_cons
   };
   constexpr int kFlight = 4;  // heads whose loads are in flight together
   if (in && f.half) {
-    for (int h0 = 0; h0 < heads_per; h0 += kFlight) {
-      uint4 a0[kFlight], a1[kFlight];
+#pragma unroll 1
+    for (int h = 0; h < heads_per; ++h) {  // (two at a time: the registers spill)
+      float x[8], y[8];
+      bf16x8_to_f32(__ldg(q + h * kChunks), x);
+      bf16x8_to_f32(__ldg(q + h * kChunks + partner), y);
 #pragma unroll
-      for (int k = 0; k < kFlight; ++k)
-        if (h0 + k < heads_per) {
-          a0[k] = __ldg(q + (h0 + k) * kChunks);
-          a1[k] = __ldg(q + (h0 + k) * kChunks + partner);
-        }
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k)
-        if (h0 + k < heads_per) {
-          float x[8], y[8];
-          bf16x8_to_f32(a0[k], x);
-          bf16x8_to_f32(a1[k], y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], sn[e], cs[e]);
-          put(h0 + k, 0, x);
-          put(h0 + k, partner, y);
-        }
+      for (int e = 0; e < 8; ++e) rotate_pair(x[e], y[e], sn[e], cs[e]);
+      put(h, 0, x);
+      put(h, partner, y);
     }
   } else {
     for (int h0 = 0; h0 < heads_per; h0 += kFlight) {
@@ -1454,8 +1447,9 @@ cudaError_t launch(const PackedArgs& a, const RopeFreq& rope, const CUtensorMap*
     // few tokens: fewer heads per thread, but for four or more the angles are worth sharing (one head each: 36 us for
     // 1888 tokens of 32, instead of 12)
     int heads = a.n_h;
-    while (heads % 2 == 0 && heads > 4 && static_cast<long long>(a.T) * (a.n_h / heads) * (D / 8) < 152LL * 2048) heads /= 2;
-    const long long items = static_cast<long long>(a.T) * (a.n_h / heads) * (D / 8);
+    const int owners = rotate_owners<D>(rope);
+    while (heads % 2 == 0 && heads > 4 && static_cast<long long>(a.T) * (a.n_h / heads) * owners < 152LL * 1024) heads /= 2;
+    const long long items = static_cast<long long>(a.T) * (a.n_h / heads) * owners;
     float* const ws = static_cast<float*>(a.workspace);
     packed_rotate_kernel<D><<<static_cast<unsigned>((items + 255) / 256), 256, 0, st>>>(
         a, rope, reinterpret_cast<__nv_bfloat16*>(ws + pl.q), reinterpret_cast<__nv_bfloat16*>(ws + pl.lo),
