@@ -22,7 +22,7 @@
 // each tile's last 64 keys are such sums too; the other weights are rounded to bf16 once.  One bf16 for both made the output's
 // error against 64 bits 1.7 times that of its own rounding behind 30000 keys (normally distributed inputs); so it is
 // 1.41 to 1.44 times.  That is half as many MMAs again with D = 128, and a quarter with D = 64, on the K and V
-// tiles that are there anyway (4 x 8192 tokens, 32 heads over 8: 2.0 ms; without RoPE, with weights rounded once, 1.44 ms).
+// tiles that are there anyway (4 x 8192 tokens, 32 heads over 8: 2.0 ms; without RoPE, with weights rounded once, 1.4 ms).
 //
 // What a row does not see.  Scores are masked by index.  A value whose weight is 0 still meets the MMA, so in
 // the tiles that some row sees in part ("care" tiles: the last ones of a segment) warp 3 clears value rows
@@ -35,10 +35,10 @@
 // 4-7 and 8-11 are the softmax of row tiles 0 and 1 (or of alternate key tiles), a row per thread.
 // TMEM: S/P of the two in columns [0, 128) and [128, 256), O behind them.
 //
-// Bounds.  Long prompts: the tensor pipe (1 x 8192 tokens, 32 heads over 8, D = 128, RoPE: its counter is active 83% of
+// Bounds.  Long prompts: the tensor pipe (1 x 8192 tokens, 32 heads over 8, D = 128, RoPE: its counter is active 82% of
 // the time; a turn of a pair piece - two row tiles, 128 keys - is 48 MMAs of 64 cycles and takes 3500 to 3600).  4 x 8192:
 // 2.0 ms, 1.1 PFLOP/s as the formula counts and 1.65 as issued.  Drafts behind long caches: HBM (59 requests of 32
-// drafts behind 4096 to 8192 tokens: 1.53 GB read in 244 us, 6.3 TB/s).  Few short requests: the chain launch, walk, TMA,
+// drafts behind 4096 to 8192 tokens: 1.53 GB read in 248 us, 6.2 TB/s).  Few short requests: the chain launch, walk, TMA,
 // MMA, softmax, MMA, store, and a join (one prompt of 77 tokens 15 us).  What limits beside these is instruction fetch:
 // five programs run side by side on an SM, and their hot loops have to fit its instruction cache together, so loops stay
 // rolled, rare code is out of line, and a start or end of a piece (some 11000 to 14000 cycles beside its turns) costs more
