@@ -70,7 +70,6 @@ constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr int kLoDims = 64;  // dims with a second part of Q: a column block
-constexpr float kTiny = 7.888609e-31f;  // 2^-100, for a second part of nothing
 constexpr int kCare = 3;   // care tiles of a piece, at most: 256 tokens of a pair, or 128 drafts
 constexpr int kQueue = 6;  // pieces in the queue; kAhead are handed out before warp 3 treats the first of them
 constexpr int kAhead = 3;
@@ -346,22 +345,21 @@ __global__ void __launch_bounds__(256, 4) packed_rotate_kernel(const __grid_cons
   const int lc = c - lo_dim / 8, partner = f.n_pairs / 8;
   const auto put = [&](int h, int at, const float* x) {  // chunk c + at
     const bool two = static_cast<unsigned>(lc + at) < static_cast<unsigned>(kLoDims / 8);
-    // With a second part the first is cut off, not rounded, and the second never 0: both have the query's sign, so that an
-    // infinite key gives both products the same infinity.
+    // With a second part the first is what bf16 cuts off the next number nearer to 0, so that what is left is never 0 and of
+    // the query's sign: an infinite key gives both products the same infinity.  (A value that bf16 holds exactly is a step
+    // of bf16 less and that step.)  0 is 0 twice, and no finite key adds anything to it.  Infinities come as the largest
+    // finite value and an infinity, NaN as NaN.
     const uint4 y = f32_to_bf16x8(x);
-    uint32_t cut[4];
+    uint32_t v[8], cut[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) cut[e] = __byte_perm(__float_as_uint(x[2 * e]), __float_as_uint(x[2 * e + 1]), 0x7632);
+    for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(x[e]) - (x[e] != 0.f ? 1u : 0u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cut[e] = __byte_perm(v[2 * e], v[2 * e + 1], 0x7632);
     o[h * kChunks + at] = two ? make_uint4(cut[0], cut[1], cut[2], cut[3]) : y;
     if (two) {
       float z[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
-        // (behind an infinity or NaN the difference is NaN: not above 0 either)
-        z[e] = x[e] - v;
-        z[e] = fabsf(z[e]) > 0.f ? z[e] : copysignf(kTiny, x[e]);
-      }
+      for (int e = 0; e < 8; ++e) z[e] = x[e] - __uint_as_float(v[e] & 0xffff0000u);
       s[h * (kLoDims / 8) + lc + at] = f32_to_bf16x8(z);
     }
   };
