@@ -66,8 +66,9 @@ ATTN_API size_t attn_packed_workspace_size(int T, int B, int n_h, int n_kv, int 
  * NaN or an infinity in a query, key or value reaches the rows that see it and no
  * other: values at places that a row does not see, of other requests or behind the last
  * token may be anything.  A key with a score of -inf has no weight, a row whose scores
- * all are comes out as one that sees no key, a score of +inf makes its row NaN, and so
- * does an infinite value whose weight is 0.
+ * all are comes out as one that sees no key, and a score of +inf makes its row NaN.  An
+ * infinite value gives its dim of the rows that see it that infinity, or NaN where the
+ * key's weight is 0 (one below 2^-110 of the row's largest may count as 0).
  * The workspace of shapes that the tensor cores take holds T * n_h * (D + 64) * 2 bytes
  * for the rotated queries, beside the partials of the pieces that requests are cut into.
  * Outputs must not overlap inputs, the workspace or each other.

@@ -1,12 +1,12 @@
-"""Steps of several tokens per request at the edges of their numbers: queries of zero and near it beside huge keys.
-Inputs, references and element-wise bars are those of tests/test_gpu_packed.py.
+"""Steps of several tokens per request at the edges of their numbers: queries of zero and near it beside huge keys, and
+infinite values whose keys have no weight.  Inputs, references and element-wise bars are those of tests/test_gpu_packed.py.
 """
 import numpy as np
 import pytest
 import torch
 
 from tests import packed_reference as ref
-from tests.test_gpu_packed import Step, lib  # noqa: F401 (lib: the module's fixture)
+from tests.test_gpu_packed import DEV, Step, lib  # noqa: F401 (lib: the module's fixture)
 from tests.tolerances import to_np
 
 pytestmark = pytest.mark.gpu
@@ -21,6 +21,11 @@ def set_key(s, b, places, dims, value, head=slice(None)):
         for d in np.atleast_1d(dims):
             s.k[int(s.table[b, p // page]), p % page, head, d] = value
             s.k_of[b][p, head, d] = float(torch.tensor(value).to(s.k.dtype))
+
+
+def set_value(s, b, place, dim, value):
+    page = s.v.shape[1]
+    s.v[int(s.table[b, place // page]), place % page, 0, dim] = value
 
 
 # ------------------------------------------------------------------------------------------- queries of zero
@@ -75,3 +80,78 @@ def test_infinite_keys_beside_exact_queries(lib, n_h, n_kv, D, tree):  # noqa: F
             o = to_np(out)
             assert np.isnan(o[:70][up]).all()
             assert np.isfinite(o[:70][~up]).all() and np.isfinite(o[70:]).all()
+
+
+# ------------------------------------------------------------------------------------------- values without weight
+@pytest.mark.parametrize("n_h,n_kv,D,dtype", ALL)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("base", [0.0, 1e4])
+def test_infinite_values_of_keys_without_weight(lib, n_h, n_kv, D, dtype, tree, base):  # noqa: F811
+    """0 times an infinity is NaN, in tiles that rows see whole and in part: keys whose score is -inf, or so low that its
+    exponential is 0 in 32 bits (2^-150 is half the least number there is; these scores are below -500 times log2 e).  A
+    key with a weight, however small, gives the infinity."""
+    sc = D ** -0.5
+    for place in (3, 127, 130, 199, 205, 210):  # of request 0: 200 tokens held, 70 new ones
+        for value in (float("inf"), float("-inf")):
+            for score in (float("-inf"), -1000.0, -30.0):
+                s = Step([70, 20], [200, 10], n_h, n_kv, D, dtype=dtype, tree=tree, base=base, dims=32 if base else None,
+                         seed=8)
+                s.q[..., 40] = 1.0
+                clean, clean_lse = s.run(lib)
+                set_key(s, 0, place, 40, score / sc, head=0)
+                low, low_lse = s.run(lib)  # what the rows are with finite values
+                set_value(s, 0, place, 9, value)
+                out, lse = s.run(lib)
+                sees = ref.causal(70, 200) if not tree else ref.tree(70, 200, s.visible[:70])
+                hit = np.zeros((s.T, n_h), bool)
+                hit[:70, :n_h // n_kv] = sees[:, place][:, None]
+                assert hit.any() and not hit[:70].all()
+                hit = torch.as_tensor(hit, device=DEV)
+                x = out[hit][:, 9].float()
+                assert (x == value).all() if score == -30.0 else torch.isnan(x).all(), (place, value, score)
+                rest = torch.arange(D, device=DEV) != 9
+                assert torch.equal(out[hit][:, rest], low[hit][:, rest]) and torch.isfinite(out[hit][:, rest]).all()
+                assert torch.equal(out[~hit], clean[~hit])
+                assert torch.equal(lse, low_lse) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("n_h,n_kv,D,dtype", ALL)
+@pytest.mark.parametrize("tree", [False, True])
+def test_infinite_values_in_parts_without_weight(lib, n_h, n_kv, D, dtype, tree):  # noqa: F811
+    """The same where the key axis is cut, and a whole part has scores of -inf alone: the value is not lost."""
+    n, ctx = 3, 9000
+    lo, hi = 2000, 7000  # keys with a score of -inf for KV head 0
+    for place in (lo, 2100, 4444, hi - 1, ctx):  # the last: of the first new token, alone with a weight of 0 in its tile
+        s = Step([n], [ctx], n_h, n_kv, D, dtype=dtype, tree=tree, page=64, seed=9)
+        s.q[..., 40] = 1.0
+        s.k.view(-1, n_kv, D)[s.table[0].long().repeat_interleave(64)[lo:hi] * 64 + torch.arange(lo, hi) % 64, 0, 40] = -float("inf")
+        set_key(s, 0, place, 40, -float("inf"), head=0)
+        low, low_lse = s.run(lib)
+        assert torch.isfinite(low).all() and torch.isfinite(low_lse).all()
+        set_value(s, 0, place, 9, float("inf"))
+        out, lse = s.run(lib)
+        sees = (ref.causal(n, ctx) if not tree else ref.tree(n, ctx, s.visible))[:, place]
+        hit = np.zeros((n, n_h), bool)
+        hit[:, :n_h // n_kv] = sees[:, None]
+        hit = torch.as_tensor(hit, device=DEV)
+        rest = torch.arange(D, device=DEV) != 9
+        assert torch.isnan(out[hit][:, 9]).all(), place
+        assert torch.equal(out[hit][:, rest], low[hit][:, rest]) and torch.equal(out[~hit], low[~hit])
+        assert torch.equal(lse, low_lse)
+
+
+@pytest.mark.parametrize("n_h,n_kv,D,dtype", ALL)
+def test_rows_without_any_weight_stay_zero(lib, n_h, n_kv, D, dtype):  # noqa: F811
+    """All scores -inf: the row is one that sees no key, whatever the values are, in one piece or many."""
+    for news, ctx in (([2, 1], 0), ([1, 5], 9000)):
+        s = Step(news, [ctx, 3], n_h, n_kv, D, dtype=dtype, page=64, seed=10)
+        s.q[..., 40] = 1.0
+        n = news[0] + ctx
+        at = s.table[0].long().repeat_interleave(64)[:n] * 64 + torch.arange(n) % 64
+        s.k.view(-1, n_kv, D)[at, 0, 40] = -float("inf")
+        s.v.view(-1, n_kv, D)[at[::3], 0, 9] = float("inf")
+        s.v.view(-1, n_kv, D)[at[1::3], 0, 10] = float("nan")
+        out, lse = s.run(lib)
+        heads = n_h // n_kv
+        assert not out[:news[0], :heads].any() and torch.isneginf(lse[:news[0], :heads]).all()
+        assert torch.isfinite(out).all() and torch.isfinite(lse[:, heads:]).all() and torch.isfinite(lse[news[0]:]).all()

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, NV == 2 ? 1 : 2)
       const int d = v * 64 + tx * 4;
       if (d >= a.D_v) continue;
       float o[4] = {acc[v][i][0].x * inv, acc[v][i][0].y * inv, acc[v][i][1].x * inv, acc[v][i][1].y * inv};
-      if (l[i] == 0.f) o[0] = o[1] = o[2] = o[3] = 0.f;
+      if (rows.place[r] < 0 || (t.whole && l[i] == 0.f)) o[0] = o[1] = o[2] = o[3] = 0.f;
       put_row<float>(a, t.whole, rows.at[r], d, o);
     }
     if (tx == 0) put_lse(a, t.whole, rows.at[r], l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads)
       else add([] { return false; });
     }
   }
-  // out, or this split's normalised part
+  // out, or this split's normalised part (of no weight: 0, or beside values that are not finite NaN, as 0 times these is)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty * 4 + i;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads)
       if (d >= a.D_v) continue;
       float o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = l[i] == 0.f ? 0.f : acc[v][i][j] * inv;
+      for (int j = 0; j < 4; ++j) o[j] = rows.place[r] < 0 || (t.whole && l[i] == 0.f) ? 0.f : acc[v][i][j] * inv;
       put_row<T>(a, t.whole, rows.at[r], d, o);
     }
     if (tx == 0) put_lse(a, t.whole, rows.at[r], l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]), n_split);
@@ -586,15 +586,14 @@ __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_c
   for (int d = lane * 4; d < a.D_v; d += 128) {
     float o[4] = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < parts; ++j) {
-      const float lj = lses[j * rows];
-      if (lj == -INFINITY) continue;
-      const float w = exp2f(lj - m_ref) * inv;
+      const float w = exp2f(lses[j * rows] - m_ref) * inv;
       const float4 x = *reinterpret_cast<const float4*>(ws + (j * rows + at) * a.D_v + d);
       o[0] = fmaf(w, x.x, o[0]);
       o[1] = fmaf(w, x.y, o[1]);
       o[2] = fmaf(w, x.z, o[2]);
       o[3] = fmaf(w, x.w, o[3]);
     }
+    if (den == 0.f) o[0] = o[1] = o[2] = o[3] = 0.f;
     store4(static_cast<T*>(a.out) + at * a.D_v + d, o);
   }
   if (lane == 0 && a.lse != nullptr)

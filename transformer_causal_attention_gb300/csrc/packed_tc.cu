@@ -135,7 +135,8 @@ struct Cfg {
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
   static constexpr int kLoOff = kVOff + kVStages * kTileBytes;
   static constexpr int kMlOff = kLoOff + 2 * kLoBytes;         // worker 1's maximum and sum of each row
-  static constexpr int kBarOff = kMlOff + BM * 8;
+  static constexpr int kMaxOff = kMlOff + BM * 8;              // the maximum of both workers
+  static constexpr int kBarOff = kMaxOff + BM * 4;
   static constexpr uint32_t kOCol = 256;                       // O of worker w at kOCol + w D
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(BM, BN, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(BM, D, true);
@@ -568,9 +569,18 @@ __device__ __noinline__ uint4 row_mask(const int* visible, int words, int tile_t
   return make_uint4(m[0], m[1], m[2], m[3]);
 }
 
-// The values that are not finite in care tiles, of dims [c0, c1), added to what has been stored of a row that sees them.
-__device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl, const Piece& u, int w, int my_tok, int c0, int c1,
-                                   __nv_bfloat16* out, float* partial) {
+// The values that are not finite in care tiles, of dims [c0, c1), added to what has been stored of a row that sees them, times
+// their weights: the infinity, or NaN where the key has no weight, as the MMA gives in the other tiles.  The weights are
+// gone by then: the score is summed once more from the query that the MMA had (row q_row of it), and m is the row's
+// maximum.
+template <int D, bool LO>
+__device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl, const Piece& u, int w, int my_tok, long long q_row,
+                                   float m_run, int c0, int c1, __nv_bfloat16* out, float* partial) {
+  if (LO) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rotated queries are there (long since)
+  const float* const ws = static_cast<const float*>(a.workspace);
+  const __nv_bfloat16* const q = (LO ? reinterpret_cast<const __nv_bfloat16*>(ws + pl.q) : static_cast<const __nv_bfloat16*>(a.q)) + q_row * D;
+  const __nv_bfloat16* const rest = reinterpret_cast<const __nv_bfloat16*>(ws + pl.lo) + q_row * kLoDims;
+  const float m_ref = m_run == -INFINITY ? 0.f : m_run;
   for (int i = 0; i < kCare; ++i) {
     const int key0 = (u.care_t + i) * BN;
     if (u.care_t + i >= u.t_end) break;
@@ -583,9 +593,18 @@ __device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl
         const int page = a.block_table[static_cast<long long>(u.b) * a.max_blocks + (key >> a.page_shift)];
         const long long slot = (static_cast<long long>(page) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
         const __nv_bfloat16* const v = static_cast<const __nv_bfloat16*>(a.v_pages) + slot * a.v_token_stride + u.g * a.D_v;
+        const __nv_bfloat16* const k = static_cast<const __nv_bfloat16*>(a.k_pages) + (slot * a.n_kv + u.g) * D;
+        float score = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) score = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), score);
+#pragma unroll 1
+        for (int d = 0; LO && d < kLoDims; ++d)
+          score = fmaf(__bfloat162float(rest[d]), __bfloat162float(k[pl.lo_first * 16 + d]), score);
+        const float weight = __bfloat162float(__float2bfloat16_rn(fast_exp2(fmaf(score, a.scale_log2, -m_ref))));
         for (int d = c0; d < c1; ++d) {
-          const float x = __bfloat162float(v[d]);
+          float x = __bfloat162float(v[d]);
           if (fabsf(x) < INFINITY) continue;
+          x *= weight;
           if (partial != nullptr) partial[d] += x;
           else out[d] = __float2bfloat16_rn(__bfloat162float(out[d]) + x);
         }
@@ -596,11 +615,11 @@ __device__ __noinline__ void add_bad(const PackedArgs& a, const PackedTcPlan& pl
 
 // Columns [c0, c1) of the rows' O times f0 (both: and the one D columns on times f1), as bf16 to the output (whole) or as
 // fp32 to a partial; `to`: where this lane's row begins, `row` its number there (-1: not a query), step bytes per row.
-// none: zeros.  Four lanes exchange 16-byte pieces of their rows, so that a store instruction writes 64 bytes of each of
+// zero: zeros.  Four lanes exchange 16-byte pieces of their rows, so that a store instruction writes 64 bytes of each of
 // eight rows: with a row per lane it made 32 lines, and the load/store unit took 550 cycles for 16 columns.  Out of line:
 // beside the softmax it had registers of that spilled.
 template <int D>
-__device__ __noinline__ void store_rows(uint32_t o_col, int c0, int c1, bool both, bool whole, bool none, float f0, float f1, char* to,
+__device__ __noinline__ void store_rows(uint32_t o_col, int c0, int c1, bool both, bool whole, bool zero, float f0, float f1, char* to,
                                       int row, int step) {
   const int lane = threadIdx.x & 31, lj = lane & 3;
   to += lj * 16;
@@ -628,7 +647,7 @@ __device__ __noinline__ void store_rows(uint32_t o_col, int c0, int c1, bool bot
         for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), f1, o[e]);
       }
     }
-    if (none) {
+    if (zero) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] = 0.f;
     }
@@ -1225,6 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f0 *= inv;
           f1 *= inv;
           *ml = make_float2(f0, f1);
+          reinterpret_cast<float*>(smem + C::kMaxOff)[r] = m;
           tc_fence_before();
           mbar_arrive(&bars->x_back);
         }
@@ -1246,16 +1266,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sh.n > 0) {
           tc_fence_after();
           const int c0 = both && w == 1 ? D / 2 : 0, c1 = both && w == 0 ? D / 2 : D;
+          // A row without any weight is 0; a piece of it is 0 or, beside values that are not finite, NaN.
+          const bool zero = whole ? none : dead;
           // rows that are no queries take the place of row 0 (they store nothing of their own)
           const long long at = whole ? (real ? out_row : 0) : slot_row;
           char* const to = whole ? static_cast<char*>(a.out) + at * (D * 2) : reinterpret_cast<char*>(ws + (real ? at : at - r) * D);
-          store_rows<D>(tmem + lane_off + C::kOCol + (both || w == 0 ? 0 : D), c0, c1, both, whole, none, f0, f1,
+          store_rows<D>(tmem + lane_off + C::kOCol + (both || w == 0 ? 0 : D), c0, c1, both, whole, zero, f0, f1,
                         to + c0 * (whole ? 2 : 4), real ? (whole ? static_cast<int>(at) : r) : -1, whole ? D * 2 : D * 4);
           if (u->bad_any) {
             __syncwarp();  // the row has been stored by four lanes
-            if (!none)
-              add_bad(a, pl, *u, w, my_tok, c0, c1, whole ? static_cast<__nv_bfloat16*>(a.out) + at * D : nullptr,
-                      whole ? nullptr : ws + slot_row * D);
+            if (!zero)
+              add_bad<D, LO>(a, pl, *u, w, my_tok, out_row, both && w == 1 ? reinterpret_cast<float*>(smem + C::kMaxOff)[r] : m_run,
+                             c0, c1, whole ? static_cast<__nv_bfloat16*>(a.out) + at * D : nullptr,
+                             whole ? nullptr : ws + slot_row * D);
           }
           tc_fence_before();
           if (!both) {
@@ -1267,6 +1290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&bars->o_empty[0]);
             mbar_arrive(&bars->o_empty[1]);
           }
+        } else if (real) {  // a pair's first row tile behind its last key: a part that holds nothing
+#pragma unroll 1
+          for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(ws + slot_row * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (both) x_ph ^= 1u;
       }
@@ -1376,8 +1402,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 6)
         for (int e = 0; e < kPer; ++e) acc[k][e] *= x;
 #pragma unroll
         for (int q = 0; q < kJoinFlight; ++q) {
-          if (l[q][k] == -INFINITY) continue;  // a part without a weight holds nothing
-          const float y = exp2f(l[q][k] - m_ref);
+          const float y = exp2f(l[q][k] - m_ref);  // a part without a weight holds 0, or NaN
           den[k] += y;
 #pragma unroll
           for (int e = 0; e < kPer; ++e) acc[k][e] = fmaf(y, v[q][k][e], acc[k][e]);
@@ -1387,12 +1412,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 6)
 #pragma unroll
     for (int k = 0; k < kJoinPer; ++k) {
       if (at[k] < 0) continue;
-      const float inv = den[k] == 0.f ? 0.f : 1.f / den[k];
+      const float inv = 1.f / den[k];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[k][e] = den[k] == 0.f ? 0.f : acc[k][e] * inv;
       uint32_t* const out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(at[k]) * D + lane * kPer);
       if constexpr (kPer == 4)
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv), pack_bf16x2(acc[k][2] * inv, acc[k][3] * inv));
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc[k][0], acc[k][1]), pack_bf16x2(acc[k][2], acc[k][3]));
       else
-        out[0] = pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv);
+        out[0] = pack_bf16x2(acc[k][0], acc[k][1]);
       if (lane == 0 && a.lse != nullptr)
         a.lse[at[k]] = den[k] == 0.f ? -INFINITY : (M[k] + log2f(den[k])) * 0.69314718055994530942f;
     }
