@@ -136,8 +136,10 @@ ATTN_API int attn_draft_plan(const int* places, const int* cu_new, const int* pa
  *   free_pages [free_cap], n_free [1], n_left [1]: the stack of attn_page_plan, or all
  *            NULL to leave the pages with their requests.  The pages
  *            ceil(new_lens[b] / page_size) .. ceil(seqlens[b] / page_size) - 1 of each
- *            row are put on its top, request after request, in rising order; n_left is
- *            its height after that, at most free_cap (pages behind it are dropped).
+ *            row are put on its top, request after request, in rising order, but for
+ *            entries outside [0, n_pages), which are no pages (a row is as long as
+ *            seqlens says); n_left is its height after that, at most free_cap (pages
+ *            behind it are dropped).
  *            The table keeps its entries.  Called twice with the same n_free, the second
  *            call puts the same pages in the same places.
  * A token with its old or new page outside [0, n_pages) is not moved.  Pages are owned

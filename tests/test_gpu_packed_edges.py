@@ -1,12 +1,13 @@
-"""Steps of several tokens per request at the edges of their numbers: queries of zero and near it beside huge keys, and
-infinite values whose keys have no weight.  Inputs, references and element-wise bars are those of tests/test_gpu_packed.py.
+"""Steps of several tokens per request at the edges of their numbers: queries of zero and near it beside huge keys,
+infinite values whose keys have no weight, and table entries of no page beside the free stack.  Inputs, references and
+element-wise bars are those of tests/test_gpu_packed.py.
 """
 import numpy as np
 import pytest
 import torch
 
 from tests import packed_reference as ref
-from tests.test_gpu_packed import DEV, Step, lib  # noqa: F401 (lib: the module's fixture)
+from tests.test_gpu_packed import DEV, Step, ints, lib  # noqa: F401 (lib: the module's fixture)
 from tests.tolerances import to_np
 
 pytestmark = pytest.mark.gpu
@@ -155,3 +156,61 @@ def test_rows_without_any_weight_stay_zero(lib, n_h, n_kv, D, dtype):  # noqa: F
         heads = n_h // n_kv
         assert not out[:news[0], :heads].any() and torch.isneginf(lse[:news[0], :heads]).all()
         assert torch.isfinite(out).all() and torch.isfinite(lse[:, heads:]).all() and torch.isfinite(lse[news[0]:]).all()
+
+
+# ------------------------------------------------------------------------------------------- the free stack
+def freed(table, lens, seqlens, kept, page, n_pages):
+    """Pages that fall free, from the definition: those of the cache among each row's surplus entries."""
+    pages = []
+    for b in range(len(lens)):
+        for j in range(-(-kept[b] // page), -(-seqlens[b] // page)):
+            if 0 <= table[b, j] < n_pages:
+                pages.append(int(table[b, j]))
+    return pages
+
+
+@pytest.mark.parametrize("B,page,most", [(3, 16, 40), (300, 16, 90), (700, 32, 200), (2, 16, 20000), (40, 16, 3000)])
+def test_pages_outside_the_cache_do_not_reach_the_stack(lib, B, page, most):  # noqa: F811
+    """Entries of no page (behind those that a request owns, or anywhere) among what a commit gives back."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, most // 2, B)
+    drafts = rng.integers(0, most // 2, B)
+    lens[B // 2], drafts[B // 2] = 0, most
+    seqlens = np.minimum(lens + drafts, most)
+    width = -(-most // page)
+    n_pages = B * width + 3
+    table = rng.permutation(n_pages)[:B * width].reshape(B, width)
+    bad = rng.random((B, width))
+    table[bad < 0.15] = -1
+    table[bad < 0.05] = n_pages
+    table[bad < 0.03] = 2 ** 31 - 1
+    table[bad < 0.01] = -2 ** 31
+    table[0] = -1  # a request that owns nothing
+    k = torch.zeros(n_pages, page, 1, 8, dtype=torch.bfloat16, device=DEV)
+    path, n_path = np.zeros((B, 1)), rng.integers(0, 2, B)
+    kept = lens + np.minimum(n_path, seqlens - lens)
+    want = freed(table, lens, seqlens, kept, page, n_pages)
+    for cap in sorted({n_pages, min(n_pages, 5 + len(want) // 2)}):
+        stack = np.full(cap, -7)
+        stack[:3] = [11, 12, 13]
+        stack_t = ints(stack)
+        new, left = lib.draft_commit(k, k.clone(), ints(table), ints(lens), ints(seqlens), ints(path), ints(n_path),
+                                     stack_t, ints([3]))
+        np.testing.assert_array_equal(new.cpu().numpy(), kept)
+        stack[3:3 + len(want)] = want[:cap - 3]
+        np.testing.assert_array_equal(stack_t.cpu().numpy(), stack)
+        assert int(left) == min(cap, 3 + len(want))
+
+
+def test_a_commit_of_lengths_above_the_table(lib):  # noqa: F811
+    """seqlens is cut to the table, whose entries behind the request's pages are -1: the next plan hands out real pages."""
+    page, n_pages, width = 16, 8, 6
+    table = ints([[4, 2, -1, -1, -1, -1], [5, 1, 0, -1, -1, -1]])
+    k = torch.zeros(n_pages, page, 1, 8, dtype=torch.bfloat16, device=DEV)
+    free = ints([3, 6, 7, -7, -7, -7, -7, -7])
+    lens, left = lib.draft_commit(k, k.clone(), table, ints([10, 30]), ints([2 ** 31 - 1, 40]), ints([[0], [0]]), ints([1, 1]),
+                                  free, ints([3]))
+    assert lens.tolist() == [11, 31] and int(left) == 5 and free.tolist() == [3, 6, 7, 2, 0, -7, -7, -7]
+    _, _, slots, positions, left = lib.page_plan(lens, ints([10, 30]), table, free, left, page_size=page, n_pages=n_pages,
+                                                 max_tokens=40)
+    assert (slots >= 0).all() and (positions >= 0).all()

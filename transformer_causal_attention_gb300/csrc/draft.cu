@@ -93,12 +93,14 @@ __device__ __forceinline__ int accepted_alone(const DraftCommitArgs& a, int b, i
 }
 
 constexpr int kCommitThreads = 256, kCommitBatch = 8;
+constexpr int kAlone = 32;  // entries of a row that a thread walks by itself
 
 // Blocks (request, 256 pieces of 16 bytes of a token): each thread moves its piece of the accepted tokens,
 // one after the other in batches of kCommitBatch loads.  Token i comes from index path[i] >= i, and later
 // ones from higher indices still, so no store hits what is loaded later; a batch is loaded before it is
-// stored.  The first block puts the pages that fall free on the stack: a thread counts a request's, a scan over
-// kCommitThreads requests at a time gives their places.  (A warp per request, one after the other, took 35 us for 512.)
+// stored.  The first block puts the pages that fall free on the stack: a thread counts a request's (a warp those of one with
+// more than kAlone entries), a scan over kCommitThreads requests at a time gives their places.  (A warp per request, one
+// after the other, took 35 us for 512.)
 __global__ void __launch_bounds__(kCommitThreads) draft_commit_kernel(const __grid_constant__ DraftCommitArgs a,
                                                                       int slices) {
   __shared__ long long src[kMaxDrafts], dst[kMaxDrafts];
@@ -146,11 +148,11 @@ __global__ void __launch_bounds__(kCommitThreads) draft_commit_kernel(const __gr
     }
     return;
   }
-  // the stack
-  __shared__ int warp_sum[kCommitThreads / 32];
+  // the stack: of each row's surplus entries those that are pages of the cache
+  __shared__ long long warp_sum[kCommitThreads / 32];
   const int page = 1 << a.page_shift;
-  const int top = min(max(*a.n_free, 0), a.free_cap);
-  long long at = top;
+  const auto is_page = [&](int id) { return id >= 0 && id < a.n_pages; };
+  long long at = min(max(*a.n_free, 0), a.free_cap);
   for (int b0 = 0; b0 < a.B; b0 += kCommitThreads) {
     const int b = b0 + threadIdx.x;
     int first = 0, mine = 0;
@@ -159,10 +161,30 @@ __global__ void __launch_bounds__(kCommitThreads) draft_commit_kernel(const __gr
       first = (kept >> a.page_shift) + ((kept & (page - 1)) != 0);
       mine = max((len >> a.page_shift) + ((len & (page - 1)) != 0) - first, 0);
     }
-    int before = mine;
+    const int* const entries = a.block_table + static_cast<long long>(b < a.B ? b : 0) * a.max_blocks + first;
+    const uint32_t many = __ballot_sync(0xffffffffu, mine > kAlone);  // requests whose entries the warp walks together
+    // f(l, n, row): the request of lane l, with n entries from `row` on
+    const auto each_of_many = [&](auto f) {
+      for (uint32_t left = many; left; left &= left - 1) {
+        const int l = __ffs(left) - 1;
+        f(l, __shfl_sync(0xffffffffu, mine, l),
+          reinterpret_cast<const int*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(entries), l)));
+      }
+    };
+    int real = 0;
+    if (mine <= kAlone)
+      for (int j = 0; j < mine; ++j) real += is_page(entries[j]);
+    each_of_many([&](int l, int n, const int* row) {
+      int sum = 0;
+#pragma unroll 4
+      for (int j = lane; j < n; j += 32) sum += is_page(row[j]);
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == l) real = sum;
+    });
+    long long before = real;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, before, o);
+      const long long x = __shfl_up_sync(0xffffffffu, before, o);
       if (lane >= o) before += x;
     }
     if (lane == 31) warp_sum[warp] = before;
@@ -173,9 +195,24 @@ __global__ void __launch_bounds__(kCommitThreads) draft_commit_kernel(const __gr
       if (w < warp) ahead += warp_sum[w];
       sum += warp_sum[w];
     }
-    const long long to = at + ahead + before - mine;
-    for (int j = 0; j < mine && to + j < a.free_cap; ++j)
-      a.free_pages[to + j] = a.block_table[static_cast<long long>(b) * a.max_blocks + first + j];
+    const long long to = at + ahead + before - real;
+    if (mine <= kAlone) {
+      long long put = to;
+      for (int j = 0; j < mine && put < a.free_cap; ++j) {
+        const int id = entries[j];
+        if (is_page(id)) a.free_pages[put++] = id;
+      }
+    }
+    each_of_many([&](int l, int n, const int* row) {
+      long long put = __shfl_sync(0xffffffffu, to, l);
+      for (int j0 = 0; j0 < n && put < a.free_cap; j0 += 32) {
+        const int id = j0 + lane < n ? row[j0 + lane] : -1;
+        const uint32_t some = __ballot_sync(0xffffffffu, is_page(id));
+        const long long mine_at = put + __popc(some & ((1u << lane) - 1u));
+        if (is_page(id) && mine_at < a.free_cap) a.free_pages[mine_at] = id;
+        put += __popc(some);
+      }
+    });
     at += sum;
     __syncthreads();
   }
