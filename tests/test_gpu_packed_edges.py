@@ -1,6 +1,6 @@
 """Steps of several tokens per request at the edges of their numbers: queries of zero and near it beside huge keys,
-infinite values whose keys have no weight, and table entries of no page beside the free stack.  Inputs, references and
-element-wise bars are those of tests/test_gpu_packed.py.
+infinite values whose keys have no weight, what two-part queries and weights are worth, and table entries of no page beside
+the free stack.  Inputs, references and element-wise bars are those of tests/test_gpu_packed.py.
 """
 import numpy as np
 import pytest
@@ -156,6 +156,71 @@ def test_rows_without_any_weight_stay_zero(lib, n_h, n_kv, D, dtype):  # noqa: F
         heads = n_h // n_kv
         assert not out[:news[0], :heads].any() and torch.isneginf(lse[:news[0], :heads]).all()
         assert torch.isfinite(out).all() and torch.isfinite(lse[:, heads:]).all() and torch.isfinite(lse[news[0]:]).all()
+
+
+# ------------------------------------------------------------------------------------------- two-part queries and weights
+def step_error(s, lib):  # noqa: F811
+    """The error of bf16 outputs against 64 bits, over that of the reference's own rounding to bf16 (norms)."""
+    out, _ = s.run(lib)
+    want = s.want()[0]
+    once = torch.as_tensor(want).to(torch.bfloat16).double().numpy()
+    return np.linalg.norm(to_np(out) - want) / np.linalg.norm(once - want)
+
+
+@pytest.mark.parametrize("D,offset,dims,pairing", [
+    (64, 0, None, "adjacent"), (64, 0, None, "half"), (64, 8, 48, "half"), (128, 0, None, "adjacent"),
+    (128, 0, None, "half"), (128, 8, 56, "adjacent"), (128, 64, 64, "half"), (128, 72, 48, "half")])
+@pytest.mark.parametrize("tree", [False, True])
+def test_error_of_two_part_queries_and_weights(lib, D, offset, dims, pairing, tree):  # noqa: F811
+    """For normally distributed inputs with scores of variance 1, in units of the output's own rounding (a relative error
+    of variance e^2): a weight rounded once adds e^2 of the output's variance (sum (p e)^2 over sum p^2), and so does a
+    query rounded once in all dims (its scores are off by e times a normal number).  Half of the weights and 64 of the query
+    dims in two parts with D = 128 leave 1 + 1/2 + 1/2 at most, all query dims with D = 64 and weights rounded once 1 + 1:
+    the square root is 1.41.  Where a whole head is rotated, second parts of half of the weights or queries lost and the
+    first ones rounded are sqrt(2.5) = 1.58; as the first ones are cut off, a part lost has an error of variance 4 e^2 or
+    more, and a factor of sqrt(1 + 1/2 + 4/2) = 1.87.  The bar is half way between 1.41 and 1.58."""
+    s = Step([40, 64], [1500, 900], 8, 2, D, page=64, base=5e5, pairing=pairing, offset=offset, dims=dims, tree=tree,
+             seed=D + offset)
+    assert step_error(s, lib) <= 1.5
+
+
+@pytest.mark.parametrize("D,offset,dims", [(64, 0, 64), (64, 16, 32), (128, 0, 64), (128, 8, 48), (128, 64, 64), (128, 72, 48)])
+@pytest.mark.parametrize("pairing", ["adjacent", "half"])
+@pytest.mark.parametrize("tree", [False, True])
+def test_second_parts_of_queries(lib, D, offset, dims, pairing, tree):  # noqa: F811
+    """Queries within the 64 dims that have second parts (from the start of the rotated span on, down to a multiple of
+    16): scores are as of 16 bits.  Each term of a score is off by 2^-8 of what one bf16 leaves, at most 2^-7 of it where
+    that is cut off: 2^-15; the rotation in fp32 with the hardware's sines (2^-21 each, two terms) and the sums add less
+    than 2^-17 of the terms.  So the log-sum-exp is off by 2^-14 of the largest sum of |terms| at most, and a hundredth
+    of what one rounding of every term may be."""
+    s = Step([40, 64], [700, 3], 8, 2, D, page=64, base=5e5, pairing=pairing, offset=offset, dims=dims, tree=tree,
+             seed=D + offset + 1)
+    first = min(offset // 16 * 16, D - 64)
+    keep = torch.zeros(D, dtype=torch.bool)
+    keep[first:first + 64] = True
+    s.q[..., ~keep] = 0
+    _, lse = s.run(lib)
+    _, want, _, err = s.want()  # err: with 2^-8 of every term
+    d = np.abs(to_np(lse) - want)
+    assert (d <= err * 2.0 ** -6 + 1e-6 * (1 + np.abs(want))).all(), float((d / err).max())
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_second_parts_of_weights(lib, tree):  # noqa: F811
+    """D = 128 with RoPE: values in the last 64 keys of each 128 alone.  Their weights are in two parts, off by 2^-15 (as above)
+    and 2^-20, and so are the queries, here within their 64 dims; what is left is the output's rounding, half a step."""
+    s = Step([40, 64], [700, 300], 8, 2, 128, page=64, base=5e5, dims=64, tree=tree, seed=5)
+    s.q[..., 64:] = 0
+    for b, n in enumerate(s.lens):
+        at = s.table[b].long().repeat_interleave(64)[:n] * 64 + torch.arange(n) % 64
+        first = torch.arange(n) % 128 < 64
+        s.v.view(-1, 2, 128)[at[first]] = 0
+        s.v_of[b][first.numpy()] = 0
+    out, _ = s.run(lib)
+    want, _, spread, err = s.want()
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -14 + np.expm1(2 * (err * 2.0 ** -6 + 1e-6))[..., None] + 1e-5) * spread
+    d = np.abs(to_np(out) - want)
+    assert (d <= tol).all(), float((d / tol).max())
 
 
 # ------------------------------------------------------------------------------------------- the free stack
