@@ -59,10 +59,11 @@ ATTN_API size_t attn_packed_workspace_size(int T, int B, int n_h, int n_kv, int 
  * bf16 with D_qk = D_v = 64 or 128, at most 128 query heads per KV head and a RoPE
  * span of whole 16-byte pieces (none, or rope_offset % 8 == 0 and rope_dims % 8 == 0,
  * % 16 with ATTN_ROPE_HALF) runs on the tensor cores, anything else on CUDA cores.
- * Sums are fp32.  On the tensor cores softmax weights are rounded to bf16 on the way
- * in, and so are rotated queries, but for what that leaves of 64 of their dims and, with
- * D = 128, of half of the weights, which is kept: an output's error is about 1.45 times
- * that of its own rounding (for normally distributed inputs).
+ * Sums are fp32.  On the tensor cores softmax weights are rounded to bf16 on the way in,
+ * and so are rotated queries (their sines are off by 2^-21).  With RoPE, what that leaves
+ * of 64 of the query's dims and, with D = 128, of half of the weights is kept; without it
+ * queries go in as they are.  Either way an output's error is about 1.45 times that of
+ * its own rounding (for normally distributed inputs).
  * NaN or an infinity in a query, key or value reaches the rows that see it and no
  * other: values at places that a row does not see, of other requests or behind the last
  * token may be anything.  A key with a score of -inf has no weight, a row whose scores

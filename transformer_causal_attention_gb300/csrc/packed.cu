@@ -12,14 +12,14 @@
 // Tiles are numbered without a table: request b's start at floor(cu_new[b] * G / 64) + b, which
 // leaves each request at least as many numbers as it has tiles, so a block finds its request by
 // bisection and a number that nobody uses ends at once.  Blocks start with the last tiles, which see the most keys,
-// of all heads (head by head, one fp32 prompt of 2000 tokens of 8 heads took 293 us instead of 203).  With few tiles the keys
+// of all heads (head by head, one fp32 prompt of 2000 tokens of 8 heads took 293 us instead of 215).  With few tiles the keys
 // of each are cut into equal parts and a second kernel joins the parts of a row by their log-sum-exps.
 //
 // fp32 with head dims up to 128 has a kernel of its own, packed_f32_kernel: the same tiles, but K and V in
 // shared memory as they lie in the cache, copied asynchronously, and packed pairs of FMAs.  Where there is room, K and V have
 // two stages, and a tile one barrier: 64 dims in two blocks per SM, 128 in one (with values of 64 dims or fewer and keys of
 // more, one stage: K of the next tile comes while this one's P V runs, V while the next scores do).  8 prompts of up to 500
-// tokens, 12 heads of 64 dims: 80 us, 16 TFLOP/s; 4 x 128 tokens behind 2000, 32 heads over 8 of 128 dims: 553 us, 31 TFLOP/s
+// tokens, 12 heads of 64 dims: 73 us, 17 TFLOP/s; 4 x 128 tokens behind 2000, 32 heads over 8 of 128 dims: 553 us, 31 TFLOP/s
 // (one stage: 573).  A tile of 64 keys takes a block some 7 us, whether it has an SM for itself or shares it: its chain of
 // shared-memory reads, FMAs and shuffles has too few warps to hide behind.  (Three blocks per SM spill; 8 x 4 scores per
 // thread of 128 threads, and weights twice in shared memory so that they are read as pairs, were not faster.)
@@ -604,8 +604,11 @@ __global__ void __launch_bounds__(kThreads) packed_combine_kernel(const __grid_c
 long long tile_numbers(const PackedArgs& a) {
   return static_cast<long long>(a.T) * (a.n_h / a.n_kv) / R + a.B;
 }
-// Parts of a tile's keys, at most: as many as leave all blocks running at once, two per SM.  (A second wave costs as much
-// as the first: with half as many parts again, 6 requests of up to 16 drafts took half as long again.  Two to four parts of
+// Parts of a tile's keys, at most: as many as make two blocks per SM of a GB300 (152; a constant, as the workspace is sized
+// by it).  With fp32 heads of up to 64 value dims, and in packed_kernel up to 256 value and some 270 query dims, these all run
+// at once.  (A second wave costs as much as the first: with half as many parts again, 6 requests of up to 16 drafts took half
+// as long again.)  Where shared memory or registers leave room for one block per SM - packed_f32_kernel<2, 2>, and
+// packed_kernel with more dims, as MLA's 576 - they run in two waves of parts half as long.  (Two to four parts of
 // 256 keys or more where there are one to four waves made 8 prompts of up to 500 tokens, 12 heads, up to 14% slower, and 4 x
 // 128 tokens behind 2000, 32 heads, 7% to 11%.  Not by the table's width: tables are as wide as a request may grow.)
 int splits(const PackedArgs& a) {

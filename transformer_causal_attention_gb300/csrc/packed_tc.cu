@@ -21,13 +21,15 @@
 // two bf16 values, the second for 64 dims (from the start of the rotated span on), and with D = 128 the weights of
 // each tile's last 64 keys are such sums too; the other weights are rounded to bf16 once.  One bf16 for both made the output's
 // error against 64 bits 1.7 times that of its own rounding behind 30000 keys (normally distributed inputs); so it is
-// 1.41 to 1.44 times.  That is half as many MMAs again with D = 128, and a quarter with D = 64, on the K and V
-// tiles that are there anyway (4 x 8192 tokens, 32 heads over 8: 2.0 ms; without RoPE, with weights rounded once, 1.4 ms).
+// 1.41 to 1.44 times, as without RoPE, where queries are exact and weights are rounded once.  The second parts are half as
+// much work again for the tensor pipe, with D = 128 (24 MMAs of 128 columns for 16 per row tile and 128 keys) and with D = 64 (4
+// of 128 columns beside 4 of 128 and 8 of 64), on the K and V tiles that are there anyway: 4 x 8192 tokens, 32 heads
+// over 8, 2.0 to 2.1 ms, without RoPE 1.4 to 1.5; with 64 dims 1.23 and 1.12.
 //
 // What a row does not see.  Scores are masked by index.  A value whose weight is 0 still meets the MMA, so in
 // the tiles that some row sees in part ("care" tiles: the last ones of a segment) warp 3 clears value rows
 // behind the last key and replaces infinities and NaN by 0, noting their keys; the epilogue adds such
-// values to the rows that do see them.  The rest of the tiles is seen whole by every row.
+// values, times their weights, to the rows that do see them.  The rest of the tiles is seen whole by every row.
 //
 // A CTA (384 threads): warp 0 loads K tiles by TMA, warp 2 query rows and V tiles, a lane per box (two stages of
 // each fill what shared memory both parts of two query tiles leave); warp 1 issues the MMAs; warp 3
@@ -37,12 +39,14 @@
 //
 // Bounds.  Long prompts: the tensor pipe (1 x 8192 tokens, 32 heads over 8, D = 128, RoPE: its counter is active 82% of
 // the time; a turn of a pair piece - two row tiles, 128 keys - is 48 MMAs of 64 cycles and takes 3500 to 3600).  4 x 8192:
-// 2.0 ms, 1.1 PFLOP/s as the formula counts and 1.65 as issued.  Drafts behind long caches: HBM (59 requests of 32
-// drafts behind 4096 to 8192 tokens: 1.53 GB read in 248 us, 6.2 TB/s).  Few short requests: the chain launch, walk, TMA,
-// MMA, softmax, MMA, store, and a join (one prompt of 77 tokens 15 us).  What limits beside these is instruction fetch:
-// five programs run side by side on an SM, and their hot loops have to fit its instruction cache together, so loops stay
-// rolled, rare code is out of line, and a start or end of a piece (some 11000 to 14000 cycles beside its turns) costs more
-// in cold code than in work.
+// 2.0 to 2.1 ms, 1.05 to 1.1 PFLOP/s as the formula counts and 1.6 as issued.  Drafts behind long caches: HBM (59 requests of 32
+// drafts behind 4096 to 8192 tokens: 1.53 GB read in 243 us, 6.3 TB/s).  Few short requests: the chain launch, walk, TMA,
+// MMA, softmax, MMA, store, and a join (one prompt of 77 tokens 14 us).  Heads of 64 dims: neither the tensor pipe (59% of
+// the time, 1 x 8192 tokens) nor the exponentials (39% of their pipe).  Short prompts, where a start and end of a piece costs
+// some 11000 to 14000 cycles beside its turns (16 prompts): per instruction issued, warps wait 3.5 cycles on long scoreboards
+// (memory, TMEM and the like) and 0.77 for an instruction; in one long prompt 3.8 and 0.25, with 0.16 requests per cycle to
+// a group of SMs' instruction cache instead of 0.43.  Five programs run side by side on an SM, so loops stay rolled and rare
+// code is out of line.
 #include <math.h>
 
 #include <atomic>
