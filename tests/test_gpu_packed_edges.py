@@ -158,6 +158,22 @@ def test_rows_without_any_weight_stay_zero(lib, n_h, n_kv, D, dtype):  # noqa: F
         assert torch.isfinite(out).all() and torch.isfinite(lse[:, heads:]).all() and torch.isfinite(lse[news[0]:]).all()
 
 
+@pytest.mark.parametrize("n_h,n_kv,D,dtype", ALL)
+@pytest.mark.parametrize("tree", [False, True])
+def test_what_the_workspace_held_does_not_matter(lib, n_h, n_kv, D, dtype, tree):  # noqa: F811
+    """Parts that hold nothing for some rows (a row tile behind its last key among them) come out alike from a workspace
+    of NaN and one of zeros; the key axis is cut at other places from case to case."""
+    for news, ctx in (([130], 0), ([200], 60), ([257, 3], 500), ([300], 1000), ([700], 90), ([1500, 140], 0), ([128], 3000)):
+        if tree:
+            news = [min(n, 128) for n in news]
+        s = Step(news, [ctx] * len(news), n_h, n_kv, D, dtype=dtype, tree=tree, base=1e4, seed=ctx + news[0])
+        args = s.tensors()
+        n = lib.packed_workspace_size(s.T, len(news), n_h, n_kv, D, D, 16, s.table.shape[1], s.k.dtype)
+        got = [s.run(lib, args, workspace=torch.full((n,), fill, dtype=torch.uint8, device=DEV)) for fill in (0, 255)]
+        assert torch.isfinite(got[1][0]).all()
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 # ------------------------------------------------------------------------------------------- two-part queries and weights
 def step_error(s, lib):  # noqa: F811
     """The error of bf16 outputs against 64 bits, over that of the reference's own rounding to bf16 (norms)."""
